@@ -13,7 +13,8 @@ LIB = os.path.join(PKG, "libqlinear.so")
 ARCH = "gfx950"
 
 SOURCES = ["k_quant.hip", "k_gemm.hip", "k_gemm1.hip", "k_misc.hip", "k_probe.hip",
-           "qlinear_api.cpp", "gamp.cpp"]
+           "k_lora.hip", "k_norm.hip", "k_clip.hip",
+           "qlinear_api.cpp", "qlinear_ops.cpp", "gamp.cpp"]
 
 # -ffp-contract=off: the epilogue's multiply-then-add order is part of the
 # numerics (no fused multiply-add). Correctly rounded fp32 division is the

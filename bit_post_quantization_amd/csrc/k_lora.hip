@@ -1,0 +1,565 @@
+// Low-rank adapters of many requests beside one shared projection.
+//
+//   forward   S = X A_a^T            (k_lora_shrink)
+//             Y = base + scale_a S B_a^T           (k_lora_expand)
+//   backward  dS = scale_a dY B_a    (k_lora_shrink)
+//             dX = dS A_a, dA_a = dS^T X           (k_lora_outer, one reading of X)
+//             dB_a = scale_a dY^T S  (k_lora_outer)
+//             sums over row ranges   (k_lora_slot_sum)
+//
+// A tile of rows never spans two requests, so it has one adapter; each
+// workgroup finds its tile from the request offsets by one scan over them.
+// Products run on the matrix cores in fp32 (v_mfma_f32_16x16x4_f32: bf16
+// inputs are widened exactly), sums are fp32 and no atomics are used, so a
+// call gives the same bits every time.
+#include "ql_device.h"
+#include "ql_ops.h"
+
+namespace ql {
+
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16;
+typedef bf16 v8h __attribute__((ext_vector_type(8)));
+typedef bf16 v4h __attribute__((ext_vector_type(4)));
+
+// Request and rows of tile t when every request's rows are cut into tiles of
+// T. Uniform over the wave; false past the last tile.
+struct Tile {
+  int row0, rows, adapter;
+};
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+__device__ bool find_tile(const Requests& q, int T, int t, Tile& out) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int done = 0;
+  for (int base = 0; base < q.n; base += kWave) {
+    const int i = base + lane;
+    int b = 0, e = 0;
+    if (i < q.n) {
+      b = clampi(q.off[i], 0, q.rows);
+      e = clampi(q.off[i + 1], b, q.rows);
+    }
+    const int nt = (e - b + T - 1) / T;
+    const int incl = wave_scan(nt, lane);
+    const int total = __builtin_amdgcn_readlane(incl, kWave - 1);
+    if (t < done + total) {
+      const int src = __ffsll((unsigned long long)__ballot(done + incl > t)) - 1;
+      const int first = done + __builtin_amdgcn_readlane(incl - nt, src);
+      const int rb = __builtin_amdgcn_readlane(b, src);
+      const int re = __builtin_amdgcn_readlane(e, src);
+      out.row0 = rb + (t - first) * T;
+      out.rows = min(T, re - out.row0);
+      const int id = q.ids[base + src];
+      out.adapter = __builtin_amdgcn_readfirstlane(id >= 0 && id < q.n_adapters ? id : -1);
+      return true;
+    }
+    done += total;
+  }
+  return false;
+}
+
+__device__ __forceinline__ int rank_of(const int32_t* ranks, int a, int rank) {
+  return ranks ? clampi(ranks[a], 0, rank) : rank;
+}
+
+// NE (4 or 8) consecutive elements as fp32; `valid` of them exist (the rest
+// are zero and not read). vec: p is aligned to NE elements of bf16 / 4 of f32.
+template <int NE>
+__device__ __forceinline__ void load_n(const float* p, int valid, bool vec, float (&v)[NE]) {
+  if (vec && valid >= NE) {
+#pragma unroll
+    for (int c = 0; c < NE / 4; ++c) {
+      const v4f x = *reinterpret_cast<const v4f*>(p + 4 * c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * c + e] = x[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < NE; ++e) v[e] = e < valid ? p[e] : 0.0f;
+  }
+}
+template <int NE>
+__device__ __forceinline__ void load_n(const bf16* p, int valid, bool vec, float (&v)[NE]) {
+  if (vec && valid >= NE) {
+    typedef bf16 vh __attribute__((ext_vector_type(NE)));
+    const vh x = *reinterpret_cast<const vh*>(p);
+#pragma unroll
+    for (int e = 0; e < NE; ++e) v[e] = (float)x[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < NE; ++e) v[e] = e < valid ? (float)p[e] : 0.0f;
+  }
+}
+
+__device__ __forceinline__ v4f mfma_f32(float a, float b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------ shrink ----
+// One workgroup: a tile of MT * 16 rows, one column split. Its four waves take
+// every fourth 32-column step and their sums are joined in LDS. In a step lane
+// l holds columns 8 (l / 16) .. + 7 of row l % 16 of both operands; element e
+// of all lanes is one 16x16x4 product (the order of the columns inside a sum
+// is free).
+template <typename XT, typename WT, int RT, int MT, bool WCOLS>
+__global__ __launch_bounds__(256) void k_lora_shrink(ShrinkArgs a, bool vec) {
+  constexpr int kRows = MT * 16;
+  __shared__ float red[3][kRows][RT * 16 + 4];
+  Tile t;
+  if (!find_tile(a.q, kRows, blockIdx.x, t) || t.adapter < 0) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const int64_t mtot = (int64_t)a.q.rows * a.halves;
+  const int64_t row0 = (int64_t)blockIdx.z * a.q.rows + t.row0;
+  const int c0 = blockIdx.y * a.split_len, c1 = min(a.D, c0 + a.split_len);
+  const XT* P = reinterpret_cast<const XT*>(a.P);
+  const WT* W = reinterpret_cast<const WT*>(a.W) + (int64_t)t.adapter * a.rank * a.D;
+  const XT* prow[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) prow[m] = P + (row0 + min(m * 16 + r16, t.rows - 1)) * a.ldp;
+  int wj[RT];  // stored rank row of this lane (clamped: its products are dropped at the end)
+#pragma unroll
+  for (int r = 0; r < RT; ++r) wj[r] = min(r * 16 + r16, a.rank - 1);
+  v4f acc[MT][RT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[m][r] = v4f{0, 0, 0, 0};
+  for (int c = c0 + wave * kShrinkStep; c < c1; c += 4 * kShrinkStep) {
+    const int k = c + 8 * g;
+    const int valid = c1 - k;
+    float x[MT][8], w[RT][8];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) load_n<8>(prow[m] + k, valid, vec, x[m]);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      if constexpr (WCOLS) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          w[r][e] = e < valid ? (float)W[(int64_t)(k + e) * a.rank + wj[r]] : 0.0f;
+      } else {
+        load_n<8>(W + (int64_t)wj[r] * a.D + k, valid, true, w[r]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[m][r] = mfma_f32(w[r][e], x[m][e], acc[m][r]);
+  }
+  // acc[m][r][i]: row m * 16 + lane % 16, rank r * 16 + 4 g + i
+  if (wave > 0) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        *reinterpret_cast<v4f*>(&red[wave - 1][m * 16 + r16][r * 16 + 4 * g]) = acc[m][r];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  const int ra = rank_of(a.ranks, t.adapter, a.rank);
+  const float sc = a.scales ? a.scales[t.adapter] : 1.0f;
+  float* out = a.part + ((int64_t)blockIdx.y * mtot + row0) * a.rank;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = m * 16 + r16;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      v4f v = acc[m][r];
+#pragma unroll
+      for (int u = 0; u < 3; ++u) v += *reinterpret_cast<v4f*>(&red[u][row][r * 16 + 4 * g]);
+      if (row >= t.rows) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = r * 16 + 4 * g + i;
+        if (j < a.rank) out[(int64_t)row * a.rank + j] = j < ra ? v[i] * sc : 0.0f;
+      }
+    }
+  }
+}
+
+// Four consecutive rank elements j.. of one row of the summed splits; elements
+// from `ra` on are zero.
+__device__ __forceinline__ void load_s4(const float* part, int splits, int64_t stride, int64_t row,
+                                        int rank, int j, int ra, float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = 0.0f;
+  const float* p = part + row * rank + j;
+  for (int s = 0; s < splits; ++s, p += stride) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e < ra) v[e] += p[e];
+  }
+}
+
+// ------------------------------------------------------------------ expand ----
+// One workgroup: a tile of MT * 16 rows times four waves of NI column tiles of
+// 16. The rows' S stays in registers; B's rows and base are streamed.
+template <typename WT, int RT, int MT, int NI>
+__global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs a, bool vec, bool bvec) {
+  constexpr int kRows = MT * 16;
+  Tile t;
+  if (!find_tile(a.q, kRows, blockIdx.x, t)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const int64_t mtot = (int64_t)a.q.rows * a.halves;
+  const bool bare = t.adapter < 0;
+  if (bare && a.base == a.Y && !a.S) return;
+  const int ra = bare ? 0 : rank_of(a.ranks, t.adapter, a.rank);
+  const float sc = bare ? 0.0f : a.scales ? a.scales[t.adapter] : 1.0f;
+  float s[MT][RT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = t.row0 + min(m * 16 + r16, t.rows - 1);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int j = r * 16 + 4 * g;
+      load_s4(a.part, a.splits, mtot * a.rank, row, a.rank, j, ra, s[m][r]);
+      float u[4];
+      if (a.halves == 2)
+        load_s4(a.part, a.splits, mtot * a.rank, row + a.q.rows, a.rank, j, ra, u);
+      if (a.S && blockIdx.y == 0 && wave == 0 && m * 16 + r16 < t.rows) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < a.rank) {
+            a.S[(int64_t)row * a.rank + j + e] = s[m][r][e];
+            if (a.halves == 2) a.S[((int64_t)row + a.q.rows) * a.rank + j + e] = u[e];
+          }
+      }
+      if (a.halves == 2) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[m][r][e] = u[e] + a.w * (s[m][r][e] - u[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[m][r][e] *= sc;
+    }
+  }
+  if (bare && a.base == a.Y) return;
+  const WT* B = reinterpret_cast<const WT*>(a.B) + (int64_t)(bare ? 0 : t.adapter) * a.N * a.rank;
+  for (int it = 0; it < NI; ++it) {
+    const int n0 = ((blockIdx.y * NI + it) * 4 + wave) * 16;
+    if (n0 >= a.N) return;
+    v4f acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = v4f{0, 0, 0, 0};
+    if (!bare) {
+      const WT* brow = B + (int64_t)min(n0 + r16, a.N - 1) * a.rank;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float b[4];
+        const int j = r * 16 + 4 * g;
+        load_n<4>(brow + j, ra - j, bvec, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            acc[m] = vec ? mfma_f32(b[e], s[m][r][e], acc[m]) : mfma_f32(s[m][r][e], b[e], acc[m]);
+      }
+    }
+    if (vec) {  // lane: row lane % 16, four consecutive columns
+      const int n = n0 + 4 * g;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int row = m * 16 + r16;
+        if (row >= t.rows || n >= a.N) continue;
+        const int64_t rr = t.row0 + row;
+        float* y = a.Y + rr * a.ldy + n;
+        const float* bp = a.base ? a.base + rr * a.ldb + n : nullptr;
+        if (n + 3 < a.N) {
+          v4f v = acc[m];
+          if (bp) v += *reinterpret_cast<const v4f*>(bp);
+          *reinterpret_cast<v4f*>(y) = v;
+        } else {
+          for (int i = 0; i < a.N - n; ++i) y[i] = bp ? bp[i] + acc[m][i] : acc[m][i];
+        }
+      }
+    } else {  // lane: column lane % 16, rows 4 g + i
+      const int n = n0 + r16;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = m * 16 + 4 * g + i;
+          if (row >= t.rows || n >= a.N) continue;
+          const int64_t rr = t.row0 + row;
+          const float bv = a.base ? a.base[rr * a.ldb + n] : 0.0f;
+          a.Y[rr * a.ldy + n] = bv + acc[m][i];
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- outer ----
+// One workgroup: 64 columns (16 a wave) of one range of rows, 32 rows at a
+// time: their Q (rank values a row) goes through LDS. Piece by piece (the rows
+// of one request in the range) the product Q^T P is summed in registers and
+// written out.
+constexpr int kOuterCols = 64;
+constexpr int kOuterRows = 32;
+
+template <typename XT, typename WT, int RT, bool DX, bool TR>
+__global__ __launch_bounds__(256) void k_lora_outer(OuterArgs a) {
+  constexpr int R = RT * 16;
+  __shared__ float qs[kOuterRows][R + 4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const int d0 = blockIdx.x * kOuterCols + wave * 16;
+  const int sp = blockIdx.y;
+  const int lo = min(sp * a.row_len, a.q.rows), hi = min(lo + a.row_len, a.q.rows);
+  const XT* P = reinterpret_cast<const XT*>(a.P);
+  XT* dX = reinterpret_cast<XT*>(a.dX);
+  const int64_t qstride = (int64_t)a.q.rows * a.rank;
+  // Requests first .. last touch this range (ends included, so that the slots
+  // s + i of neighbouring ranges join without gaps).
+  int first = 0, last = a.q.n - 1;
+  {
+    int cl = 0, ch = 0;  // requests that end at or before lo / hi
+    for (int base = 0; base < a.q.n; base += kWave) {
+      const int i = base + lane;
+      const int e = i < a.q.n ? clampi(a.q.off[i + 1], 0, a.q.rows) : 0x7fffffff;
+      cl += __popcll(__ballot(e <= lo));
+      ch += __popcll(__ballot(e <= hi));
+    }
+    if (sp > 0) first = min(cl, a.q.n - 1);
+    if (sp + 1 < (int)gridDim.y) last = min(ch, a.q.n - 1);
+  }
+  v4f acc[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) acc[r] = v4f{0, 0, 0, 0};
+  bool pending = false;
+  for (int i = first; i <= last; ++i) {
+    const int b = clampi(a.q.off[i], 0, a.q.rows), e = clampi(a.q.off[i + 1], b, a.q.rows);
+    const int r0 = max(b, lo), r1 = min(e, hi);
+    const int id = a.q.ids[i];
+    const int ad = id >= 0 && id < a.q.n_adapters ? id : -1;
+    const int ra = ad < 0 ? 0 : rank_of(a.ranks, ad, a.rank);
+    float af[RT][4];
+    if constexpr (DX) {  // A of this wave's columns: lane: column r16, ranks 4 g + e
+      const WT* A = reinterpret_cast<const WT*>(a.A) + (int64_t)max(ad, 0) * a.rank * a.D;
+      const int d = min(d0 + r16, a.D - 1);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int j = r * 16 + 4 * g + u;
+          af[r][u] = j < ra ? (float)A[(int64_t)j * a.D + d] : 0.0f;
+        }
+    }
+    for (int m0 = r0; m0 < r1; m0 += kOuterRows) {
+      __syncthreads();
+      for (int u = threadIdx.x; u < kOuterRows * R; u += 256) {
+        const int m = u / R, j = u % R;
+        float v = 0.0f;
+        if (m0 + m < r1 && j < ra) {
+          const float* p = a.part + (int64_t)(m0 + m) * a.rank + j;
+          for (int s = 0; s < a.q_splits; ++s) v += p[s * qstride];
+        }
+        qs[m][j] = v;
+      }
+      __syncthreads();
+      if (ad >= 0) {
+        const int d = d0 + r16;
+#pragma unroll
+        for (int kk = 0; kk < kOuterRows / 4; ++kk) {
+          const int m = kk * 4 + g;
+          const float p = d < a.D && m0 + m < r1 ? (float)P[(int64_t)(m0 + m) * a.ldp + d] : 0.0f;
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const float qv = qs[m][r * 16 + r16];
+            acc[r] = TR ? mfma_f32(qv, p, acc[r]) : mfma_f32(p, qv, acc[r]);
+          }
+        }
+      }
+      if constexpr (DX) {
+#pragma unroll
+        for (int mt = 0; mt < kOuterRows / 16; ++mt) {
+          v4f v{0, 0, 0, 0};
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const v4f qv = *reinterpret_cast<const v4f*>(&qs[mt * 16 + r16][r * 16 + 4 * g]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v = mfma_f32(af[r][u], qv[u], v);
+          }
+          const int m = m0 + mt * 16 + r16;
+          if (m < r1) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int d = d0 + 4 * g + u;
+              if (d < a.D) dX[(int64_t)m * a.lddx + d] = (XT)v[u];
+            }
+          }
+        }
+      }
+      pending = pending || ad >= 0;
+    }
+    // Write the sum unless the next request goes on with the same adapter.
+    bool flush = pending;
+    if (pending && i < last) {
+      const int nid = a.q.ids[i + 1];
+      flush = nid != id;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.slot_id[sp + i] = flush ? ad : -1;
+    if (flush) {
+      float* out = a.out + (int64_t)(sp + i) * a.D * a.rank;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int j = TR ? r * 16 + 4 * g + u : r * 16 + r16;
+          const int d = TR ? d0 + r16 : d0 + 4 * g + u;
+          if (j < a.rank && d < a.D)
+            out[TR ? (int64_t)j * a.D + d : (int64_t)d * a.rank + j] = acc[r][u];
+        }
+        acc[r] = v4f{0, 0, 0, 0};
+      }
+      pending = false;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- slot sum ----
+template <typename WT>
+__global__ __launch_bounds__(256) void k_lora_slot_sum(SlotSumArgs a) {
+  const int64_t len = (int64_t)a.D * a.rank;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int ad = blockIdx.y;
+  float v = 0.0f;
+  for (int s = 0; s < a.slots; ++s) {
+    if (a.slot_id[s] != ad) continue;
+    if (e < len) v += a.part[s * len + e];
+  }
+  if (e >= len) return;
+  const int j = a.transposed ? (int)(e / a.D) : (int)(e % a.rank);
+  const float sc = a.scales ? a.scales[ad] : 1.0f;
+  const float r = j < rank_of(a.ranks, ad, a.rank) ? v * sc : 0.0f;
+  reinterpret_cast<WT*>(a.out)[ad * len + e] = (WT)r;
+}
+
+int max_tiles(const Requests& q, int T) {
+  const int64_t t = (int64_t)q.rows / T + q.n;
+  return (int)(t < q.rows ? t : q.rows);
+}
+
+template <typename XT, typename WT, bool WCOLS>
+hipError_t shrink_rt(const ShrinkArgs& a, hipStream_t s) {
+  const bool vec = (reinterpret_cast<uintptr_t>(a.P) % 16) == 0 && (a.ldp * sizeof(XT)) % 16 == 0;
+#define QL_SHRINK(RT, MT)                                                                      \
+  hipLaunchKernelGGL((k_lora_shrink<XT, WT, RT, MT, WCOLS>),                                   \
+                     dim3(max_tiles(a.q, MT * 16), a.splits, a.halves), dim3(256), 0, s, a, vec)
+  if (a.rank <= 16)
+    QL_SHRINK(1, 1);
+  else if (a.rank <= 32)
+    QL_SHRINK(2, 1);
+  else if (a.rank <= 64)
+    QL_SHRINK(4, 1);
+  else
+    QL_SHRINK(8, 1);
+#undef QL_SHRINK
+  return hipGetLastError();
+}
+
+template <typename WT>
+hipError_t expand_rt(const ExpandArgs& a, hipStream_t s) {
+  const bool vec = (reinterpret_cast<uintptr_t>(a.Y) % 16) == 0 && a.ldy % 4 == 0 &&
+                   (!a.base || ((reinterpret_cast<uintptr_t>(a.base) % 16) == 0 && a.ldb % 4 == 0));
+  const bool bvec =
+      (reinterpret_cast<uintptr_t>(a.B) % (4 * sizeof(WT))) == 0 && a.rank % 4 == 0;
+#define QL_EXPAND(RT, MT, NI)                                                                 \
+  hipLaunchKernelGGL((k_lora_expand<WT, RT, MT, NI>),                                         \
+                     dim3(max_tiles(a.q, MT * 16), (a.N + 64 * NI - 1) / (64 * NI)), dim3(256), \
+                     0, s, a, vec, bvec)
+  if (a.rank <= 16)
+    QL_EXPAND(1, 1, 2);
+  else if (a.rank <= 32)
+    QL_EXPAND(2, 1, 2);
+  else if (a.rank <= 64)
+    QL_EXPAND(4, 1, 2);
+  else
+    QL_EXPAND(8, 1, 2);
+#undef QL_EXPAND
+  return hipGetLastError();
+}
+
+template <typename XT, typename WT, bool DX, bool TR>
+hipError_t outer_rt(const OuterArgs& a, hipStream_t s) {
+  const dim3 grid((a.D + kOuterCols - 1) / kOuterCols, a.splits);
+#define QL_OUTER(RT) \
+  hipLaunchKernelGGL((k_lora_outer<XT, WT, RT, DX, TR>), grid, dim3(256), 0, s, a)
+  if (a.rank <= 16)
+    QL_OUTER(1);
+  else if (a.rank <= 32)
+    QL_OUTER(2);
+  else if (a.rank <= 64)
+    QL_OUTER(4);
+  else
+    QL_OUTER(8);
+#undef QL_OUTER
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int lora_shrink_splits(int rows, int n_req, int D, int rank) {
+  (void)rank;
+  const int64_t tiles = (int64_t)rows / 16 + n_req;
+  int64_t s = 512 / (tiles > 0 ? tiles : 1);
+  const int64_t cap = D / 256;
+  s = s < cap ? s : cap;
+  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+}
+
+int lora_outer_splits(int rows, int D) {
+  const int cols = (D + kOuterCols - 1) / kOuterCols;
+  int64_t s = (1024 + cols - 1) / cols;
+  const int64_t cap = (rows + 63) / 64;
+  s = s < cap ? s : cap;
+  return (int)(s < 1 ? 1 : s);
+}
+
+hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t s) {
+  if (a.w_cols) {  // P is dY: fp32
+    return a.w_bf16 ? shrink_rt<float, bf16, true>(a, s) : shrink_rt<float, float, true>(a, s);
+  }
+  if (a.p_bf16)
+    return a.w_bf16 ? shrink_rt<bf16, bf16, false>(a, s) : shrink_rt<bf16, float, false>(a, s);
+  return a.w_bf16 ? shrink_rt<float, bf16, false>(a, s) : shrink_rt<float, float, false>(a, s);
+}
+
+hipError_t launch_lora_expand(const ExpandArgs& a, hipStream_t s) {
+  return a.w_bf16 ? expand_rt<bf16>(a, s) : expand_rt<float>(a, s);
+}
+
+hipError_t launch_lora_outer(const OuterArgs& a, hipStream_t s) {
+  if (!a.transposed)  // dB: P is dY, fp32; no dX
+    return outer_rt<float, float, false, false>(a, s);
+  if (a.dX) {
+    if (a.p_bf16)
+      return a.w_bf16 ? outer_rt<bf16, bf16, true, true>(a, s)
+                      : outer_rt<bf16, float, true, true>(a, s);
+    return a.w_bf16 ? outer_rt<float, bf16, true, true>(a, s)
+                    : outer_rt<float, float, true, true>(a, s);
+  }
+  return a.p_bf16 ? outer_rt<bf16, float, false, true>(a, s)
+                  : outer_rt<float, float, false, true>(a, s);
+}
+
+hipError_t launch_lora_slot_sum(const SlotSumArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(((int64_t)a.D * a.rank + 255) / 256), a.n_adapters);
+  if (a.w_bf16)
+    hipLaunchKernelGGL(k_lora_slot_sum<bf16>, grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(k_lora_slot_sum<float>, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace ql

@@ -1,0 +1,135 @@
+// Internal interface between the C ABI of the operators beside the layer
+// (qlinear_ops.cpp) and their kernels (k_lora.hip, k_norm.hip, k_clip.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/qlinear.h"
+
+namespace ql {
+
+// ---------------------------------------------------------------- adapters ----
+
+// Rows of a batch split into requests: request i owns rows [off[i], off[i+1])
+// and runs adapter ids[i] (none where that is outside [0, n_adapters)). All of
+// it is device data, so kernels clamp what they read.
+struct Requests {
+  const int32_t* off;
+  const int32_t* ids;
+  int n;
+  int rows;        // rows that the offsets partition
+  int n_adapters;
+};
+
+// part[split][row][j] = scale * sum over the split's columns d of
+// P[row][d] * W_a[j][d], for the rows of every request with an adapter.
+struct ShrinkArgs {
+  const void* P;      // [rows * halves, D], row stride ldp elements
+  int64_t ldp;
+  const void* W;      // [n_adapters, rank, D], or [n_adapters, D, rank] (w_cols)
+  const float* scales;// per adapter, or nullptr (1)
+  const int32_t* ranks;
+  Requests q;
+  int D, rank;
+  int halves;         // 2: the requests also cover rows [rows, 2 * rows)
+  int splits, split_len;  // columns per split, a multiple of kShrinkStep
+  float* part;        // [splits][rows * halves][rank]
+  bool p_bf16, w_bf16, w_cols;
+};
+constexpr int kShrinkStep = 32;
+
+// Y[row][n] = base[row][n] + scale_a * sum_j S[row][j] * B_a[n][j], with S the
+// sum of the splits, combined over the row's two halves when guided.
+struct ExpandArgs {
+  const float* part;  // [splits][rows * halves][rank]
+  int splits, halves;
+  float w;            // guidance weight (halves == 2)
+  const void* B;      // [n_adapters, N, rank]
+  const float* scales;
+  const int32_t* ranks;
+  Requests q;
+  int N, rank;
+  const float* base;  // nullptr: zero
+  float* Y;
+  int64_t ldb, ldy;
+  float* S;           // nullptr, or [rows * halves, rank]: the summed splits
+  bool w_bf16;
+};
+
+// Row ranges s = 0 .. splits-1 of row_len rows each. For every range and the
+// requests i in it, slot s + i of `out` receives the sum over the common rows
+// of Q[row][j] * P[row][d] (transposed: [j][d] for dA, else [d][j] for dB);
+// slot_id[s + i] says which adapter it belongs to (-1: nothing was written).
+// With dX, dX[row][d] = sum_j Q[row][j] * A_a[j][d] too (zero for rows without
+// an adapter).
+struct OuterArgs {
+  const void* P;      // [rows, D]
+  int64_t ldp;
+  const float* part;  // Q: [q_splits][rows][rank]
+  int q_splits;
+  const void* A;      // [n_adapters, rank, D] (dX)
+  const int32_t* ranks;
+  Requests q;
+  int D, rank;
+  void* dX;           // nullptr: none; else of P's type
+  int64_t lddx;
+  float* out;         // [slots][D * rank]
+  int32_t* slot_id;   // [slots]
+  int splits, row_len;
+  bool p_bf16, w_bf16, transposed;
+};
+
+// dW[a][e] = scale_a * sum over the slots of adapter a of part[slot][e].
+struct SlotSumArgs {
+  const float* part;
+  const int32_t* slot_id;
+  int slots, n_adapters, D, rank;
+  const float* scales;  // nullptr: 1
+  const int32_t* ranks;
+  void* out;
+  bool w_bf16, transposed;
+};
+
+hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t s);
+hipError_t launch_lora_expand(const ExpandArgs& a, hipStream_t s);
+hipError_t launch_lora_outer(const OuterArgs& a, hipStream_t s);
+hipError_t launch_lora_slot_sum(const SlotSumArgs& a, hipStream_t s);
+// Splits of a shrink over D columns for `rows` rows (halves included).
+int lora_shrink_splits(int rows, int n_req, int D, int rank);
+// Row ranges of an outer product over D columns.
+int lora_outer_splits(int rows, int D);
+
+// -------------------------------------------------------------- group norm ----
+
+struct NormArgs {
+  const void* x;
+  int64_t xb, xr;     // element strides of an image and of a position
+  const void* dy;     // gradient only
+  int64_t dyb, dyr;
+  void* y;            // y, or dx
+  int64_t yb, yr;
+  const void* gamma;
+  const void* beta;
+  int B, L, C, G;
+  float eps;
+  int act;
+  float* mean;        // [B, G]: out (may be nullptr) / in (gradient)
+  float* rstd;
+  void* dgamma;
+  void* dbeta;
+  void* ws;
+  bool x_bf16, w_bf16;
+};
+int64_t norm_ws_bytes(int B, int L, int C, int G, bool grad);
+hipError_t launch_group_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_group_norm_grad(const NormArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------- clipping ----
+
+hipError_t launch_grad_norm(const ql_grad* table, int n, int64_t units, double* partials,
+                            hipStream_t s);
+hipError_t launch_grad_clip(const ql_grad* table, int n, int64_t units, const double* partials,
+                            float max_norm, float* norm, hipStream_t s);
+
+}  // namespace ql

@@ -322,6 +322,162 @@ ql_status qlinear_cfg_combine(const float* Y, int32_t M, int32_t N, float w, flo
 ql_status qlinear_probe_mfma(const void* operands, int32_t iters, int32_t waves_per_simd,
                              int32_t* sink, int64_t sink_len, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators beside the layer: what trains, adapts and feeds a linear whose
+ * weights are frozen codes. They take no plan; the descriptors below are HOST
+ * structs holding DEVICE pointers, read during the call and not retained.
+ * Each call enqueues kernel launches only, uses the workspace that the caller
+ * passes (DEVICE, 16-byte aligned, at least the size its query gives, free for
+ * other use once the call's work is done, contents undefined) and gives the
+ * same bits every time (no atomics). Calls on different streams may run at
+ * once if their workspaces and outputs differ.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Low-rank adapters beside one shared projection (HQ-DM explainer 2.2: the
+ * weight with its adapter is W + B A; here scale_a B_a A_a, and many adapters
+ * at once). Adapter a is A_a [rank, K] and B_a [N, rank]; only its first
+ * ranks[a] rank rows / columns are used (the storage past them is not).
+ */
+typedef struct {
+  int32_t N, K;          /* as in ql_desc: 1 <= N, K % 16 == 0, 16 <= K <= 65536 */
+  int32_t rank;          /* stored rank, 1 .. 128 */
+  int32_t n_adapters;    /* 1 .. 65535 */
+  ql_dtype x_dtype;      /* X and dX */
+  ql_dtype w_dtype;      /* A, B, dA and dB */
+  const void* A;         /* DEVICE [n_adapters, rank, K], 16-byte aligned */
+  const void* B;         /* DEVICE [n_adapters, N, rank] */
+  const float* scales;   /* DEVICE [n_adapters], or NULL for 1 */
+  const int32_t* ranks;  /* DEVICE [n_adapters], clamped to [0, rank], or NULL for rank */
+} ql_lora;
+
+/* The rows of a batch by request: request i owns rows [row_offsets[i],
+ * row_offsets[i+1]) and runs adapter[i]; a value outside [0, n_adapters) is
+ * no adapter. Offsets ascend from 0 to the number of rows (a request may be
+ * empty); others are clamped, never followed out of the tensors, and the rows
+ * they leave out are unspecified. */
+typedef struct {
+  int32_t n_requests;          /* >= 1 */
+  const int32_t* row_offsets;  /* DEVICE [n_requests + 1] */
+  const int32_t* adapter;      /* DEVICE [n_requests] */
+} ql_requests;
+
+/* Workspace bytes (HOST out) of qlinear_lora (grad = 0) or qlinear_lora_grad
+ * (grad = 1) with M rows and n_requests requests. The pointers in d are not
+ * looked at. */
+ql_status qlinear_lora_workspace(const ql_lora* d, int32_t M, int32_t n_requests, int32_t grad,
+                                 int64_t* bytes);
+
+/*
+ * Y[m,:] = base[m,:] + scale_a (X[m,:] A_a^T) B_a^T for the rows of every
+ * request; rows without an adapter get base. Sums in fp32.
+ *   X     : DEVICE [M,K] of x_dtype, row stride ldx >= K elements.
+ *   cfg   : 0, or 1: the rows are conditional [0, M/2) and unconditional
+ *           [M/2, M), the offsets partition [0, M/2) and hold for both halves,
+ *           and base and Y have M/2 rows, the guided ones: the adapters'
+ *           part is d_u + w (d_c - d_u), as the combine in qlinear_gemm.
+ *   base  : DEVICE fp32, row stride ldb >= N (the output of qlinear_gemm), or
+ *           NULL for zero. May be Y itself.
+ *   Y     : DEVICE fp32 out, row stride ldy >= N; overlaps nothing else.
+ *   S     : NULL, or DEVICE fp32 out [M, rank]: X A_a^T, which qlinear_lora_grad
+ *           takes (zero past ranks[a] and for rows without an adapter).
+ * M = 0 enqueues nothing.
+ */
+ql_status qlinear_lora(const ql_lora* d, const void* X, int64_t ldx, int32_t M,
+                       const ql_requests* q, int32_t cfg, float w, const float* base, int64_t ldb,
+                       float* Y, int64_t ldy, float* S, void* workspace, int64_t workspace_bytes,
+                       void* stream);
+
+/*
+ * Gradients of qlinear_lora with cfg = 0, for dY [M,N] fp32 (row stride lddy):
+ * with dS = scale_a dY B_a,
+ *   dX : DEVICE [M,K] of x_dtype, row stride lddx, = dS A_a (the adapters' part;
+ *        zero for rows without an adapter), or NULL;
+ *   dA : DEVICE [n_adapters, rank, K] of w_dtype, = sum over the adapter's rows
+ *        of dS^T X, or NULL;
+ *   dB : DEVICE [n_adapters, N, rank] of w_dtype, = scale_a dY^T S, or NULL.
+ * Sums in fp32, rounded once. Every element of dA and dB is written (zero
+ * past ranks[a] and for adapters without rows). S as saved by qlinear_lora.
+ */
+ql_status qlinear_lora_grad(const ql_lora* d, const void* X, int64_t ldx, int32_t M,
+                            const ql_requests* q, const float* S, const float* dY, int64_t lddy,
+                            void* dX, int64_t lddx, void* dA, void* dB, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+
+/*
+ * Group normalisation with an activation over channels-last images: the
+ * images that a diffusion network's linears and convolutions read.
+ * An image is [positions, channels]; element (b, l, c) of x lies at
+ * b * batch stride + l * row stride + c (strides in elements, row stride >=
+ * channels), so an NHWC tensor or a slice of its channels is taken as it is.
+ */
+typedef enum { QL_ACT_NONE = 0, QL_ACT_SILU = 1 } ql_act;
+typedef struct {
+  int32_t batch, positions;   /* >= 0; batch <= 65535 */
+  int32_t channels, groups;   /* 1 .. 8192 channels, a multiple of groups; groups <= 2048 */
+  ql_dtype x_dtype;           /* x, y, dy, dx */
+  ql_dtype w_dtype;           /* gamma, beta, dgamma, dbeta */
+  ql_act act;
+  float eps;                  /* > 0 */
+  const void* gamma;          /* DEVICE [channels], or NULL for 1 */
+  const void* beta;           /* DEVICE [channels], or NULL for 0 */
+} ql_norm;
+
+/* Workspace bytes (HOST out) of qlinear_group_norm (grad = 0) or
+ * qlinear_group_norm_grad (grad = 1). */
+ql_status qlinear_group_norm_workspace(const ql_norm* d, int32_t grad, int64_t* bytes);
+
+/*
+ * z = (x - mean) rstd gamma + beta with the mean and 1 / sqrt(variance + eps)
+ * of the image's group (biased variance); y = z, or z / (1 + exp(-z)) (SILU).
+ * Statistics are joined in fp64. y may be x itself with the same strides.
+ *   mean, rstd : NULL, or DEVICE fp32 out [batch, groups] for the gradient.
+ */
+ql_status qlinear_group_norm(const ql_norm* d, const void* x, int64_t x_batch, int64_t x_row,
+                             void* y, int64_t y_batch, int64_t y_row, float* mean, float* rstd,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Gradients for dy: dx (may be dy or x itself with the same strides), and
+ * dgamma, dbeta [channels] of w_dtype (either may be NULL), from x and the
+ * mean and rstd that the forward call gave. Sums in fp32 or wider.
+ */
+ql_status qlinear_group_norm_grad(const ql_norm* d, const void* dy, int64_t dy_batch,
+                                  int64_t dy_row, const void* x, int64_t x_batch, int64_t x_row,
+                                  const float* mean, const float* rstd, void* dx, int64_t dx_batch,
+                                  int64_t dx_row, void* dgamma, void* dbeta, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
+/*
+ * Global norm of many gradients and their clipping. The tensors are listed in
+ * a DEVICE table, cut into units of QL_GRAD_UNIT elements (each tensor's last
+ * one may be short): entry i covers units [start_i, start_i + ceil(n_i /
+ * QL_GRAD_UNIT)), with start_0 = 0 and start_i+1 the end of entry i.
+ */
+#define QL_GRAD_UNIT 4096
+#define QL_GRAD_PARTIALS 1024
+typedef struct {
+  const void* src;    /* contiguous, aligned to its element; NULL is skipped */
+  void* dst;          /* qlinear_grad_clip: out; src itself (same dtype) for in place */
+  int64_t n;          /* elements, >= 0 */
+  int64_t start;      /* first unit */
+  int32_t src_dtype, dst_dtype; /* ql_dtype */
+} ql_grad;
+
+/* partials[p], p < QL_GRAD_PARTIALS: sums of squares (fp64) whose total is the
+ * square of the norm of the listed tensors. Where gradients are sharded over
+ * processes, add the ranks' partials (an all-reduce) before qlinear_grad_clip.
+ *   table : DEVICE [n] as above, n >= 0;  units : the end of the last entry. */
+ql_status qlinear_grad_norm(const ql_grad* table, int32_t n, int64_t units, double* partials,
+                            void* stream);
+
+/* norm (DEVICE fp32 out [1]) = sqrt(sum of partials); dst = src * coef with
+ * coef = min(1, max_norm / (norm + 1e-6)), rounded once to dst's type. An
+ * infinite norm gives coef 0 (infinite elements become NaN), a NaN norm makes
+ * every element NaN. In place with coef = 1 nothing is written. */
+ql_status qlinear_grad_clip(const ql_grad* table, int32_t n, int64_t units, const double* partials,
+                            float max_norm, float* norm, void* stream);
+
 /* Message for the last non-OK status on this thread ("" if none). */
 const char* qlinear_last_error(void);
 
