@@ -190,112 +190,375 @@ __global__ __launch_bounds__(256) void k_lora_shrink(ShrinkArgs a, bool vec) {
   }
 }
 
-// Four consecutive rank elements j.. of one row of the summed splits; elements
-// from `ra` on are zero.
-__device__ __forceinline__ void load_s4(const float* part, int splits, int64_t stride, int64_t row,
-                                        int rank, int j, int ra, float (&v)[4]) {
+// ----------------------------------------------------------------- forward ----
+// One workgroup: a tile of MT * 16 rows (of both halves when guided) and a
+// share of the output columns. First the tile's S = X A^T, the waves taking
+// every NW-th chunk of K and joining their sums in LDS; then the waves stream
+// 32 columns at a time: base in, base + S B^T out. S never leaves the
+// workgroup, so nothing is put through memory between the two products; the
+// workgroups that share a tile each compute its S.
+//
+// With bf16 adapters the second product runs on bf16 matrix instructions: S is
+// split into three bf16 terms whose sum is S to 24 bits, so that no digit of
+// fp32 is given up (B is bf16 already), at a fifth of the fp32 rate's cost.
+
+__device__ __forceinline__ v4f mfma_bf16(v8h a, v8h b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// v = h + m + l with bf16 terms (24 bits together); a non-finite v stays in h.
+__device__ __forceinline__ void split3(float v, bf16& h, bf16& m, bf16& l) {
+  h = (bf16)v;
+  const float r = __builtin_isfinite((float)h) ? v - (float)h : 0.0f;
+  m = (bf16)r;
+  l = (bf16)(r - (float)m);
+}
+
+// One operand of a 32-column step: elements 8 g .. 8 g + 7 of a row.
+template <typename T>
+struct Frag8;
+template <>
+struct Frag8<bf16> {
+  v8h v;
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const v8h*>(p); }
+  __device__ __forceinline__ void load(const bf16* p, int valid) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = 0.0f;
-  const float* p = part + row * rank + j;
-  for (int s = 0; s < splits; ++s, p += stride) {
+    for (int e = 0; e < 8; ++e) v[e] = e < valid ? p[e] : (bf16)0.0f;
+  }
+  __device__ __forceinline__ float get(int e) const { return (float)v[e]; }
+};
+template <>
+struct Frag8<float> {
+  v4f a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const v4f*>(p);
+    b = *reinterpret_cast<const v4f*>(p + 4);
+  }
+  __device__ __forceinline__ void load(const float* p, int valid) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (j + e < ra) v[e] += p[e];
+    for (int e = 0; e < 4; ++e) {
+      a[e] = e < valid ? p[e] : 0.0f;
+      b[e] = e + 4 < valid ? p[e + 4] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ float get(int e) const { return e < 4 ? a[e] : b[e - 4]; }
+};
+
+// c += a b over 32 columns (the order of the columns within a sum is free).
+template <typename TA, typename TB>
+__device__ __forceinline__ v4f step32(const Frag8<TA>& a, const Frag8<TB>& b, v4f c) {
+  if constexpr (sizeof(TA) == 2 && sizeof(TB) == 2) {
+    return mfma_bf16(a.v, b.v, c);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = mfma_f32(a.get(e), b.get(e), c);
+    return c;
   }
 }
 
-// ------------------------------------------------------------------ expand ----
-// One workgroup: a tile of MT * 16 rows times four waves of NI column tiles of
-// 16. The rows' S stays in registers; B's rows and base are streamed.
-template <typename WT, int RT, int MT, int NI>
-__global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs a, bool vec, bool bvec) {
-  constexpr int kRows = MT * 16;
+// S fragments of MT row tiles in registers, for products with rows of B.
+template <typename WT, int RT, int MT>
+struct SFrag;
+template <int RT, int MT>
+struct SFrag<float, RT, MT> {  // element e: rank 16 r + 4 g + e
+  v4f s[MT][RT];
+  __device__ __forceinline__ void load(const float* lds, int ld, int r16, int g) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        s[m][r] = *reinterpret_cast<const v4f*>(lds + (m * 16 + r16) * ld + r * 16 + 4 * g);
+  }
+};
+template <int RT, int MT>
+struct SFrag<bf16, RT, MT> {  // element e: rank 32 k + 8 g + e (RT = 1: see below)
+  static constexpr int KS = RT == 1 ? 2 : 3 * RT / 2;
+  v8h s[MT][KS];
+  __device__ __forceinline__ void load(const float* lds, int ld, int r16, int g) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float* p = lds + (m * 16 + r16) * ld;
+      if constexpr (RT == 1) {  // 16 ranks: terms h and m in one product, l in the other
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          bf16 h, mi, l;
+          split3(p[8 * (g & 1) + e], h, mi, l);
+          s[m][0][e] = g < 2 ? h : mi;
+          s[m][1][e] = g < 2 ? l : (bf16)0.0f;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < RT / 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            bf16 h, mi, l;
+            split3(p[32 * k + 8 * g + e], h, mi, l);
+            s[m][3 * k][e] = h;
+            s[m][3 * k + 1][e] = mi;
+            s[m][3 * k + 2][e] = l;
+          }
+      }
+    }
+  }
+};
+
+// One row of B (16 RT ranks at most, `ra` of them used), shared by all rows of S.
+template <typename WT, int RT>
+struct BFrag;
+template <int RT>
+struct BFrag<float, RT> {
+  float b[RT][4];
+  __device__ __forceinline__ void load(const float* row, int ra, bool vec, int g) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) load_n<4>(row + r * 16 + 4 * g, ra - r * 16 - 4 * g, vec, b[r]);
+  }
+  template <bool SWAP, int MT>
+  __device__ __forceinline__ v4f times(const SFrag<float, RT, MT>& s, int m) const {
+    v4f c{0, 0, 0, 0};
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        c = SWAP ? mfma_f32(s.s[m][r][e], b[r][e], c) : mfma_f32(b[r][e], s.s[m][r][e], c);
+    return c;
+  }
+};
+template <int RT>
+struct BFrag<bf16, RT> {
+  static constexpr int KB = RT == 1 ? 1 : RT / 2;
+  v8h b[KB];
+  __device__ __forceinline__ void load(const bf16* row, int ra, bool vec, int g) {
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int j = RT == 1 ? 8 * (g & 1) : 32 * k + 8 * g;
+      if (vec && ra - j >= 8) {
+        b[k] = *reinterpret_cast<const v8h*>(row + j);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[k][e] = j + e < ra ? row[j + e] : (bf16)0.0f;
+      }
+    }
+  }
+  template <bool SWAP, int MT>
+  __device__ __forceinline__ v4f times(const SFrag<bf16, RT, MT>& s, int m) const {
+    v4f c{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < SFrag<bf16, RT, MT>::KS; ++k) {
+      const v8h bk = b[RT == 1 ? 0 : k / 3];
+      c = SWAP ? mfma_bf16(s.s[m][k], bk, c) : mfma_bf16(bk, s.s[m][k], c);
+    }
+    return c;
+  }
+};
+
+template <typename XT, typename WT, int RT, int MT, int H, int NW, bool YVEC>
+__global__ __launch_bounds__(64 * NW) void k_lora_forward(ForwardArgs a, bool xvec, bool bvec) {
+  constexpr int T = MT * 16, R = RT * 16, LD = R + 4;
+  constexpr int CH = sizeof(XT) == 2 ? 64 : 32;  // columns of 128 bytes of X
+  __shared__ __align__(16) float red[NW][H * T][LD];
+  // Workgroups of one tile follow each other on one chiplet (workgroup ids go
+  // round the eight of them), so that they find the tile's X in its L2.
+  const int xcd = blockIdx.x & 7, loc = blockIdx.x >> 3;
+  const int tile = loc / a.shares * 8 + xcd, share = loc % a.shares;
   Tile t;
-  if (!find_tile(a.q, kRows, blockIdx.x, t)) return;
+  if (!find_tile(a.q, T, tile, t)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  const int64_t mtot = (int64_t)a.q.rows * a.halves;
   const bool bare = t.adapter < 0;
   if (bare && a.base == a.Y && !a.S) return;
   const int ra = bare ? 0 : rank_of(a.ranks, t.adapter, a.rank);
   const float sc = bare ? 0.0f : a.scales ? a.scales[t.adapter] : 1.0f;
-  float s[MT][RT][4];
+  if (!bare) {
+    const XT* X = reinterpret_cast<const XT*>(a.X);
+    const WT* A = reinterpret_cast<const WT*>(a.A) + (int64_t)t.adapter * a.rank * a.K;
+    const XT* xp[H * MT];
+    const WT* wp[RT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = t.row0 + min(m * 16 + r16, t.rows - 1);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int j = r * 16 + 4 * g;
-      load_s4(a.part, a.splits, mtot * a.rank, row, a.rank, j, ra, s[m][r]);
-      float u[4];
-      if (a.halves == 2)
-        load_s4(a.part, a.splits, mtot * a.rank, row + a.q.rows, a.rank, j, ra, u);
-      if (a.S && blockIdx.y == 0 && wave == 0 && m * 16 + r16 < t.rows) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + e < a.rank) {
-            a.S[(int64_t)row * a.rank + j + e] = s[m][r][e];
-            if (a.halves == 2) a.S[((int64_t)row + a.q.rows) * a.rank + j + e] = u[e];
-          }
-      }
-      if (a.halves == 2) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[m][r][e] = u[e] + a.w * (s[m][r][e] - u[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[m][r][e] *= sc;
-    }
-  }
-  if (bare && a.base == a.Y) return;
-  const WT* B = reinterpret_cast<const WT*>(a.B) + (int64_t)(bare ? 0 : t.adapter) * a.N * a.rank;
-  for (int it = 0; it < NI; ++it) {
-    const int n0 = ((blockIdx.y * NI + it) * 4 + wave) * 16;
-    if (n0 >= a.N) return;
-    v4f acc[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m] = v4f{0, 0, 0, 0};
-    if (!bare) {
-      const WT* brow = B + (int64_t)min(n0 + r16, a.N - 1) * a.rank;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float b[4];
-        const int j = r * 16 + 4 * g;
-        load_n<4>(brow + j, ra - j, bvec, b);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            acc[m] = vec ? mfma_f32(b[e], s[m][r][e], acc[m]) : mfma_f32(s[m][r][e], b[e], acc[m]);
-      }
-    }
-    if (vec) {  // lane: row lane % 16, four consecutive columns
-      const int n = n0 + 4 * g;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int row = m * 16 + r16;
-        if (row >= t.rows || n >= a.N) continue;
-        const int64_t rr = t.row0 + row;
-        float* y = a.Y + rr * a.ldy + n;
-        const float* bp = a.base ? a.base + rr * a.ldb + n : nullptr;
-        if (n + 3 < a.N) {
-          v4f v = acc[m];
-          if (bp) v += *reinterpret_cast<const v4f*>(bp);
-          *reinterpret_cast<v4f*>(y) = v;
-        } else {
-          for (int i = 0; i < a.N - n; ++i) y[i] = bp ? bp[i] + acc[m][i] : acc[m][i];
-        }
-      }
-    } else {  // lane: column lane % 16, rows 4 g + i
-      const int n = n0 + r16;
+    for (int h = 0; h < H; ++h)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
+        xp[h * MT + m] = X + (int64_t)(h * a.q.rows + t.row0 + min(m * 16 + r16, t.rows - 1)) * a.ldx +
+                         8 * g;
+    // rank rows past the stored ones: another row, dropped below
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = m * 16 + 4 * g + i;
-          if (row >= t.rows || n >= a.N) continue;
-          const int64_t rr = t.row0 + row;
-          const float bv = a.base ? a.base[rr * a.ldb + n] : 0.0f;
-          a.Y[rr * a.ldy + n] = bv + acc[m][i];
+    for (int r = 0; r < RT; ++r) wp[r] = A + (int64_t)min(r * 16 + r16, a.rank - 1) * a.K + 8 * g;
+    v4f acc[H * MT][RT];
+#pragma unroll
+    for (int m = 0; m < H * MT; ++m)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[m][r] = v4f{0, 0, 0, 0};
+    int c = wave * CH;
+    if (xvec && c + CH <= a.K) {  // whole chunks, the next one's loads ahead of this one's products
+      Frag8<XT> x[CH / 32][H * MT], nx[CH / 32][H * MT];
+      Frag8<WT> w[CH / 32][RT], nw[CH / 32][RT];
+      auto load = [&](int at, Frag8<XT>(&fx)[CH / 32][H * MT], Frag8<WT>(&fw)[CH / 32][RT]) {
+#pragma unroll
+        for (int u = 0; u < CH / 32; ++u) {
+#pragma unroll
+          for (int m = 0; m < H * MT; ++m) fx[u][m].load(xp[m] + at + 32 * u);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) fw[u][r].load(wp[r] + at + 32 * u);
         }
+      };
+      load(c, x, w);
+      for (; c + CH <= a.K; c += NW * CH) {
+        if (c + NW * CH + CH <= a.K) load(c + NW * CH, nx, nw);
+#pragma unroll
+        for (int u = 0; u < CH / 32; ++u)
+#pragma unroll
+          for (int m = 0; m < H * MT; ++m)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) acc[m][r] = step32(w[u][r], x[u][m], acc[m][r]);
+#pragma unroll
+        for (int u = 0; u < CH / 32; ++u) {
+#pragma unroll
+          for (int m = 0; m < H * MT; ++m) x[u][m] = nx[u][m];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) w[u][r] = nw[u][r];
+        }
+      }
+    }
+    for (; c < a.K; c += NW * CH) {  // the last, short chunk, and unaligned X
+      for (int k = c; k < min(c + CH, a.K); k += 32) {
+        const int valid = k + 8 * g < a.K ? 8 : 0;  // K % 16 == 0
+        Frag8<XT> x[H * MT];
+        Frag8<WT> w[RT];
+#pragma unroll
+        for (int m = 0; m < H * MT; ++m) x[m].load(xp[m] + k, valid);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) w[r].load(wp[r] + k, valid);
+#pragma unroll
+        for (int m = 0; m < H * MT; ++m)
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[m][r] = step32(w[r], x[m], acc[m][r]);
+      }
+    }
+    // acc[m][r][i]: row 16 m + lane % 16, rank 16 r + 4 g + i
+#pragma unroll
+    for (int m = 0; m < H * MT; ++m)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        *reinterpret_cast<v4f*>(&red[wave][m * 16 + r16][r * 16 + 4 * g]) = acc[m][r];
+  }
+  __syncthreads();
+  // Sum over the waves, the guided combine, the scale: red[0][row][rank].
+  for (int u = threadIdx.x; u < T * R / 4; u += 64 * NW) {
+    const int row = u / (R / 4), j = u % (R / 4) * 4;
+    v4f s{0, 0, 0, 0};
+    if (!bare) {
+      s = *reinterpret_cast<v4f*>(&red[0][row][j]);
+#pragma unroll
+      for (int w = 1; w < NW; ++w) s += *reinterpret_cast<v4f*>(&red[w][row][j]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e >= ra) s[e] = 0.0f;
+    if (a.S && share == 0 && row < t.rows) {
+      float* o = a.S + (int64_t)(t.row0 + row) * a.rank + j;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < a.rank) o[e] = s[e];
+    }
+    if constexpr (H == 2) {
+      v4f n{0, 0, 0, 0};
+      if (!bare) {
+        n = *reinterpret_cast<v4f*>(&red[0][T + row][j]);
+#pragma unroll
+        for (int w = 1; w < NW; ++w) n += *reinterpret_cast<v4f*>(&red[w][T + row][j]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e >= ra) n[e] = 0.0f;
+      if (a.S && share == 0 && row < t.rows) {
+        float* o = a.S + (int64_t)(a.q.rows + t.row0 + row) * a.rank + j;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < a.rank) o[e] = n[e];
+      }
+      s = n + a.w * (s - n);
+    }
+    *reinterpret_cast<v4f*>(&red[0][row][j]) = s * sc;
+  }
+  if (bare && a.base == a.Y) return;
+  __syncthreads();
+  SFrag<WT, RT, MT> sf;
+  if (!bare) sf.load(&red[0][0][0], LD, r16, g);
+  const WT* B = reinterpret_cast<const WT*>(a.B) + (int64_t)(bare ? 0 : t.adapter) * a.N * a.rank;
+  const int tiles = (a.N + 31) / 32;
+  const int c0 = tiles * share / a.shares + wave, c1 = tiles * (share + 1) / a.shares;
+  // Columns [32 ct, 32 ct + 32): two products of 16. YVEC: a lane has row
+  // lane % 16 and four columns 4 g ..; else column lane % 16 and rows 4 g ...
+  auto load_base = [&](int ct, v4f(&bs)[2][MT]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        bs[u][m] = v4f{0, 0, 0, 0};
+        if (!a.base) continue;
+        const int n0 = ct * 32 + u * 16;
+        if constexpr (YVEC) {
+          const int n = n0 + 4 * g;
+          const float* p = a.base + (int64_t)(t.row0 + min(m * 16 + r16, t.rows - 1)) * a.ldb + n;
+          if (n + 4 <= a.N)
+            bs[u][m] = *reinterpret_cast<const v4f*>(p);
+          else
+            for (int i = 0; i < 4; ++i)
+              if (n + i < a.N) bs[u][m][i] = p[i];
+        } else {
+          const int n = min(n0 + r16, a.N - 1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            bs[u][m][i] =
+                a.base[(int64_t)(t.row0 + min(m * 16 + 4 * g + i, t.rows - 1)) * a.ldb + n];
+        }
+      }
+  };
+  auto load_b = [&](int ct, BFrag<WT, RT>(&b)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      b[u].load(B + (int64_t)min(ct * 32 + u * 16 + r16, a.N - 1) * a.rank, ra, bvec, g);
+  };
+  if (c0 >= c1) return;
+  v4f bs[2][MT];
+  BFrag<WT, RT> b[2];
+  load_base(c0, bs);
+  if (!bare) load_b(c0, b);
+  for (int ct = c0; ct < c1; ct += NW) {
+    v4f nbs[2][MT];
+    BFrag<WT, RT> nb[2];
+    const int nx = min(ct + NW, c1 - 1);  // the last one is loaded again, unused
+    load_base(nx, nbs);
+    if (!bare) load_b(nx, nb);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        v4f v = bs[u][m];
+        if (!bare) v += b[u].template times<!YVEC, MT>(sf, m);
+        const int n0 = ct * 32 + u * 16;
+        if constexpr (YVEC) {
+          const int row = m * 16 + r16, n = n0 + 4 * g;
+          if (row < t.rows) {
+            float* y = a.Y + (int64_t)(t.row0 + row) * a.ldy + n;
+            if (n + 4 <= a.N)
+              *reinterpret_cast<v4f*>(y) = v;
+            else
+              for (int i = 0; i < 4; ++i)
+                if (n + i < a.N) y[i] = v[i];
+          }
+        } else {
+          const int n = n0 + r16;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = m * 16 + 4 * g + i;
+            if (row < t.rows && n < a.N) a.Y[(int64_t)(t.row0 + row) * a.ldy + n] = v[i];
+          }
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      b[u] = nb[u];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) bs[u][m] = nbs[u][m];
     }
   }
 }
@@ -445,6 +708,22 @@ __global__ __launch_bounds__(256) void k_lora_slot_sum(SlotSumArgs a) {
   reinterpret_cast<WT*>(a.out)[ad * len + e] = (WT)r;
 }
 
+// Tiles of 64 rows from which on the taller tiles are used.
+#ifndef QL_WIDE
+#define QL_WIDE 128
+#endif
+#ifndef QL_WGS
+#define QL_WGS 1024
+#endif
+constexpr int kWideTiles = QL_WIDE;
+
+// Workgroups that share one tile of rows: about QL_WGS in all, none with fewer
+// than 128 columns.
+int forward_shares(int tiles, int N) {
+  const int want = (QL_WGS + tiles - 1) / tiles, cap = (N + 127) / 128;
+  return want < cap ? want : cap;
+}
+
 int max_tiles(const Requests& q, int T) {
   const int64_t t = (int64_t)q.rows / T + q.n;
   return (int)(t < q.rows ? t : q.rows);
@@ -468,26 +747,37 @@ hipError_t shrink_rt(const ShrinkArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename WT>
-hipError_t expand_rt(const ExpandArgs& a, hipStream_t s) {
-  const bool vec = (reinterpret_cast<uintptr_t>(a.Y) % 16) == 0 && a.ldy % 4 == 0 &&
-                   (!a.base || ((reinterpret_cast<uintptr_t>(a.base) % 16) == 0 && a.ldb % 4 == 0));
-  const bool bvec =
-      (reinterpret_cast<uintptr_t>(a.B) % (4 * sizeof(WT))) == 0 && a.rank % 4 == 0;
-#define QL_EXPAND(RT, MT, NI)                                                                 \
-  hipLaunchKernelGGL((k_lora_expand<WT, RT, MT, NI>),                                         \
-                     dim3(max_tiles(a.q, MT * 16), (a.N + 64 * NI - 1) / (64 * NI)), dim3(256), \
-                     0, s, a, vec, bvec)
-  if (a.rank <= 16)
-    QL_EXPAND(1, 1, 2);
-  else if (a.rank <= 32)
-    QL_EXPAND(2, 1, 2);
-  else if (a.rank <= 64)
-    QL_EXPAND(4, 1, 2);
+template <typename XT, typename WT, int RT, int MT, int H, int NW>
+hipError_t forward_run(ForwardArgs a, bool xvec, bool yvec, bool bvec, hipStream_t s) {
+  const int tiles = (max_tiles(a.q, MT * 16) + 7) / 8 * 8;
+  a.shares = forward_shares(tiles, a.N);
+  const dim3 grid(tiles * a.shares), block(64 * NW);
+#define QL_FWD(YV)                                                                           \
+  hipLaunchKernelGGL((k_lora_forward<XT, WT, RT, MT, H, NW, YV>), grid, block, 0, s, a, xvec, \
+                     bvec)
+  if (yvec)
+    QL_FWD(true);
   else
-    QL_EXPAND(8, 1, 2);
-#undef QL_EXPAND
+    QL_FWD(false);
+#undef QL_FWD
   return hipGetLastError();
+}
+
+template <typename XT, typename WT>
+hipError_t forward_rt(const ForwardArgs& a, hipStream_t s) {
+  const bool xvec = reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && (a.ldx * sizeof(XT)) % 16 == 0;
+  const bool yvec = reinterpret_cast<uintptr_t>(a.Y) % 16 == 0 && a.ldy % 4 == 0 &&
+                    (!a.base || (reinterpret_cast<uintptr_t>(a.base) % 16 == 0 && a.ldb % 4 == 0));
+  const bool bvec = reinterpret_cast<uintptr_t>(a.B) % 16 == 0 && a.rank % (16 / sizeof(WT)) == 0;
+  const bool wide = max_tiles(a.q, 64) >= kWideTiles;
+#define QL_RUN(RT, MT, NW)                                                      \
+  (a.halves == 2 ? forward_run<XT, WT, RT, MT, 2, NW>(a, xvec, yvec, bvec, s)   \
+                 : forward_run<XT, WT, RT, MT, 1, NW>(a, xvec, yvec, bvec, s))
+  if (a.rank <= 16) return wide ? QL_RUN(1, 4, 4) : QL_RUN(1, 1, 4);
+  if (a.rank <= 32) return wide ? QL_RUN(2, 4, 4) : QL_RUN(2, 1, 4);
+  if (a.rank <= 64) return wide ? QL_RUN(4, 2, 4) : QL_RUN(4, 1, 4);
+  return QL_RUN(8, 1, 4);
+#undef QL_RUN
 }
 
 template <typename XT, typename WT, bool DX, bool TR>
@@ -535,8 +825,9 @@ hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t s) {
   return a.w_bf16 ? shrink_rt<float, bf16, false>(a, s) : shrink_rt<float, float, false>(a, s);
 }
 
-hipError_t launch_lora_expand(const ExpandArgs& a, hipStream_t s) {
-  return a.w_bf16 ? expand_rt<bf16>(a, s) : expand_rt<float>(a, s);
+hipError_t launch_lora_forward(const ForwardArgs& a, hipStream_t s) {
+  if (a.x_bf16) return a.w_bf16 ? forward_rt<bf16, bf16>(a, s) : forward_rt<bf16, float>(a, s);
+  return a.w_bf16 ? forward_rt<float, bf16>(a, s) : forward_rt<float, float>(a, s);
 }
 
 hipError_t launch_lora_outer(const OuterArgs& a, hipStream_t s) {

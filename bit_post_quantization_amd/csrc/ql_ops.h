@@ -39,22 +39,24 @@ struct ShrinkArgs {
 };
 constexpr int kShrinkStep = 32;
 
-// Y[row][n] = base[row][n] + scale_a * sum_j S[row][j] * B_a[n][j], with S the
-// sum of the splits, combined over the row's two halves when guided.
-struct ExpandArgs {
-  const float* part;  // [splits][rows * halves][rank]
-  int splits, halves;
-  float w;            // guidance weight (halves == 2)
+// Y[row][n] = base[row][n] + scale_a * sum_j S[row][j] * B_a[n][j] with
+// S = X A_a^T, combined over the row's two halves when guided.
+struct ForwardArgs {
+  const void* X;      // [rows * halves, K], row stride ldx elements
+  int64_t ldx;
+  const void* A;      // [n_adapters, rank, K]
   const void* B;      // [n_adapters, N, rank]
   const float* scales;
   const int32_t* ranks;
   Requests q;
-  int N, rank;
+  int N, K, rank, halves;
+  float w;            // guidance weight (halves == 2)
   const float* base;  // nullptr: zero
   float* Y;
   int64_t ldb, ldy;
-  float* S;           // nullptr, or [rows * halves, rank]: the summed splits
-  bool w_bf16;
+  float* S;           // nullptr, or [rows * halves, rank]
+  int shares;         // workgroups of one tile of rows (set by the launch)
+  bool x_bf16, w_bf16;
 };
 
 // Row ranges s = 0 .. splits-1 of row_len rows each. For every range and the
@@ -92,7 +94,7 @@ struct SlotSumArgs {
 };
 
 hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t s);
-hipError_t launch_lora_expand(const ExpandArgs& a, hipStream_t s);
+hipError_t launch_lora_forward(const ForwardArgs& a, hipStream_t s);
 hipError_t launch_lora_outer(const OuterArgs& a, hipStream_t s);
 hipError_t launch_lora_slot_sum(const SlotSumArgs& a, hipStream_t s);
 // Splits of a shrink over D columns for `rows` rows (halves included).

@@ -200,20 +200,17 @@ ql_status check_grads(const ql_grad* table, int32_t n, int64_t units, const doub
 
 extern "C" {
 
-ql_status qlinear_lora_workspace(const ql_lora* d, int32_t M, int32_t n_requests, int32_t grad,
-                                 int64_t* bytes) {
+ql_status qlinear_lora_grad_workspace(const ql_lora* d, int32_t M, int32_t n_requests,
+                                      int64_t* bytes) {
   QL_CHECK(check_lora(d, M, n_requests));
   if (!bytes) return fail(QL_ERR_ARG, "bytes is NULL");
-  if (grad != 0 && grad != 1) return fail(QL_ERR_ARG, "grad = %d must be 0 or 1", grad);
-  *bytes = grad ? grad_ws(d, M, n_requests).total
-                : part_bytes(ql::lora_shrink_splits(M, n_requests, d->K, d->rank), M, d->rank);
+  *bytes = grad_ws(d, M, n_requests).total;
   return ok();
 }
 
 ql_status qlinear_lora(const ql_lora* d, const void* X, int64_t ldx, int32_t M,
                        const ql_requests* q, int32_t cfg, float w, const float* base, int64_t ldb,
-                       float* Y, int64_t ldy, float* S, void* workspace, int64_t workspace_bytes,
-                       void* stream) {
+                       float* Y, int64_t ldy, float* S, void* stream) {
   if (!q) return fail(QL_ERR_ARG, "requests is NULL");
   QL_CHECK(check_lora(d, M, q->n_requests));
   if (cfg != 0 && cfg != 1) return fail(QL_ERR_ARG, "cfg = %d must be 0 or 1", cfg);
@@ -231,43 +228,28 @@ ql_status qlinear_lora(const ql_lora* d, const void* X, int64_t ldx, int32_t M,
   if (base == Y && ldb != ldy)
     return fail(QL_ERR_ARG, "base is Y with another row stride (%lld, %lld)", (long long)ldb,
                 (long long)ldy);
-  const int splits = ql::lora_shrink_splits(M, q->n_requests, d->K, d->rank);
-  QL_CHECK(check_workspace(workspace, workspace_bytes, part_bytes(splits, M, d->rank)));
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const int halves = cfg ? 2 : 1;
-  ql::ShrinkArgs a{};
-  a.P = X;
-  a.ldp = ldx;
-  a.W = d->A;
+  ql::ForwardArgs a{};
+  a.X = X;
+  a.ldx = ldx;
+  a.A = d->A;
+  a.B = d->B;
+  a.scales = d->scales;
   a.ranks = d->ranks;
-  a.q = requests(d, q, M / halves);
-  a.D = d->K;
+  a.halves = cfg ? 2 : 1;
+  a.q = requests(d, q, M / a.halves);
+  a.N = d->N;
+  a.K = d->K;
   a.rank = d->rank;
-  a.halves = halves;
-  a.splits = splits;
-  a.split_len = split_len(d->K, splits);
-  a.part = reinterpret_cast<float*>(workspace);
-  a.p_bf16 = d->x_dtype == QL_BF16;
+  a.w = w;
+  a.base = base;
+  a.Y = Y;
+  a.ldb = ldb;
+  a.ldy = ldy;
+  a.S = S;
+  a.x_bf16 = d->x_dtype == QL_BF16;
   a.w_bf16 = d->w_dtype == QL_BF16;
-  QL_LAUNCH(ql::launch_lora_shrink(a, s), "launching the adapters' first product");
-  ql::ExpandArgs e{};
-  e.part = a.part;
-  e.splits = splits;
-  e.halves = halves;
-  e.w = w;
-  e.B = d->B;
-  e.scales = d->scales;
-  e.ranks = d->ranks;
-  e.q = a.q;
-  e.N = d->N;
-  e.rank = d->rank;
-  e.base = base;
-  e.Y = Y;
-  e.ldb = ldb;
-  e.ldy = ldy;
-  e.S = S;
-  e.w_bf16 = a.w_bf16;
-  QL_LAUNCH(ql::launch_lora_expand(e, s), "launching the adapters' second product");
+  QL_LAUNCH(ql::launch_lora_forward(a, reinterpret_cast<hipStream_t>(stream)),
+            "launching the adapters");
   return ok();
 }
 

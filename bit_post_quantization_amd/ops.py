@@ -37,35 +37,45 @@ def _ptr(t) -> Optional[int]:
 
 
 def _check(t, name: str, dtype, shape=None) -> None:
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and
-          t.device.index == torch.cuda.current_device(),
-          f"{name} must be a tensor on the current device")
-    _need(t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
-    if shape is not None:
-        _need(tuple(t.shape) == tuple(shape), f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and
+            t.get_device() == torch.cuda.current_device()):
+        raise QLError(QL_ERR_ARG, f"{name} must be a tensor on the current device")
+    if t.dtype != dtype:
+        raise QLError(QL_ERR_ARG, f"{name} is {t.dtype}, not {dtype}")
+    if shape is not None and t.shape != shape:
+        raise QLError(QL_ERR_ARG, f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
 
 
 def _flat(t, name: str, dtype, shape=None) -> None:
     _check(t, name, dtype, shape)
-    _need(t.is_contiguous(), f"{name} is not contiguous")
+    if not t.is_contiguous():
+        raise QLError(QL_ERR_ARG, f"{name} is not contiguous")
 
 
 def _rows(t, name: str, dtype, shape) -> int:
     """Row stride of a matrix whose rows are contiguous."""
     _check(t, name, dtype, shape)
     rows, cols = shape
-    if rows <= 1 or cols == 0:
-        _need(cols <= 1 or t.stride(1) == 1, f"{name}: rows are not contiguous")
-        return max(cols, 1)
+    if t.is_contiguous() or rows == 0:
+        return cols
     _need(cols == 1 or t.stride(1) == 1, f"{name}: rows are not contiguous")
+    if rows == 1:
+        return cols
     _need(t.stride(0) >= cols, f"{name}: rows overlap")
     return t.stride(0)
+
+
+# Raw handle of the current stream. torch's Stream object costs 3 us to make,
+# a third of a small call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_HERE = contextlib.nullcontext()
 
 
 def _on(stream):
     """(context under which to allocate, raw stream) of a call."""
     if stream is None:
-        return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
+        return _HERE, _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     return torch.cuda.stream(stream), stream.cuda_stream
@@ -77,17 +87,16 @@ def _workspace(nbytes: int):
 
 # ------------------------------------------------------- C ABI, same names ----
 
-def qlinear_lora_workspace(desc: QlLora, M: int, n_requests: int, grad: int = 0) -> int:
-    n = ctypes.c_int64()
-    check(_lib.load().qlinear_lora_workspace(_byref(desc), M, n_requests, grad, _byref(n)))
-    return n.value
-
-
 def qlinear_lora(desc: QlLora, X, ldx, M, requests: QlRequests, cfg, w, base, ldb, Y, ldy, S,
-                 workspace, stream) -> None:
-    check(_lib.load().qlinear_lora(_byref(desc), _ptr(X), ldx, M, _byref(requests), cfg, float(w),
-                                   _ptr(base), ldb, _ptr(Y), ldy, _ptr(S), _ptr(workspace),
-                                   workspace.numel(), stream))
+                 stream) -> None:
+    check(_lib.load().qlinear_lora(_byref(desc), _ptr(X), ldx, M, _byref(requests), cfg, w,
+                                   _ptr(base), ldb, _ptr(Y), ldy, _ptr(S), stream))
+
+
+def qlinear_lora_grad_workspace(desc: QlLora, M: int, n_requests: int) -> int:
+    n = ctypes.c_int64()
+    check(_lib.load().qlinear_lora_grad_workspace(_byref(desc), M, n_requests, _byref(n)))
+    return n.value
 
 
 def qlinear_lora_grad(desc: QlLora, X, ldx, M, requests: QlRequests, S, dY, lddy, dX, lddx, dA, dB,
@@ -155,7 +164,7 @@ class LoraAdapters:
         self.desc = QlLora(N=self.N, K=self.K, rank=self.rank, n_adapters=n,
                            x_dtype=_DT[self.x_dtype], w_dtype=_DT[A.dtype], A=_ptr(A), B=_ptr(B),
                            scales=_ptr(scales), ranks=_ptr(ranks))
-        qlinear_lora_workspace(self.desc, 0, 1)  # its checks
+        qlinear_lora_grad_workspace(self.desc, 0, 1)  # its checks
 
     def _requests(self, row_offsets, adapter) -> QlRequests:
         n = adapter.numel()
@@ -177,10 +186,9 @@ class LoraAdapters:
             if out is None:
                 out = torch.empty((rows, self.N), dtype=torch.float32, device="cuda")
             S = torch.empty((M, self.rank), dtype=torch.float32, device="cuda") if save else None
-            ws = _workspace(qlinear_lora_workspace(self.desc, M, q.n_requests))
         ldy = _rows(out, "out", torch.float32, (rows, self.N))
         ldb = 0 if base is None else _rows(base, "base", torch.float32, (rows, self.N))
-        qlinear_lora(self.desc, X, ldx, M, q, cfg, w, base, ldb, out, ldy, S, ws, s)
+        qlinear_lora(self.desc, X, ldx, M, q, cfg, w, base, ldb, out, ldy, S, s)
         return (out, S) if save else out
 
     def grad(self, X, row_offsets, adapter, S, dY, need_dx: bool = True, stream=None):
@@ -195,7 +203,7 @@ class LoraAdapters:
         with ctx:
             dX = torch.empty((M, self.K), dtype=self.x_dtype, device="cuda") if need_dx else None
             dA, dB = torch.empty_like(self.A), torch.empty_like(self.B)
-            ws = _workspace(qlinear_lora_workspace(self.desc, M, q.n_requests, 1))
+            ws = _workspace(qlinear_lora_grad_workspace(self.desc, M, q.n_requests))
         qlinear_lora_grad(self.desc, X, ldx, M, q, S, dY, lddy, dX, self.K, dA, dB, ws, s)
         return dX, dA, dB
 

@@ -326,10 +326,10 @@ ql_status qlinear_probe_mfma(const void* operands, int32_t iters, int32_t waves_
  * Operators beside the layer: what trains, adapts and feeds a linear whose
  * weights are frozen codes. They take no plan; the descriptors below are HOST
  * structs holding DEVICE pointers, read during the call and not retained.
- * Each call enqueues kernel launches only, uses the workspace that the caller
- * passes (DEVICE, 16-byte aligned, at least the size its query gives, free for
- * other use once the call's work is done, contents undefined) and gives the
- * same bits every time (no atomics). Calls on different streams may run at
+ * Each call enqueues kernel launches only and gives the same bits every time
+ * (no atomics). A workspace, where a call takes one, is the caller's: DEVICE,
+ * 16-byte aligned, at least the size its query gives, free for other use once
+ * the call's work is done, contents undefined. Calls on different streams may run at
  * once if their workspaces and outputs differ.
  * ------------------------------------------------------------------------ */
 
@@ -362,12 +362,6 @@ typedef struct {
   const int32_t* adapter;      /* DEVICE [n_requests] */
 } ql_requests;
 
-/* Workspace bytes (HOST out) of qlinear_lora (grad = 0) or qlinear_lora_grad
- * (grad = 1) with M rows and n_requests requests. The pointers in d are not
- * looked at. */
-ql_status qlinear_lora_workspace(const ql_lora* d, int32_t M, int32_t n_requests, int32_t grad,
-                                 int64_t* bytes);
-
 /*
  * Y[m,:] = base[m,:] + scale_a (X[m,:] A_a^T) B_a^T for the rows of every
  * request; rows without an adapter get base. Sums in fp32.
@@ -385,8 +379,12 @@ ql_status qlinear_lora_workspace(const ql_lora* d, int32_t M, int32_t n_requests
  */
 ql_status qlinear_lora(const ql_lora* d, const void* X, int64_t ldx, int32_t M,
                        const ql_requests* q, int32_t cfg, float w, const float* base, int64_t ldb,
-                       float* Y, int64_t ldy, float* S, void* workspace, int64_t workspace_bytes,
-                       void* stream);
+                       float* Y, int64_t ldy, float* S, void* stream);
+
+/* Workspace bytes (HOST out) of qlinear_lora_grad with M rows and n_requests
+ * requests. The pointers in d are not looked at. */
+ql_status qlinear_lora_grad_workspace(const ql_lora* d, int32_t M, int32_t n_requests,
+                                      int64_t* bytes);
 
 /*
  * Gradients of qlinear_lora with cfg = 0, for dY [M,N] fp32 (row stride lddy):

@@ -42,10 +42,10 @@ def test_lora_descriptor(kw, status, frag):
     L = _lib.load()
     n = ctypes.c_int64()
     d = _lora(**kw)
-    assert L.qlinear_lora_workspace(ctypes.byref(d), 16, 1, 0, ctypes.byref(n)) == status
+    assert L.qlinear_lora_grad_workspace(ctypes.byref(d), 16, 1, ctypes.byref(n)) == status
     assert frag in _msg()
     assert L.qlinear_lora(ctypes.byref(d), A, 64, 16, ctypes.byref(_req()), 0, 1.0, A, 100, A, 100,
-                          U, A, 1 << 30, U) == status
+                          U, U) == status
     assert L.qlinear_lora_grad(ctypes.byref(d), A, 64, 16, ctypes.byref(_req()), A, A, 100, A, 64,
                                A, A, A, 1 << 30, U) == status
 
@@ -54,24 +54,21 @@ def test_lora_workspace_query():
     L = _lib.load()
     n = ctypes.c_int64()
     d = _lora()
-    assert L.qlinear_lora_workspace(U, 16, 1, 0, ctypes.byref(n)) == _lib.QL_ERR_ARG
-    assert L.qlinear_lora_workspace(ctypes.byref(d), -1, 1, 0, ctypes.byref(n)) == _lib.QL_ERR_ARG
-    assert L.qlinear_lora_workspace(ctypes.byref(d), 16, 0, 0, ctypes.byref(n)) == _lib.QL_ERR_ARG
-    assert L.qlinear_lora_workspace(ctypes.byref(d), 16, 1, 2, ctypes.byref(n)) == _lib.QL_ERR_ARG
-    assert L.qlinear_lora_workspace(ctypes.byref(d), 16, 1, 0, U) == _lib.QL_ERR_ARG
-    assert L.qlinear_lora_workspace(ctypes.byref(d), (1 << 23) + 1, 1, 0, ctypes.byref(n)) == \
-        _lib.QL_ERR_UNSUPPORTED
-    for grad in (0, 1):
-        assert L.qlinear_lora_workspace(ctypes.byref(d), 16, 1, grad, ctypes.byref(n)) == _lib.QL_OK
-        assert n.value >= 16 * 8 * 4
+    query = L.qlinear_lora_grad_workspace
+    assert query(U, 16, 1, ctypes.byref(n)) == _lib.QL_ERR_ARG
+    assert query(ctypes.byref(d), -1, 1, ctypes.byref(n)) == _lib.QL_ERR_ARG
+    assert query(ctypes.byref(d), 16, 0, ctypes.byref(n)) == _lib.QL_ERR_ARG
+    assert query(ctypes.byref(d), 16, 1, U) == _lib.QL_ERR_ARG
+    assert query(ctypes.byref(d), (1 << 23) + 1, 1, ctypes.byref(n)) == _lib.QL_ERR_UNSUPPORTED
+    assert query(ctypes.byref(d), 16, 1, ctypes.byref(n)) == _lib.QL_OK
+    assert n.value >= 16 * 8 * 4
 
 
-def _apply(d=None, X=A, ldx=64, M=16, q="ok", cfg=0, base=A, ldb=100, Y=A + 64, ldy=100, S=U, ws=A,
-           nb=1 << 30):
+def _apply(d=None, X=A, ldx=64, M=16, q="ok", cfg=0, base=A, ldb=100, Y=A + 64, ldy=100, S=U):
     d = _lora() if d is None else d
     q = _req() if q == "ok" else q
     return _lib.load().qlinear_lora(ctypes.byref(d), X, ldx, M, ctypes.byref(q) if q else U, cfg,
-                                    1.0, base, ldb, Y, ldy, S, ws, nb, U)
+                                    1.0, base, ldb, Y, ldy, S, U)
 
 
 @pytest.mark.parametrize("kw,frag", [
@@ -91,9 +88,6 @@ def _apply(d=None, X=A, ldx=64, M=16, q="ok", cfg=0, base=A, ldb=100, Y=A + 64, 
     (dict(ldy=99), "ldy = 99"),
     (dict(ldb=99), "ldb = 99"),
     (dict(base=A, Y=A, ldb=100, ldy=101), "another row stride"),
-    (dict(ws=U), "workspace is NULL"),
-    (dict(ws=A + 8), "16-byte"),
-    (dict(nb=16 * 8 * 4 - 1), "workspace holds"),
     (dict(d=_lora(A=U)), "A or B"),
     (dict(d=_lora(B=U)), "A or B"),
     (dict(d=_lora(A=A + 4)), "A must be"),
@@ -119,7 +113,8 @@ def test_lora_empty_is_a_no_op():
     (dict(ldx=63), "ldx = 63"),
     (dict(lddy=99), "lddy = 99"),
     (dict(lddx=60), "lddx = 60"),
-    (dict(ws=U), "workspace"),
+    (dict(ws=U), "workspace is NULL"),
+    (dict(ws=A + 8), "16-byte"),
     (dict(nb=64), "workspace holds"),
 ])
 def test_lora_grad_refusals(kw, frag):
