@@ -20,7 +20,7 @@ from .qlinear import (  # noqa: F401
 
 _OPS = ("GradSet", "GroupNormAct", "LoraAdapters", "qlinear_grad_clip", "qlinear_grad_norm",
         "qlinear_group_norm", "qlinear_group_norm_grad", "qlinear_group_norm_workspace",
-        "qlinear_lora", "qlinear_lora_grad", "qlinear_lora_grad_workspace")
+        "qlinear_lora", "qlinear_lora_grad", "qlinear_lora_workspace")
 
 
 def __getattr__(name):  # ops.py needs torch, which the layer's binding imports only when used

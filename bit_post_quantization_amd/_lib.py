@@ -25,7 +25,7 @@ EXPORTS = (
     "qlinear_gemm", "qlinear_cfg_combine", "qlinear_last_error", "qlinear_version",
     "qlinear_plan_lsb_view", "qlinear_plan_lsb_update", "qlinear_gamp_allocate",
     "qlinear_quantize_act_noalloc", "qlinear_probe_mfma",
-    "qlinear_lora", "qlinear_lora_grad_workspace", "qlinear_lora_grad",
+    "qlinear_lora_workspace", "qlinear_lora", "qlinear_lora_grad",
     "qlinear_group_norm_workspace", "qlinear_group_norm", "qlinear_group_norm_grad",
     "qlinear_grad_norm", "qlinear_grad_clip",
 )
@@ -98,8 +98,9 @@ def load() -> ctypes.CDLL:
         "qlinear_gemm": ([P, P, P, I32, I32, F32, P, P, P], ctypes.c_int),
         "qlinear_cfg_combine": ([P, I32, I32, F32, P, P], ctypes.c_int),
         "qlinear_probe_mfma": ([P, I32, I32, P, ctypes.c_int64, P], ctypes.c_int),
-        "qlinear_lora": ([LORA, P, I64, I32, REQ, I32, F32, P, I64, P, I64, P, P], ctypes.c_int),
-        "qlinear_lora_grad_workspace": ([LORA, I32, I32, ctypes.POINTER(I64)], ctypes.c_int),
+        "qlinear_lora_workspace": ([LORA, I32, I32, I32, I32, ctypes.POINTER(I64)], ctypes.c_int),
+        "qlinear_lora": ([LORA, P, I64, I32, REQ, I32, F32, P, I64, P, I64, P, P, I64, P],
+                         ctypes.c_int),
         "qlinear_lora_grad": ([LORA, P, I64, I32, REQ, P, P, I64, P, I64, P, P, P, I64, P],
                               ctypes.c_int),
         "qlinear_group_norm_workspace": ([NORM, I32, ctypes.POINTER(I64)], ctypes.c_int),

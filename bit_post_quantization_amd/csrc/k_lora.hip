@@ -261,7 +261,8 @@ template <typename WT, int RT, int MT>
 struct SFrag;
 template <int RT, int MT>
 struct SFrag<float, RT, MT> {  // element e: rank 16 r + 4 g + e
-  v4f s[MT][RT];
+  typedef v4f vec;
+  vec s[MT][RT];
   __device__ __forceinline__ void load(const float* lds, int ld, int r16, int g) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -273,7 +274,8 @@ struct SFrag<float, RT, MT> {  // element e: rank 16 r + 4 g + e
 template <int RT, int MT>
 struct SFrag<bf16, RT, MT> {  // element e: rank 32 k + 8 g + e (RT = 1: see below)
   static constexpr int KS = RT == 1 ? 2 : 3 * RT / 2;
-  v8h s[MT][KS];
+  typedef v8h vec;
+  vec s[MT][KS];
   __device__ __forceinline__ void load(const float* lds, int ld, int r16, int g) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -312,14 +314,14 @@ struct BFrag<float, RT> {
 #pragma unroll
     for (int r = 0; r < RT; ++r) load_n<4>(row + r * 16 + 4 * g, ra - r * 16 - 4 * g, vec, b[r]);
   }
-  template <bool SWAP, int MT>
+  // lane: row 4 g + i of S's tile, the product with this lane's row of B
+  template <int MT>
   __device__ __forceinline__ v4f times(const SFrag<float, RT, MT>& s, int m) const {
     v4f c{0, 0, 0, 0};
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        c = SWAP ? mfma_f32(s.s[m][r][e], b[r][e], c) : mfma_f32(b[r][e], s.s[m][r][e], c);
+      for (int e = 0; e < 4; ++e) c = mfma_f32(s.s[m][r][e], b[r][e], c);
     return c;
   }
 };
@@ -339,34 +341,108 @@ struct BFrag<bf16, RT> {
       }
     }
   }
-  template <bool SWAP, int MT>
+  template <int MT>
   __device__ __forceinline__ v4f times(const SFrag<bf16, RT, MT>& s, int m) const {
     v4f c{0, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < SFrag<bf16, RT, MT>::KS; ++k) {
-      const v8h bk = b[RT == 1 ? 0 : k / 3];
-      c = SWAP ? mfma_bf16(s.s[m][k], bk, c) : mfma_bf16(bk, s.s[m][k], c);
-    }
+    for (int k = 0; k < SFrag<bf16, RT, MT>::KS; ++k)
+      c = mfma_bf16(s.s[m][k], b[RT == 1 ? 0 : k / 3], c);
     return c;
   }
 };
 
-template <typename XT, typename WT, int RT, int MT, int H, int NW, bool YVEC>
-__global__ __launch_bounds__(64 * NW) void k_lora_forward(ForwardArgs a, bool xvec, bool bvec) {
-  constexpr int T = MT * 16, R = RT * 16, LD = R + 4;
+// A wave's output block: MT * 16 rows times 64 columns, four products side by
+// side. Neighbouring lanes have neighbouring addresses, which the load path
+// needs (it takes 64 bytes of neighbouring lanes at a time, else 16): with VEC
+// product u has columns 4 (lane % 16) + u, so a lane ends up with four columns
+// in a row of each of its four rows 4 g + i; without, columns 16 u + lane % 16
+// and single elements.
+constexpr int kBlockCols = 64;
+template <bool VEC>
+__device__ __forceinline__ int block_col(int u, int r16) {
+  return VEC ? 4 * r16 + u : 16 * u + r16;
+}
+
+template <int MT, bool VEC>
+struct Block {
+  float v[MT][4][4];  // [row tile][row 4 g + i][u]
+
+  __device__ __forceinline__ void load(const float* base, int64_t ld, int row0, int rows, int n0,
+                                       int N, int r16, int g) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* p = base + (int64_t)(row0 + min(m * 16 + 4 * g + i, rows - 1)) * ld + n0;
+        if (VEC && n0 + 4 * r16 + 4 <= N) {
+          const v4f x = *reinterpret_cast<const v4f*>(p + 4 * r16);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) v[m][i][u] = x[u];
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int c = block_col<VEC>(u, r16);
+            v[m][i][u] = n0 + c < N ? p[c] : 0.0f;
+          }
+        }
+      }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[m][i][u] = 0.0f;
+  }
+  template <typename WT, int RT>
+  __device__ __forceinline__ void add(const SFrag<WT, RT, MT>& s, const BFrag<WT, RT>& b, int u) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const v4f c = b.times(s, m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[m][i][u] += c[i];
+    }
+  }
+  __device__ __forceinline__ void store(float* Y, int64_t ld, int row0, int rows, int n0, int N,
+                                        int r16, int g) const {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = m * 16 + 4 * g + i;
+        if (row >= rows) continue;
+        float* p = Y + (int64_t)(row0 + row) * ld + n0;
+        if (VEC && n0 + 4 * r16 + 4 <= N) {
+          *reinterpret_cast<v4f*>(p + 4 * r16) = v4f{v[m][i][0], v[m][i][1], v[m][i][2], v[m][i][3]};
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int c = block_col<VEC>(u, r16);
+            if (n0 + c < N) p[c] = v[m][i][u];
+          }
+        }
+      }
+  }
+};
+
+template <int RT, int MT, int H, int NW>
+struct SBuf {  // partial sums of the waves; [0][row][rank] holds S in the end
+  float v[NW][H * MT * 16][RT * 16 + 4];
+};
+
+// S = X A^T of one tile by the whole workgroup, combined over the halves and
+// scaled, into buf.v[0] (ranks past `ra` and rows of a bare tile are zero). The
+// waves take every NW-th chunk of K and join their sums in LDS. With `save`,
+// the tile's rows of a.S receive S as it was before the combine and the scale.
+template <typename XT, typename WT, int RT, int MT, int H, int NW>
+__device__ void tile_s(const ForwardArgs& a, const Tile& t, int ra, float sc, bool xvec, bool save,
+                       SBuf<RT, MT, H, NW>& buf) {
+  constexpr int T = MT * 16, R = RT * 16;
   constexpr int CH = sizeof(XT) == 2 ? 64 : 32;  // columns of 128 bytes of X
-  __shared__ __align__(16) float red[NW][H * T][LD];
-  // Workgroups of one tile follow each other on one chiplet (workgroup ids go
-  // round the eight of them), so that they find the tile's X in its L2.
-  const int xcd = blockIdx.x & 7, loc = blockIdx.x >> 3;
-  const int tile = loc / a.shares * 8 + xcd, share = loc % a.shares;
-  Tile t;
-  if (!find_tile(a.q, T, tile, t)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   const bool bare = t.adapter < 0;
-  if (bare && a.base == a.Y && !a.S) return;
-  const int ra = bare ? 0 : rank_of(a.ranks, t.adapter, a.rank);
-  const float sc = bare ? 0.0f : a.scales ? a.scales[t.adapter] : 1.0f;
+  auto& red = buf.v;
   if (!bare) {
     const XT* X = reinterpret_cast<const XT*>(a.X);
     const WT* A = reinterpret_cast<const WT*>(a.A) + (int64_t)t.adapter * a.rank * a.K;
@@ -452,7 +528,7 @@ __global__ __launch_bounds__(64 * NW) void k_lora_forward(ForwardArgs a, bool xv
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (j + e >= ra) s[e] = 0.0f;
-    if (a.S && share == 0 && row < t.rows) {
+    if (save && row < t.rows) {
       float* o = a.S + (int64_t)(t.row0 + row) * a.rank + j;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -468,7 +544,7 @@ __global__ __launch_bounds__(64 * NW) void k_lora_forward(ForwardArgs a, bool xv
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (j + e >= ra) n[e] = 0.0f;
-      if (a.S && share == 0 && row < t.rows) {
+      if (save && row < t.rows) {
         float* o = a.S + (int64_t)(a.q.rows + t.row0 + row) * a.rank + j;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -478,89 +554,143 @@ __global__ __launch_bounds__(64 * NW) void k_lora_forward(ForwardArgs a, bool xv
     }
     *reinterpret_cast<v4f*>(&red[0][row][j]) = s * sc;
   }
-  if (bare && a.base == a.Y) return;
   __syncthreads();
+}
+
+// All in one: right for calls so small that a second launch costs more than
+// computing S again in the workgroups that share a tile.
+template <typename XT, typename WT, int RT, int MT, int H, int NW, bool YVEC>
+__global__ __launch_bounds__(64 * NW) void k_lora_forward(ForwardArgs a, bool xvec, bool bvec) {
+  constexpr int T = MT * 16, LD = RT * 16 + 4;
+  __shared__ __align__(16) SBuf<RT, MT, H, NW> buf;
+  // Workgroups of one tile follow each other on one chiplet (workgroup ids go
+  // round the eight of them), so that they find the tile's X in its L2.
+  const int xcd = blockIdx.x & 7, loc = blockIdx.x >> 3;
+  const int tile = loc / a.shares * 8 + xcd, share = loc % a.shares;
+  Tile t;
+  if (!find_tile(a.q, T, tile, t)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const bool bare = t.adapter < 0;
+  if (bare && a.base == a.Y && !a.S) return;
+  const int ra = bare ? 0 : rank_of(a.ranks, t.adapter, a.rank);
+  const float sc = bare ? 0.0f : a.scales ? a.scales[t.adapter] : 1.0f;
+  tile_s<XT, WT, RT, MT, H, NW>(a, t, ra, sc, xvec, a.S && share == 0, buf);
+  if (bare && a.base == a.Y) return;
   SFrag<WT, RT, MT> sf;
-  if (!bare) sf.load(&red[0][0][0], LD, r16, g);
+  if (!bare) sf.load(&buf.v[0][0][0], LD, r16, g);
   const WT* B = reinterpret_cast<const WT*>(a.B) + (int64_t)(bare ? 0 : t.adapter) * a.N * a.rank;
-  const int tiles = (a.N + 31) / 32;
-  const int c0 = tiles * share / a.shares + wave, c1 = tiles * (share + 1) / a.shares;
-  // Columns [32 ct, 32 ct + 32): two products of 16. YVEC: a lane has row
-  // lane % 16 and four columns 4 g ..; else column lane % 16 and rows 4 g ...
-  auto load_base = [&](int ct, v4f(&bs)[2][MT]) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        bs[u][m] = v4f{0, 0, 0, 0};
-        if (!a.base) continue;
-        const int n0 = ct * 32 + u * 16;
-        if constexpr (YVEC) {
-          const int n = n0 + 4 * g;
-          const float* p = a.base + (int64_t)(t.row0 + min(m * 16 + r16, t.rows - 1)) * a.ldb + n;
-          if (n + 4 <= a.N)
-            bs[u][m] = *reinterpret_cast<const v4f*>(p);
-          else
-            for (int i = 0; i < 4; ++i)
-              if (n + i < a.N) bs[u][m][i] = p[i];
-        } else {
-          const int n = min(n0 + r16, a.N - 1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            bs[u][m][i] =
-                a.base[(int64_t)(t.row0 + min(m * 16 + 4 * g + i, t.rows - 1)) * a.ldb + n];
-        }
-      }
-  };
-  auto load_b = [&](int ct, BFrag<WT, RT>(&b)[2]) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      b[u].load(B + (int64_t)min(ct * 32 + u * 16 + r16, a.N - 1) * a.rank, ra, bvec, g);
-  };
+  const int blocks = (a.N + kBlockCols - 1) / kBlockCols;
+  const int c0 = blocks * share / a.shares + wave, c1 = blocks * (share + 1) / a.shares;
   if (c0 >= c1) return;
-  v4f bs[2][MT];
-  BFrag<WT, RT> b[2];
-  load_base(c0, bs);
-  if (!bare) load_b(c0, b);
-  for (int ct = c0; ct < c1; ct += NW) {
-    v4f nbs[2][MT];
-    BFrag<WT, RT> nb[2];
-    const int nx = min(ct + NW, c1 - 1);  // the last one is loaded again, unused
-    load_base(nx, nbs);
-    if (!bare) load_b(nx, nb);
+  auto load = [&](int c, Block<MT, YVEC>& y, BFrag<WT, RT>(&b)[4]) {
+    const int n0 = c * kBlockCols;
+    if (a.base)
+      y.load(a.base, a.ldb, t.row0, t.rows, n0, a.N, r16, g);
+    else
+      y.zero();
+    if (bare) return;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 4; ++u)
+      b[u].load(B + (int64_t)min(n0 + block_col<YVEC>(u, r16), a.N - 1) * a.rank, ra, bvec, g);
+  };
+  Block<MT, YVEC> y, ny;
+  BFrag<WT, RT> b[4], nb[4];
+  load(c0, y, b);
+  for (int c = c0; c < c1; c += NW) {
+    if (c + NW < c1) load(c + NW, ny, nb);
+    if (!bare) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        v4f v = bs[u][m];
-        if (!bare) v += b[u].template times<!YVEC, MT>(sf, m);
-        const int n0 = ct * 32 + u * 16;
-        if constexpr (YVEC) {
-          const int row = m * 16 + r16, n = n0 + 4 * g;
-          if (row < t.rows) {
-            float* y = a.Y + (int64_t)(t.row0 + row) * a.ldy + n;
-            if (n + 4 <= a.N)
-              *reinterpret_cast<v4f*>(y) = v;
-            else
-              for (int i = 0; i < 4; ++i)
-                if (n + i < a.N) y[i] = v[i];
-          }
-        } else {
-          const int n = n0 + r16;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = m * 16 + 4 * g + i;
-            if (row < t.rows && n < a.N) a.Y[(int64_t)(t.row0 + row) * a.ldy + n] = v[i];
-          }
-        }
-      }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      b[u] = nb[u];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) bs[u][m] = nbs[u][m];
+      for (int u = 0; u < 4; ++u) y.add(sf, b[u], u);
     }
+    y.store(a.Y, a.ldy, t.row0, t.rows, c * kBlockCols, a.N, r16, g);
+    y = ny;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) b[u] = nb[u];
   }
+}
+
+// In two launches, for large outputs: k_lora_s computes S of every tile once and
+// lays it out as the second product's operand; k_lora_expand adds S B^T to base.
+// A streaming workgroup here has 256 columns of 32 rows only: workgroups that
+// live short, started in address order, keep the chip's reads and writes in a
+// narrow window of memory. A copy of a [16384, 8192] fp32 matrix with this
+// kernel's accesses took 181 us with 256 columns a workgroup, 222 us with 2048
+// and 254 us with whole rows (1024 columns: 199, a flat copy: 185).
+//
+// S lies in the workspace as the second product reads it: for every 16 rows of a
+// tile SFrag's vectors, lane after lane.
+template <typename WT, int RT>
+constexpr int s_vectors() {
+  return sizeof(WT) == 4 ? RT : SFrag<bf16, RT, 1>::KS;
+}
+constexpr int kExpandRows = 32, kExpandCols = 256;
+
+template <typename XT, typename WT, int RT, int MT, int H, int NW>
+__global__ __launch_bounds__(64 * NW) void k_lora_s(ForwardArgs a, bool xvec, v4f* s_rows,
+                                                    int4* table) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int T = MT * 16, R = RT * 16, PARTS = kExpandRows / T;
+  __shared__ __align__(16) SBuf<RT, MT, H, NW> buf;
+  Tile t;
+  const int tile = blockIdx.x / PARTS, part = blockIdx.x % PARTS;
+  const bool found = find_tile(a.q, kExpandRows, tile, t);
+  if (part == 0 && threadIdx.x == 0)
+    table[tile] = found ? int4{t.row0, t.rows, t.adapter, 0} : int4{0, 0, -1, 0};
+  if (!found || t.rows <= part * T || (t.adapter < 0 && !a.S)) return;
+  t.row0 += part * T;
+  t.rows = min(T, t.rows - part * T);
+  const bool bare = t.adapter < 0;
+  const int ra = bare ? 0 : rank_of(a.ranks, t.adapter, a.rank);
+  const float sc = bare ? 0.0f : a.scales ? a.scales[t.adapter] : 1.0f;
+  tile_s<XT, WT, RT, MT, H, NW>(a, t, ra, sc, xvec, a.S != nullptr, buf);
+  if (bare) return;
+  constexpr int V = s_vectors<WT, RT>();
+  for (int m = wave; m < MT; m += NW) {
+    SFrag<WT, RT, 1> f;
+    f.load(&buf.v[0][m * 16][0], R + 4, lane & 15, lane >> 4);
+    v4f* o = s_rows + ((int64_t)(tile * (kExpandRows / 16) + part * MT + m) * V) * kWave + lane;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k * kWave] = __builtin_bit_cast(v4f, f.s[0][k]);
+  }
+}
+
+template <typename WT, int RT, bool YVEC>
+__global__ __launch_bounds__(256) void k_lora_expand(ForwardArgs a, bool bvec, const v4f* s_rows,
+                                                     const int4* table) {
+  constexpr int MT = kExpandRows / 16, V = s_vectors<WT, RT>();
+  const int xcd = blockIdx.x & 7, loc = blockIdx.x >> 3;
+  const int tile = loc / a.shares * 8 + xcd, share = loc % a.shares;
+  const int4 t = table[tile];
+  const int row0 = __builtin_amdgcn_readfirstlane(t.x), rows = __builtin_amdgcn_readfirstlane(t.y);
+  const int ad = __builtin_amdgcn_readfirstlane(t.z);
+  const bool bare = ad < 0;
+  if (rows == 0 || (bare && a.base == a.Y)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const int n0 = share * kExpandCols + wave * kBlockCols;
+  if (n0 >= a.N) return;
+  Block<MT, YVEC> y;  // base first: it waits for nothing else
+  if (a.base)
+    y.load(a.base, a.ldb, row0, rows, n0, a.N, r16, g);
+  else
+    y.zero();
+  if (!bare) {
+    const int ra = rank_of(a.ranks, ad, a.rank);
+    const WT* B = reinterpret_cast<const WT*>(a.B) + (int64_t)ad * a.N * a.rank;
+    BFrag<WT, RT> b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      b[u].load(B + (int64_t)min(n0 + block_col<YVEC>(u, r16), a.N - 1) * a.rank, ra, bvec, g);
+    SFrag<WT, RT, MT> sf;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        sf.s[m][k] = __builtin_bit_cast(typename SFrag<WT, RT, MT>::vec,
+                                        s_rows[((int64_t)(tile * MT + m) * V + k) * kWave + lane]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) y.add(sf, b[u], u);
+  }
+  y.store(a.Y, a.ldy, row0, rows, n0, a.N, r16, g);
 }
 
 // ------------------------------------------------------------------- outer ----
@@ -708,22 +838,6 @@ __global__ __launch_bounds__(256) void k_lora_slot_sum(SlotSumArgs a) {
   reinterpret_cast<WT*>(a.out)[ad * len + e] = (WT)r;
 }
 
-// Tiles of 64 rows from which on the taller tiles are used.
-#ifndef QL_WIDE
-#define QL_WIDE 128
-#endif
-#ifndef QL_WGS
-#define QL_WGS 1024
-#endif
-constexpr int kWideTiles = QL_WIDE;
-
-// Workgroups that share one tile of rows: about QL_WGS in all, none with fewer
-// than 128 columns.
-int forward_shares(int tiles, int N) {
-  const int want = (QL_WGS + tiles - 1) / tiles, cap = (N + 127) / 128;
-  return want < cap ? want : cap;
-}
-
 int max_tiles(const Requests& q, int T) {
   const int64_t t = (int64_t)q.rows / T + q.n;
   return (int)(t < q.rows ? t : q.rows);
@@ -747,36 +861,80 @@ hipError_t shrink_rt(const ShrinkArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename XT, typename WT, int RT, int MT, int H, int NW>
-hipError_t forward_run(ForwardArgs a, bool xvec, bool yvec, bool bvec, hipStream_t s) {
-  const int tiles = (max_tiles(a.q, MT * 16) + 7) / 8 * 8;
-  a.shares = forward_shares(tiles, a.N);
+// Calls with fewer outputs than this take one launch. Measured (one launch / two):
+// 1024 x 4608, K 1152, rank 16, fp32: 15.3 / 17.9 us; 1024 x 4608, K 2048, rank 64,
+// bf16: 21.9 / 24.8; guided 2048 x 4608, K 1152, rank 16, fp32: 38.4 / 27.5;
+// 16384 x 8192, K 2048, rank 64, bf16: 298 / 239.
+constexpr int64_t kTwoLaunches = 1 << 23;
+bool two_launches(int rows, int N) { return (int64_t)rows * N >= kTwoLaunches; }
+
+// Padded tiles of the two-launch form.
+int expand_tiles(int rows, int n_req) {
+  Requests q{};
+  q.rows = rows;
+  q.n = n_req;
+  return (max_tiles(q, kExpandRows) + 7) / 8 * 8;
+}
+// Bytes of S of one tile.
+int64_t s_bytes(int rank, bool w_bf16) {
+  const int rt = rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8;
+  const int vectors = !w_bf16 ? rt : rt == 1 ? 2 : 3 * rt / 2;
+  return (int64_t)(kExpandRows / 16) * vectors * kWave * 16;
+}
+
+template <typename XT, typename WT, int RT, int H>
+hipError_t forward_run(ForwardArgs a, hipStream_t s) {
+  const bool xvec = reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && (a.ldx * sizeof(XT)) % 16 == 0;
+  const bool yvec = reinterpret_cast<uintptr_t>(a.Y) % 16 == 0 && a.ldy % 4 == 0 &&
+                    (!a.base || (reinterpret_cast<uintptr_t>(a.base) % 16 == 0 && a.ldb % 4 == 0));
+  const bool bvec = reinterpret_cast<uintptr_t>(a.B) % 16 == 0 && a.rank % (16 / sizeof(WT)) == 0;
+  if (two_launches(a.q.rows, a.N)) {
+    constexpr int NW = RT * H >= 8 ? 4 : 8;  // the waves' sums fit LDS
+    const int tiles = expand_tiles(a.q.rows, a.q.n);
+    int4* table = reinterpret_cast<int4*>(a.ws);
+    v4f* s_rows = reinterpret_cast<v4f*>(table + tiles);
+    if (tiles < 512)
+      hipLaunchKernelGGL((k_lora_s<XT, WT, RT, 1, H, 8>), dim3(2 * tiles), dim3(512), 0, s, a, xvec,
+                         s_rows, table);
+    else
+      hipLaunchKernelGGL((k_lora_s<XT, WT, RT, 2, H, NW>), dim3(tiles), dim3(64 * NW), 0, s, a, xvec,
+                         s_rows, table);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.shares = (a.N + kExpandCols - 1) / kExpandCols;
+    const dim3 grid(tiles * a.shares);
+    if (yvec)
+      hipLaunchKernelGGL((k_lora_expand<WT, RT, true>), grid, dim3(256), 0, s, a, bvec, s_rows,
+                         table);
+    else
+      hipLaunchKernelGGL((k_lora_expand<WT, RT, false>), grid, dim3(256), 0, s, a, bvec, s_rows,
+                         table);
+    return hipGetLastError();
+  }
+  constexpr int NW = 8;
+  const int tiles = (max_tiles(a.q, 16) + 7) / 8 * 8;
+  // About one workgroup a compute unit: more of them would compute S again (512
+  // instead of 256: 1003 ragged rows 14.7 instead of 12.0 us).
+  const int want = (256 + tiles - 1) / tiles, cap = (a.N + 127) / 128;
+  a.shares = want < cap ? want : cap;
   const dim3 grid(tiles * a.shares), block(64 * NW);
-#define QL_FWD(YV)                                                                           \
-  hipLaunchKernelGGL((k_lora_forward<XT, WT, RT, MT, H, NW, YV>), grid, block, 0, s, a, xvec, \
-                     bvec)
   if (yvec)
-    QL_FWD(true);
+    hipLaunchKernelGGL((k_lora_forward<XT, WT, RT, 1, H, NW, true>), grid, block, 0, s, a, xvec,
+                       bvec);
   else
-    QL_FWD(false);
-#undef QL_FWD
+    hipLaunchKernelGGL((k_lora_forward<XT, WT, RT, 1, H, NW, false>), grid, block, 0, s, a, xvec,
+                       bvec);
   return hipGetLastError();
 }
 
 template <typename XT, typename WT>
 hipError_t forward_rt(const ForwardArgs& a, hipStream_t s) {
-  const bool xvec = reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && (a.ldx * sizeof(XT)) % 16 == 0;
-  const bool yvec = reinterpret_cast<uintptr_t>(a.Y) % 16 == 0 && a.ldy % 4 == 0 &&
-                    (!a.base || (reinterpret_cast<uintptr_t>(a.base) % 16 == 0 && a.ldb % 4 == 0));
-  const bool bvec = reinterpret_cast<uintptr_t>(a.B) % 16 == 0 && a.rank % (16 / sizeof(WT)) == 0;
-  const bool wide = max_tiles(a.q, 64) >= kWideTiles;
-#define QL_RUN(RT, MT, NW)                                                      \
-  (a.halves == 2 ? forward_run<XT, WT, RT, MT, 2, NW>(a, xvec, yvec, bvec, s)   \
-                 : forward_run<XT, WT, RT, MT, 1, NW>(a, xvec, yvec, bvec, s))
-  if (a.rank <= 16) return wide ? QL_RUN(1, 4, 4) : QL_RUN(1, 1, 4);
-  if (a.rank <= 32) return wide ? QL_RUN(2, 4, 4) : QL_RUN(2, 1, 4);
-  if (a.rank <= 64) return wide ? QL_RUN(4, 2, 4) : QL_RUN(4, 1, 4);
-  return QL_RUN(8, 1, 4);
+#define QL_RUN(RT) \
+  (a.halves == 2 ? forward_run<XT, WT, RT, 2>(a, s) : forward_run<XT, WT, RT, 1>(a, s))
+  if (a.rank <= 16) return QL_RUN(1);
+  if (a.rank <= 32) return QL_RUN(2);
+  if (a.rank <= 64) return QL_RUN(4);
+  return QL_RUN(8);
 #undef QL_RUN
 }
 
@@ -823,6 +981,11 @@ hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t s) {
   if (a.p_bf16)
     return a.w_bf16 ? shrink_rt<bf16, bf16, false>(a, s) : shrink_rt<bf16, float, false>(a, s);
   return a.w_bf16 ? shrink_rt<float, bf16, false>(a, s) : shrink_rt<float, float, false>(a, s);
+}
+
+int64_t lora_forward_ws(int rows, int n_req, int N, int rank, bool w_bf16) {
+  if (!two_launches(rows, N)) return 0;
+  return expand_tiles(rows, n_req) * ((int64_t)sizeof(int4) + s_bytes(rank, w_bf16));
 }
 
 hipError_t launch_lora_forward(const ForwardArgs& a, hipStream_t s) {

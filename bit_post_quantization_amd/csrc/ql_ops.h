@@ -55,6 +55,7 @@ struct ForwardArgs {
   float* Y;
   int64_t ldb, ldy;
   float* S;           // nullptr, or [rows * halves, rank]
+  void* ws;           // lora_forward_ws() bytes
   int shares;         // workgroups of one tile of rows (set by the launch)
   bool x_bf16, w_bf16;
 };
@@ -94,6 +95,8 @@ struct SlotSumArgs {
 };
 
 hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t s);
+// Workspace of a forward call with `rows` output rows.
+int64_t lora_forward_ws(int rows, int n_req, int N, int rank, bool w_bf16);
 hipError_t launch_lora_forward(const ForwardArgs& a, hipStream_t s);
 hipError_t launch_lora_outer(const OuterArgs& a, hipStream_t s);
 hipError_t launch_lora_slot_sum(const SlotSumArgs& a, hipStream_t s);

@@ -200,17 +200,22 @@ ql_status check_grads(const ql_grad* table, int32_t n, int64_t units, const doub
 
 extern "C" {
 
-ql_status qlinear_lora_grad_workspace(const ql_lora* d, int32_t M, int32_t n_requests,
-                                      int64_t* bytes) {
+ql_status qlinear_lora_workspace(const ql_lora* d, int32_t M, int32_t n_requests, int32_t cfg,
+                                 int32_t grad, int64_t* bytes) {
   QL_CHECK(check_lora(d, M, n_requests));
   if (!bytes) return fail(QL_ERR_ARG, "bytes is NULL");
-  *bytes = grad_ws(d, M, n_requests).total;
+  if (cfg != 0 && cfg != 1) return fail(QL_ERR_ARG, "cfg = %d must be 0 or 1", cfg);
+  if (grad != 0 && grad != 1) return fail(QL_ERR_ARG, "grad = %d must be 0 or 1", grad);
+  *bytes = grad ? grad_ws(d, M, n_requests).total
+                : ql::lora_forward_ws(cfg ? M / 2 : M, n_requests, d->N, d->rank,
+                                      d->w_dtype == QL_BF16);
   return ok();
 }
 
 ql_status qlinear_lora(const ql_lora* d, const void* X, int64_t ldx, int32_t M,
                        const ql_requests* q, int32_t cfg, float w, const float* base, int64_t ldb,
-                       float* Y, int64_t ldy, float* S, void* stream) {
+                       float* Y, int64_t ldy, float* S, void* workspace, int64_t workspace_bytes,
+                       void* stream) {
   if (!q) return fail(QL_ERR_ARG, "requests is NULL");
   QL_CHECK(check_lora(d, M, q->n_requests));
   if (cfg != 0 && cfg != 1) return fail(QL_ERR_ARG, "cfg = %d must be 0 or 1", cfg);
@@ -229,14 +234,17 @@ ql_status qlinear_lora(const ql_lora* d, const void* X, int64_t ldx, int32_t M,
     return fail(QL_ERR_ARG, "base is Y with another row stride (%lld, %lld)", (long long)ldb,
                 (long long)ldy);
   ql::ForwardArgs a{};
+  a.halves = cfg ? 2 : 1;
+  a.q = requests(d, q, M / a.halves);
+  QL_CHECK(check_workspace(workspace, workspace_bytes,
+                           ql::lora_forward_ws(a.q.rows, q->n_requests, d->N, d->rank,
+                                               d->w_dtype == QL_BF16)));
   a.X = X;
   a.ldx = ldx;
   a.A = d->A;
   a.B = d->B;
   a.scales = d->scales;
   a.ranks = d->ranks;
-  a.halves = cfg ? 2 : 1;
-  a.q = requests(d, q, M / a.halves);
   a.N = d->N;
   a.K = d->K;
   a.rank = d->rank;
@@ -246,6 +254,7 @@ ql_status qlinear_lora(const ql_lora* d, const void* X, int64_t ldx, int32_t M,
   a.ldb = ldb;
   a.ldy = ldy;
   a.S = S;
+  a.ws = workspace;
   a.x_bf16 = d->x_dtype == QL_BF16;
   a.w_bf16 = d->w_dtype == QL_BF16;
   QL_LAUNCH(ql::launch_lora_forward(a, reinterpret_cast<hipStream_t>(stream)),

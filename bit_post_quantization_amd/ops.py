@@ -82,28 +82,34 @@ def _on(stream):
 
 
 def _workspace(nbytes: int):
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cuda")
+    return torch.empty(nbytes, dtype=torch.uint8, device="cuda") if nbytes else None
+
+
+def _nbytes(workspace) -> int:
+    return 0 if workspace is None else workspace.numel()
 
 
 # ------------------------------------------------------- C ABI, same names ----
 
-def qlinear_lora(desc: QlLora, X, ldx, M, requests: QlRequests, cfg, w, base, ldb, Y, ldy, S,
-                 stream) -> None:
-    check(_lib.load().qlinear_lora(_byref(desc), _ptr(X), ldx, M, _byref(requests), cfg, w,
-                                   _ptr(base), ldb, _ptr(Y), ldy, _ptr(S), stream))
-
-
-def qlinear_lora_grad_workspace(desc: QlLora, M: int, n_requests: int) -> int:
+def qlinear_lora_workspace(desc: QlLora, M: int, n_requests: int, cfg: int = 0,
+                           grad: int = 0) -> int:
     n = ctypes.c_int64()
-    check(_lib.load().qlinear_lora_grad_workspace(_byref(desc), M, n_requests, _byref(n)))
+    check(_lib.load().qlinear_lora_workspace(_byref(desc), M, n_requests, cfg, grad, _byref(n)))
     return n.value
+
+
+def qlinear_lora(desc: QlLora, X, ldx, M, requests: QlRequests, cfg, w, base, ldb, Y, ldy, S,
+                 workspace, stream) -> None:
+    check(_lib.load().qlinear_lora(_byref(desc), _ptr(X), ldx, M, _byref(requests), cfg, w,
+                                   _ptr(base), ldb, _ptr(Y), ldy, _ptr(S), _ptr(workspace),
+                                   _nbytes(workspace), stream))
 
 
 def qlinear_lora_grad(desc: QlLora, X, ldx, M, requests: QlRequests, S, dY, lddy, dX, lddx, dA, dB,
                       workspace, stream) -> None:
     check(_lib.load().qlinear_lora_grad(_byref(desc), _ptr(X), ldx, M, _byref(requests), _ptr(S),
                                         _ptr(dY), lddy, _ptr(dX), lddx, _ptr(dA), _ptr(dB),
-                                        _ptr(workspace), workspace.numel(), stream))
+                                        _ptr(workspace), _nbytes(workspace), stream))
 
 
 def qlinear_group_norm_workspace(desc: QlNorm, grad: int = 0) -> int:
@@ -116,7 +122,7 @@ def qlinear_group_norm(desc: QlNorm, x, x_strides, y, y_strides, mean, rstd, wor
                        stream) -> None:
     check(_lib.load().qlinear_group_norm(_byref(desc), _ptr(x), *x_strides, _ptr(y), *y_strides,
                                          _ptr(mean), _ptr(rstd), _ptr(workspace),
-                                         workspace.numel(), stream))
+                                         _nbytes(workspace), stream))
 
 
 def qlinear_group_norm_grad(desc: QlNorm, dy, dy_strides, x, x_strides, mean, rstd, dx, dx_strides,
@@ -124,7 +130,7 @@ def qlinear_group_norm_grad(desc: QlNorm, dy, dy_strides, x, x_strides, mean, rs
     check(_lib.load().qlinear_group_norm_grad(_byref(desc), _ptr(dy), *dy_strides, _ptr(x),
                                               *x_strides, _ptr(mean), _ptr(rstd), _ptr(dx),
                                               *dx_strides, _ptr(dgamma), _ptr(dbeta),
-                                              _ptr(workspace), workspace.numel(), stream))
+                                              _ptr(workspace), _nbytes(workspace), stream))
 
 
 def qlinear_grad_norm(table, n: int, units: int, partials, stream) -> None:
@@ -164,7 +170,7 @@ class LoraAdapters:
         self.desc = QlLora(N=self.N, K=self.K, rank=self.rank, n_adapters=n,
                            x_dtype=_DT[self.x_dtype], w_dtype=_DT[A.dtype], A=_ptr(A), B=_ptr(B),
                            scales=_ptr(scales), ranks=_ptr(ranks))
-        qlinear_lora_grad_workspace(self.desc, 0, 1)  # its checks
+        qlinear_lora_workspace(self.desc, 0, 1)  # its checks
 
     def _requests(self, row_offsets, adapter) -> QlRequests:
         n = adapter.numel()
@@ -186,9 +192,10 @@ class LoraAdapters:
             if out is None:
                 out = torch.empty((rows, self.N), dtype=torch.float32, device="cuda")
             S = torch.empty((M, self.rank), dtype=torch.float32, device="cuda") if save else None
+            ws = _workspace(qlinear_lora_workspace(self.desc, M, q.n_requests, cfg))
         ldy = _rows(out, "out", torch.float32, (rows, self.N))
         ldb = 0 if base is None else _rows(base, "base", torch.float32, (rows, self.N))
-        qlinear_lora(self.desc, X, ldx, M, q, cfg, w, base, ldb, out, ldy, S, s)
+        qlinear_lora(self.desc, X, ldx, M, q, cfg, w, base, ldb, out, ldy, S, ws, s)
         return (out, S) if save else out
 
     def grad(self, X, row_offsets, adapter, S, dY, need_dx: bool = True, stream=None):
@@ -203,7 +210,7 @@ class LoraAdapters:
         with ctx:
             dX = torch.empty((M, self.K), dtype=self.x_dtype, device="cuda") if need_dx else None
             dA, dB = torch.empty_like(self.A), torch.empty_like(self.B)
-            ws = _workspace(qlinear_lora_grad_workspace(self.desc, M, q.n_requests))
+            ws = _workspace(qlinear_lora_workspace(self.desc, M, q.n_requests, 0, 1))
         qlinear_lora_grad(self.desc, X, ldx, M, q, S, dY, lddy, dX, self.K, dA, dB, ws, s)
         return dX, dA, dB
 

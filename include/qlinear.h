@@ -362,6 +362,12 @@ typedef struct {
   const int32_t* adapter;      /* DEVICE [n_requests] */
 } ql_requests;
 
+/* Workspace bytes (HOST out, may be 0) of qlinear_lora (grad = 0) or
+ * qlinear_lora_grad (grad = 1, cfg ignored) with M rows and n_requests requests.
+ * The pointers in d are not looked at. */
+ql_status qlinear_lora_workspace(const ql_lora* d, int32_t M, int32_t n_requests, int32_t cfg,
+                                 int32_t grad, int64_t* bytes);
+
 /*
  * Y[m,:] = base[m,:] + scale_a (X[m,:] A_a^T) B_a^T for the rows of every
  * request; rows without an adapter get base. Sums in fp32.
@@ -379,13 +385,8 @@ typedef struct {
  */
 ql_status qlinear_lora(const ql_lora* d, const void* X, int64_t ldx, int32_t M,
                        const ql_requests* q, int32_t cfg, float w, const float* base, int64_t ldb,
-                       float* Y, int64_t ldy, float* S, void* stream);
-
-/* Workspace bytes (HOST out) of qlinear_lora_grad with M rows and n_requests
- * requests. The pointers in d are not looked at. */
-ql_status qlinear_lora_grad_workspace(const ql_lora* d, int32_t M, int32_t n_requests,
-                                      int64_t* bytes);
-
+                       float* Y, int64_t ldy, float* S, void* workspace, int64_t workspace_bytes,
+                       void* stream);
 /*
  * Gradients of qlinear_lora with cfg = 0, for dY [M,N] fp32 (row stride lddy):
  * with dS = scale_a dY B_a,

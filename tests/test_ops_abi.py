@@ -42,10 +42,10 @@ def test_lora_descriptor(kw, status, frag):
     L = _lib.load()
     n = ctypes.c_int64()
     d = _lora(**kw)
-    assert L.qlinear_lora_grad_workspace(ctypes.byref(d), 16, 1, ctypes.byref(n)) == status
+    assert L.qlinear_lora_workspace(ctypes.byref(d), 16, 1, 0, 0, ctypes.byref(n)) == status
     assert frag in _msg()
     assert L.qlinear_lora(ctypes.byref(d), A, 64, 16, ctypes.byref(_req()), 0, 1.0, A, 100, A, 100,
-                          U, U) == status
+                          U, A, 1 << 30, U) == status
     assert L.qlinear_lora_grad(ctypes.byref(d), A, 64, 16, ctypes.byref(_req()), A, A, 100, A, 64,
                                A, A, A, 1 << 30, U) == status
 
@@ -54,21 +54,26 @@ def test_lora_workspace_query():
     L = _lib.load()
     n = ctypes.c_int64()
     d = _lora()
-    query = L.qlinear_lora_grad_workspace
-    assert query(U, 16, 1, ctypes.byref(n)) == _lib.QL_ERR_ARG
-    assert query(ctypes.byref(d), -1, 1, ctypes.byref(n)) == _lib.QL_ERR_ARG
-    assert query(ctypes.byref(d), 16, 0, ctypes.byref(n)) == _lib.QL_ERR_ARG
-    assert query(ctypes.byref(d), 16, 1, U) == _lib.QL_ERR_ARG
-    assert query(ctypes.byref(d), (1 << 23) + 1, 1, ctypes.byref(n)) == _lib.QL_ERR_UNSUPPORTED
-    assert query(ctypes.byref(d), 16, 1, ctypes.byref(n)) == _lib.QL_OK
-    assert n.value >= 16 * 8 * 4
+    query = L.qlinear_lora_workspace
+    assert query(U, 16, 1, 0, 0, ctypes.byref(n)) == _lib.QL_ERR_ARG
+    assert query(ctypes.byref(d), -1, 1, 0, 0, ctypes.byref(n)) == _lib.QL_ERR_ARG
+    assert query(ctypes.byref(d), 16, 0, 0, 0, ctypes.byref(n)) == _lib.QL_ERR_ARG
+    assert query(ctypes.byref(d), 16, 1, 2, 0, ctypes.byref(n)) == _lib.QL_ERR_ARG
+    assert query(ctypes.byref(d), 16, 1, 0, 2, ctypes.byref(n)) == _lib.QL_ERR_ARG
+    assert query(ctypes.byref(d), 16, 1, 0, 0, U) == _lib.QL_ERR_ARG
+    assert query(ctypes.byref(d), (1 << 23) + 1, 1, 0, 0, ctypes.byref(n)) == \
+        _lib.QL_ERR_UNSUPPORTED
+    for M, grad, least in ((16, 0, 0), (16, 1, 16 * 8 * 4), (1 << 20, 0, (1 << 20) * 8 * 4)):
+        assert query(ctypes.byref(d), M, 1, 0, grad, ctypes.byref(n)) == _lib.QL_OK
+        assert n.value >= least
 
 
-def _apply(d=None, X=A, ldx=64, M=16, q="ok", cfg=0, base=A, ldb=100, Y=A + 64, ldy=100, S=U):
+def _apply(d=None, X=A, ldx=64, M=16, q="ok", cfg=0, base=A, ldb=100, Y=A + 64, ldy=100, S=U, ws=A,
+           nb=1 << 30):
     d = _lora() if d is None else d
     q = _req() if q == "ok" else q
     return _lib.load().qlinear_lora(ctypes.byref(d), X, ldx, M, ctypes.byref(q) if q else U, cfg,
-                                    1.0, base, ldb, Y, ldy, S, U)
+                                    1.0, base, ldb, Y, ldy, S, ws, nb, U)
 
 
 @pytest.mark.parametrize("kw,frag", [
@@ -88,6 +93,9 @@ def _apply(d=None, X=A, ldx=64, M=16, q="ok", cfg=0, base=A, ldb=100, Y=A + 64, 
     (dict(ldy=99), "ldy = 99"),
     (dict(ldb=99), "ldb = 99"),
     (dict(base=A, Y=A, ldb=100, ldy=101), "another row stride"),
+    (dict(M=1 << 20, ws=U), "workspace is NULL"),
+    (dict(ws=A + 8), "16-byte"),
+    (dict(M=1 << 20, nb=1 << 20), "workspace holds"),
     (dict(d=_lora(A=U)), "A or B"),
     (dict(d=_lora(B=U)), "A or B"),
     (dict(d=_lora(A=A + 4)), "A must be"),
