@@ -107,89 +107,6 @@ __device__ __forceinline__ v4f mfma_f32(float a, float b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// ------------------------------------------------------------------ shrink ----
-// One workgroup: a tile of MT * 16 rows, one column split. Its four waves take
-// every fourth 32-column step and their sums are joined in LDS. In a step lane
-// l holds columns 8 (l / 16) .. + 7 of row l % 16 of both operands; element e
-// of all lanes is one 16x16x4 product (the order of the columns inside a sum
-// is free).
-template <typename XT, typename WT, int RT, int MT, bool WCOLS>
-__global__ __launch_bounds__(256) void k_lora_shrink(ShrinkArgs a, bool vec) {
-  constexpr int kRows = MT * 16;
-  __shared__ float red[3][kRows][RT * 16 + 4];
-  Tile t;
-  if (!find_tile(a.q, kRows, blockIdx.x, t) || t.adapter < 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  const int64_t mtot = (int64_t)a.q.rows * a.halves;
-  const int64_t row0 = (int64_t)blockIdx.z * a.q.rows + t.row0;
-  const int c0 = blockIdx.y * a.split_len, c1 = min(a.D, c0 + a.split_len);
-  const XT* P = reinterpret_cast<const XT*>(a.P);
-  const WT* W = reinterpret_cast<const WT*>(a.W) + (int64_t)t.adapter * a.rank * a.D;
-  const XT* prow[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) prow[m] = P + (row0 + min(m * 16 + r16, t.rows - 1)) * a.ldp;
-  int wj[RT];  // stored rank row of this lane (clamped: its products are dropped at the end)
-#pragma unroll
-  for (int r = 0; r < RT; ++r) wj[r] = min(r * 16 + r16, a.rank - 1);
-  v4f acc[MT][RT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) acc[m][r] = v4f{0, 0, 0, 0};
-  for (int c = c0 + wave * kShrinkStep; c < c1; c += 4 * kShrinkStep) {
-    const int k = c + 8 * g;
-    const int valid = c1 - k;
-    float x[MT][8], w[RT][8];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) load_n<8>(prow[m] + k, valid, vec, x[m]);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      if constexpr (WCOLS) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          w[r][e] = e < valid ? (float)W[(int64_t)(k + e) * a.rank + wj[r]] : 0.0f;
-      } else {
-        load_n<8>(W + (int64_t)wj[r] * a.D + k, valid, true, w[r]);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[m][r] = mfma_f32(w[r][e], x[m][e], acc[m][r]);
-  }
-  // acc[m][r][i]: row m * 16 + lane % 16, rank r * 16 + 4 g + i
-  if (wave > 0) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-        *reinterpret_cast<v4f*>(&red[wave - 1][m * 16 + r16][r * 16 + 4 * g]) = acc[m][r];
-  }
-  __syncthreads();
-  if (wave > 0) return;
-  const int ra = rank_of(a.ranks, t.adapter, a.rank);
-  const float sc = a.scales ? a.scales[t.adapter] : 1.0f;
-  float* out = a.part + ((int64_t)blockIdx.y * mtot + row0) * a.rank;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = m * 16 + r16;
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      v4f v = acc[m][r];
-#pragma unroll
-      for (int u = 0; u < 3; ++u) v += *reinterpret_cast<v4f*>(&red[u][row][r * 16 + 4 * g]);
-      if (row >= t.rows) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = r * 16 + 4 * g + i;
-        if (j < a.rank) out[(int64_t)row * a.rank + j] = j < ra ? v[i] * sc : 0.0f;
-      }
-    }
-  }
-}
-
 // ----------------------------------------------------------------- forward ----
 // One workgroup: a tile of MT * 16 rows (of both halves when guided) and a
 // share of the output columns. First the tile's S = X A^T, the waves taking
@@ -314,6 +231,16 @@ struct BFrag<float, RT> {
 #pragma unroll
     for (int r = 0; r < RT; ++r) load_n<4>(row + r * 16 + 4 * g, ra - r * 16 - 4 * g, vec, b[r]);
   }
+  // The same from a column of A: element j at p[j * ld].
+  __device__ __forceinline__ void load_column(const float* p, int64_t ld, int ra, int g) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = r * 16 + 4 * g + e;
+        b[r][e] = j < ra ? p[j * ld] : 0.0f;
+      }
+  }
   // lane: row 4 g + i of S's tile, the product with this lane's row of B
   template <int MT>
   __device__ __forceinline__ v4f times(const SFrag<float, RT, MT>& s, int m) const {
@@ -340,6 +267,15 @@ struct BFrag<bf16, RT> {
         for (int e = 0; e < 8; ++e) b[k][e] = j + e < ra ? row[j + e] : (bf16)0.0f;
       }
     }
+  }
+  __device__ __forceinline__ void load_column(const bf16* p, int64_t ld, int ra, int g) {
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = (RT == 1 ? 8 * (g & 1) : 32 * k + 8 * g) + e;
+        b[k][e] = j < ra ? p[j * ld] : (bf16)0.0f;
+      }
   }
   template <int MT>
   __device__ __forceinline__ v4f times(const SFrag<bf16, RT, MT>& s, int m) const {
@@ -693,24 +629,134 @@ __global__ __launch_bounds__(256) void k_lora_expand(ForwardArgs a, bool bvec, c
   y.store(a.Y, a.ldy, row0, rows, n0, a.N, r16, g);
 }
 
-// ------------------------------------------------------------------- outer ----
-// One workgroup: 64 columns (16 a wave) of one range of rows, 32 rows at a
-// time: their Q (rank values a row) goes through LDS. Piece by piece (the rows
-// of one request in the range) the product Q^T P is summed in registers and
-// written out.
-constexpr int kOuterCols = 64;
-constexpr int kOuterRows = 32;
-
-template <typename XT, typename WT, int RT, bool DX, bool TR>
-__global__ __launch_bounds__(256) void k_lora_outer(OuterArgs a) {
-  constexpr int R = RT * 16;
-  __shared__ float qs[kOuterRows][R + 4];
+// ------------------------------------------------------------------ dS = dY B ----
+// One workgroup: a tile of MT * 16 rows and one split of the columns of dY. The
+// waves take every NW-th 32 columns, the next step's loads ahead of this one's
+// products, and join their sums in LDS. Lane l of a step has columns
+// 8 (l / 16) .. + 7 of row l % 16 of dY, and rank l % 16 of the same rows of B.
+template <typename WT, int RT, int MT, int NW>
+__global__ __launch_bounds__(64 * NW) void k_lora_ds(DsArgs a, bool vec) {
+  constexpr int T = MT * 16;
+  __shared__ __align__(16) float red[NW][T][RT * 16 + 4];
+  Tile t;
+  if (!find_tile(a.q, T, blockIdx.x, t) || t.adapter < 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  const int d0 = blockIdx.x * kOuterCols + wave * 16;
-  const int sp = blockIdx.y;
+  const int c0 = blockIdx.y * a.split_len, c1 = min(a.N, c0 + a.split_len);
+  const WT* B = reinterpret_cast<const WT*>(a.B) + (int64_t)t.adapter * a.N * a.rank;
+  const float* prow[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    prow[m] = a.dY + (int64_t)(t.row0 + min(m * 16 + r16, t.rows - 1)) * a.ldy;
+  int wj[RT];  // stored rank of this lane (clamped: its sums are dropped at the end)
+#pragma unroll
+  for (int r = 0; r < RT; ++r) wj[r] = min(r * 16 + r16, a.rank - 1);
+  v4f acc[MT][RT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[m][r] = v4f{0, 0, 0, 0};
+  Frag8<float> x[MT], nx[MT];
+  WT w[RT][8], nw[RT][8];
+  auto load = [&](int c, Frag8<float>(&fx)[MT], WT(&fw)[RT][8]) {
+    const int k = c + 8 * g, valid = c1 - k;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (vec && valid >= 8)
+        fx[m].load(prow[m] + k);
+      else
+        fx[m].load(prow[m] + k, valid);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // past the end dY is zero; the row of B read there is the last one, whose
+      // elements may not be finite, so it is zero too
+      const WT* row = B + (int64_t)min(k + e, a.N - 1) * a.rank;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) fw[r][e] = e < valid ? row[wj[r]] : (WT)0.0f;
+    }
+  };
+  int c = c0 + wave * kDsStep;
+  if (c < c1) load(c, x, w);
+  for (; c < c1; c += NW * kDsStep) {
+    if (c + NW * kDsStep < c1) load(c + NW * kDsStep, nx, nw);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[m][r] = mfma_f32((float)w[r][e], x[m].get(e), acc[m][r]);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) x[m] = nx[m];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[r][e] = nw[r][e];
+  }
+  // acc[m][r][i]: row 16 m + lane % 16, rank 16 r + 4 g + i
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      *reinterpret_cast<v4f*>(&red[wave][m * 16 + r16][r * 16 + 4 * g]) = acc[m][r];
+  __syncthreads();
+  const int ra = rank_of(a.ranks, t.adapter, a.rank);
+  const float sc = a.scales ? a.scales[t.adapter] : 1.0f;
+  float* out = a.part + ((int64_t)blockIdx.y * a.q.rows + t.row0) * a.rank;
+  for (int u = threadIdx.x; u < t.rows * a.rank; u += 64 * NW) {
+    const int row = u / a.rank, j = u % a.rank;
+    float v = red[0][row][j];
+#pragma unroll
+    for (int k = 1; k < NW; ++k) v += red[k][row][j];
+    out[u] = j < ra ? v * sc : 0.0f;
+  }
+}
+
+// ------------------------------------------------------------------- outer ----
+// dA_a = dS^T X with dX = dS A_a on the way (one reading of X), and dB_a = dY^T S.
+// One workgroup: 64 U columns (16 U a wave) of one range of rows, 32 rows at a
+// time. Q (dS or S, rank values a row) goes through LDS; piece by piece (the
+// rows of one request in the range) Q^T P is summed in registers and written to
+// a slot of its own, and A's columns stay in registers for the whole range.
+//
+// bf16 X takes bf16 matrix instructions, with Q in three bf16 terms that sum to
+// it exactly; both operands of dA are read from LDS transposed
+// (ds_read_b64_tr_b16: lane c of 16 gets four rows of column c). fp32 P takes
+// the fp32 instructions, element by element from memory: lanes side by side
+// have addresses side by side.
+constexpr int kOuterRows = 32;
+constexpr int outer_u(int rt) { return rt == 8 ? 2 : 4; }  // 16-column tiles of a wave
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s* lds_v4s;
+
+// Rows 4 g .. + 3 and 16 + 4 g .. + 3 of column lane % 16 of a [32][ld] tile of bf16.
+__device__ __forceinline__ v8h read_transposed(const bf16* tile, int ld, int r16, int g) {
+  const bf16* p = tile + (4 * g + r16 / 4) * ld + 4 * (r16 % 4);
+  const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p));
+  const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p + 16 * ld));
+  return __builtin_bit_cast(v8h, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <typename XT, int RT>
+struct OuterLds {
+  static constexpr int R = RT * 16, U = outer_u(RT);
+  static constexpr int XLD = 64 * U + 8, QLD = R + 8;
+  static constexpr int kPlanes = RT == 1 ? 4 : 3;
+  float q[kOuterRows][R + 4];
+  bf16 x[sizeof(XT) == 2 ? kOuterRows : 1][XLD];
+  bf16 h[kPlanes][kOuterRows][QLD];  // the terms of q (a fourth one of zeros for R = 16)
+};
+
+template <typename PT, typename WT, int RT, bool DX, bool TR>
+__device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, RT>& lds) {
+  constexpr int R = RT * 16, U = outer_u(RT);
+  constexpr bool PB = sizeof(PT) == 2;        // bf16 products for Q^T P
+  constexpr bool XB = DX && sizeof(WT) == 2;  // bf16 products for dX
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
+  const int dw = chunk * 64 * U, d0 = dw + wave * 16 * U;  // the workgroup's, the wave's columns
   const int lo = min(sp * a.row_len, a.q.rows), hi = min(lo + a.row_len, a.q.rows);
-  const XT* P = reinterpret_cast<const XT*>(a.P);
-  XT* dX = reinterpret_cast<XT*>(a.dX);
+  const PT* P = reinterpret_cast<const PT*>(a.P);
+  PT* dX = reinterpret_cast<PT*>(a.dX);
   const int64_t qstride = (int64_t)a.q.rows * a.rank;
   // Requests first .. last touch this range (ends included, so that the slots
   // s + i of neighbouring ranges join without gaps).
@@ -724,112 +770,224 @@ __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs a) {
       ch += __popcll(__ballot(e <= hi));
     }
     if (sp > 0) first = min(cl, a.q.n - 1);
-    if (sp + 1 < (int)gridDim.y) last = min(ch, a.q.n - 1);
+    if (sp + 1 < a.splits) last = min(ch, a.q.n - 1);
   }
-  v4f acc[RT];
+  v4f acc[RT][U];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) acc[r] = v4f{0, 0, 0, 0};
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc[r][u] = v4f{0, 0, 0, 0};
+  BFrag<WT, RT> af[U];  // A's columns d0 + col(u), like rows of B
+  int af_of = -1;
   bool pending = false;
+  const auto col = [&](int u) { return U == 4 ? 4 * r16 + u : 2 * r16 + u; };
   for (int i = first; i <= last; ++i) {
     const int b = clampi(a.q.off[i], 0, a.q.rows), e = clampi(a.q.off[i + 1], b, a.q.rows);
     const int r0 = max(b, lo), r1 = min(e, hi);
     const int id = a.q.ids[i];
     const int ad = id >= 0 && id < a.q.n_adapters ? id : -1;
-    const int ra = ad < 0 ? 0 : rank_of(a.ranks, ad, a.rank);
-    float af[RT][4];
-    if constexpr (DX) {  // A of this wave's columns: lane: column r16, ranks 4 g + e
-      const WT* A = reinterpret_cast<const WT*>(a.A) + (int64_t)max(ad, 0) * a.rank * a.D;
-      const int d = min(d0 + r16, a.D - 1);
+    if (r0 < r1 && ad >= 0) {
+      const int ra = rank_of(a.ranks, ad, a.rank);
+      if (DX && af_of != ad) {
+        af_of = ad;
+        const WT* A = reinterpret_cast<const WT*>(a.A) + (int64_t)ad * a.rank * a.D;
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int j = r * 16 + 4 * g + u;
-          af[r][u] = j < ra ? (float)A[(int64_t)j * a.D + d] : 0.0f;
-        }
-    }
-    for (int m0 = r0; m0 < r1; m0 += kOuterRows) {
-      __syncthreads();
-      for (int u = threadIdx.x; u < kOuterRows * R; u += 256) {
-        const int m = u / R, j = u % R;
-        float v = 0.0f;
-        if (m0 + m < r1 && j < ra) {
-          const float* p = a.part + (int64_t)(m0 + m) * a.rank + j;
-          for (int s = 0; s < a.q_splits; ++s) v += p[s * qstride];
-        }
-        qs[m][j] = v;
+        for (int u = 0; u < U; ++u)
+          af[u].load_column(A + min(d0 + col(u), a.D - 1), a.D, ra, g);
       }
-      __syncthreads();
-      if (ad >= 0) {
-        const int d = d0 + r16;
+      // this thread's part of a tile: Q values and, for bf16 P, 16-byte pieces of P
+      constexpr int QN = kOuterRows * R / 256, XN = PB ? kOuterRows * U * 64 / 8 / 256 : 1;
+      float qr[QN];
+      v8h xr[XN];
+      float pr[PB ? 1 : 8][PB ? 1 : U];
+      auto fetch = [&](int m0) {
 #pragma unroll
-        for (int kk = 0; kk < kOuterRows / 4; ++kk) {
-          const int m = kk * 4 + g;
-          const float p = d < a.D && m0 + m < r1 ? (float)P[(int64_t)(m0 + m) * a.ldp + d] : 0.0f;
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const float qv = qs[m][r * 16 + r16];
-            acc[r] = TR ? mfma_f32(qv, p, acc[r]) : mfma_f32(p, qv, acc[r]);
+        for (int k = 0; k < QN; ++k) {
+          const int v = k * 256 + threadIdx.x, m = v / R, j = v % R;
+          qr[k] = 0.0f;
+          if (m0 + m < r1 && j < ra) {
+            const float* p = a.part + (int64_t)(m0 + m) * a.rank + j;
+            for (int s = 0; s < a.q_splits; ++s) qr[k] += p[s * qstride];
           }
         }
-      }
-      if constexpr (DX) {
+        if constexpr (PB) {
 #pragma unroll
-        for (int mt = 0; mt < kOuterRows / 16; ++mt) {
-          v4f v{0, 0, 0, 0};
+          for (int k = 0; k < XN; ++k) {
+            const int v = k * 256 + threadIdx.x, m = v / (8 * U), d = dw + v % (8 * U) * 8;
+            const bool in = m0 + m < r1 && d < a.D;  // D % 8 == 0 for bf16 P
+            const PT* p = P + (int64_t)(m0 + m) * a.ldp + d;
+            if (a.p_vec) {
+              xr[k] = in ? *reinterpret_cast<const v8h*>(p) : v8h{0, 0, 0, 0, 0, 0, 0, 0};
+            } else {
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const v4f qv = *reinterpret_cast<const v4f*>(&qs[mt * 16 + r16][r * 16 + 4 * g]);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v = mfma_f32(af[r][u], qv[u], v);
+              for (int c = 0; c < 8; ++c) xr[k][c] = in ? p[c] : (bf16)0.0f;
+            }
           }
-          const int m = m0 + mt * 16 + r16;
-          if (m < r1) {
+        } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int d = d0 + 4 * g + u;
-              if (d < a.D) dX[(int64_t)m * a.lddx + d] = (XT)v[u];
+          for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int m = m0 + kk * 4 + g, d = d0 + 16 * u + r16;
+              pr[kk][u] = m < r1 && d < a.D ? (float)P[(int64_t)m * a.ldp + d] : 0.0f;
+            }
+        }
+      };
+      fetch(r0);
+      for (int m0 = r0; m0 < r1; m0 += kOuterRows) {
+        __syncthreads();  // the last tile has been read
+#pragma unroll
+        for (int k = 0; k < QN; ++k) {
+          const int v = k * 256 + threadIdx.x, m = v / R, j = v % R;
+          if constexpr (!PB || (DX && !XB)) lds.q[m][j] = qr[k];
+          if constexpr (PB || XB) {
+            bf16 h, mi, l;
+            split3(qr[k], h, mi, l);
+            lds.h[0][m][j] = h;
+            lds.h[1][m][j] = mi;
+            lds.h[2][m][j] = l;
+            if constexpr (RT == 1) lds.h[3][m][j] = (bf16)0.0f;
+          }
+        }
+        float pc[PB ? 1 : 8][PB ? 1 : U];
+        if constexpr (PB) {
+#pragma unroll
+          for (int k = 0; k < XN; ++k) {
+            const int v = k * 256 + threadIdx.x;
+            *reinterpret_cast<v8h*>(&lds.x[v / (8 * U)][v % (8 * U) * 8]) = xr[k];
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int u = 0; u < U; ++u) pc[kk][u] = pr[kk][u];
+        }
+        __syncthreads();
+        if (m0 + kOuterRows < r1) fetch(m0 + kOuterRows);
+        if constexpr (PB) {
+          v8h xt[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            xt[u] = read_transposed(&lds.x[0][wave * 16 * U + 16 * u], lds.XLD, r16, g);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              const v8h qt = read_transposed(&lds.h[k][0][16 * r], lds.QLD, r16, g);
+#pragma unroll
+              for (int u = 0; u < U; ++u) acc[r][u] = mfma_bf16(qt, xt[u], acc[r][u]);
+            }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              const float qv = lds.q[kk * 4 + g][16 * r + r16];
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+                acc[r][u] = TR ? mfma_f32(qv, pc[kk][u], acc[r][u]) : mfma_f32(pc[kk][u], qv, acc[r][u]);
+            }
+        }
+        if constexpr (DX) {
+#pragma unroll
+          for (int m = 0; m < kOuterRows / 16; ++m) {
+            SFrag<WT, RT, 1> sf;
+            if constexpr (XB) {
+#pragma unroll
+              for (int k = 0; k < SFrag<bf16, RT, 1>::KS; ++k) {
+                const int plane = RT == 1 ? 2 * k + g / 2 : k % 3;
+                const int j = RT == 1 ? 8 * (g & 1) : 32 * (k / 3) + 8 * g;
+                sf.s[0][k] = *reinterpret_cast<const v8h*>(&lds.h[plane][m * 16 + r16][j]);
+              }
+            } else {
+              sf.load(&lds.q[m * 16][0], R + 4, r16, g);
+            }
+            v4f y[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) y[u] = af[u].times(sf, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = m0 + m * 16 + 4 * g + k, d = d0 + col(0);
+              if (row >= r1 || d >= a.D) continue;  // D % 16 == 0 for dX
+              PT* o = dX + (int64_t)row * a.lddx + d;
+              typedef PT vu __attribute__((ext_vector_type(U)));
+              vu v;
+#pragma unroll
+              for (int u = 0; u < U; ++u) v[u] = (PT)y[u][k];
+              if (a.dx_vec) {
+                *reinterpret_cast<vu*>(o) = v;
+              } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) o[u] = v[u];
+              }
             }
           }
         }
       }
-      pending = pending || ad >= 0;
+      pending = true;
+    } else if (DX && r0 < r1) {  // no adapter: zero rows
+      for (int v = threadIdx.x; v < (r1 - r0) * 64 * U; v += 256) {
+        const int d = dw + v % (64 * U);
+        if (d < a.D) dX[(int64_t)(r0 + v / (64 * U)) * a.lddx + d] = (PT)0.0f;
+      }
     }
     // Write the sum unless the next request goes on with the same adapter.
-    bool flush = pending;
-    if (pending && i < last) {
-      const int nid = a.q.ids[i + 1];
-      flush = nid != id;
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.slot_id[sp + i] = flush ? ad : -1;
+    const bool flush = pending && (i == last || a.q.ids[i + 1] != id);
+    if (chunk == 0 && threadIdx.x == 0) a.slot_id[sp + i] = flush ? ad : -1;
     if (flush) {
       float* out = a.out + (int64_t)(sp + i) * a.D * a.rank;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int j = TR ? r * 16 + 4 * g + u : r * 16 + r16;
-          const int d = TR ? d0 + r16 : d0 + 4 * g + u;
-          if (j < a.rank && d < a.D)
-            out[TR ? (int64_t)j * a.D + d : (int64_t)d * a.rank + j] = acc[r][u];
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = TR ? r * 16 + 4 * g + k : r * 16 + r16;
+            const int d = d0 + 16 * u + (TR ? r16 : 4 * g + k);
+            if (j < a.rank && d < a.D)
+              out[TR ? (int64_t)j * a.D + d : (int64_t)d * a.rank + j] = acc[r][u][k];
+          }
+          acc[r][u] = v4f{0, 0, 0, 0};
         }
-        acc[r] = v4f{0, 0, 0, 0};
-      }
       pending = false;
     }
   }
 }
 
+// The X side and the dY side in one launch: workgroups [0, x_groups) and the rest.
+template <typename XT, typename WT, int RT, bool DX>
+__global__ __launch_bounds__(256) void k_lora_outer(OuterArgs x, OuterArgs y, int x_groups) {
+  __shared__ __align__(16) union Lds {
+    OuterLds<XT, RT> x;
+    OuterLds<float, RT> y;
+    __device__ Lds() {}
+  } lds;
+  const int id = blockIdx.x;
+  if (id < x_groups)
+    outer_body<XT, WT, RT, DX, true>(x, id % x.chunks, id / x.chunks, lds.x);
+  else
+    outer_body<float, WT, RT, false, false>(y, (id - x_groups) % y.chunks, (id - x_groups) / y.chunks,
+                                            lds.y);
+}
+
 // ---------------------------------------------------------------- slot sum ----
+// dW[a][e] = scale_a * the sum of the slots of adapter a, in the slots' order.
 template <typename WT>
-__global__ __launch_bounds__(256) void k_lora_slot_sum(SlotSumArgs a) {
+__global__ __launch_bounds__(256) void k_lora_slot_sum(SlotSumArgs p, SlotSumArgs s, int p_groups) {
+  const bool second = (int)blockIdx.x >= p_groups;
+  const SlotSumArgs& a = second ? s : p;
   const int64_t len = (int64_t)a.D * a.rank;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int ad = blockIdx.y;
+  const int64_t e = (int64_t)(second ? blockIdx.x - p_groups : blockIdx.x) * 256 + threadIdx.x;
+  const int ad = blockIdx.y, lane = threadIdx.x & 63;
   float v = 0.0f;
-  for (int s = 0; s < a.slots; ++s) {
-    if (a.slot_id[s] != ad) continue;
-    if (e < len) v += a.part[s * len + e];
+  for (int base = 0; base < a.slots; base += kWave) {
+    const int i = base + lane;
+    uint64_t hit = __ballot(i < a.slots && a.slot_id[i] == ad);
+    while (hit) {
+      const int k = __ffsll((unsigned long long)hit) - 1;
+      hit &= hit - 1;
+      if (e < len) v += a.part[(base + k) * len + e];
+    }
   }
   if (e >= len) return;
   const int j = a.transposed ? (int)(e / a.D) : (int)(e % a.rank);
@@ -841,24 +999,6 @@ __global__ __launch_bounds__(256) void k_lora_slot_sum(SlotSumArgs a) {
 int max_tiles(const Requests& q, int T) {
   const int64_t t = (int64_t)q.rows / T + q.n;
   return (int)(t < q.rows ? t : q.rows);
-}
-
-template <typename XT, typename WT, bool WCOLS>
-hipError_t shrink_rt(const ShrinkArgs& a, hipStream_t s) {
-  const bool vec = (reinterpret_cast<uintptr_t>(a.P) % 16) == 0 && (a.ldp * sizeof(XT)) % 16 == 0;
-#define QL_SHRINK(RT, MT)                                                                      \
-  hipLaunchKernelGGL((k_lora_shrink<XT, WT, RT, MT, WCOLS>),                                   \
-                     dim3(max_tiles(a.q, MT * 16), a.splits, a.halves), dim3(256), 0, s, a, vec)
-  if (a.rank <= 16)
-    QL_SHRINK(1, 1);
-  else if (a.rank <= 32)
-    QL_SHRINK(2, 1);
-  else if (a.rank <= 64)
-    QL_SHRINK(4, 1);
-  else
-    QL_SHRINK(8, 1);
-#undef QL_SHRINK
-  return hipGetLastError();
 }
 
 // Calls with fewer outputs than this take one launch. Measured (one launch / two):
@@ -938,49 +1078,76 @@ hipError_t forward_rt(const ForwardArgs& a, hipStream_t s) {
 #undef QL_RUN
 }
 
-template <typename XT, typename WT, bool DX, bool TR>
-hipError_t outer_rt(const OuterArgs& a, hipStream_t s) {
-  const dim3 grid((a.D + kOuterCols - 1) / kOuterCols, a.splits);
-#define QL_OUTER(RT) \
-  hipLaunchKernelGGL((k_lora_outer<XT, WT, RT, DX, TR>), grid, dim3(256), 0, s, a)
-  if (a.rank <= 16)
-    QL_OUTER(1);
-  else if (a.rank <= 32)
-    QL_OUTER(2);
-  else if (a.rank <= 64)
-    QL_OUTER(4);
+template <typename WT, int RT>
+hipError_t ds_run(const DsArgs& a, hipStream_t s) {
+  const bool vec = reinterpret_cast<uintptr_t>(a.dY) % 16 == 0 && a.ldy % 4 == 0;
+  constexpr int NW = RT == 8 ? 4 : 8;
+  if (a.tall)
+    hipLaunchKernelGGL((k_lora_ds<WT, RT, 2, NW>), dim3(max_tiles(a.q, 32), a.splits), dim3(64 * NW),
+                       0, s, a, vec);
   else
-    QL_OUTER(8);
-#undef QL_OUTER
+    hipLaunchKernelGGL((k_lora_ds<WT, RT, 1, 8>), dim3(max_tiles(a.q, 16), a.splits), dim3(512), 0,
+                       s, a, vec);
   return hipGetLastError();
+}
+
+template <typename XT, typename WT, int RT, bool DX>
+hipError_t outer_run(OuterArgs x, OuterArgs y, hipStream_t s) {
+  constexpr int cols = 64 * outer_u(RT);
+  x.chunks = (x.D + cols - 1) / cols;
+  y.chunks = (y.D + cols - 1) / cols;
+  const int xg = x.out ? x.chunks * x.splits : 0, yg = y.out ? y.chunks * y.splits : 0;
+  x.p_vec = reinterpret_cast<uintptr_t>(x.P) % 16 == 0 && (x.ldp * sizeof(XT)) % 16 == 0;
+  x.dx_vec = reinterpret_cast<uintptr_t>(x.dX) % (4 * sizeof(XT)) == 0 && x.lddx % 4 == 0;
+  hipLaunchKernelGGL((k_lora_outer<XT, WT, RT, DX>), dim3(xg + yg), dim3(256), 0, s, x, y, xg);
+  return hipGetLastError();
+}
+
+template <typename XT, typename WT>
+hipError_t outer_rt(const OuterArgs& x, const OuterArgs& y, hipStream_t s) {
+#define QL_OUTER(RT) \
+  (x.dX ? outer_run<XT, WT, RT, true>(x, y, s) : outer_run<XT, WT, RT, false>(x, y, s))
+  if (y.rank <= 16) return QL_OUTER(1);
+  if (y.rank <= 32) return QL_OUTER(2);
+  if (y.rank <= 64) return QL_OUTER(4);
+  return QL_OUTER(8);
+#undef QL_OUTER
+}
+
+template <typename WT>
+hipError_t ds_rt(const DsArgs& a, hipStream_t s) {
+  if (a.rank <= 16) return ds_run<WT, 1>(a, s);
+  if (a.rank <= 32) return ds_run<WT, 2>(a, s);
+  if (a.rank <= 64) return ds_run<WT, 4>(a, s);
+  return ds_run<WT, 8>(a, s);
 }
 
 }  // namespace
 
-int lora_shrink_splits(int rows, int n_req, int D, int rank) {
-  (void)rank;
+// Tall tiles (32 rows) read B half as often; used where they still fill the
+// chip. Otherwise 16 rows, and the columns of dY split over workgroups.
+bool lora_ds_tall(int rows, int n_req) { return (int64_t)rows / 32 + n_req >= 256; }
+
+int lora_ds_splits(int rows, int n_req, int N) {
+  if (lora_ds_tall(rows, n_req)) return 1;
   const int64_t tiles = (int64_t)rows / 16 + n_req;
-  int64_t s = 512 / (tiles > 0 ? tiles : 1);
-  const int64_t cap = D / 256;
+  int64_t s = 256 / tiles;
+  const int64_t cap = N / 512;
   s = s < cap ? s : cap;
-  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+  return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
 }
 
-int lora_outer_splits(int rows, int D) {
-  const int cols = (D + kOuterCols - 1) / kOuterCols;
-  int64_t s = (1024 + cols - 1) / cols;
+// Row ranges: about kOuterGroups workgroups, none with fewer than 64 rows.
+#ifndef QL_OG
+#define QL_OG 512
+#endif
+int lora_outer_splits(int rows, int rank, int K, int N) {
+  const int cols = 64 * outer_u(rank <= 64 ? 4 : 8);
+  const int chunks = (K + cols - 1) / cols + (N + cols - 1) / cols;
+  int64_t s = (QL_OG + chunks - 1) / chunks;
   const int64_t cap = (rows + 63) / 64;
   s = s < cap ? s : cap;
   return (int)(s < 1 ? 1 : s);
-}
-
-hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t s) {
-  if (a.w_cols) {  // P is dY: fp32
-    return a.w_bf16 ? shrink_rt<float, bf16, true>(a, s) : shrink_rt<float, float, true>(a, s);
-  }
-  if (a.p_bf16)
-    return a.w_bf16 ? shrink_rt<bf16, bf16, false>(a, s) : shrink_rt<bf16, float, false>(a, s);
-  return a.w_bf16 ? shrink_rt<float, bf16, false>(a, s) : shrink_rt<float, float, false>(a, s);
 }
 
 int64_t lora_forward_ws(int rows, int n_req, int N, int rank, bool w_bf16) {
@@ -993,26 +1160,24 @@ hipError_t launch_lora_forward(const ForwardArgs& a, hipStream_t s) {
   return a.w_bf16 ? forward_rt<float, bf16>(a, s) : forward_rt<float, float>(a, s);
 }
 
-hipError_t launch_lora_outer(const OuterArgs& a, hipStream_t s) {
-  if (!a.transposed)  // dB: P is dY, fp32; no dX
-    return outer_rt<float, float, false, false>(a, s);
-  if (a.dX) {
-    if (a.p_bf16)
-      return a.w_bf16 ? outer_rt<bf16, bf16, true, true>(a, s)
-                      : outer_rt<bf16, float, true, true>(a, s);
-    return a.w_bf16 ? outer_rt<float, bf16, true, true>(a, s)
-                    : outer_rt<float, float, true, true>(a, s);
-  }
-  return a.p_bf16 ? outer_rt<bf16, float, false, true>(a, s)
-                  : outer_rt<float, float, false, true>(a, s);
+hipError_t launch_lora_ds(const DsArgs& a, hipStream_t s) {
+  return a.w_bf16 ? ds_rt<bf16>(a, s) : ds_rt<float>(a, s);
 }
 
-hipError_t launch_lora_slot_sum(const SlotSumArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)a.D * a.rank + 255) / 256), a.n_adapters);
-  if (a.w_bf16)
-    hipLaunchKernelGGL(k_lora_slot_sum<bf16>, grid, dim3(256), 0, s, a);
+hipError_t launch_lora_outer(const OuterArgs& x, const OuterArgs& y, hipStream_t s) {
+  if (x.p_bf16) return y.w_bf16 ? outer_rt<bf16, bf16>(x, y, s) : outer_rt<bf16, float>(x, y, s);
+  return y.w_bf16 ? outer_rt<float, bf16>(x, y, s) : outer_rt<float, float>(x, y, s);
+}
+
+hipError_t launch_lora_slot_sum(const SlotSumArgs& p, const SlotSumArgs& q, hipStream_t s) {
+  auto groups = [](const SlotSumArgs& a) {
+    return a.out ? (unsigned)(((int64_t)a.D * a.rank + 255) / 256) : 0u;
+  };
+  const dim3 grid(groups(p) + groups(q), q.n_adapters);
+  if (q.w_bf16)
+    hipLaunchKernelGGL(k_lora_slot_sum<bf16>, grid, dim3(256), 0, s, p, q, (int)groups(p));
   else
-    hipLaunchKernelGGL(k_lora_slot_sum<float>, grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_lora_slot_sum<float>, grid, dim3(256), 0, s, p, q, (int)groups(p));
   return hipGetLastError();
 }
 

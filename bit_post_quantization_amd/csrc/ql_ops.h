@@ -22,22 +22,21 @@ struct Requests {
   int n_adapters;
 };
 
-// part[split][row][j] = scale * sum over the split's columns d of
-// P[row][d] * W_a[j][d], for the rows of every request with an adapter.
-struct ShrinkArgs {
-  const void* P;      // [rows * halves, D], row stride ldp elements
-  int64_t ldp;
-  const void* W;      // [n_adapters, rank, D], or [n_adapters, D, rank] (w_cols)
+// part[split][row][j] = scale_a * sum over the split's columns n of
+// dY[row][n] * B_a[n][j], for the rows of every request with an adapter.
+struct DsArgs {
+  const float* dY;    // [rows, N], row stride ldy elements
+  int64_t ldy;
+  const void* B;      // [n_adapters, N, rank]
   const float* scales;// per adapter, or nullptr (1)
   const int32_t* ranks;
   Requests q;
-  int D, rank;
-  int halves;         // 2: the requests also cover rows [rows, 2 * rows)
-  int splits, split_len;  // columns per split, a multiple of kShrinkStep
-  float* part;        // [splits][rows * halves][rank]
-  bool p_bf16, w_bf16, w_cols;
+  int N, rank;
+  int splits, split_len;  // columns of a split, a multiple of kDsStep
+  float* part;        // [splits][rows][rank]
+  bool w_bf16, tall;
 };
-constexpr int kShrinkStep = 32;
+constexpr int kDsStep = 32;
 
 // Y[row][n] = base[row][n] + scale_a * sum_j S[row][j] * B_a[n][j] with
 // S = X A_a^T, combined over the row's two halves when guided.
@@ -62,7 +61,7 @@ struct ForwardArgs {
 
 // Row ranges s = 0 .. splits-1 of row_len rows each. For every range and the
 // requests i in it, slot s + i of `out` receives the sum over the common rows
-// of Q[row][j] * P[row][d] (transposed: [j][d] for dA, else [d][j] for dB);
+// of Q[row][j] * P[row][d] ([j][d] for dA, [d][j] for dB);
 // slot_id[s + i] says which adapter it belongs to (-1: nothing was written).
 // With dX, dX[row][d] = sum_j Q[row][j] * A_a[j][d] too (zero for rows without
 // an adapter).
@@ -77,10 +76,12 @@ struct OuterArgs {
   int D, rank;
   void* dX;           // nullptr: none; else of P's type
   int64_t lddx;
-  float* out;         // [slots][D * rank]
+  float* out;         // [slots][D * rank]; nullptr: this side is not wanted
   int32_t* slot_id;   // [slots]
   int splits, row_len;
-  bool p_bf16, w_bf16, transposed;
+  bool p_bf16, w_bf16;
+  int chunks;         // set by the launch, as are the next two
+  bool p_vec, dx_vec; // 16-byte pieces of P, vectors of dX
 };
 
 // dW[a][e] = scale_a * sum over the slots of adapter a of part[slot][e].
@@ -94,16 +95,18 @@ struct SlotSumArgs {
   bool w_bf16, transposed;
 };
 
-hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t s);
 // Workspace of a forward call with `rows` output rows.
 int64_t lora_forward_ws(int rows, int n_req, int N, int rank, bool w_bf16);
 hipError_t launch_lora_forward(const ForwardArgs& a, hipStream_t s);
-hipError_t launch_lora_outer(const OuterArgs& a, hipStream_t s);
-hipError_t launch_lora_slot_sum(const SlotSumArgs& a, hipStream_t s);
-// Splits of a shrink over D columns for `rows` rows (halves included).
-int lora_shrink_splits(int rows, int n_req, int D, int rank);
-// Row ranges of an outer product over D columns.
-int lora_outer_splits(int rows, int D);
+bool lora_ds_tall(int rows, int n_req);
+int lora_ds_splits(int rows, int n_req, int N);
+hipError_t launch_lora_ds(const DsArgs& a, hipStream_t s);
+// Row ranges of the outer products over K and N columns.
+int lora_outer_splits(int rows, int rank, int K, int N);
+// x: the X side (dA, dX); y: the dY side (dB).
+hipError_t launch_lora_outer(const OuterArgs& x, const OuterArgs& y, hipStream_t s);
+// The sums of both sides; one without `out` is left out.
+hipError_t launch_lora_slot_sum(const SlotSumArgs& p, const SlotSumArgs& q, hipStream_t s);
 
 // -------------------------------------------------------------- group norm ----
 

@@ -35,7 +35,6 @@ ql_status hip_fail(hipError_t e, const char* what) {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool dtype_ok(ql_dtype t) { return t == QL_F32 || t == QL_BF16; }
 size_t size_of(ql_dtype t) { return t == QL_BF16 ? 2 : 4; }
-int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 
 ql_status check_workspace(const void* ws, int64_t have, int64_t need) {
   if (need > 0 && !ws) return fail(QL_ERR_ARG, "workspace is NULL");
@@ -85,38 +84,33 @@ ql_status check_lora_pointers(const ql_lora* d, const ql_requests* q) {
   return QL_OK;
 }
 
-int64_t part_bytes(int splits, int64_t rows, int rank) {
-  return up16((int64_t)splits * rows * rank * 4);
-}
-
 int split_len(int D, int splits) {
   const int len = (D + splits - 1) / splits;
-  return (len + ql::kShrinkStep - 1) / ql::kShrinkStep * ql::kShrinkStep;
+  return (len + ql::kDsStep - 1) / ql::kDsStep * ql::kDsStep;
 }
 
 // Workspace of the backward call: the partial sums of dS, then the slots of
 // dA and dB and their adapters.
 struct GradWs {
-  int s_splits, a_splits, b_splits;
+  int s_splits, splits, slots;
   int64_t ds, da, db, aid, bid, total;
 };
 GradWs grad_ws(const ql_lora* d, int32_t M, int32_t n) {
   GradWs w;
-  w.s_splits = ql::lora_shrink_splits(M, n, d->N, d->rank);
-  w.a_splits = ql::lora_outer_splits(M, d->K);
-  w.b_splits = ql::lora_outer_splits(M, d->N);
+  w.s_splits = ql::lora_ds_splits(M, n, d->N);
+  w.splits = ql::lora_outer_splits(M, d->rank, d->K, d->N);
+  w.slots = w.splits + n - 1;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
-    at += up16(bytes);
+    at += (bytes + 15) / 16 * 16;
     return here;
   };
-  const int64_t as = (int64_t)w.a_splits + n - 1, bs = (int64_t)w.b_splits + n - 1;
-  w.ds = take(part_bytes(w.s_splits, M, d->rank));
-  w.da = take(as * d->K * d->rank * 4);
-  w.db = take(bs * d->N * d->rank * 4);
-  w.aid = take(as * 4);
-  w.bid = take(bs * 4);
+  w.ds = take((int64_t)w.s_splits * M * d->rank * 4);
+  w.da = take((int64_t)w.slots * d->K * d->rank * 4);
+  w.db = take((int64_t)w.slots * d->N * d->rank * 4);
+  w.aid = take((int64_t)w.slots * 4);
+  w.bid = take((int64_t)w.slots * 4);
   w.total = at;
   return w;
 }
@@ -285,83 +279,74 @@ ql_status qlinear_lora_grad(const ql_lora* d, const void* X, int64_t ldx, int32_
   char* ws = reinterpret_cast<char*>(workspace);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const bool w_bf16 = d->w_dtype == QL_BF16;
-  ql::SlotSumArgs sum{};
-  sum.n_adapters = d->n_adapters;
-  sum.rank = d->rank;
-  sum.ranks = M > 0 ? d->ranks : nullptr;
-  sum.w_bf16 = w_bf16;
-  ql::OuterArgs o{};
-  o.ranks = d->ranks;
-  o.q = requests(d, q, M);
-  o.rank = d->rank;
-  o.w_bf16 = w_bf16;
-  if (M > 0 && (dX || dA)) {
-    ql::ShrinkArgs a{};
-    a.P = dY;
-    a.ldp = lddy;
-    a.W = d->B;
+  const bool x_side = dX || dA;
+  ql::OuterArgs x{}, y{};
+  x.rank = y.rank = d->rank;
+  x.w_bf16 = y.w_bf16 = w_bf16;
+  x.p_bf16 = d->x_dtype == QL_BF16;
+  if (M > 0 && x_side) {
+    ql::DsArgs a{};
+    a.dY = dY;
+    a.ldy = lddy;
+    a.B = d->B;
     a.scales = d->scales;
     a.ranks = d->ranks;
-    a.q = o.q;
-    a.D = d->N;
+    a.q = requests(d, q, M);
+    a.N = d->N;
     a.rank = d->rank;
-    a.halves = 1;
     a.splits = w.s_splits;
     a.split_len = split_len(d->N, w.s_splits);
     a.part = reinterpret_cast<float*>(ws + w.ds);
     a.w_bf16 = w_bf16;
-    a.w_cols = true;
-    QL_LAUNCH(ql::launch_lora_shrink(a, s), "launching dS");
-    o.P = X;
-    o.ldp = ldx;
-    o.part = a.part;
-    o.q_splits = w.s_splits;
-    o.A = d->A;
-    o.D = d->K;
-    o.dX = dX;
-    o.lddx = lddx;
-    o.out = reinterpret_cast<float*>(ws + w.da);
-    o.slot_id = reinterpret_cast<int32_t*>(ws + w.aid);
-    o.splits = w.a_splits;
-    o.row_len = (M + w.a_splits - 1) / w.a_splits;
-    o.p_bf16 = d->x_dtype == QL_BF16;
-    o.transposed = true;
-    QL_LAUNCH(ql::launch_lora_outer(o, s), "launching dX and dA");
+    a.tall = ql::lora_ds_tall(M, q->n_requests);
+    QL_LAUNCH(ql::launch_lora_ds(a, s), "launching dS");
+    x.P = X;
+    x.ldp = ldx;
+    x.part = a.part;
+    x.q_splits = w.s_splits;
+    x.A = d->A;
+    x.ranks = d->ranks;
+    x.q = a.q;
+    x.D = d->K;
+    x.dX = dX;
+    x.lddx = lddx;
+    x.out = reinterpret_cast<float*>(ws + w.da);
+    x.slot_id = reinterpret_cast<int32_t*>(ws + w.aid);
+    x.splits = w.splits;
+    x.row_len = (M + w.splits - 1) / w.splits;
   }
-  if (dA) {
-    sum.part = reinterpret_cast<float*>(ws + w.da);
-    sum.slot_id = reinterpret_cast<int32_t*>(ws + w.aid);
-    sum.slots = M > 0 ? w.a_splits + q->n_requests - 1 : 0;
-    sum.D = d->K;
-    sum.scales = nullptr;  // dS has the scale
-    sum.out = dA;
-    sum.transposed = true;
-    QL_LAUNCH(ql::launch_lora_slot_sum(sum, s), "launching the sum of dA");
+  if (M > 0 && dB) {
+    y.P = dY;
+    y.ldp = lddy;
+    y.part = S;
+    y.q_splits = 1;
+    y.ranks = d->ranks;
+    y.q = requests(d, q, M);
+    y.D = d->N;
+    y.out = reinterpret_cast<float*>(ws + w.db);
+    y.slot_id = reinterpret_cast<int32_t*>(ws + w.bid);
+    y.splits = w.splits;
+    y.row_len = (M + w.splits - 1) / w.splits;
   }
-  if (dB) {
-    if (M > 0) {
-      o.P = dY;
-      o.ldp = lddy;
-      o.part = S;
-      o.q_splits = 1;
-      o.D = d->N;
-      o.dX = nullptr;
-      o.out = reinterpret_cast<float*>(ws + w.db);
-      o.slot_id = reinterpret_cast<int32_t*>(ws + w.bid);
-      o.splits = w.b_splits;
-      o.row_len = (M + w.b_splits - 1) / w.b_splits;
-      o.p_bf16 = false;
-      o.transposed = false;
-      QL_LAUNCH(ql::launch_lora_outer(o, s), "launching dB");
-    }
-    sum.part = reinterpret_cast<float*>(ws + w.db);
-    sum.slot_id = reinterpret_cast<int32_t*>(ws + w.bid);
-    sum.slots = M > 0 ? w.b_splits + q->n_requests - 1 : 0;
-    sum.D = d->N;
-    sum.scales = M > 0 ? d->scales : nullptr;
-    sum.out = dB;
-    sum.transposed = false;
-    QL_LAUNCH(ql::launch_lora_slot_sum(sum, s), "launching the sum of dB");
+  if (x.out || y.out) QL_LAUNCH(ql::launch_lora_outer(x, y, s), "launching the outer products");
+  if (dA || dB) {
+    ql::SlotSumArgs sa{}, sb{};
+    sa.n_adapters = sb.n_adapters = d->n_adapters;
+    sa.rank = sb.rank = d->rank;
+    sa.ranks = sb.ranks = M > 0 ? d->ranks : nullptr;
+    sa.w_bf16 = sb.w_bf16 = w_bf16;
+    sa.slots = sb.slots = M > 0 ? w.slots : 0;
+    sa.part = x.out;
+    sa.slot_id = x.slot_id;
+    sa.D = d->K;
+    sa.out = dA;  // dS has the scale already
+    sa.transposed = true;
+    sb.part = y.out;
+    sb.slot_id = y.slot_id;
+    sb.D = d->N;
+    sb.scales = M > 0 ? d->scales : nullptr;
+    sb.out = dB;
+    QL_LAUNCH(ql::launch_lora_slot_sum(sa, sb, s), "launching the sums of dA and dB");
   }
   return ok();
 }
