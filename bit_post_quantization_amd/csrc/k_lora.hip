@@ -659,20 +659,27 @@ __global__ __launch_bounds__(64 * NW) void k_lora_ds(DsArgs a, bool vec) {
   WT w[RT][8], nw[RT][8];
   auto load = [&](int c, Frag8<float>(&fx)[MT], WT(&fw)[RT][8]) {
     const int k = c + 8 * g, valid = c1 - k;
+    if (vec && c + kDsStep <= c1) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (vec && valid >= 8)
-        fx[m].load(prow[m] + k);
-      else
-        fx[m].load(prow[m] + k, valid);
+      for (int m = 0; m < MT; ++m) fx[m].load(prow[m] + k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) fw[r][e] = B[(int64_t)(k + e) * a.rank + wj[r]];
+      return;
     }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) fx[m].load(prow[m] + k, valid);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       // past the end dY is zero; the row of B read there is the last one, whose
       // elements may not be finite, so it is zero too
       const WT* row = B + (int64_t)min(k + e, a.N - 1) * a.rank;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) fw[r][e] = e < valid ? row[wj[r]] : (WT)0.0f;
+      for (int r = 0; r < RT; ++r) {
+        const WT v = row[wj[r]];
+        fw[r][e] = e < valid ? v : (WT)0.0f;
+      }
     }
   };
   int c = c0 + wave * kDsStep;
@@ -796,71 +803,104 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
           af[u].load_column(A + min(d0 + col(u), a.D - 1), a.D, ra, g);
       }
       // this thread's part of a tile: Q values and, for bf16 P, 16-byte pieces of P
-      constexpr int QN = kOuterRows * R / 256, XN = PB ? kOuterRows * U * 64 / 8 / 256 : 1;
-      float qr[QN];
+      // Addresses are clamped into the piece and what lies past it is zeroed when
+      // the tile is used: the loads wait for nothing and nothing waits for them.
+      constexpr int QN = kOuterRows * R / 256, XN = PB ? U : 1, QW = QN < 4 ? QN : 4;
+      typedef float vq __attribute__((ext_vector_type(QW)));
+      const int qm = threadIdx.x * QN / R, qj = threadIdx.x * QN % R;
+      vq qr[QN / QW];
       v8h xr[XN];
-      float pr[PB ? 1 : 8][PB ? 1 : U];
-      auto fetch = [&](int m0) {
+      PT pr[PB ? 1 : 8][PB ? 1 : U];
+      auto fetch_q = [&](int m0, int split, vq(&v)[QN / QW]) {
+        const float* qp = a.part + split * qstride + (int64_t)min(m0 + qm, r1 - 1) * a.rank;
 #pragma unroll
-        for (int k = 0; k < QN; ++k) {
-          const int v = k * 256 + threadIdx.x, m = v / R, j = v % R;
-          qr[k] = 0.0f;
-          if (m0 + m < r1 && j < ra) {
-            const float* p = a.part + (int64_t)(m0 + m) * a.rank + j;
-            for (int s = 0; s < a.q_splits; ++s) qr[k] += p[s * qstride];
+        for (int k = 0; k < QN / QW; ++k) {
+          if (a.q_vec) {
+            const int j = qj + k * QW;
+            v[k] = *reinterpret_cast<const vq*>(qp + (j < a.rank ? j : 0));
+          } else {
+#pragma unroll
+            for (int c = 0; c < QW; ++c) v[k][c] = qp[min(qj + k * QW + c, a.rank - 1)];
           }
         }
+      };
+      auto fetch = [&](int m0) {
+        fetch_q(m0, 0, qr);
         if constexpr (PB) {
 #pragma unroll
           for (int k = 0; k < XN; ++k) {
-            const int v = k * 256 + threadIdx.x, m = v / (8 * U), d = dw + v % (8 * U) * 8;
-            const bool in = m0 + m < r1 && d < a.D;  // D % 8 == 0 for bf16 P
-            const PT* p = P + (int64_t)(m0 + m) * a.ldp + d;
+            const int v = k * 256 + threadIdx.x, d = dw + v % (8 * U) * 8;
+            // D % 8 == 0 for bf16 P
+            const PT* p = P + (int64_t)min(m0 + v / (8 * U), r1 - 1) * a.ldp + min(d, a.D - 8);
             if (a.p_vec) {
-              xr[k] = in ? *reinterpret_cast<const v8h*>(p) : v8h{0, 0, 0, 0, 0, 0, 0, 0};
+              xr[k] = *reinterpret_cast<const v8h*>(p);
             } else {
 #pragma unroll
-              for (int c = 0; c < 8; ++c) xr[k][c] = in ? p[c] : (bf16)0.0f;
+              for (int c = 0; c < 8; ++c) xr[k][c] = p[c];
             }
           }
         } else {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 0; kk < 8; ++kk) {
+            const PT* p = P + (int64_t)min(m0 + kk * 4 + g, r1 - 1) * a.ldp;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const int m = m0 + kk * 4 + g, d = d0 + 16 * u + r16;
-              pr[kk][u] = m < r1 && d < a.D ? (float)P[(int64_t)m * a.ldp + d] : 0.0f;
-            }
+            for (int u = 0; u < U; ++u) pr[kk][u] = p[min(d0 + 16 * u + r16, a.D - 1)];
+          }
         }
       };
       fetch(r0);
       for (int m0 = r0; m0 < r1; m0 += kOuterRows) {
         __syncthreads();  // the last tile has been read
+        float qz[QN];
 #pragma unroll
-        for (int k = 0; k < QN; ++k) {
-          const int v = k * 256 + threadIdx.x, m = v / R, j = v % R;
-          if constexpr (!PB || (DX && !XB)) lds.q[m][j] = qr[k];
-          if constexpr (PB || XB) {
-            bf16 h, mi, l;
-            split3(qr[k], h, mi, l);
-            lds.h[0][m][j] = h;
-            lds.h[1][m][j] = mi;
-            lds.h[2][m][j] = l;
-            if constexpr (RT == 1) lds.h[3][m][j] = (bf16)0.0f;
+        for (int k = 0; k < QN; ++k) qz[k] = qr[k / QW][k % QW];
+        for (int sq = 1; sq < a.q_splits; ++sq) {
+          vq more[QN / QW];
+          fetch_q(m0, sq, more);
+#pragma unroll
+          for (int k = 0; k < QN; ++k) qz[k] += more[k / QW][k % QW];
+        }
+#pragma unroll
+        for (int k = 0; k < QN; ++k)
+          if (m0 + qm >= r1 || qj + k >= ra) qz[k] = 0.0f;
+        if constexpr (!PB || (DX && !XB)) {
+#pragma unroll
+          for (int k = 0; k < QN; ++k) lds.q[qm][qj + k] = qz[k];
+        }
+        if constexpr (PB || XB) {
+          typedef bf16 vt __attribute__((ext_vector_type(QN < 8 ? QN : 8)));
+          constexpr int W = QN < 8 ? QN : 8;
+#pragma unroll
+          for (int c = 0; c < QN / W; ++c) {
+            vt h, mi, l;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+              bf16 x, y, z;
+              split3(qz[c * W + k], x, y, z);
+              h[k] = x;
+              mi[k] = y;
+              l[k] = z;
+            }
+            *reinterpret_cast<vt*>(&lds.h[0][qm][qj + c * W]) = h;
+            *reinterpret_cast<vt*>(&lds.h[1][qm][qj + c * W]) = mi;
+            *reinterpret_cast<vt*>(&lds.h[2][qm][qj + c * W]) = l;
+            if constexpr (RT == 1) *reinterpret_cast<vt*>(&lds.h[3][qm][qj]) = vt(0.0f);
           }
         }
         float pc[PB ? 1 : 8][PB ? 1 : U];
         if constexpr (PB) {
 #pragma unroll
           for (int k = 0; k < XN; ++k) {
-            const int v = k * 256 + threadIdx.x;
-            *reinterpret_cast<v8h*>(&lds.x[v / (8 * U)][v % (8 * U) * 8]) = xr[k];
+            const int v = k * 256 + threadIdx.x, m = v / (8 * U), c = v % (8 * U) * 8;
+            const bool in = m0 + m < r1 && dw + c < a.D;
+            *reinterpret_cast<v8h*>(&lds.x[m][c]) = in ? xr[k] : v8h(0.0f);
           }
         } else {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
-            for (int u = 0; u < U; ++u) pc[kk][u] = pr[kk][u];
+            for (int u = 0; u < U; ++u)
+              pc[kk][u] = m0 + kk * 4 + g < r1 && d0 + 16 * u + r16 < a.D ? (float)pr[kk][u] : 0.0f;
         }
         __syncthreads();
         if (m0 + kOuterRows < r1) fetch(m0 + kOuterRows);
@@ -1098,6 +1138,11 @@ hipError_t outer_run(OuterArgs x, OuterArgs y, hipStream_t s) {
   y.chunks = (y.D + cols - 1) / cols;
   const int xg = x.out ? x.chunks * x.splits : 0, yg = y.out ? y.chunks * y.splits : 0;
   x.p_vec = reinterpret_cast<uintptr_t>(x.P) % 16 == 0 && (x.ldp * sizeof(XT)) % 16 == 0;
+  auto q_vec = [](const OuterArgs& o) {
+    return reinterpret_cast<uintptr_t>(o.part) % 16 == 0 && o.rank % 4 == 0;
+  };
+  x.q_vec = q_vec(x);
+  y.q_vec = q_vec(y);
   x.dx_vec = reinterpret_cast<uintptr_t>(x.dX) % (4 * sizeof(XT)) == 0 && x.lddx % 4 == 0;
   hipLaunchKernelGGL((k_lora_outer<XT, WT, RT, DX>), dim3(xg + yg), dim3(256), 0, s, x, y, xg);
   return hipGetLastError();

@@ -80,8 +80,8 @@ struct OuterArgs {
   int32_t* slot_id;   // [slots]
   int splits, row_len;
   bool p_bf16, w_bf16;
-  int chunks;         // set by the launch, as are the next two
-  bool p_vec, dx_vec; // 16-byte pieces of P, vectors of dX
+  int chunks;         // set by the launch, as are the next three
+  bool p_vec, q_vec, dx_vec;  // vectors of P, Q and dX are aligned
 };
 
 // dW[a][e] = scale_a * sum over the slots of adapter a of part[slot][e].
