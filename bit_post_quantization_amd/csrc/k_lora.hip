@@ -730,8 +730,9 @@ __global__ __launch_bounds__(64 * NW) void k_lora_ds(DsArgs a, bool vec) {
 // (ds_read_b64_tr_b16: lane c of 16 gets four rows of column c). fp32 P takes
 // the fp32 instructions, element by element from memory: lanes side by side
 // have addresses side by side.
-constexpr int kOuterRows = 32;
-constexpr int outer_u(int rt) { return rt == 8 ? 2 : 4; }  // 16-column tiles of a wave
+constexpr int kOuterRows = 32, kOuterThreads = 512;
+constexpr int kOuterU = 2;  // 16-column tiles of a wave
+constexpr int kOuterCols = kOuterThreads / 64 * 16 * kOuterU;
 
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s* lds_v4s;
@@ -746,8 +747,8 @@ __device__ __forceinline__ v8h read_transposed(const bf16* tile, int ld, int r16
 
 template <typename XT, int RT>
 struct OuterLds {
-  static constexpr int R = RT * 16, U = outer_u(RT);
-  static constexpr int XLD = 64 * U + 8, QLD = R + 8;
+  static constexpr int R = RT * 16;
+  static constexpr int XLD = kOuterCols + 8, QLD = R + 8;
   static constexpr int kPlanes = RT == 1 ? 4 : 3;
   float q[kOuterRows][R + 4];
   bf16 x[sizeof(XT) == 2 ? kOuterRows : 1][XLD];
@@ -756,11 +757,11 @@ struct OuterLds {
 
 template <typename PT, typename WT, int RT, bool DX, bool TR>
 __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, RT>& lds) {
-  constexpr int R = RT * 16, U = outer_u(RT);
+  constexpr int R = RT * 16, U = kOuterU;
   constexpr bool PB = sizeof(PT) == 2;        // bf16 products for Q^T P
   constexpr bool XB = DX && sizeof(WT) == 2;  // bf16 products for dX
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  const int dw = chunk * 64 * U, d0 = dw + wave * 16 * U;  // the workgroup's, the wave's columns
+  const int dw = chunk * kOuterCols, d0 = dw + wave * 16 * U;  // the workgroup's, the wave's columns
   const int lo = min(sp * a.row_len, a.q.rows), hi = min(lo + a.row_len, a.q.rows);
   const PT* P = reinterpret_cast<const PT*>(a.P);
   PT* dX = reinterpret_cast<PT*>(a.dX);
@@ -787,7 +788,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
   BFrag<WT, RT> af[U];  // A's columns d0 + col(u), like rows of B
   int af_of = -1;
   bool pending = false;
-  const auto col = [&](int u) { return U == 4 ? 4 * r16 + u : 2 * r16 + u; };
+  const auto col = [&](int u) { return U * r16 + u; };
   for (int i = first; i <= last; ++i) {
     const int b = clampi(a.q.off[i], 0, a.q.rows), e = clampi(a.q.off[i + 1], b, a.q.rows);
     const int r0 = max(b, lo), r1 = min(e, hi);
@@ -805,7 +806,8 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
       // this thread's part of a tile: Q values and, for bf16 P, 16-byte pieces of P
       // Addresses are clamped into the piece and what lies past it is zeroed when
       // the tile is used: the loads wait for nothing and nothing waits for them.
-      constexpr int QN = kOuterRows * R / 256, XN = PB ? U : 1, QW = QN < 4 ? QN : 4;
+      constexpr int QN = kOuterRows * R / kOuterThreads, QW = QN < 4 ? QN : 4;
+      constexpr int XP = kOuterCols / 8, XN = PB ? kOuterRows * XP / kOuterThreads : 1;
       typedef float vq __attribute__((ext_vector_type(QW)));
       const int qm = threadIdx.x * QN / R, qj = threadIdx.x * QN % R;
       vq qr[QN / QW];
@@ -829,9 +831,9 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
         if constexpr (PB) {
 #pragma unroll
           for (int k = 0; k < XN; ++k) {
-            const int v = k * 256 + threadIdx.x, d = dw + v % (8 * U) * 8;
+            const int v = k * kOuterThreads + threadIdx.x, d = dw + v % XP * 8;
             // D % 8 == 0 for bf16 P
-            const PT* p = P + (int64_t)min(m0 + v / (8 * U), r1 - 1) * a.ldp + min(d, a.D - 8);
+            const PT* p = P + (int64_t)min(m0 + v / XP, r1 - 1) * a.ldp + min(d, a.D - 8);
             if (a.p_vec) {
               xr[k] = *reinterpret_cast<const v8h*>(p);
             } else {
@@ -891,7 +893,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
         if constexpr (PB) {
 #pragma unroll
           for (int k = 0; k < XN; ++k) {
-            const int v = k * 256 + threadIdx.x, m = v / (8 * U), c = v % (8 * U) * 8;
+            const int v = k * kOuterThreads + threadIdx.x, m = v / XP, c = v % XP * 8;
             const bool in = m0 + m < r1 && dw + c < a.D;
             *reinterpret_cast<v8h*>(&lds.x[m][c]) = in ? xr[k] : v8h(0.0f);
           }
@@ -966,9 +968,9 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
       }
       pending = true;
     } else if (DX && r0 < r1) {  // no adapter: zero rows
-      for (int v = threadIdx.x; v < (r1 - r0) * 64 * U; v += 256) {
-        const int d = dw + v % (64 * U);
-        if (d < a.D) dX[(int64_t)(r0 + v / (64 * U)) * a.lddx + d] = (PT)0.0f;
+      for (int v = threadIdx.x; v < (r1 - r0) * kOuterCols; v += kOuterThreads) {
+        const int d = dw + v % kOuterCols;
+        if (d < a.D) dX[(int64_t)(r0 + v / kOuterCols) * a.lddx + d] = (PT)0.0f;
       }
     }
     // Write the sum unless the next request goes on with the same adapter.
@@ -996,7 +998,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
 
 // The X side and the dY side in one launch: workgroups [0, x_groups) and the rest.
 template <typename XT, typename WT, int RT, bool DX>
-__global__ __launch_bounds__(256) void k_lora_outer(OuterArgs x, OuterArgs y, int x_groups) {
+__global__ __launch_bounds__(kOuterThreads) void k_lora_outer(OuterArgs x, OuterArgs y, int x_groups) {
   __shared__ __align__(16) union Lds {
     OuterLds<XT, RT> x;
     OuterLds<float, RT> y;
@@ -1133,9 +1135,8 @@ hipError_t ds_run(const DsArgs& a, hipStream_t s) {
 
 template <typename XT, typename WT, int RT, bool DX>
 hipError_t outer_run(OuterArgs x, OuterArgs y, hipStream_t s) {
-  constexpr int cols = 64 * outer_u(RT);
-  x.chunks = (x.D + cols - 1) / cols;
-  y.chunks = (y.D + cols - 1) / cols;
+  x.chunks = (x.D + kOuterCols - 1) / kOuterCols;
+  y.chunks = (y.D + kOuterCols - 1) / kOuterCols;
   const int xg = x.out ? x.chunks * x.splits : 0, yg = y.out ? y.chunks * y.splits : 0;
   x.p_vec = reinterpret_cast<uintptr_t>(x.P) % 16 == 0 && (x.ldp * sizeof(XT)) % 16 == 0;
   auto q_vec = [](const OuterArgs& o) {
@@ -1143,8 +1144,8 @@ hipError_t outer_run(OuterArgs x, OuterArgs y, hipStream_t s) {
   };
   x.q_vec = q_vec(x);
   y.q_vec = q_vec(y);
-  x.dx_vec = reinterpret_cast<uintptr_t>(x.dX) % (4 * sizeof(XT)) == 0 && x.lddx % 4 == 0;
-  hipLaunchKernelGGL((k_lora_outer<XT, WT, RT, DX>), dim3(xg + yg), dim3(256), 0, s, x, y, xg);
+  x.dx_vec = reinterpret_cast<uintptr_t>(x.dX) % (kOuterU * sizeof(XT)) == 0 && x.lddx % kOuterU == 0;
+  hipLaunchKernelGGL((k_lora_outer<XT, WT, RT, DX>), dim3(xg + yg), dim3(kOuterThreads), 0, s, x, y, xg);
   return hipGetLastError();
 }
 
@@ -1182,14 +1183,14 @@ int lora_ds_splits(int rows, int n_req, int N) {
   return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
 }
 
-// Row ranges: about kOuterGroups workgroups, none with fewer than 64 rows.
-#ifndef QL_OG
-#define QL_OG 512
-#endif
-int lora_outer_splits(int rows, int rank, int K, int N) {
-  const int cols = 64 * outer_u(rank <= 64 ? 4 : 8);
-  const int chunks = (K + cols - 1) / cols + (N + cols - 1) / cols;
-  int64_t s = (QL_OG + chunks - 1) / chunks;
+// Row ranges: about kOuterGroups workgroups (three a compute unit), none with
+// fewer than 64 rows. Measured for 256 / 512 / 768 / 1024 of them: fc2 (16384 rows,
+// rank 64, bf16) 281 / 237 / 231 / 230 us, fc1 (2048 rows, rank 16, fp32) 52.6 /
+// 49.1 / 50.1 / 50.1 us.
+constexpr int kOuterGroups = 768;
+int lora_outer_splits(int rows, int K, int N) {
+  const int chunks = (K + kOuterCols - 1) / kOuterCols + (N + kOuterCols - 1) / kOuterCols;
+  int64_t s = (kOuterGroups + chunks - 1) / chunks;
   const int64_t cap = (rows + 63) / 64;
   s = s < cap ? s : cap;
   return (int)(s < 1 ? 1 : s);

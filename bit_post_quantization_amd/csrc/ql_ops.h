@@ -102,7 +102,7 @@ bool lora_ds_tall(int rows, int n_req);
 int lora_ds_splits(int rows, int n_req, int N);
 hipError_t launch_lora_ds(const DsArgs& a, hipStream_t s);
 // Row ranges of the outer products over K and N columns.
-int lora_outer_splits(int rows, int rank, int K, int N);
+int lora_outer_splits(int rows, int K, int N);
 // x: the X side (dA, dX); y: the dY side (dB).
 hipError_t launch_lora_outer(const OuterArgs& x, const OuterArgs& y, hipStream_t s);
 // The sums of both sides; one without `out` is left out.

@@ -98,7 +98,7 @@ struct GradWs {
 GradWs grad_ws(const ql_lora* d, int32_t M, int32_t n) {
   GradWs w;
   w.s_splits = ql::lora_ds_splits(M, n, d->N);
-  w.splits = ql::lora_outer_splits(M, d->rank, d->K, d->N);
+  w.splits = ql::lora_outer_splits(M, d->K, d->N);
   w.slots = w.splits + n - 1;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
