@@ -5,12 +5,17 @@
 //             dx = rstd (dz gamma - s1 - xhat s2), s1 / s2 the group's means
 //             of dz gamma and dz gamma xhat
 //
-// Both directions read their inputs in chunks of positions. A thread keeps the
-// same channels for all its positions, so a channel's sums stay in registers;
-// they are joined in a fixed order (LDS, then the chunks), with no atomics.
-// Sums of x and x^2 are kept as shifted fp32 sums inside a thread (the shift is
-// the thread's first value of the channel) and in fp64 beyond it, so a mean
-// far from zero costs no digits of the variance.
+// Where one image's group (its slab) fits a workgroup's registers, one workgroup
+// takes it whole: everything is read once and written once, in one launch
+// (k_norm_slab, k_norm_slab_grad). Otherwise the inputs are read twice, in chunks
+// of positions: sums, their joining, then the result (the second reading mostly
+// comes from the chip's last-level cache). A thread keeps the same channels for
+// all its positions, four positions' loads in flight; sums are joined in a fixed
+// order, with no atomics.
+//
+// Sums of x are taken about a value of x (the thread's or the slab's first) and
+// joined in fp64, or squares are taken about the mean itself, so a mean far from
+// zero costs no digits of the variance.
 #include "ql_device.h"
 #include "ql_ops.h"
 
@@ -20,6 +25,7 @@ namespace {
 
 typedef __bf16 bf16;
 constexpr int kNormThreads = 512;
+constexpr int kSlabVectors = 12;  // vectors of a slab that a thread holds at most
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <typename T, int V>
@@ -32,11 +38,14 @@ struct Vec<T, 1> {
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
+__device__ __forceinline__ typename Vec<T, V>::type raw_v(const T* p) {
+  return *reinterpret_cast<const typename Vec<T, V>::type*>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void widen(const typename Vec<T, V>::type& x, float (&v)[V]) {
   if constexpr (V == 1) {
-    v[0] = (float)p[0];
+    v[0] = (float)x;
   } else {
-    const typename Vec<T, V>::type x = *reinterpret_cast<const typename Vec<T, V>::type*>(p);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = (float)x[i];
   }
@@ -58,6 +67,28 @@ __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
 }
+
+template <bool SILU>
+__device__ __forceinline__ float act(float z) {
+  return SILU ? z * sigmoid(z) : z;
+}
+
+// gamma and beta of V channels from c on (1 and 0 where there is none).
+template <typename W, int V>
+struct Affine {
+  float ga[V], be[V];
+  __device__ __forceinline__ void load(const void* gamma, const void* beta, int c) {
+    const W* g = reinterpret_cast<const W*>(gamma);
+    const W* b = reinterpret_cast<const W*>(beta);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      ga[i] = g ? (float)g[c + i] : 1.0f;
+      be[i] = b ? (float)b[c + i] : 0.0f;
+    }
+  }
+};
+
+constexpr int kAhead = 4;  // positions whose loads a thread has in flight
 
 // Position p of image b is chunk-local; thread (tx, ty) of a workgroup takes
 // channel vectors tx, tx + TX, ... of positions ty, ty + TY, ...
@@ -85,18 +116,29 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_stats(StatsK a) {
       float k[V], s1[V], s2[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) k[i] = s1[i] = s2[i] = 0.0f;
-      if (l0 + ty < l1) load_v<T, V>(x + (int64_t)(l0 + ty) * a.xr + v * V, k);
+      const T* p = x + v * V;
       int n = 0;
-      for (int l = l0 + ty; l < l1; l += s.ty, ++n) {
+      auto add = [&](const typename Vec<T, V>::type& xv) {
         float e[V];
-        load_v<T, V>(x + (int64_t)l * a.xr + v * V, e);
+        widen<T, V>(xv, e);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+          if (n == 0) k[i] = e[i];
           const float d = e[i] - k[i];
           s1[i] += d;
           s2[i] = __builtin_fmaf(d, d, s2[i]);
         }
+        ++n;
+      };
+      int l = l0 + ty;
+      for (; l + (kAhead - 1) * s.ty < l1; l += kAhead * s.ty) {
+        typename Vec<T, V>::type e[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) e[j] = raw_v<T, V>(p + (int64_t)(l + j * s.ty) * a.xr);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) add(e[j]);
       }
+      for (; l < l1; l += s.ty) add(raw_v<T, V>(p + (int64_t)l * a.xr));
       const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -127,6 +169,37 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_stats(StatsK a) {
   }
 }
 
+// mean and rstd of every image's group from its chunks: one wave a group.
+struct StatsOut {
+  float2* stats;  // [B][G]: mean, rstd
+  float* mean;    // the caller's, or nullptr
+  float* rstd;
+  float eps;
+};
+
+__global__ __launch_bounds__(256) void k_norm_stats_join(const double2* part, StatsOut o, Shape s) {
+  const int lane = threadIdx.x & 63, id = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (id >= s.B * s.G) return;
+  const int b = id / s.G, g = id % s.G;
+  double S = 0.0, Q = 0.0;
+  for (int c = lane; c < s.chunks; c += kWave) {
+    const double2 v = part[((int64_t)b * s.chunks + c) * s.G + g];
+    S += v.x;
+    Q += v.y;
+  }
+#pragma unroll
+  for (int d = kWave / 2; d > 0; d /= 2) {
+    S += __shfl_xor(S, d);
+    Q += __shfl_xor(Q, d);
+  }
+  if (lane != 0) return;
+  const double n = (double)s.L * s.cpg, m = S / n, var = fmax(Q / n - m * m, 0.0);
+  const float2 r{(float)m, (float)(1.0 / sqrt(var + (double)o.eps))};
+  o.stats[id] = r;
+  if (o.mean) o.mean[id] = r.x;
+  if (o.rstd) o.rstd[id] = r.y;
+}
+
 struct ApplyK {
   const void* x;
   int64_t xb, xr;
@@ -134,77 +207,46 @@ struct ApplyK {
   int64_t yb, yr;
   const void* gamma;
   const void* beta;
-  const double2* part;
-  float* mean;
-  float* rstd;
-  float eps;
+  const float2* stats;
   Shape s;
 };
 
 template <typename T, typename W, int V, bool SILU>
 __global__ __launch_bounds__(kNormThreads) void k_norm_apply(ApplyK a) {
-  extern __shared__ float2 lds2[];  // [G]: mean, rstd
-  __shared__ double2 sub[kNormThreads];
   const Shape& s = a.s;
   const int b = blockIdx.y, chunk = blockIdx.x;
-  {
-    const int gb = min(s.G, (int)blockDim.x), ns = blockDim.x / gb;
-    const int gi = threadIdx.x % gb, si = threadIdx.x / gb;
-    for (int g0 = 0; g0 < s.G; g0 += gb) {
-      double S = 0.0, Q = 0.0;
-      const int g = g0 + gi;
-      if (si < ns && g < s.G) {
-        const double2* p = a.part + (int64_t)b * s.chunks * s.G + g;
-        for (int c = si; c < s.chunks; c += ns) {
-          S += p[(int64_t)c * s.G].x;
-          Q += p[(int64_t)c * s.G].y;
-        }
-      }
-      sub[threadIdx.x] = double2{S, Q};
-      __syncthreads();
-      if (si == 0 && g < s.G) {
-        for (int u = 1; u < ns; ++u) {
-          S += sub[u * gb + gi].x;
-          Q += sub[u * gb + gi].y;
-        }
-        const double n = (double)s.L * s.cpg, m = S / n, var = fmax(Q / n - m * m, 0.0);
-        const float2 r{(float)m, (float)(1.0 / sqrt(var + (double)a.eps))};
-        lds2[g] = r;
-        if (chunk == 0) {
-          if (a.mean) a.mean[b * s.G + g] = r.x;
-          if (a.rstd) a.rstd[b * s.G + g] = r.y;
-        }
-      }
-      __syncthreads();
-    }
-  }
   const int tx = threadIdx.x % s.tx, ty = threadIdx.x / s.tx;
   if (ty >= s.ty) return;
   const int l0 = chunk * s.rows, l1 = min(s.L, l0 + s.rows);
   const T* x = reinterpret_cast<const T*>(a.x) + b * a.xb;
   T* y = reinterpret_cast<T*>(a.y) + b * a.yb;
-  const W* gamma = reinterpret_cast<const W*>(a.gamma);
-  const W* beta = reinterpret_cast<const W*>(a.beta);
   for (int v = tx; v < s.cv; v += s.tx) {
-    float m[V], sc[V], sh[V];
+    Affine<W, V> f;
+    f.load(a.gamma, a.beta, v * V);
+    float m[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = v * V + i;
-      const float2 r = lds2[c / s.cpg];
+      const float2 r = a.stats[b * s.G + (v * V + i) / s.cpg];
       m[i] = r.x;
-      sc[i] = r.y * (gamma ? (float)gamma[c] : 1.0f);
-      sh[i] = beta ? (float)beta[c] : 0.0f;
+      f.ga[i] *= r.y;
     }
-    for (int l = l0 + ty; l < l1; l += s.ty) {
+    auto put = [&](const typename Vec<T, V>::type& xv, int l) {
       float e[V];
-      load_v<T, V>(x + (int64_t)l * a.xr + v * V, e);
+      widen<T, V>(xv, e);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float z = __builtin_fmaf(e[i] - m[i], sc[i], sh[i]);
-        e[i] = SILU ? z * sigmoid(z) : z;
-      }
+      for (int i = 0; i < V; ++i) e[i] = act<SILU>(__builtin_fmaf(e[i] - m[i], f.ga[i], f.be[i]));
       store_v<T, V>(y + (int64_t)l * a.yr + v * V, e);
+    };
+    const T* p = x + v * V;
+    int l = l0 + ty;
+    for (; l + (kAhead - 1) * s.ty < l1; l += kAhead * s.ty) {
+      typename Vec<T, V>::type e[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) e[j] = raw_v<T, V>(p + (int64_t)(l + j * s.ty) * a.xr);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) put(e[j], l + j * s.ty);
     }
+    for (; l < l1; l += s.ty) put(raw_v<T, V>(p + (int64_t)l * a.xr), l);
   }
 }
 
@@ -247,32 +289,45 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_grad_sums(GradK a) {
   const int l0 = chunk * s.rows, l1 = min(s.L, l0 + s.rows);
   const T* x = reinterpret_cast<const T*>(a.x) + b * a.xb;
   const T* dy = reinterpret_cast<const T*>(a.dy) + b * a.dyb;
-  const W* gamma = reinterpret_cast<const W*>(a.gamma);
-  const W* beta = reinterpret_cast<const W*>(a.beta);
   if (ty < s.ty) {
     for (int v = tx; v < s.cv; v += s.tx) {
-      float m[V], r[V], ga[V], be[V], p[V], q[V];
+      Affine<W, V> f;
+      f.load(a.gamma, a.beta, v * V);
+      float m[V], r[V], p[V], q[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = v * V + i, g = b * s.G + c / s.cpg;
+        const int g = b * s.G + (v * V + i) / s.cpg;
         m[i] = a.mean[g];
         r[i] = a.rstd[g];
-        ga[i] = gamma ? (float)gamma[c] : 1.0f;
-        be[i] = beta ? (float)beta[c] : 0.0f;
         p[i] = q[i] = 0.0f;
       }
-      for (int l = l0 + ty; l < l1; l += s.ty) {
+      auto add = [&](const typename Vec<T, V>::type& xv, const typename Vec<T, V>::type& dv) {
         float e[V], d[V];
-        load_v<T, V>(x + (int64_t)l * a.xr + v * V, e);
-        load_v<T, V>(dy + (int64_t)l * a.dyr + v * V, d);
+        widen<T, V>(xv, e);
+        widen<T, V>(dv, d);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           float xh;
-          const float dz = grad_z<SILU>(e[i], d[i], m[i], r[i], ga[i], be[i], xh);
+          const float dz = grad_z<SILU>(e[i], d[i], m[i], r[i], f.ga[i], f.be[i], xh);
           p[i] += dz;
           q[i] = __builtin_fmaf(dz, xh, q[i]);
         }
+      };
+      const T* px = x + v * V;
+      const T* pd = dy + v * V;
+      int l = l0 + ty;
+      for (; l + (kAhead - 1) * s.ty < l1; l += kAhead * s.ty) {
+        typename Vec<T, V>::type e[kAhead], d[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          e[j] = raw_v<T, V>(px + (int64_t)(l + j * s.ty) * a.xr);
+          d[j] = raw_v<T, V>(pd + (int64_t)(l + j * s.ty) * a.dyr);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) add(e[j], d[j]);
       }
+      for (; l < l1; l += s.ty)
+        add(raw_v<T, V>(px + (int64_t)l * a.xr), raw_v<T, V>(pd + (int64_t)l * a.dyr));
 #pragma unroll
       for (int i = 0; i < V; ++i) lds2[ty * s.C + v * V + i] = float2{p[i], q[i]};
     }
@@ -336,20 +391,33 @@ __global__ __launch_bounds__(256) void k_norm_grad_reduce(GradK a) {
   }
 }
 
+// dgamma and dbeta of channel c: sums over the images.
+template <typename W>
+__device__ __forceinline__ void sum_images(const float2* pq, int B, int C, int c, void* dgamma,
+                                           void* dbeta) {
+  if (c >= C) return;
+  double p = 0.0, q = 0.0;
+  for (int b = 0; b < B; ++b) {
+    const float2 v = pq[(int64_t)b * C + c];
+    p += v.x;
+    q += v.y;
+  }
+  if (dgamma) reinterpret_cast<W*>(dgamma)[c] = (W)(float)q;
+  if (dbeta) reinterpret_cast<W*>(dbeta)[c] = (W)(float)p;
+}
+template <typename W>
+__global__ __launch_bounds__(256) void k_norm_sum_images(const float2* pq, int B, int C, void* dgamma,
+                                                         void* dbeta) {
+  sum_images<W>(pq, B, C, blockIdx.x * 256 + threadIdx.x, dgamma, dbeta);
+}
+
 template <typename T, typename W, int V, bool SILU>
 __global__ __launch_bounds__(kNormThreads) void k_norm_grad_apply(GradK a) {
   const Shape& s = a.s;
-  if ((int)blockIdx.x >= s.chunks) {  // dgamma and dbeta: sums over the images
-    const int c = ((int)blockIdx.x - s.chunks) * kNormThreads + threadIdx.x;
-    if (blockIdx.y != 0 || c >= s.C) return;
-    double p = 0.0, q = 0.0;
-    for (int b = 0; b < s.B; ++b) {
-      const float2 v = a.pq[(int64_t)b * s.C + c];
-      p += v.x;
-      q += v.y;
-    }
-    if (a.dgamma) reinterpret_cast<W*>(a.dgamma)[c] = (W)(float)q;
-    if (a.dbeta) reinterpret_cast<W*>(a.dbeta)[c] = (W)(float)p;
+  if ((int)blockIdx.x >= s.chunks) {
+    if (blockIdx.y == 0)
+      sum_images<W>(a.pq, s.B, s.C, ((int)blockIdx.x - s.chunks) * kNormThreads + threadIdx.x,
+                    a.dgamma, a.dbeta);
     return;
   }
   const int tx = threadIdx.x % s.tx, ty = threadIdx.x / s.tx;
@@ -359,43 +427,246 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_grad_apply(GradK a) {
   const T* x = reinterpret_cast<const T*>(a.x) + b * a.xb;
   const T* dy = reinterpret_cast<const T*>(a.dy) + b * a.dyb;
   T* dx = reinterpret_cast<T*>(a.dx) + b * a.dxb;
-  const W* gamma = reinterpret_cast<const W*>(a.gamma);
-  const W* beta = reinterpret_cast<const W*>(a.beta);
   for (int v = tx; v < s.cv; v += s.tx) {
-    float m[V], r[V], ga[V], be[V], s1[V], s2[V];
+    Affine<W, V> f;
+    f.load(a.gamma, a.beta, v * V);
+    float m[V], r[V], s1[V], s2[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = v * V + i, g = b * s.G + c / s.cpg;
+      const int g = b * s.G + (v * V + i) / s.cpg;
       m[i] = a.mean[g];
       r[i] = a.rstd[g];
-      ga[i] = gamma ? (float)gamma[c] : 1.0f;
-      be[i] = beta ? (float)beta[c] : 0.0f;
       const float2 t = a.s12[g];
       s1[i] = t.x;
       s2[i] = t.y;
     }
-    for (int l = l0 + ty; l < l1; l += s.ty) {
+    auto put = [&](const typename Vec<T, V>::type& xv, const typename Vec<T, V>::type& dv, int l) {
       float e[V], d[V];
-      load_v<T, V>(x + (int64_t)l * a.xr + v * V, e);
-      load_v<T, V>(dy + (int64_t)l * a.dyr + v * V, d);
+      widen<T, V>(xv, e);
+      widen<T, V>(dv, d);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         float xh;
-        const float dz = grad_z<SILU>(e[i], d[i], m[i], r[i], ga[i], be[i], xh);
-        e[i] = r[i] * (dz * ga[i] - s1[i] - xh * s2[i]);
+        const float dz = grad_z<SILU>(e[i], d[i], m[i], r[i], f.ga[i], f.be[i], xh);
+        e[i] = r[i] * (dz * f.ga[i] - s1[i] - xh * s2[i]);
       }
       store_v<T, V>(dx + (int64_t)l * a.dxr + v * V, e);
+    };
+    const T* px = x + v * V;
+    const T* pd = dy + v * V;
+    int l = l0 + ty;
+    for (; l + (kAhead - 1) * s.ty < l1; l += kAhead * s.ty) {
+      typename Vec<T, V>::type e[kAhead], d[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        e[j] = raw_v<T, V>(px + (int64_t)(l + j * s.ty) * a.xr);
+        d[j] = raw_v<T, V>(pd + (int64_t)(l + j * s.ty) * a.dyr);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) put(e[j], d[j], l + j * s.ty);
     }
+    for (; l < l1; l += s.ty)
+      put(raw_v<T, V>(px + (int64_t)l * a.xr), raw_v<T, V>(pd + (int64_t)l * a.dyr), l);
   }
 }
 
-// Elements that one access may cover: 16 bytes where every row starts aligned
-// and C divides, else one element.
-bool rows_aligned(const void* p, int64_t sb, int64_t sr, int es) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (sb * es) % 16 == 0 && (sr * es) % 16 == 0;
+// ------------------------------------------------------------------- slabs ----
+// One workgroup: one group of one image, [L, cpg] values at a row stride, in NV
+// vectors a thread. Thread (tx, ty) has channel vector tx of positions ty,
+// ty + TY, ...
+struct SlabK {
+  const void* x;
+  int64_t xb, xr;
+  const void* dy;
+  int64_t dyb, dyr;
+  void* y;  // y, or dx
+  int64_t yb, yr;
+  const void* gamma;
+  const void* beta;
+  float* mean;
+  float* rstd;
+  float2* pq;     // gradient: [B][C] sums of dz and dz xhat; nullptr with one image
+  void* dgamma;   // gradient with one image
+  void* dbeta;
+  int B, L, C, G, cpg, vpr, ty;
+  float eps;
+};
+
+// Workgroup to (image, group): neighbouring groups share cache lines, so one
+// chiplet (ids go round the eight) gets neighbours.
+__device__ __forceinline__ void slab_of(const SlabK& a, int id, int& b, int& g) {
+  b = id / a.G;
+  const int i = id % a.G;
+  g = a.G % 8 == 0 ? (i % 8) * (a.G / 8) + i / 8 : i;
 }
 
-Shape shape_of(int B, int L, int C, int G, int V) {
+__device__ __forceinline__ float wave_sum(float v) {
+  v += xor_lane<1>(v);
+  v += xor_lane<2>(v);
+  v += xor_lane<4>(v);
+  v += xor_lane<8>(v);
+  v += xor_lane<16>(v);
+  return v + __shfl_xor(v, 32);
+}
+
+// Sums of two values over the workgroup, the waves' in fp64; valid in all threads.
+__device__ __forceinline__ double2 slab_sum2(float u, float v, float2* lds) {
+  u = wave_sum(u);
+  v = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = float2{u, v};
+  __syncthreads();
+  double2 s{0.0, 0.0};
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
+    s.x += lds[w].x;
+    s.y += lds[w].y;
+  }
+  return s;
+}
+
+template <typename T, typename W, int V, int NV, bool SILU>
+__global__ __launch_bounds__(kNormThreads) void k_norm_slab(SlabK a) {
+  __shared__ float2 red[kNormThreads / 64];
+  int b, g;
+  slab_of(a, blockIdx.x, b, g);
+  const int tx = threadIdx.x % a.vpr, ty = threadIdx.x / a.vpr, c = g * a.cpg + tx * V;
+  const bool live = ty < a.ty;
+  const T* x = reinterpret_cast<const T*>(a.x) + b * a.xb + c;
+  typename Vec<T, V>::type xv[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) xv[k] = raw_v<T, V>(x + (int64_t)min(ty + k * a.ty, a.L - 1) * a.xr);
+  const float first = (float)(reinterpret_cast<const T*>(a.x) + b * a.xb)[g * a.cpg];
+  Affine<W, V> f;
+  f.load(a.gamma, a.beta, c);
+  const double n = (double)a.L * a.cpg;
+  float s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (live && ty + k * a.ty < a.L) {
+      float e[V];
+      widen<T, V>(xv[k], e);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s += e[i] - first;
+    }
+  const double md = (double)first + slab_sum2(s, 0.0f, red).x / n;
+  const float m = (float)md;
+  float q = 0.0f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (live && ty + k * a.ty < a.L) {
+      float e[V];
+      widen<T, V>(xv[k], e);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = e[i] - m;
+        q = __builtin_fmaf(d, d, q);
+      }
+    }
+  const double off = md - (double)m;  // squares about m, not about md
+  const double var = fmax(slab_sum2(q, 0.0f, red).x / n - off * off, 0.0);
+  const float r = (float)(1.0 / sqrt(var + (double)a.eps));
+  if (threadIdx.x == 0) {
+    if (a.mean) a.mean[b * a.G + g] = m;
+    if (a.rstd) a.rstd[b * a.G + g] = r;
+  }
+  T* y = reinterpret_cast<T*>(a.y) + b * a.yb + c;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int l = ty + k * a.ty;
+    if (!live || l >= a.L) continue;
+    float e[V];
+    widen<T, V>(xv[k], e);
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = act<SILU>(__builtin_fmaf(e[i] - m, r * f.ga[i], f.be[i]));
+    store_v<T, V>(y + (int64_t)l * a.yr, e);
+  }
+}
+
+template <typename T, typename W, int V, int NV, bool SILU>
+__global__ __launch_bounds__(kNormThreads) void k_norm_slab_grad(SlabK a) {
+  __shared__ float2 red[kNormThreads / 64];
+  __shared__ float2 sums[kNormThreads * V];  // [ty][channel of the group]
+  int b, g;
+  slab_of(a, blockIdx.x, b, g);
+  const int tx = threadIdx.x % a.vpr, ty = threadIdx.x / a.vpr, c = g * a.cpg + tx * V;
+  const bool live = ty < a.ty;
+  const T* x = reinterpret_cast<const T*>(a.x) + b * a.xb + c;
+  const T* dy = reinterpret_cast<const T*>(a.dy) + b * a.dyb + c;
+  typename Vec<T, V>::type xv[NV], dv[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int64_t l = min(ty + k * a.ty, a.L - 1);
+    xv[k] = raw_v<T, V>(x + l * a.xr);
+    dv[k] = raw_v<T, V>(dy + l * a.dyr);
+  }
+  Affine<W, V> f;
+  f.load(a.gamma, a.beta, c);
+  const float m = a.mean[b * a.G + g], r = a.rstd[b * a.G + g];
+  float p[V], q[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) p[i] = q[i] = 0.0f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (live && ty + k * a.ty < a.L) {
+      float e[V], d[V];
+      widen<T, V>(xv[k], e);
+      widen<T, V>(dv[k], d);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float xh;
+        const float dz = grad_z<SILU>(e[i], d[i], m, r, f.ga[i], f.be[i], xh);
+        p[i] += dz;
+        q[i] = __builtin_fmaf(dz, xh, q[i]);
+      }
+    }
+  float u1 = 0.0f, u2 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (live) sums[ty * a.cpg + tx * V + i] = float2{p[i], q[i]};
+    u1 = __builtin_fmaf(f.ga[i], p[i], u1);
+    u2 = __builtin_fmaf(f.ga[i], q[i], u2);
+  }
+  const double2 t = slab_sum2(u1, u2, red);  // its barriers publish `sums` too
+  const double n = (double)a.L * a.cpg;
+  const float s1 = (float)(t.x / n), s2 = (float)(t.y / n);
+  for (int ch = threadIdx.x; ch < a.cpg; ch += blockDim.x) {
+    float P = 0.0f, Q = 0.0f;
+    for (int y = 0; y < a.ty; ++y) {
+      P += sums[y * a.cpg + ch].x;
+      Q += sums[y * a.cpg + ch].y;
+    }
+    if (a.pq) {
+      a.pq[(int64_t)b * a.C + g * a.cpg + ch] = float2{P, Q};
+    } else {
+      if (a.dgamma) reinterpret_cast<W*>(a.dgamma)[g * a.cpg + ch] = (W)Q;
+      if (a.dbeta) reinterpret_cast<W*>(a.dbeta)[g * a.cpg + ch] = (W)P;
+    }
+  }
+  T* dx = reinterpret_cast<T*>(a.y) + b * a.yb + c;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int l = ty + k * a.ty;
+    if (!live || l >= a.L) continue;
+    float e[V], d[V];
+    widen<T, V>(xv[k], e);
+    widen<T, V>(dv[k], d);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float xh;
+      const float dz = grad_z<SILU>(e[i], d[i], m, r, f.ga[i], f.be[i], xh);
+      e[i] = r * (dz * f.ga[i] - s1 - xh * s2);
+    }
+    store_v<T, V>(dx + (int64_t)l * a.yr, e);
+  }
+}
+
+bool rows_aligned(const void* p, int64_t sb, int64_t sr, int es, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (sb * es) % bytes == 0 &&
+         (sr * es) % bytes == 0;
+}
+
+// Chunks for `groups` workgroups in all.
+Shape shape_of(int B, int L, int C, int G, int V, int groups) {
   Shape s;
   s.B = B;
   s.L = L;
@@ -405,60 +676,71 @@ Shape shape_of(int B, int L, int C, int G, int V) {
   s.cv = C / V;
   s.tx = s.cv < kNormThreads ? s.cv : kNormThreads;
   s.ty = kNormThreads / s.tx;
-  // About 1024 workgroups in all, none with fewer positions than it has rows
-  // of threads.
-  int64_t want = (1024 + B - 1) / B;
-  const int64_t cap = (L + s.ty - 1) / s.ty;
+  const int step = kAhead * s.ty;
+  int64_t want = (groups + B - 1) / B;
+  const int64_t cap = ((int64_t)L + step - 1) / step;
   want = want < cap ? want : cap;
   s.rows = (int)(((int64_t)L + want - 1) / want);
-  s.rows = (s.rows + s.ty - 1) / s.ty * s.ty;
+  s.rows = (s.rows + step - 1) / step * step;
   s.chunks = (L + s.rows - 1) / s.rows;
   return s;
 }
+#ifndef QL_NS
+#define QL_NS 512
+#endif
+#ifndef QL_NA
+#define QL_NA 2048
+#endif
+constexpr int kSumGroups = QL_NS, kApplyGroups = QL_NA;
 
 template <typename T, typename W, int V>
 hipError_t norm_run(const NormArgs& a, hipStream_t st) {
-  const Shape s = shape_of(a.B, a.L, a.C, a.G, V);
+  const Shape s = shape_of(a.B, a.L, a.C, a.G, V, kSumGroups);
   double2* part = reinterpret_cast<double2*>(a.ws);
+  float2* stats = reinterpret_cast<float2*>(part + (int64_t)s.B * s.chunks * s.G);
   const int threads = (s.tx * s.ty + 63) / 64 * 64;
   hipLaunchKernelGGL((k_norm_stats<T, V>), dim3(s.chunks, s.B), dim3(threads),
                      (size_t)s.ty * s.C * sizeof(float2), st, StatsK{a.x, a.xb, a.xr, part, s});
+  hipLaunchKernelGGL(k_norm_stats_join, dim3((s.B * s.G + 3) / 4), dim3(256), 0, st, part,
+                     StatsOut{stats, a.mean, a.rstd, a.eps}, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const ApplyK k{a.x, a.xb, a.xr, a.y, a.yb, a.yr, a.gamma, a.beta, part, a.mean, a.rstd, a.eps, s};
-  const size_t lds = (size_t)s.G * sizeof(float2);
+  const Shape t = shape_of(a.B, a.L, a.C, a.G, V, kApplyGroups);
+  const ApplyK k{a.x, a.xb, a.xr, a.y, a.yb, a.yr, a.gamma, a.beta, stats, t};
   if (a.act)
-    hipLaunchKernelGGL((k_norm_apply<T, W, V, true>), dim3(s.chunks, s.B), dim3(threads), lds, st, k);
+    hipLaunchKernelGGL((k_norm_apply<T, W, V, true>), dim3(t.chunks, t.B), dim3(threads), 0, st, k);
   else
-    hipLaunchKernelGGL((k_norm_apply<T, W, V, false>), dim3(s.chunks, s.B), dim3(threads), lds, st,
-                       k);
+    hipLaunchKernelGGL((k_norm_apply<T, W, V, false>), dim3(t.chunks, t.B), dim3(threads), 0, st, k);
   return hipGetLastError();
 }
 
 template <typename T, typename W, int V>
 hipError_t norm_grad_run(const NormArgs& a, hipStream_t st) {
   const bool empty = a.B == 0 || a.L == 0;  // dgamma and dbeta are still written: zero
-  Shape s = shape_of(empty ? 1 : a.B, empty ? 1 : a.L, a.C, a.G, V);
-  if (empty) s.B = s.chunks = 0;
   float2* pq = reinterpret_cast<float2*>(a.ws);
+  if (empty) {
+    hipLaunchKernelGGL(k_norm_sum_images<W>, dim3((a.C + 255) / 256), dim3(256), 0, st, pq, 0, a.C,
+                       a.dgamma, a.dbeta);
+    return hipGetLastError();
+  }
+  const Shape s = shape_of(a.B, a.L, a.C, a.G, V, kSumGroups);
   float2* s12 = pq + (int64_t)s.B * s.C;
   float2* part = s12 + (int64_t)s.B * s.G;
-  const GradK k{a.x,     a.xb,    a.xr, a.dy, a.dyb, a.dyr, a.y,      a.yb,    a.yr, a.gamma, a.beta,
-                a.mean, a.rstd, part, pq,   s12,   a.dgamma, a.dbeta, s};
+  GradK k{a.x,    a.xb,   a.xr, a.dy, a.dyb, a.dyr,    a.y,     a.yb, a.yr, a.gamma, a.beta,
+          a.mean, a.rstd, part, pq,   s12,   a.dgamma, a.dbeta, s};
   const int threads = (s.tx * s.ty + 63) / 64 * 64;
   const size_t lds = (size_t)s.ty * s.C * sizeof(float2);
-  if (!empty) {
-    if (a.act)
-      hipLaunchKernelGGL((k_norm_grad_sums<T, W, V, true>), dim3(s.chunks, s.B), dim3(threads), lds,
-                         st, k);
-    else
-      hipLaunchKernelGGL((k_norm_grad_sums<T, W, V, false>), dim3(s.chunks, s.B), dim3(threads),
-                         lds, st, k);
-    hipLaunchKernelGGL(k_norm_grad_reduce<W>, dim3(s.B * s.G), dim3(256), 0, st, k);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  const dim3 grid(s.chunks + (s.C + kNormThreads - 1) / kNormThreads, empty ? 1 : s.B);
+  if (a.act)
+    hipLaunchKernelGGL((k_norm_grad_sums<T, W, V, true>), dim3(s.chunks, s.B), dim3(threads), lds,
+                       st, k);
+  else
+    hipLaunchKernelGGL((k_norm_grad_sums<T, W, V, false>), dim3(s.chunks, s.B), dim3(threads), lds,
+                       st, k);
+  hipLaunchKernelGGL(k_norm_grad_reduce<W>, dim3(s.B * s.G), dim3(256), 0, st, k);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k.s = shape_of(a.B, a.L, a.C, a.G, V, kApplyGroups);
+  const dim3 grid(k.s.chunks + (s.C + kNormThreads - 1) / kNormThreads, s.B);
   if (a.act)
     hipLaunchKernelGGL((k_norm_grad_apply<T, W, V, true>), grid, dim3(kNormThreads), 0, st, k);
   else
@@ -466,15 +748,92 @@ hipError_t norm_grad_run(const NormArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Vectors a thread holds when one workgroup takes a slab, 0 where it does not fit.
+template <int V>
+int slab_vectors(const NormArgs& a) {
+  const int cpg = a.C / a.G;
+  if (cpg % V != 0 || cpg / V > kNormThreads || a.B == 0 || a.L == 0) return 0;
+  const int ty = kNormThreads / (cpg / V);
+  const int64_t nv = ((int64_t)a.L + ty - 1) / ty;
+  return nv <= kSlabVectors ? (int)nv : 0;
+}
+
+template <typename T, typename W, int V, int NV>
+hipError_t slab_run(const NormArgs& a, bool grad, hipStream_t st) {
+  SlabK k{};
+  k.x = a.x;
+  k.xb = a.xb;
+  k.xr = a.xr;
+  k.dy = a.dy;
+  k.dyb = a.dyb;
+  k.dyr = a.dyr;
+  k.y = a.y;
+  k.yb = a.yb;
+  k.yr = a.yr;
+  k.gamma = a.gamma;
+  k.beta = a.beta;
+  k.mean = a.mean;
+  k.rstd = a.rstd;
+  k.dgamma = a.dgamma;
+  k.dbeta = a.dbeta;
+  k.pq = grad && a.B > 1 ? reinterpret_cast<float2*>(a.ws) : nullptr;
+  k.B = a.B;
+  k.L = a.L;
+  k.C = a.C;
+  k.G = a.G;
+  k.cpg = a.C / a.G;
+  k.vpr = k.cpg / V;
+  k.eps = a.eps;
+  // no more threads than positions ask for
+  const int most = kNormThreads / k.vpr;
+  const int need = (a.L + NV - 1) / NV;
+  k.ty = most < need ? most : need;
+  const dim3 grid(a.B * a.G), block((k.vpr * k.ty + 63) / 64 * 64);
+  if (!grad) {
+    if (a.act)
+      hipLaunchKernelGGL((k_norm_slab<T, W, V, NV, true>), grid, block, 0, st, k);
+    else
+      hipLaunchKernelGGL((k_norm_slab<T, W, V, NV, false>), grid, block, 0, st, k);
+    return hipGetLastError();
+  }
+  if (a.act)
+    hipLaunchKernelGGL((k_norm_slab_grad<T, W, V, NV, true>), grid, block, 0, st, k);
+  else
+    hipLaunchKernelGGL((k_norm_slab_grad<T, W, V, NV, false>), grid, block, 0, st, k);
+  if (k.pq && (a.dgamma || a.dbeta))
+    hipLaunchKernelGGL(k_norm_sum_images<W>, dim3((a.C + 255) / 256), dim3(256), 0, st, k.pq, a.B,
+                       a.C, a.dgamma, a.dbeta);
+  return hipGetLastError();
+}
+
+template <typename T, typename W, int V>
+hipError_t norm_width(const NormArgs& a, bool slabs, bool grad, hipStream_t st) {
+  const int nv = slabs ? slab_vectors<V>(a) : 0;
+  if (nv > 0) {
+    if (nv <= 3) return slab_run<T, W, V, 3>(a, grad, st);
+    if (nv <= 6) return slab_run<T, W, V, 6>(a, grad, st);
+    return slab_run<T, W, V, kSlabVectors>(a, grad, st);
+  }
+  return grad ? norm_grad_run<T, W, V>(a, st) : norm_run<T, W, V>(a, st);
+}
+
 template <typename T, typename W>
 hipError_t norm_dispatch(const NormArgs& a, bool grad, hipStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const int es = sizeof(T);
-  const bool vec = a.C % V == 0 && rows_aligned(a.x, a.xb, a.xr, es) &&
-                   rows_aligned(a.y, a.yb, a.yr, es) &&
-                   (!grad || rows_aligned(a.dy, a.dyb, a.dyr, es));
-  if (grad) return vec ? norm_grad_run<T, W, V>(a, st) : norm_grad_run<T, W, 1>(a, st);
-  return vec ? norm_run<T, W, V>(a, st) : norm_run<T, W, 1>(a, st);
+  const int es = sizeof(T), cpg = a.C / a.G;
+  auto aligned = [&](int bytes) {
+    return a.C * es % bytes == 0 && rows_aligned(a.x, a.xb, a.xr, es, bytes) &&
+           rows_aligned(a.y, a.yb, a.yr, es, bytes) &&
+           (!grad || rows_aligned(a.dy, a.dyb, a.dyr, es, bytes));
+  };
+  // A slab's rows have cpg channels: the widest vector that divides them.
+  if (aligned(16) && slab_vectors<V>(a)) return norm_width<T, W, V>(a, true, grad, st);
+  if (aligned(8) && cpg % (V / 2) == 0 && slab_vectors<V / 2>(a))
+    return norm_width<T, W, V / 2>(a, true, grad, st);
+  if (V == 8 && aligned(4) && slab_vectors<2>(a)) return norm_width<T, W, 2>(a, true, grad, st);
+  if (aligned(16)) return norm_width<T, W, V>(a, false, grad, st);
+  if (slab_vectors<1>(a)) return norm_width<T, W, 1>(a, true, grad, st);
+  return norm_width<T, W, 1>(a, false, grad, st);
 }
 
 hipError_t norm_types(const NormArgs& a, bool grad, hipStream_t s) {
@@ -487,12 +846,13 @@ hipError_t norm_types(const NormArgs& a, bool grad, hipStream_t s) {
 
 int64_t norm_ws_bytes(int B, int L, int C, int G, bool grad) {
   int64_t chunks = 0;  // the most of any vector width
-  for (int V : {1, 4, 8}) {
+  for (int V : {1, 2, 4, 8}) {
     if (C % V) continue;
-    const Shape s = shape_of(B, L, C, G, V);
+    const Shape s = shape_of(B, L, C, G, V, kSumGroups);
     chunks = chunks > s.chunks ? chunks : s.chunks;
   }
-  if (!grad) return (int64_t)B * chunks * G * (int64_t)sizeof(double2);
+  if (!grad)
+    return (int64_t)B * G * (chunks * (int64_t)sizeof(double2) + (int64_t)sizeof(float2));
   return ((int64_t)B * C + (int64_t)B * G + (int64_t)B * chunks * C) * (int64_t)sizeof(float2);
 }
 

@@ -132,6 +132,9 @@ ql_status check_norm(const ql_norm* d) {
   if (d->channels > 8192 || d->groups > 2048)
     return fail(QL_ERR_UNSUPPORTED, "channels = %d, groups = %d: at most 8192 and 2048",
                 d->channels, d->groups);
+  if ((int64_t)d->batch * d->groups > 1 << 22)
+    return fail(QL_ERR_UNSUPPORTED, "batch = %d times groups = %d: at most 4194304", d->batch,
+                d->groups);
   if (!dtype_ok(d->x_dtype)) return fail(QL_ERR_ARG, "bad x_dtype %d", (int)d->x_dtype);
   if (!dtype_ok(d->w_dtype)) return fail(QL_ERR_ARG, "bad w_dtype %d", (int)d->w_dtype);
   if (d->act != QL_ACT_NONE && d->act != QL_ACT_SILU)

@@ -413,7 +413,8 @@ ql_status qlinear_lora_grad(const ql_lora* d, const void* X, int64_t ldx, int32_
 typedef enum { QL_ACT_NONE = 0, QL_ACT_SILU = 1 } ql_act;
 typedef struct {
   int32_t batch, positions;   /* >= 0; batch <= 65535 */
-  int32_t channels, groups;   /* 1 .. 8192 channels, a multiple of groups; groups <= 2048 */
+  int32_t channels, groups;   /* 1 .. 8192 channels, a multiple of groups; groups <= 2048,
+                                 batch * groups <= 2^22 */
   ql_dtype x_dtype;           /* x, y, dy, dx */
   ql_dtype w_dtype;           /* gamma, beta, dgamma, dbeta */
   ql_act act;

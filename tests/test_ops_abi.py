@@ -150,6 +150,7 @@ def _norm(**kw):
     (dict(batch=65536), _lib.QL_ERR_UNSUPPORTED, "batch"),
     (dict(channels=8200), _lib.QL_ERR_UNSUPPORTED, "8192"),
     (dict(channels=4098, groups=2049), _lib.QL_ERR_UNSUPPORTED, "2048"),
+    (dict(batch=2049, channels=2048, groups=2048), _lib.QL_ERR_UNSUPPORTED, "4194304"),
     (dict(x_dtype=3), _lib.QL_ERR_ARG, "x_dtype"),
     (dict(w_dtype=3), _lib.QL_ERR_ARG, "w_dtype"),
     (dict(act=2), _lib.QL_ERR_ARG, "act"),
