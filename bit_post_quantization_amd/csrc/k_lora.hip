@@ -725,8 +725,7 @@ __global__ __launch_bounds__(64 * NW) void k_lora_ds(DsArgs a, bool vec) {
 // rows of one request in the range) Q^T P is summed in registers and written to
 // a slot of its own, and A's columns stay in registers for the whole range.
 //
-// bf16 X takes bf16 matrix instructions, with Q in three bf16 terms that sum to
-// it exactly; both operands of dA are read from LDS transposed
+// bf16 X takes bf16 matrix instructions, with Q in bf16 terms that sum to it; both operands of dA are read from LDS transposed
 // (ds_read_b64_tr_b16: lane c of 16 gets four rows of column c). fp32 P takes
 // the fp32 instructions, element by element from memory: lanes side by side
 // have addresses side by side.
@@ -750,9 +749,12 @@ struct OuterLds {
   static constexpr int R = RT * 16;
   static constexpr int XLD = kOuterCols + 8, QLD = R + 8;
   static constexpr int kPlanes = RT == 1 ? 4 : 3;
-  float q[kOuterRows][R + 4];
-  bf16 x[sizeof(XT) == 2 ? kOuterRows : 1][XLD];
-  bf16 h[kPlanes][kOuterRows][QLD];  // the terms of q (a fourth one of zeros for R = 16)
+  struct Tile {
+    float q[kOuterRows][R + 4];
+    bf16 x[sizeof(XT) == 2 ? kOuterRows : 1][XLD];
+    bf16 h[kPlanes][kOuterRows][QLD];  // the terms of q (a fourth one of zeros for R = 16)
+  };
+  Tile tile[2];  // one is used while the next is written
 };
 
 template <typename PT, typename WT, int RT, bool DX, bool TR>
@@ -760,6 +762,11 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
   constexpr int R = RT * 16, U = kOuterU;
   constexpr bool PB = sizeof(PT) == 2;        // bf16 products for Q^T P
   constexpr bool XB = DX && sizeof(WT) == 2;  // bf16 products for dX
+  // Terms of Q: all three (24 bits) where the result is fp32, two (16 bits) where
+  // it is rounded to bf16's 8.
+  constexpr int kTermsA = PB ? (sizeof(WT) == 2 ? 2 : 3) : 0;
+  constexpr int kTermsX = XB ? (sizeof(PT) == 2 ? 2 : 3) : 0;
+  constexpr int t_xld = OuterLds<PT, RT>::XLD, t_qld = OuterLds<PT, RT>::QLD;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   const int dw = chunk * kOuterCols, d0 = dw + wave * 16 * U;  // the workgroup's, the wave's columns
   const int lo = min(sp * a.row_len, a.q.rows), hi = min(lo + a.row_len, a.q.rows);
@@ -850,9 +857,9 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
           }
         }
       };
-      fetch(r0);
-      for (int m0 = r0; m0 < r1; m0 += kOuterRows) {
-        __syncthreads();  // the last tile has been read
+      // Puts the fetched tile into LDS (and, for fp32 P, into pc).
+      float pc[PB ? 1 : 8][PB ? 1 : U];
+      auto put = [&](int m0, typename OuterLds<PT, RT>::Tile& t) {
         float qz[QN];
 #pragma unroll
         for (int k = 0; k < QN; ++k) qz[k] = qr[k / QW][k % QW];
@@ -867,7 +874,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
           if (m0 + qm >= r1 || qj + k >= ra) qz[k] = 0.0f;
         if constexpr (!PB || (DX && !XB)) {
 #pragma unroll
-          for (int k = 0; k < QN; ++k) lds.q[qm][qj + k] = qz[k];
+          for (int k = 0; k < QN; ++k) t.q[qm][qj + k] = qz[k];
         }
         if constexpr (PB || XB) {
           typedef bf16 vt __attribute__((ext_vector_type(QN < 8 ? QN : 8)));
@@ -883,19 +890,19 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
               mi[k] = y;
               l[k] = z;
             }
-            *reinterpret_cast<vt*>(&lds.h[0][qm][qj + c * W]) = h;
-            *reinterpret_cast<vt*>(&lds.h[1][qm][qj + c * W]) = mi;
-            *reinterpret_cast<vt*>(&lds.h[2][qm][qj + c * W]) = l;
-            if constexpr (RT == 1) *reinterpret_cast<vt*>(&lds.h[3][qm][qj]) = vt(0.0f);
+            *reinterpret_cast<vt*>(&t.h[0][qm][qj + c * W]) = h;
+            *reinterpret_cast<vt*>(&t.h[1][qm][qj + c * W]) = mi;
+            if constexpr (kTermsA == 3 || kTermsX == 3)
+              *reinterpret_cast<vt*>(&t.h[2][qm][qj + c * W]) = l;
+            if constexpr (RT == 1 && kTermsX == 3) *reinterpret_cast<vt*>(&t.h[3][qm][qj]) = vt(0.0f);
           }
         }
-        float pc[PB ? 1 : 8][PB ? 1 : U];
         if constexpr (PB) {
 #pragma unroll
           for (int k = 0; k < XN; ++k) {
             const int v = k * kOuterThreads + threadIdx.x, m = v / XP, c = v % XP * 8;
             const bool in = m0 + m < r1 && dw + c < a.D;
-            *reinterpret_cast<v8h*>(&lds.x[m][c]) = in ? xr[k] : v8h(0.0f);
+            *reinterpret_cast<v8h*>(&t.x[m][c]) = in ? xr[k] : v8h(0.0f);
           }
         } else {
 #pragma unroll
@@ -904,18 +911,25 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
             for (int u = 0; u < U; ++u)
               pc[kk][u] = m0 + kk * 4 + g < r1 && d0 + 16 * u + r16 < a.D ? (float)pr[kk][u] : 0.0f;
         }
-        __syncthreads();
-        if (m0 + kOuterRows < r1) fetch(m0 + kOuterRows);
+      };
+      __syncthreads();  // the last piece's tiles have been read
+      fetch(r0);
+      put(r0, lds.tile[0]);
+      fetch(r0 + kOuterRows);
+      int cur = 0;
+      for (int m0 = r0; m0 < r1; m0 += kOuterRows, cur ^= 1) {
+        __syncthreads();  // tile `cur` is written, the other one has been read
+        const auto& t = lds.tile[cur];
         if constexpr (PB) {
           v8h xt[U];
 #pragma unroll
           for (int u = 0; u < U; ++u)
-            xt[u] = read_transposed(&lds.x[0][wave * 16 * U + 16 * u], lds.XLD, r16, g);
+            xt[u] = read_transposed(&t.x[0][wave * 16 * U + 16 * u], t_xld, r16, g);
 #pragma unroll
           for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              const v8h qt = read_transposed(&lds.h[k][0][16 * r], lds.QLD, r16, g);
+            for (int k = 0; k < kTermsA; ++k) {
+              const v8h qt = read_transposed(&t.h[k][0][16 * r], t_qld, r16, g);
 #pragma unroll
               for (int u = 0; u < U; ++u) acc[r][u] = mfma_bf16(qt, xt[u], acc[r][u]);
             }
@@ -924,7 +938,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
           for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-              const float qv = lds.q[kk * 4 + g][16 * r + r16];
+              const float qv = t.q[kk * 4 + g][16 * r + r16];
 #pragma unroll
               for (int u = 0; u < U; ++u)
                 acc[r][u] = TR ? mfma_f32(qv, pc[kk][u], acc[r][u]) : mfma_f32(pc[kk][u], qv, acc[r][u]);
@@ -933,20 +947,27 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
         if constexpr (DX) {
 #pragma unroll
           for (int m = 0; m < kOuterRows / 16; ++m) {
-            SFrag<WT, RT, 1> sf;
+            v4f y[U];
             if constexpr (XB) {
+              constexpr int KS = SFrag<bf16, RT, 1>::KS;
 #pragma unroll
-              for (int k = 0; k < SFrag<bf16, RT, 1>::KS; ++k) {
+              for (int u = 0; u < U; ++u) y[u] = v4f{0, 0, 0, 0};
+#pragma unroll
+              for (int k = 0; k < KS; ++k) {
+                if (kTermsX == 2 && (RT == 1 ? k == 1 : k % 3 == 2)) continue;
                 const int plane = RT == 1 ? 2 * k + g / 2 : k % 3;
                 const int j = RT == 1 ? 8 * (g & 1) : 32 * (k / 3) + 8 * g;
-                sf.s[0][k] = *reinterpret_cast<const v8h*>(&lds.h[plane][m * 16 + r16][j]);
+                const v8h sv = *reinterpret_cast<const v8h*>(&t.h[plane][m * 16 + r16][j]);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                  y[u] = mfma_bf16(sv, af[u].b[RT == 1 ? 0 : k / 3], y[u]);
               }
             } else {
-              sf.load(&lds.q[m * 16][0], R + 4, r16, g);
-            }
-            v4f y[U];
+              SFrag<WT, RT, 1> sf;
+              sf.load(&t.q[m * 16][0], R + 4, r16, g);
 #pragma unroll
-            for (int u = 0; u < U; ++u) y[u] = af[u].times(sf, 0);
+              for (int u = 0; u < U; ++u) y[u] = af[u].times(sf, 0);
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int row = m0 + m * 16 + 4 * g + k, d = d0 + col(0);
@@ -964,6 +985,10 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
               }
             }
           }
+        }
+        if (m0 + kOuterRows < r1) {
+          put(m0 + kOuterRows, lds.tile[cur ^ 1]);
+          fetch(m0 + 2 * kOuterRows);  // past the end: the last row again, unused
         }
       }
       pending = true;
@@ -1025,10 +1050,17 @@ __global__ __launch_bounds__(256) void k_lora_slot_sum(SlotSumArgs p, SlotSumArg
   for (int base = 0; base < a.slots; base += kWave) {
     const int i = base + lane;
     uint64_t hit = __ballot(i < a.slots && a.slot_id[i] == ad);
-    while (hit) {
-      const int k = __ffsll((unsigned long long)hit) - 1;
-      hit &= hit - 1;
-      if (e < len) v += a.part[(base + k) * len + e];
+    while (hit) {  // eight slots' loads at a time
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool any = hit != 0;
+        const int at = base + (any ? __ffsll((unsigned long long)hit) - 1 : 0);
+        hit &= hit - 1;
+        x[k] = any && e < len ? a.part[at * len + e] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += x[k];
     }
   }
   if (e >= len) return;
@@ -1123,13 +1155,13 @@ hipError_t forward_rt(const ForwardArgs& a, hipStream_t s) {
 template <typename WT, int RT>
 hipError_t ds_run(const DsArgs& a, hipStream_t s) {
   const bool vec = reinterpret_cast<uintptr_t>(a.dY) % 16 == 0 && a.ldy % 4 == 0;
-  constexpr int NW = RT == 8 ? 4 : 8;
+  constexpr int NW = RT == 8 ? 4 : 8, NS = RT <= 2 ? 16 : 8;
   if (a.tall)
     hipLaunchKernelGGL((k_lora_ds<WT, RT, 2, NW>), dim3(max_tiles(a.q, 32), a.splits), dim3(64 * NW),
                        0, s, a, vec);
   else
-    hipLaunchKernelGGL((k_lora_ds<WT, RT, 1, 8>), dim3(max_tiles(a.q, 16), a.splits), dim3(512), 0,
-                       s, a, vec);
+    hipLaunchKernelGGL((k_lora_ds<WT, RT, 1, NS>), dim3(max_tiles(a.q, 16), a.splits),
+                       dim3(64 * NS), 0, s, a, vec);
   return hipGetLastError();
 }
 
