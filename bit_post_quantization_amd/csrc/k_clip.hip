@@ -13,10 +13,8 @@
 // values keeps all its fp32 digits. The order of every sum is fixed.
 //
 // Bound by memory: 446M bf16 gradients clipped into fp32 (892 MB read twice, 1784 MB
-// written) take 640 us, 5.6 TB/s, where a large copy reaches 5.4. With runs of one
-// unit instead of kRun the same took 952 us (the look-up of a run is a chain of
-// loads); 224 adapter gradients of 33 MB (27 us) and smaller sets (13 us, the host's time) measured
-// the same with runs of one, two and four.
+// written) take 640 us, 5.6 TB/s, where a large copy reaches 5.4. The look-up of a
+// run is a chain of loads, so long lists take long runs.
 #include "ql_device.h"
 #include "ql_ops.h"
 
@@ -31,7 +29,6 @@ typedef bf16 v4h __attribute__((ext_vector_type(4)));
 constexpr int kUnit = QL_GRAD_UNIT;
 constexpr int kParts = QL_GRAD_PARTIALS;
 constexpr int kThreads = 512;
-constexpr int kRun = 4;  // units of a run
 
 // Last entry whose first unit is <= u (entries are in order): a 64-way search.
 __device__ int find_entry(const ql_grad* t, int n, int64_t u) {
@@ -130,18 +127,19 @@ __device__ __forceinline__ double squares(const void* src, int64_t at) {
   return run_squares<R>(reinterpret_cast<const T*>(src) + at);
 }
 
+template <int R>
 __global__ __launch_bounds__(kThreads) void k_grad_norm(const ql_grad* t, int n, int64_t units,
                                                         double* partials) {
   double s = 0.0;
-  for (int64_t u0 = (int64_t)blockIdx.x * kRun; u0 < units; u0 += (int64_t)gridDim.x * kRun) {
-    const Run r = find_run(t, n, u0, kRun);
+  for (int64_t u0 = (int64_t)blockIdx.x * R; u0 < units; u0 += (int64_t)gridDim.x * R) {
+    const Run r = find_run(t, n, u0, R);
     if (r.whole && reinterpret_cast<uintptr_t>(t[r.e].src) % 16 == 0) {
-      s += t[r.e].src_dtype == QL_BF16 ? squares<kRun, bf16>(t[r.e].src, r.at)
-                                       : squares<kRun, float>(t[r.e].src, r.at);
+      s += t[r.e].src_dtype == QL_BF16 ? squares<R, bf16>(t[r.e].src, r.at)
+                                       : squares<R, float>(t[r.e].src, r.at);
       continue;
     }
     int e = r.e;
-    for (int64_t u = u0; u < min(u0 + kRun, units); ++u) {
+    for (int64_t u = u0; u < min(u0 + R, units); ++u) {
       while (e + 1 < n && t[e + 1].start <= u) ++e;
       const int64_t at = (u - t[e].start) * kUnit;
       if (at < 0 || at >= t[e].n || !t[e].src) continue;
@@ -227,6 +225,7 @@ __device__ __forceinline__ void scale_any(const ql_grad& g, int64_t at, int len,
   }
 }
 
+template <int R>
 __global__ __launch_bounds__(kThreads) void k_grad_clip(const ql_grad* t, int n, int64_t units,
                                                         const double* partials, float max_norm,
                                                         float* norm) {
@@ -237,15 +236,15 @@ __global__ __launch_bounds__(kThreads) void k_grad_clip(const ql_grad* t, int n,
     known = true;
     return c;
   };
-  for (int64_t u0 = (int64_t)blockIdx.x * kRun; u0 < units; u0 += (int64_t)gridDim.x * kRun) {
-    const Run r = find_run(t, n, u0, kRun);
+  for (int64_t u0 = (int64_t)blockIdx.x * R; u0 < units; u0 += (int64_t)gridDim.x * R) {
+    const Run r = find_run(t, n, u0, R);
     const ql_grad g = t[r.e];
     if (r.whole && g.dst) {
-      scale_any<kRun>(g, r.at, kRun * kUnit, factor);
+      scale_any<R>(g, r.at, R * kUnit, factor);
       continue;
     }
     int e = r.e;
-    for (int64_t u = u0; u < min(u0 + kRun, units); ++u) {
+    for (int64_t u = u0; u < min(u0 + R, units); ++u) {
       while (e + 1 < n && t[e + 1].start <= u) ++e;
       const ql_grad h = t[e];
       const int64_t at = (u - h.start) * kUnit;
@@ -256,22 +255,33 @@ __global__ __launch_bounds__(kThreads) void k_grad_clip(const ql_grad* t, int n,
   factor();  // without a unit of its own the first workgroup still writes the norm
 }
 
+// Units of a run. With runs of one / four: 3.3M fp32 gradients 10.2 / 13.3 us, 8.3M
+// (224 adapter tensors) 27.2 / 28.4 us, 33M 80 / 84 us; 446M bf16 ones 1001 / 645 us.
+int run_units(int64_t units) { return units >= 16384 ? 4 : 1; }
+
 }  // namespace
 
 hipError_t launch_grad_norm(const ql_grad* table, int n, int64_t units, double* partials,
                             hipStream_t s) {
-  const int64_t runs = (units + kRun - 1) / kRun;
-  const int grid = (int)(runs < 1 ? 1 : runs < kParts ? runs : kParts);
-  hipLaunchKernelGGL(k_grad_norm, dim3(grid), dim3(kThreads), 0, s, table, n, units, partials);
+  const int run = run_units(units);
+  const int64_t runs = (units + run - 1) / run;
+  const dim3 grid((unsigned)(runs < 1 ? 1 : runs < kParts ? runs : kParts)), block(kThreads);
+  if (run == 4)
+    hipLaunchKernelGGL(k_grad_norm<4>, grid, block, 0, s, table, n, units, partials);
+  else
+    hipLaunchKernelGGL(k_grad_norm<1>, grid, block, 0, s, table, n, units, partials);
   return hipGetLastError();
 }
 
 hipError_t launch_grad_clip(const ql_grad* table, int n, int64_t units, const double* partials,
                             float max_norm, float* norm, hipStream_t s) {
-  const int64_t runs = (units + kRun - 1) / kRun, most = 1 << 20;
-  const int grid = (int)(runs < 1 ? 1 : runs < most ? runs : most);
-  hipLaunchKernelGGL(k_grad_clip, dim3(grid), dim3(kThreads), 0, s, table, n, units, partials,
-                     max_norm, norm);
+  const int run = run_units(units);
+  const int64_t runs = (units + run - 1) / run, most = 1 << 20;
+  const dim3 grid((unsigned)(runs < 1 ? 1 : runs < most ? runs : most)), block(kThreads);
+  if (run == 4)
+    hipLaunchKernelGGL(k_grad_clip<4>, grid, block, 0, s, table, n, units, partials, max_norm, norm);
+  else
+    hipLaunchKernelGGL(k_grad_clip<1>, grid, block, 0, s, table, n, units, partials, max_norm, norm);
   return hipGetLastError();
 }
 

@@ -634,14 +634,38 @@ __global__ __launch_bounds__(256) void k_lora_expand(ForwardArgs a, bool bvec, c
 // waves take every NW-th 32 columns, the next step's loads ahead of this one's
 // products, and join their sums in LDS. Lane l of a step has columns
 // 8 (l / 16) .. + 7 of row l % 16 of dY, and rank l % 16 of the same rows of B.
+//
+// A single element of B as it is held until its use: bf16 in a register of its own
+// (loads into register halves would wait for one another).
+template <typename WT>
+struct Held;
+template <>
+struct Held<float> {
+  float v;
+  __device__ __forceinline__ void load(const float* p) { v = *p; }
+  __device__ __forceinline__ float get() const { return v; }
+};
+template <>
+struct Held<bf16> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const uint16_t*>(p); }
+  __device__ __forceinline__ float get() const { return __uint_as_float(v << 16); }
+};
+
+template <int RT, int MT, int NW>
+struct DsLds {
+  float red[NW][MT * 16][RT * 16 + 4];
+};
+
 template <typename WT, int RT, int MT, int NW>
-__global__ __launch_bounds__(64 * NW) void k_lora_ds(DsArgs a, bool vec) {
+__device__ void ds_body(const DsArgs& a, int tile, int split, DsLds<RT, MT, NW>& lds) {
   constexpr int T = MT * 16;
-  __shared__ __align__(16) float red[NW][T][RT * 16 + 4];
+  auto& red = lds.red;
+  const bool vec = a.vec;
   Tile t;
-  if (!find_tile(a.q, T, blockIdx.x, t) || t.adapter < 0) return;
+  if (!find_tile(a.q, T, tile, t) || t.adapter < 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  const int c0 = blockIdx.y * a.split_len, c1 = min(a.N, c0 + a.split_len);
+  const int c0 = split * a.split_len, c1 = min(a.N, c0 + a.split_len);
   const WT* B = reinterpret_cast<const WT*>(a.B) + (int64_t)t.adapter * a.N * a.rank;
   const float* prow[MT];
 #pragma unroll
@@ -656,8 +680,8 @@ __global__ __launch_bounds__(64 * NW) void k_lora_ds(DsArgs a, bool vec) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[m][r] = v4f{0, 0, 0, 0};
   Frag8<float> x[MT], nx[MT];
-  WT w[RT][8], nw[RT][8];
-  auto load = [&](int c, Frag8<float>(&fx)[MT], WT(&fw)[RT][8]) {
+  Held<WT> w[RT][8], nw[RT][8];
+  auto load = [&](int c, Frag8<float>(&fx)[MT], Held<WT>(&fw)[RT][8]) {
     const int k = c + 8 * g, valid = c1 - k;
     if (vec && c + kDsStep <= c1) {
 #pragma unroll
@@ -665,7 +689,7 @@ __global__ __launch_bounds__(64 * NW) void k_lora_ds(DsArgs a, bool vec) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) fw[r][e] = B[(int64_t)(k + e) * a.rank + wj[r]];
+        for (int r = 0; r < RT; ++r) fw[r][e].load(B + (int64_t)(k + e) * a.rank + wj[r]);
       return;
     }
 #pragma unroll
@@ -677,8 +701,8 @@ __global__ __launch_bounds__(64 * NW) void k_lora_ds(DsArgs a, bool vec) {
       const WT* row = B + (int64_t)min(k + e, a.N - 1) * a.rank;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const WT v = row[wj[r]];
-        fw[r][e] = e < valid ? v : (WT)0.0f;
+        fw[r][e].load(row + wj[r]);
+        if (e >= valid) fw[r][e].v = 0;
       }
     }
   };
@@ -691,7 +715,7 @@ __global__ __launch_bounds__(64 * NW) void k_lora_ds(DsArgs a, bool vec) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[m][r] = mfma_f32((float)w[r][e], x[m].get(e), acc[m][r]);
+        for (int r = 0; r < RT; ++r) acc[m][r] = mfma_f32(w[r][e].get(), x[m].get(e), acc[m][r]);
 #pragma unroll
     for (int m = 0; m < MT; ++m) x[m] = nx[m];
 #pragma unroll
@@ -708,7 +732,7 @@ __global__ __launch_bounds__(64 * NW) void k_lora_ds(DsArgs a, bool vec) {
   __syncthreads();
   const int ra = rank_of(a.ranks, t.adapter, a.rank);
   const float sc = a.scales ? a.scales[t.adapter] : 1.0f;
-  float* out = a.part + ((int64_t)blockIdx.y * a.q.rows + t.row0) * a.rank;
+  float* out = a.part + ((int64_t)split * a.q.rows + t.row0) * a.rank;
   for (int u = threadIdx.x; u < t.rows * a.rank; u += 64 * NW) {
     const int row = u / a.rank, j = u % a.rank;
     float v = red[0][row][j];
@@ -1021,20 +1045,29 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
   }
 }
 
-// The X side and the dY side in one launch: workgroups [0, x_groups) and the rest.
-template <typename XT, typename WT, int RT, bool DX>
-__global__ __launch_bounds__(kOuterThreads) void k_lora_outer(OuterArgs x, OuterArgs y, int x_groups) {
+// What needs dY alone, in one launch: dS in workgroups [0, ds_groups), dB in the
+// rest. Both wait for memory more than they compute, and what one reads of dY the
+// other finds in the caches.
+template <typename WT, int RT, int MT>
+__global__ __launch_bounds__(kOuterThreads) void k_lora_grad_y(DsArgs d, OuterArgs y, int ds_groups) {
   __shared__ __align__(16) union Lds {
-    OuterLds<XT, RT> x;
+    DsLds<RT, MT, kOuterThreads / 64> d;
     OuterLds<float, RT> y;
     __device__ Lds() {}
   } lds;
   const int id = blockIdx.x;
-  if (id < x_groups)
-    outer_body<XT, WT, RT, DX, true>(x, id % x.chunks, id / x.chunks, lds.x);
+  if (id < ds_groups)
+    ds_body<WT, RT, MT, kOuterThreads / 64>(d, id / d.splits, id % d.splits, lds.d);
   else
-    outer_body<float, WT, RT, false, false>(y, (id - x_groups) % y.chunks, (id - x_groups) / y.chunks,
+    outer_body<float, WT, RT, false, false>(y, (id - ds_groups) % y.chunks, (id - ds_groups) / y.chunks,
                                             lds.y);
+}
+
+// What needs X and dS: dA and dX.
+template <typename XT, typename WT, int RT, bool DX>
+__global__ __launch_bounds__(kOuterThreads) void k_lora_grad_x(OuterArgs x) {
+  __shared__ __align__(16) OuterLds<XT, RT> lds;
+  outer_body<XT, WT, RT, DX, true>(x, blockIdx.x % x.chunks, blockIdx.x / x.chunks, lds);
 }
 
 // ---------------------------------------------------------------- slot sum ----
@@ -1152,52 +1185,54 @@ hipError_t forward_rt(const ForwardArgs& a, hipStream_t s) {
 #undef QL_RUN
 }
 
+bool q_vec(const OuterArgs& o) {
+  return reinterpret_cast<uintptr_t>(o.part) % 16 == 0 && o.rank % 4 == 0;
+}
+
 template <typename WT, int RT>
-hipError_t ds_run(const DsArgs& a, hipStream_t s) {
-  const bool vec = reinterpret_cast<uintptr_t>(a.dY) % 16 == 0 && a.ldy % 4 == 0;
-  constexpr int NW = RT == 8 ? 4 : 8, NS = RT <= 2 ? 16 : 8;
-  if (a.tall)
-    hipLaunchKernelGGL((k_lora_ds<WT, RT, 2, NW>), dim3(max_tiles(a.q, 32), a.splits), dim3(64 * NW),
-                       0, s, a, vec);
+hipError_t grad_y_run(DsArgs d, OuterArgs y, hipStream_t s) {
+  constexpr int MT = RT == 8 ? 1 : 2;  // rows of a tall tile: the waves' sums fit LDS
+  d.vec = reinterpret_cast<uintptr_t>(d.dY) % 16 == 0 && d.ldy % 4 == 0;
+  y.chunks = (y.D + kOuterCols - 1) / kOuterCols;
+  y.q_vec = q_vec(y);
+  const int yg = y.out ? y.chunks * y.splits : 0;
+  const bool tall = d.tall && MT == 2;
+  const int dg = d.part ? max_tiles(d.q, tall ? 32 : 16) * d.splits : 0;
+  if (tall)
+    hipLaunchKernelGGL((k_lora_grad_y<WT, RT, MT>), dim3(dg + yg), dim3(kOuterThreads), 0, s, d, y, dg);
   else
-    hipLaunchKernelGGL((k_lora_ds<WT, RT, 1, NS>), dim3(max_tiles(a.q, 16), a.splits),
-                       dim3(64 * NS), 0, s, a, vec);
+    hipLaunchKernelGGL((k_lora_grad_y<WT, RT, 1>), dim3(dg + yg), dim3(kOuterThreads), 0, s, d, y, dg);
   return hipGetLastError();
 }
 
-template <typename XT, typename WT, int RT, bool DX>
-hipError_t outer_run(OuterArgs x, OuterArgs y, hipStream_t s) {
+template <typename XT, typename WT, int RT>
+hipError_t grad_x_run(OuterArgs x, hipStream_t s) {
   x.chunks = (x.D + kOuterCols - 1) / kOuterCols;
-  y.chunks = (y.D + kOuterCols - 1) / kOuterCols;
-  const int xg = x.out ? x.chunks * x.splits : 0, yg = y.out ? y.chunks * y.splits : 0;
   x.p_vec = reinterpret_cast<uintptr_t>(x.P) % 16 == 0 && (x.ldp * sizeof(XT)) % 16 == 0;
-  auto q_vec = [](const OuterArgs& o) {
-    return reinterpret_cast<uintptr_t>(o.part) % 16 == 0 && o.rank % 4 == 0;
-  };
   x.q_vec = q_vec(x);
-  y.q_vec = q_vec(y);
   x.dx_vec = reinterpret_cast<uintptr_t>(x.dX) % (kOuterU * sizeof(XT)) == 0 && x.lddx % kOuterU == 0;
-  hipLaunchKernelGGL((k_lora_outer<XT, WT, RT, DX>), dim3(xg + yg), dim3(kOuterThreads), 0, s, x, y, xg);
+  const dim3 grid(x.chunks * x.splits), block(kOuterThreads);
+  if (x.dX)
+    hipLaunchKernelGGL((k_lora_grad_x<XT, WT, RT, true>), grid, block, 0, s, x);
+  else
+    hipLaunchKernelGGL((k_lora_grad_x<XT, WT, RT, false>), grid, block, 0, s, x);
   return hipGetLastError();
 }
 
 template <typename XT, typename WT>
-hipError_t outer_rt(const OuterArgs& x, const OuterArgs& y, hipStream_t s) {
-#define QL_OUTER(RT) \
-  (x.dX ? outer_run<XT, WT, RT, true>(x, y, s) : outer_run<XT, WT, RT, false>(x, y, s))
-  if (y.rank <= 16) return QL_OUTER(1);
-  if (y.rank <= 32) return QL_OUTER(2);
-  if (y.rank <= 64) return QL_OUTER(4);
-  return QL_OUTER(8);
-#undef QL_OUTER
+hipError_t grad_x_rt(const OuterArgs& x, hipStream_t s) {
+  if (x.rank <= 16) return grad_x_run<XT, WT, 1>(x, s);
+  if (x.rank <= 32) return grad_x_run<XT, WT, 2>(x, s);
+  if (x.rank <= 64) return grad_x_run<XT, WT, 4>(x, s);
+  return grad_x_run<XT, WT, 8>(x, s);
 }
 
 template <typename WT>
-hipError_t ds_rt(const DsArgs& a, hipStream_t s) {
-  if (a.rank <= 16) return ds_run<WT, 1>(a, s);
-  if (a.rank <= 32) return ds_run<WT, 2>(a, s);
-  if (a.rank <= 64) return ds_run<WT, 4>(a, s);
-  return ds_run<WT, 8>(a, s);
+hipError_t grad_y_rt(const DsArgs& d, const OuterArgs& y, hipStream_t s) {
+  if (y.rank <= 16) return grad_y_run<WT, 1>(d, y, s);
+  if (y.rank <= 32) return grad_y_run<WT, 2>(d, y, s);
+  if (y.rank <= 64) return grad_y_run<WT, 4>(d, y, s);
+  return grad_y_run<WT, 8>(d, y, s);
 }
 
 }  // namespace
@@ -1215,18 +1250,22 @@ int lora_ds_splits(int rows, int n_req, int N) {
   return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
 }
 
-// Row ranges: about kOuterGroups workgroups (three a compute unit), none with
-// fewer than 64 rows. Measured for 256 / 512 / 768 / 1024 of them: fc2 (16384 rows,
-// rank 64, bf16) 281 / 237 / 231 / 230 us, fc1 (2048 rows, rank 16, fp32) 52.6 /
-// 49.1 / 50.1 / 50.1 us.
-constexpr int kOuterGroups = 768;
-int lora_outer_splits(int rows, int K, int N) {
-  const int chunks = (K + kOuterCols - 1) / kOuterCols + (N + kOuterCols - 1) / kOuterCols;
-  int64_t s = (kOuterGroups + chunks - 1) / chunks;
+// Row ranges: about `groups` workgroups, none with fewer than 64 rows.
+#ifndef QL_GX
+#define QL_GX 768
+#endif
+#ifndef QL_GY
+#define QL_GY 256
+#endif
+static int outer_splits(int rows, int D, int groups) {
+  const int chunks = (D + kOuterCols - 1) / kOuterCols;
+  int64_t s = (groups + chunks - 1) / chunks;
   const int64_t cap = (rows + 63) / 64;
   s = s < cap ? s : cap;
   return (int)(s < 1 ? 1 : s);
 }
+int lora_x_splits(int rows, int K) { return outer_splits(rows, K, QL_GX); }
+int lora_y_splits(int rows, int N) { return outer_splits(rows, N, QL_GY); }
 
 int64_t lora_forward_ws(int rows, int n_req, int N, int rank, bool w_bf16) {
   if (!two_launches(rows, N)) return 0;
@@ -1238,13 +1277,13 @@ hipError_t launch_lora_forward(const ForwardArgs& a, hipStream_t s) {
   return a.w_bf16 ? forward_rt<float, bf16>(a, s) : forward_rt<float, float>(a, s);
 }
 
-hipError_t launch_lora_ds(const DsArgs& a, hipStream_t s) {
-  return a.w_bf16 ? ds_rt<bf16>(a, s) : ds_rt<float>(a, s);
+hipError_t launch_lora_grad_y(const DsArgs& d, const OuterArgs& y, hipStream_t s) {
+  return y.w_bf16 ? grad_y_rt<bf16>(d, y, s) : grad_y_rt<float>(d, y, s);
 }
 
-hipError_t launch_lora_outer(const OuterArgs& x, const OuterArgs& y, hipStream_t s) {
-  if (x.p_bf16) return y.w_bf16 ? outer_rt<bf16, bf16>(x, y, s) : outer_rt<bf16, float>(x, y, s);
-  return y.w_bf16 ? outer_rt<float, bf16>(x, y, s) : outer_rt<float, float>(x, y, s);
+hipError_t launch_lora_grad_x(const OuterArgs& x, hipStream_t s) {
+  if (x.p_bf16) return x.w_bf16 ? grad_x_rt<bf16, bf16>(x, s) : grad_x_rt<bf16, float>(x, s);
+  return x.w_bf16 ? grad_x_rt<float, bf16>(x, s) : grad_x_rt<float, float>(x, s);
 }
 
 hipError_t launch_lora_slot_sum(const SlotSumArgs& p, const SlotSumArgs& q, hipStream_t s) {

@@ -33,8 +33,9 @@ struct DsArgs {
   Requests q;
   int N, rank;
   int splits, split_len;  // columns of a split, a multiple of kDsStep
-  float* part;        // [splits][rows][rank]
-  bool w_bf16, tall;
+  float* part;        // [splits][rows][rank]; nullptr: not wanted
+  bool tall;
+  bool vec;           // 16-byte pieces of dY (set by the launch)
 };
 constexpr int kDsStep = 32;
 
@@ -100,11 +101,13 @@ int64_t lora_forward_ws(int rows, int n_req, int N, int rank, bool w_bf16);
 hipError_t launch_lora_forward(const ForwardArgs& a, hipStream_t s);
 bool lora_ds_tall(int rows, int n_req);
 int lora_ds_splits(int rows, int n_req, int N);
-hipError_t launch_lora_ds(const DsArgs& a, hipStream_t s);
-// Row ranges of the outer products over K and N columns.
-int lora_outer_splits(int rows, int K, int N);
-// x: the X side (dA, dX); y: the dY side (dB).
-hipError_t launch_lora_outer(const OuterArgs& x, const OuterArgs& y, hipStream_t s);
+// Row ranges of dA's and dB's sums.
+int lora_x_splits(int rows, int K);
+int lora_y_splits(int rows, int N);
+// dS and dB.
+hipError_t launch_lora_grad_y(const DsArgs& d, const OuterArgs& y, hipStream_t s);
+// dA and dX.
+hipError_t launch_lora_grad_x(const OuterArgs& x, hipStream_t s);
 // The sums of both sides; one without `out` is left out.
 hipError_t launch_lora_slot_sum(const SlotSumArgs& p, const SlotSumArgs& q, hipStream_t s);
 

@@ -92,14 +92,16 @@ int split_len(int D, int splits) {
 // Workspace of the backward call: the partial sums of dS, then the slots of
 // dA and dB and their adapters.
 struct GradWs {
-  int s_splits, splits, slots;
+  int s_splits, x_splits, y_splits, x_slots, y_slots;
   int64_t ds, da, db, aid, bid, total;
 };
 GradWs grad_ws(const ql_lora* d, int32_t M, int32_t n) {
   GradWs w;
   w.s_splits = ql::lora_ds_splits(M, n, d->N);
-  w.splits = ql::lora_outer_splits(M, d->K, d->N);
-  w.slots = w.splits + n - 1;
+  w.x_splits = ql::lora_x_splits(M, d->K);
+  w.y_splits = ql::lora_y_splits(M, d->N);
+  w.x_slots = w.x_splits + n - 1;
+  w.y_slots = w.y_splits + n - 1;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -107,10 +109,10 @@ GradWs grad_ws(const ql_lora* d, int32_t M, int32_t n) {
     return here;
   };
   w.ds = take((int64_t)w.s_splits * M * d->rank * 4);
-  w.da = take((int64_t)w.slots * d->K * d->rank * 4);
-  w.db = take((int64_t)w.slots * d->N * d->rank * 4);
-  w.aid = take((int64_t)w.slots * 4);
-  w.bid = take((int64_t)w.slots * 4);
+  w.da = take((int64_t)w.x_slots * d->K * d->rank * 4);
+  w.db = take((int64_t)w.y_slots * d->N * d->rank * 4);
+  w.aid = take((int64_t)w.x_slots * 4);
+  w.bid = take((int64_t)w.y_slots * 4);
   w.total = at;
   return w;
 }
@@ -282,63 +284,60 @@ ql_status qlinear_lora_grad(const ql_lora* d, const void* X, int64_t ldx, int32_
   char* ws = reinterpret_cast<char*>(workspace);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const bool w_bf16 = d->w_dtype == QL_BF16;
-  const bool x_side = dX || dA;
   ql::OuterArgs x{}, y{};
+  ql::DsArgs a{};
   x.rank = y.rank = d->rank;
   x.w_bf16 = y.w_bf16 = w_bf16;
   x.p_bf16 = d->x_dtype == QL_BF16;
-  if (M > 0 && x_side) {
-    ql::DsArgs a{};
+  if (M > 0) {
+    x.q = y.q = a.q = requests(d, q, M);
+    x.ranks = y.ranks = a.ranks = d->ranks;
+  }
+  if (M > 0 && (dX || dA)) {
     a.dY = dY;
     a.ldy = lddy;
     a.B = d->B;
     a.scales = d->scales;
-    a.ranks = d->ranks;
-    a.q = requests(d, q, M);
     a.N = d->N;
     a.rank = d->rank;
     a.splits = w.s_splits;
     a.split_len = split_len(d->N, w.s_splits);
     a.part = reinterpret_cast<float*>(ws + w.ds);
-    a.w_bf16 = w_bf16;
     a.tall = ql::lora_ds_tall(M, q->n_requests);
-    QL_LAUNCH(ql::launch_lora_ds(a, s), "launching dS");
     x.P = X;
     x.ldp = ldx;
     x.part = a.part;
     x.q_splits = w.s_splits;
     x.A = d->A;
-    x.ranks = d->ranks;
-    x.q = a.q;
     x.D = d->K;
     x.dX = dX;
     x.lddx = lddx;
     x.out = reinterpret_cast<float*>(ws + w.da);
     x.slot_id = reinterpret_cast<int32_t*>(ws + w.aid);
-    x.splits = w.splits;
-    x.row_len = (M + w.splits - 1) / w.splits;
+    x.splits = w.x_splits;
+    x.row_len = (M + w.x_splits - 1) / w.x_splits;
   }
   if (M > 0 && dB) {
     y.P = dY;
     y.ldp = lddy;
     y.part = S;
     y.q_splits = 1;
-    y.ranks = d->ranks;
-    y.q = requests(d, q, M);
     y.D = d->N;
     y.out = reinterpret_cast<float*>(ws + w.db);
     y.slot_id = reinterpret_cast<int32_t*>(ws + w.bid);
-    y.splits = w.splits;
-    y.row_len = (M + w.splits - 1) / w.splits;
+    y.splits = w.y_splits;
+    y.row_len = (M + w.y_splits - 1) / w.y_splits;
   }
-  if (x.out || y.out) QL_LAUNCH(ql::launch_lora_outer(x, y, s), "launching the outer products");
+  if (a.part || y.out) QL_LAUNCH(ql::launch_lora_grad_y(a, y, s), "launching dS and dB");
+  if (x.out) QL_LAUNCH(ql::launch_lora_grad_x(x, s), "launching dA and dX");
   if (dA || dB) {
     ql::SlotSumArgs sa{}, sb{};
     sa.n_adapters = sb.n_adapters = d->n_adapters;
     sa.rank = sb.rank = d->rank;
     sa.ranks = sb.ranks = M > 0 ? d->ranks : nullptr;
     sa.w_bf16 = sb.w_bf16 = w_bf16;
-    sa.slots = sb.slots = M > 0 ? w.slots : 0;
+    sa.slots = M > 0 ? w.x_slots : 0;
+    sb.slots = M > 0 ? w.y_slots : 0;
     sa.part = x.out;
     sa.slot_id = x.slot_id;
     sa.D = d->K;
