@@ -753,7 +753,10 @@ __device__ void ds_body(const DsArgs& a, int tile, int split, DsLds<RT, MT, NW>&
 // (ds_read_b64_tr_b16: lane c of 16 gets four rows of column c). fp32 P takes
 // the fp32 instructions, element by element from memory: lanes side by side
 // have addresses side by side.
-constexpr int kOuterRows = 32, kOuterThreads = 512;
+#ifndef QL_OT
+#define QL_OT 512
+#endif
+constexpr int kOuterRows = 32, kOuterThreads = QL_OT;
 constexpr int kOuterU = 2;  // 16-column tiles of a wave
 constexpr int kOuterCols = kOuterThreads / 64 * 16 * kOuterU;
 
@@ -768,29 +771,33 @@ __device__ __forceinline__ v8h read_transposed(const bf16* tile, int ld, int r16
   return __builtin_bit_cast(v8h, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-template <typename XT, int RT>
+template <typename PT, typename WT, int RT, bool DX>
 struct OuterLds {
   static constexpr int R = RT * 16;
-  static constexpr int XLD = kOuterCols + 8, QLD = R + 8;
-  static constexpr int kPlanes = RT == 1 ? 4 : 3;
+  static constexpr int XLD = kOuterCols + 8, QLD = R + 8, FLD = R + 16;
+  static constexpr bool PB = sizeof(PT) == 2;        // bf16 products for Q^T P
+  static constexpr bool XB = DX && sizeof(WT) == 2;  // bf16 products for dX
+  // Terms of Q: all three (24 bits) where the result is fp32, two (16 bits) where
+  // it is rounded to bf16's 8.
+  static constexpr int kTermsA = PB ? (sizeof(WT) == 2 ? 2 : 3) : 0;
+  static constexpr int kTermsX = XB ? (sizeof(PT) == 2 ? 2 : 3) : 0;
+  static constexpr int kTerms = kTermsA > kTermsX ? kTermsA : kTermsX;
+  static constexpr bool kFloat = !PB || (DX && !XB);  // fp32 products read Q itself
+  static constexpr int kPlanes = RT == 1 && kTermsX == 3 ? 4 : kTerms;
   struct Tile {
-    float q[kOuterRows][R + 4];
-    bf16 x[sizeof(XT) == 2 ? kOuterRows : 1][XLD];
-    bf16 h[kPlanes][kOuterRows][QLD];  // the terms of q (a fourth one of zeros for R = 16)
+    float q[kFloat ? kOuterRows : 1][FLD];
+    bf16 x[PB ? kOuterRows : 1][XLD];
+    bf16 h[kPlanes ? kPlanes : 1][kPlanes ? kOuterRows : 1][QLD];  // (a fourth one of zeros)
   };
   Tile tile[2];  // one is used while the next is written
 };
 
 template <typename PT, typename WT, int RT, bool DX, bool TR>
-__device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, RT>& lds) {
-  constexpr int R = RT * 16, U = kOuterU;
-  constexpr bool PB = sizeof(PT) == 2;        // bf16 products for Q^T P
-  constexpr bool XB = DX && sizeof(WT) == 2;  // bf16 products for dX
-  // Terms of Q: all three (24 bits) where the result is fp32, two (16 bits) where
-  // it is rounded to bf16's 8.
-  constexpr int kTermsA = PB ? (sizeof(WT) == 2 ? 2 : 3) : 0;
-  constexpr int kTermsX = XB ? (sizeof(PT) == 2 ? 2 : 3) : 0;
-  constexpr int t_xld = OuterLds<PT, RT>::XLD, t_qld = OuterLds<PT, RT>::QLD;
+__device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, WT, RT, DX>& lds) {
+  typedef OuterLds<PT, WT, RT, DX> L;
+  constexpr int R = RT * 16, U = kOuterU, kTermsA = L::kTermsA, kTermsX = L::kTermsX;
+  constexpr bool PB = L::PB, XB = L::XB;
+  constexpr int t_xld = L::XLD, t_qld = L::QLD, t_fld = L::FLD;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   const int dw = chunk * kOuterCols, d0 = dw + wave * 16 * U;  // the workgroup's, the wave's columns
   const int lo = min(sp * a.row_len, a.q.rows), hi = min(lo + a.row_len, a.q.rows);
@@ -883,7 +890,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
       };
       // Puts the fetched tile into LDS (and, for fp32 P, into pc).
       float pc[PB ? 1 : 8][PB ? 1 : U];
-      auto put = [&](int m0, typename OuterLds<PT, RT>::Tile& t) {
+      auto put = [&](int m0, typename L::Tile& t) {
         float qz[QN];
 #pragma unroll
         for (int k = 0; k < QN; ++k) qz[k] = qr[k / QW][k % QW];
@@ -896,7 +903,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
 #pragma unroll
         for (int k = 0; k < QN; ++k)
           if (m0 + qm >= r1 || qj + k >= ra) qz[k] = 0.0f;
-        if constexpr (!PB || (DX && !XB)) {
+        if constexpr (L::kFloat) {
 #pragma unroll
           for (int k = 0; k < QN; ++k) t.q[qm][qj + k] = qz[k];
         }
@@ -916,7 +923,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
             }
             *reinterpret_cast<vt*>(&t.h[0][qm][qj + c * W]) = h;
             *reinterpret_cast<vt*>(&t.h[1][qm][qj + c * W]) = mi;
-            if constexpr (kTermsA == 3 || kTermsX == 3)
+            if constexpr (L::kTerms == 3)
               *reinterpret_cast<vt*>(&t.h[2][qm][qj + c * W]) = l;
             if constexpr (RT == 1 && kTermsX == 3) *reinterpret_cast<vt*>(&t.h[3][qm][qj]) = vt(0.0f);
           }
@@ -988,7 +995,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
               }
             } else {
               SFrag<WT, RT, 1> sf;
-              sf.load(&t.q[m * 16][0], R + 4, r16, g);
+              sf.load(&t.q[m * 16][0], t_fld, r16, g);
 #pragma unroll
               for (int u = 0; u < U; ++u) y[u] = af[u].times(sf, 0);
             }
@@ -1045,28 +1052,28 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, R
   }
 }
 
-// What needs dY alone, in one launch: dS in workgroups [0, ds_groups), dB in the
-// rest. Both wait for memory more than they compute, and what one reads of dY the
+// What needs dY alone, in one launch: dB in workgroups [0, y_groups), which run
+// longest, dS in the rest. Both wait for memory more than they compute, and what one reads of dY the
 // other finds in the caches.
 template <typename WT, int RT, int MT>
-__global__ __launch_bounds__(kOuterThreads) void k_lora_grad_y(DsArgs d, OuterArgs y, int ds_groups) {
+__global__ __launch_bounds__(kOuterThreads) void k_lora_grad_y(DsArgs d, OuterArgs y, int y_groups) {
   __shared__ __align__(16) union Lds {
     DsLds<RT, MT, kOuterThreads / 64> d;
-    OuterLds<float, RT> y;
+    OuterLds<float, WT, RT, false> y;
     __device__ Lds() {}
   } lds;
   const int id = blockIdx.x;
-  if (id < ds_groups)
-    ds_body<WT, RT, MT, kOuterThreads / 64>(d, id / d.splits, id % d.splits, lds.d);
+  if (id < y_groups)
+    outer_body<float, WT, RT, false, false>(y, id % y.chunks, id / y.chunks, lds.y);
   else
-    outer_body<float, WT, RT, false, false>(y, (id - ds_groups) % y.chunks, (id - ds_groups) / y.chunks,
-                                            lds.y);
+    ds_body<WT, RT, MT, kOuterThreads / 64>(d, (id - y_groups) / d.splits, (id - y_groups) % d.splits,
+                                            lds.d);
 }
 
 // What needs X and dS: dA and dX.
 template <typename XT, typename WT, int RT, bool DX>
 __global__ __launch_bounds__(kOuterThreads) void k_lora_grad_x(OuterArgs x) {
-  __shared__ __align__(16) OuterLds<XT, RT> lds;
+  __shared__ __align__(16) OuterLds<XT, WT, RT, DX> lds;
   outer_body<XT, WT, RT, DX, true>(x, blockIdx.x % x.chunks, blockIdx.x / x.chunks, lds);
 }
 
@@ -1199,9 +1206,9 @@ hipError_t grad_y_run(DsArgs d, OuterArgs y, hipStream_t s) {
   const bool tall = d.tall && MT == 2;
   const int dg = d.part ? max_tiles(d.q, tall ? 32 : 16) * d.splits : 0;
   if (tall)
-    hipLaunchKernelGGL((k_lora_grad_y<WT, RT, MT>), dim3(dg + yg), dim3(kOuterThreads), 0, s, d, y, dg);
+    hipLaunchKernelGGL((k_lora_grad_y<WT, RT, MT>), dim3(dg + yg), dim3(kOuterThreads), 0, s, d, y, yg);
   else
-    hipLaunchKernelGGL((k_lora_grad_y<WT, RT, 1>), dim3(dg + yg), dim3(kOuterThreads), 0, s, d, y, dg);
+    hipLaunchKernelGGL((k_lora_grad_y<WT, RT, 1>), dim3(dg + yg), dim3(kOuterThreads), 0, s, d, y, yg);
   return hipGetLastError();
 }
 
