@@ -710,12 +710,41 @@ __device__ void ds_body(const DsArgs& a, int tile, int split, DsLds<RT, MT, NW>&
   if (c < c1) load(c, x, w);
   for (; c < c1; c += NW * kDsStep) {
     if (c + NW * kDsStep < c1) load(c + NW * kDsStep, nx, nw);
+    if constexpr (sizeof(WT) == 2) {  // dY in three bf16 terms, B as it is
+      v8h wf[RT];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+      for (int r = 0; r < RT; ++r) {
+        uint32_t u[4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int e = 0; e < 4; ++e) u[e] = w[r][2 * e].v | (w[r][2 * e + 1].v << 16);
+        __builtin_memcpy(&wf[r], u, 16);
+      }
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[m][r] = mfma_f32(w[r][e].get(), x[m].get(e), acc[m][r]);
+      for (int m = 0; m < MT; ++m) {
+        v8h h, mi, l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          bf16 p, q, o;
+          split3(x[m].get(e), p, q, o);
+          h[e] = p;
+          mi[e] = q;
+          l[e] = o;
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          acc[m][r] = mfma_bf16(wf[r], h, acc[m][r]);
+          acc[m][r] = mfma_bf16(wf[r], mi, acc[m][r]);
+          acc[m][r] = mfma_bf16(wf[r], l, acc[m][r]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[m][r] = mfma_f32(w[r][e].get(), x[m].get(e), acc[m][r]);
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m) x[m] = nx[m];
 #pragma unroll
@@ -753,10 +782,7 @@ __device__ void ds_body(const DsArgs& a, int tile, int split, DsLds<RT, MT, NW>&
 // (ds_read_b64_tr_b16: lane c of 16 gets four rows of column c). fp32 P takes
 // the fp32 instructions, element by element from memory: lanes side by side
 // have addresses side by side.
-#ifndef QL_OT
-#define QL_OT 512
-#endif
-constexpr int kOuterRows = 32, kOuterThreads = QL_OT;
+constexpr int kOuterRows = 32, kOuterThreads = 512;
 constexpr int kOuterU = 2;  // 16-column tiles of a wave
 constexpr int kOuterCols = kOuterThreads / 64 * 16 * kOuterU;
 
