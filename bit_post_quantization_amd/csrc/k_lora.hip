@@ -801,14 +801,15 @@ template <typename PT, typename WT, int RT, bool DX>
 struct OuterLds {
   static constexpr int R = RT * 16;
   static constexpr int XLD = kOuterCols + 8, QLD = R + 8, FLD = R + 16;
-  static constexpr bool PB = sizeof(PT) == 2;        // bf16 products for Q^T P
+  static constexpr bool PB = sizeof(PT) == 2;  // bf16 products for Q^T P, P through LDS
+  static constexpr bool PS = !PB && sizeof(WT) == 2;  // the same, fp32 P split in registers
   static constexpr bool XB = DX && sizeof(WT) == 2;  // bf16 products for dX
   // Terms of Q: all three (24 bits) where the result is fp32, two (16 bits) where
   // it is rounded to bf16's 8.
-  static constexpr int kTermsA = PB ? (sizeof(WT) == 2 ? 2 : 3) : 0;
+  static constexpr int kTermsA = PB || PS ? (sizeof(WT) == 2 ? 2 : 3) : 0;
   static constexpr int kTermsX = XB ? (sizeof(PT) == 2 ? 2 : 3) : 0;
   static constexpr int kTerms = kTermsA > kTermsX ? kTermsA : kTermsX;
-  static constexpr bool kFloat = !PB || (DX && !XB);  // fp32 products read Q itself
+  static constexpr bool kFloat = (!PB && !PS) || (DX && !XB);  // fp32 products read Q itself
   static constexpr int kPlanes = RT == 1 && kTermsX == 3 ? 4 : kTerms;
   struct Tile {
     float q[kFloat ? kOuterRows : 1][FLD];
@@ -822,7 +823,7 @@ template <typename PT, typename WT, int RT, bool DX, bool TR>
 __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, WT, RT, DX>& lds) {
   typedef OuterLds<PT, WT, RT, DX> L;
   constexpr int R = RT * 16, U = kOuterU, kTermsA = L::kTermsA, kTermsX = L::kTermsX;
-  constexpr bool PB = L::PB, XB = L::XB;
+  constexpr bool PB = L::PB, PS = L::PS, XB = L::XB;
   constexpr int t_xld = L::XLD, t_qld = L::QLD, t_fld = L::FLD;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
   const int dw = chunk * kOuterCols, d0 = dw + wave * 16 * U;  // the workgroup's, the wave's columns
@@ -853,6 +854,8 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
   int af_of = -1;
   bool pending = false;
   const auto col = [&](int u) { return U * r16 + u; };
+  // Row of element k of a lane: split P's must be those of read_transposed.
+  const auto p_row = [&](int k) { return PS ? (k < 4 ? 4 * g + k : 12 + 4 * g + k) : 4 * k + g; };
   for (int i = first; i <= last; ++i) {
     const int b = clampi(a.q.off[i], 0, a.q.rows), e = clampi(a.q.off[i + 1], b, a.q.rows);
     const int r0 = max(b, lo), r1 = min(e, hi);
@@ -908,7 +911,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
         } else {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            const PT* p = P + (int64_t)min(m0 + kk * 4 + g, r1 - 1) * a.ldp;
+            const PT* p = P + (int64_t)min(m0 + p_row(kk), r1 - 1) * a.ldp;
 #pragma unroll
             for (int u = 0; u < U; ++u) pr[kk][u] = p[min(d0 + 16 * u + r16, a.D - 1)];
           }
@@ -933,7 +936,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
 #pragma unroll
           for (int k = 0; k < QN; ++k) t.q[qm][qj + k] = qz[k];
         }
-        if constexpr (PB || XB) {
+        if constexpr (L::kTerms > 0) {
           typedef bf16 vt __attribute__((ext_vector_type(QN < 8 ? QN : 8)));
           constexpr int W = QN < 8 ? QN : 8;
 #pragma unroll
@@ -966,7 +969,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
           for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
             for (int u = 0; u < U; ++u)
-              pc[kk][u] = m0 + kk * 4 + g < r1 && d0 + 16 * u + r16 < a.D ? (float)pr[kk][u] : 0.0f;
+              pc[kk][u] = m0 + p_row(kk) < r1 && d0 + 16 * u + r16 < a.D ? (float)pr[kk][u] : 0.0f;
         }
       };
       __syncthreads();  // the last piece's tiles have been read
@@ -990,6 +993,31 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
 #pragma unroll
               for (int u = 0; u < U; ++u) acc[r][u] = mfma_bf16(qt, xt[u], acc[r][u]);
             }
+        } else if constexpr (PS) {
+          v8h ph[U], pm[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              bf16 h, m, l;
+              split3(pc[k][u], h, m, l);
+              ph[u][k] = h;
+              pm[u][k] = m;
+            }
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const v8h qh = read_transposed(&t.h[0][0][16 * r], t_qld, r16, g);
+            const v8h qm = read_transposed(&t.h[1][0][16 * r], t_qld, r16, g);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              auto add = [&](const v8h& q, const v8h& p) {
+                acc[r][u] = TR ? mfma_bf16(q, p, acc[r][u]) : mfma_bf16(p, q, acc[r][u]);
+              };
+              add(qh, ph[u]);
+              add(qm, ph[u]);
+              add(qh, pm[u]);
+            }
+          }
         } else {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
