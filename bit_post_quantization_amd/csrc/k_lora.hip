@@ -46,8 +46,9 @@ __device__ bool find_tile(const Requests& q, int T, int t, Tile& out) {
   int done = 0;
   for (int base = 0; base < q.n; base += kWave) {
     const int i = base + lane;
-    int b = 0, e = 0;
+    int b = 0, e = 0, id = -1;
     if (i < q.n) {
+      id = q.ids[i];  // of every request looked at: one trip to memory, not two
       b = clampi(q.off[i], 0, q.rows);
       e = clampi(q.off[i + 1], b, q.rows);
     }
@@ -61,8 +62,8 @@ __device__ bool find_tile(const Requests& q, int T, int t, Tile& out) {
       const int re = __builtin_amdgcn_readlane(e, src);
       out.row0 = rb + (t - first) * T;
       out.rows = min(T, re - out.row0);
-      const int id = q.ids[base + src];
-      out.adapter = __builtin_amdgcn_readfirstlane(id >= 0 && id < q.n_adapters ? id : -1);
+      id = __builtin_amdgcn_readlane(id, src);
+      out.adapter = id >= 0 && id < q.n_adapters ? id : -1;
       return true;
     }
     done += total;
@@ -863,13 +864,6 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
     const int ad = id >= 0 && id < a.q.n_adapters ? id : -1;
     if (r0 < r1 && ad >= 0) {
       const int ra = rank_of(a.ranks, ad, a.rank);
-      if (DX && af_of != ad) {
-        af_of = ad;
-        const WT* A = reinterpret_cast<const WT*>(a.A) + (int64_t)ad * a.rank * a.D;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          af[u].load_column(A + min(d0 + col(u), a.D - 1), a.D, ra, g);
-      }
       // this thread's part of a tile: Q values and, for bf16 P, 16-byte pieces of P
       // Addresses are clamped into the piece and what lies past it is zeroed when
       // the tile is used: the loads wait for nothing and nothing waits for them.
@@ -974,6 +968,13 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
       };
       __syncthreads();  // the last piece's tiles have been read
       fetch(r0);
+      if (DX && af_of != ad) {
+        af_of = ad;
+        const WT* A = reinterpret_cast<const WT*>(a.A) + (int64_t)ad * a.rank * a.D;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          af[u].load_column(A + min(d0 + col(u), a.D - 1), a.D, ra, g);
+      }
       put(r0, lds.tile[0]);
       fetch(r0 + kOuterRows);
       int cur = 0;
