@@ -25,7 +25,8 @@ namespace {
 
 typedef __bf16 bf16;
 constexpr int kNormThreads = 512;
-constexpr int kSlabVectors = 12;  // vectors of a slab that a thread holds at most
+// Vectors of a slab that a thread holds at most: 192 bytes, 48 vectors.
+constexpr int slab_most(int bytes) { return 192 / bytes < 48 ? 192 / bytes : 48; }
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <typename T, int V>
@@ -748,13 +749,13 @@ hipError_t norm_grad_run(const NormArgs& a, hipStream_t st) {
 }
 
 // Vectors a thread holds when one workgroup takes a slab, 0 where it does not fit.
-template <int V>
+template <typename T, int V>
 int slab_vectors(const NormArgs& a) {
   const int cpg = a.C / a.G;
   if (cpg % V != 0 || cpg / V > kNormThreads || a.B == 0 || a.L == 0) return 0;
   const int ty = kNormThreads / (cpg / V);
   const int64_t nv = ((int64_t)a.L + ty - 1) / ty;
-  return nv <= kSlabVectors ? (int)nv : 0;
+  return nv <= slab_most(V * (int)sizeof(T)) ? (int)nv : 0;
 }
 
 template <typename T, typename W, int V, int NV>
@@ -807,11 +808,16 @@ hipError_t slab_run(const NormArgs& a, bool grad, hipStream_t st) {
 
 template <typename T, typename W, int V>
 hipError_t norm_width(const NormArgs& a, bool slabs, bool grad, hipStream_t st) {
-  const int nv = slabs ? slab_vectors<V>(a) : 0;
+  const int nv = slabs ? slab_vectors<T, V>(a) : 0;
   if (nv > 0) {
+    constexpr int most = slab_most(V * (int)sizeof(T));
     if (nv <= 3) return slab_run<T, W, V, 3>(a, grad, st);
     if (nv <= 6) return slab_run<T, W, V, 6>(a, grad, st);
-    return slab_run<T, W, V, kSlabVectors>(a, grad, st);
+    if (nv <= 12) return slab_run<T, W, V, 12>(a, grad, st);
+    if constexpr (most >= 24) {
+      if (nv <= 24) return slab_run<T, W, V, 24>(a, grad, st);
+    }
+    if constexpr (most >= 48) return slab_run<T, W, V, 48>(a, grad, st);
   }
   return grad ? norm_grad_run<T, W, V>(a, st) : norm_run<T, W, V>(a, st);
 }
@@ -825,13 +831,21 @@ hipError_t norm_dispatch(const NormArgs& a, bool grad, hipStream_t st) {
            rows_aligned(a.y, a.yb, a.yr, es, bytes) &&
            (!grad || rows_aligned(a.dy, a.dyb, a.dyr, es, bytes));
   };
-  // A slab's rows have cpg channels: the widest vector that divides them.
-  if (aligned(16) && slab_vectors<V>(a)) return norm_width<T, W, V>(a, true, grad, st);
-  if (aligned(8) && cpg % (V / 2) == 0 && slab_vectors<V / 2>(a))
+  // A slab's rows have cpg channels: the widest vector that divides them. Narrow
+  // vectors cost the load path more, so with them only tensors of up to 24 MiB go
+  // by slabs. Measured, slabs / two readings: 8x2048x640 bf16 (8-byte vectors, 21 MB)
+  // 18.0 / 29.4 us; 16x1024x320 bf16 (4 bytes, 10 MB) 13.8 / 23.9; 16x4096x320 bf16
+  // (4 bytes, 42 MB) 50.8 / 37.5; 2x500x224 bf16 (2 bytes, 0.4 MB) 12.9 / 17.9;
+  // gradients of 2x500x224 bf16 15.3 / 23.7 and of 16x2048x320 fp32 (8 bytes, 42 MB)
+  // 52.1 / 44.3.
+  const bool small = (int64_t)a.B * a.L * a.C * es <= 24 << 20;
+  if (aligned(16) && slab_vectors<T, V>(a)) return norm_width<T, W, V>(a, true, grad, st);
+  if (small && aligned(8) && cpg % (V / 2) == 0 && slab_vectors<T, V / 2>(a))
     return norm_width<T, W, V / 2>(a, true, grad, st);
-  if (V == 8 && aligned(4) && slab_vectors<2>(a)) return norm_width<T, W, 2>(a, true, grad, st);
+  if (small && V == 8 && aligned(4) && slab_vectors<T, 2>(a))
+    return norm_width<T, W, 2>(a, true, grad, st);
+  if (small && slab_vectors<T, 1>(a)) return norm_width<T, W, 1>(a, true, grad, st);
   if (aligned(16)) return norm_width<T, W, V>(a, false, grad, st);
-  if (slab_vectors<1>(a)) return norm_width<T, W, 1>(a, true, grad, st);
   return norm_width<T, W, 1>(a, false, grad, st);
 }
 
