@@ -52,6 +52,13 @@ __device__ __forceinline__ void widen(const typename Vec<T, V>::type& x, float (
   }
 }
 template <typename T, int V>
+__device__ __forceinline__ void put_v(typename Vec<T, V>::type& x, int i, float v) {
+  if constexpr (V == 1)
+    x = (T)v;
+  else
+    x[i] = (T)v;
+}
+template <typename T, int V>
 __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
   if constexpr (V == 1) {
     p[0] = (T)v[0];
@@ -585,6 +592,9 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_slab(SlabK a) {
 
 template <typename T, typename W, int V, int NV, bool SILU>
 __global__ __launch_bounds__(kNormThreads) void k_norm_slab_grad(SlabK a) {
+  // With few workgroups arithmetic is what bounds this (a SiLU's gradient for every
+  // value, twice): fp32 registers take xhat and dz gamma in place of x and dy.
+  constexpr bool kKeep = sizeof(T) == 4;
   __shared__ float2 red[kNormThreads / 64];
   __shared__ float2 sums[kNormThreads * V];  // [ty][channel of the group]
   int b, g;
@@ -618,6 +628,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_slab_grad(SlabK a) {
         const float dz = grad_z<SILU>(e[i], d[i], m, r, f.ga[i], f.be[i], xh);
         p[i] += dz;
         q[i] = __builtin_fmaf(dz, xh, q[i]);
+        if constexpr (kKeep) put_v<T, V>(xv[k], i, xh), put_v<T, V>(dv[k], i, dz * f.ga[i]);
       }
     }
   float u1 = 0.0f, u2 = 0.0f;
@@ -630,9 +641,26 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_slab_grad(SlabK a) {
   const double2 t = slab_sum2(u1, u2, red);  // its barriers publish `sums` too
   const double n = (double)a.L * a.cpg;
   const float s1 = (float)(t.x / n), s2 = (float)(t.y / n);
+  // A channel's sums in two rounds where there are threads for it: `parts` threads
+  // a channel, then one.
+  const int parts = max(1, min((int)blockDim.x / a.cpg, 8));
+  int rows = a.ty;
+  if (parts > 1) {
+    const int part = threadIdx.x / a.cpg, pc = threadIdx.x % a.cpg, len = (a.ty + parts - 1) / parts;
+    float2 t{0.0f, 0.0f};
+    if (part < parts)
+      for (int y = part * len; y < min((part + 1) * len, a.ty); ++y) {
+        t.x += sums[y * a.cpg + pc].x;
+        t.y += sums[y * a.cpg + pc].y;
+      }
+    __syncthreads();
+    if (part < parts) sums[part * a.cpg + pc] = t;
+    __syncthreads();
+    rows = parts;
+  }
   for (int ch = threadIdx.x; ch < a.cpg; ch += blockDim.x) {
     float P = 0.0f, Q = 0.0f;
-    for (int y = 0; y < a.ty; ++y) {
+    for (int y = 0; y < rows; ++y) {
       P += sums[y * a.cpg + ch].x;
       Q += sums[y * a.cpg + ch].y;
     }
@@ -653,9 +681,9 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_slab_grad(SlabK a) {
     widen<T, V>(dv[k], d);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float xh;
-      const float dz = grad_z<SILU>(e[i], d[i], m, r, f.ga[i], f.be[i], xh);
-      e[i] = r * (dz * f.ga[i] - s1 - xh * s2);
+      float xh = e[i], t = d[i];
+      if constexpr (!kKeep) t = grad_z<SILU>(e[i], d[i], m, r, f.ga[i], f.be[i], xh) * f.ga[i];
+      e[i] = r * (t - s1 - xh * s2);
     }
     store_v<T, V>(dx + (int64_t)l * a.yr, e);
   }
