@@ -1,17 +1,32 @@
 // Low-rank adapters of many requests beside one shared projection.
 //
-//   forward   S = X A_a^T            (k_lora_shrink)
-//             Y = base + scale_a S B_a^T           (k_lora_expand)
-//   backward  dS = scale_a dY B_a    (k_lora_shrink)
-//             dX = dS A_a, dA_a = dS^T X           (k_lora_outer, one reading of X)
-//             dB_a = scale_a dY^T S  (k_lora_outer)
-//             sums over row ranges   (k_lora_slot_sum)
+//   forward   S = X A_a^T,  Y = base + scale_a S B_a^T
+//             small outputs: k_lora_forward; large ones: k_lora_s, k_lora_expand
+//   backward  dS = scale_a dY B_a and dB_a = scale_a dY^T S    (k_lora_grad_y)
+//             dX = dS A_a and dA_a = dS^T X                    (k_lora_grad_x)
+//             dA, dB summed over the row ranges                (k_lora_slot_sum)
 //
-// A tile of rows never spans two requests, so it has one adapter; each
-// workgroup finds its tile from the request offsets by one scan over them.
-// Products run on the matrix cores in fp32 (v_mfma_f32_16x16x4_f32: bf16
-// inputs are widened exactly), sums are fp32 and no atomics are used, so a
-// call gives the same bits every time.
+// All of it is bound by memory: a rank of 64 makes 2 r = 128 operations an element
+// of base that is read and written, far below what the matrix cores do in that
+// time. So what the kernels are built for is one reading of every large operand,
+// loads that run ahead, and addresses in an order that memory likes.
+//
+// A tile of rows never spans two requests, so it has one adapter; each workgroup
+// finds its tile from the request offsets by one scan over them. Sums are fp32, with
+// no atomics and in a fixed order, so a call gives the same bits every time.
+//
+// Products: where both operands are bf16, v_mfma_f32_16x16x32_bf16. An fp32 operand
+// beside a bf16 one is split into bf16 terms (v = h + m + l holds fp32's 24 bits):
+// three terms where the result stays fp32, two (16 bits) where the result is rounded
+// to bf16's 8 anyway. Where both are fp32, v_mfma_f32_16x16x4_f32.
+//
+// Measured per call (MI355X; what a copy of the same bytes would take in brackets):
+//   8 rows, K 1152, N 6912, rank 16, bf16, 8 adapters: 6.4 us of kernel, 7.7 us a call
+//   1003 rows of 23 requests, N 1001, rank 12: 11.5 us
+//   guided 4096 rows, K 1152, N 4608, rank 16, fp32: 24.4 us (17)
+//   16384 rows, K 2048, N 8192, rank 64, bf16: 239 us, 4.8 TB/s (212)
+//   gradients of 2048 rows, K 1152, N 4608, rank 16, fp32: 38.7 us (11)
+//   gradients of 16384 rows, K 4608, N 1152, rank 64, bf16: 177 us (72)
 #include "ql_device.h"
 #include "ql_ops.h"
 
@@ -112,13 +127,11 @@ __device__ __forceinline__ v4f mfma_f32(float a, float b, v4f c) {
 // One workgroup: a tile of MT * 16 rows (of both halves when guided) and a
 // share of the output columns. First the tile's S = X A^T, the waves taking
 // every NW-th chunk of K and joining their sums in LDS; then the waves stream
-// 32 columns at a time: base in, base + S B^T out. S never leaves the
-// workgroup, so nothing is put through memory between the two products; the
-// workgroups that share a tile each compute its S.
+// 64 columns at a time: base in, base + S B^T out.
 //
-// With bf16 adapters the second product runs on bf16 matrix instructions: S is
-// split into three bf16 terms whose sum is S to 24 bits, so that no digit of
-// fp32 is given up (B is bf16 already), at a fifth of the fp32 rate's cost.
+// With bf16 adapters the second product takes S in three bf16 terms (24 bits: Y is
+// fp32): 6 matrix instructions of 16 cycles for 16x16 outputs at rank 64, where the
+// fp32 instructions would take 512 cycles.
 
 __device__ __forceinline__ v4f mfma_bf16(v8h a, v8h b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -290,7 +303,8 @@ struct BFrag<bf16, RT> {
 
 // A wave's output block: MT * 16 rows times 64 columns, four products side by
 // side. Neighbouring lanes have neighbouring addresses, which the load path
-// needs (it takes 64 bytes of neighbouring lanes at a time, else 16): with VEC
+// needs (it takes 64 bytes of neighbouring lanes at a time, else 16: with rows side
+// by side in the lanes instead, 16384 x 8192 at rank 64 took 299 us, now 207): with VEC
 // product u has columns 4 (lane % 16) + u, so a lane ends up with four columns
 // in a row of each of its four rows 4 g + i; without, columns 16 u + lane % 16
 // and single elements.
@@ -495,7 +509,9 @@ __device__ void tile_s(const ForwardArgs& a, const Tile& t, int ra, float sc, bo
 }
 
 // All in one: right for calls so small that a second launch costs more than
-// computing S again in the workgroups that share a tile.
+// computing S again in the workgroups that share a tile. What bounds it is latency:
+// about four trips to memory one after another (offsets, X and A, base and B, Y),
+// 6.4 us for 8 rows, most of the host's time for the call.
 template <typename XT, typename WT, int RT, int MT, int H, int NW, bool YVEC>
 __global__ __launch_bounds__(64 * NW) void k_lora_forward(ForwardArgs a, bool xvec, bool bvec) {
   constexpr int T = MT * 16, LD = RT * 16 + 4;
@@ -635,6 +651,8 @@ __global__ __launch_bounds__(256) void k_lora_expand(ForwardArgs a, bool bvec, c
 // waves take every NW-th 32 columns, the next step's loads ahead of this one's
 // products, and join their sums in LDS. Lane l of a step has columns
 // 8 (l / 16) .. + 7 of row l % 16 of dY, and rank l % 16 of the same rows of B.
+// With bf16 B, dY goes in three bf16 terms: 16384 x 1152 at rank 64 with dB beside it
+// took 88 us with fp32 instructions, 71 so.
 //
 // A single element of B as it is held until its use: bf16 in a register of its own
 // (loads into register halves would wait for one another).
@@ -774,15 +792,22 @@ __device__ void ds_body(const DsArgs& a, int tile, int split, DsLds<RT, MT, NW>&
 
 // ------------------------------------------------------------------- outer ----
 // dA_a = dS^T X with dX = dS A_a on the way (one reading of X), and dB_a = dY^T S.
-// One workgroup: 64 U columns (16 U a wave) of one range of rows, 32 rows at a
-// time. Q (dS or S, rank values a row) goes through LDS; piece by piece (the
-// rows of one request in the range) Q^T P is summed in registers and written to
-// a slot of its own, and A's columns stay in registers for the whole range.
+// One workgroup: 256 columns (32 a wave) of one range of rows, 32 rows at a time.
+// Q (dS or S, rank values a row) goes through LDS, double-buffered; piece by piece
+// (the rows of one request in the range) Q^T P is summed in registers and written to
+// a slot of its own, and A's columns stay in registers for the whole range. Long
+// ranges keep the slots few: they are written and read once more, D * rank * 4 bytes
+// each.
 //
-// bf16 X takes bf16 matrix instructions, with Q in bf16 terms that sum to it; both operands of dA are read from LDS transposed
-// (ds_read_b64_tr_b16: lane c of 16 gets four rows of column c). fp32 P takes
-// the fp32 instructions, element by element from memory: lanes side by side
-// have addresses side by side.
+// bf16 P (or bf16 results) take bf16 matrix instructions, whose operands run along
+// the rows: LDS is read transposed (ds_read_b64_tr_b16: lane c of 16 gets four rows
+// of column c). fp32 P comes element by element from memory, lanes side by side at
+// addresses side by side: split in registers for bf16 results, as it is for fp32.
+//
+// Measured at 16384 rows, K 4608, rank 64, bf16: 112 us for 302 MB of X and dX and 58
+// MB of slots, 3.2 TB/s; bound by the rows' latency between barriers (matrix cores
+// 15 %, LDS 15 % busy). Four waves of 64 columns instead of eight of 32: 268 instead
+// of 231 us for the whole gradient; 256 threads and 128 columns: 260 instead of 200.
 constexpr int kOuterRows = 32, kOuterThreads = 512;
 constexpr int kOuterU = 2;  // 16-column tiles of a wave
 constexpr int kOuterCols = kOuterThreads / 64 * 16 * kOuterU;
@@ -1108,8 +1133,9 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
 }
 
 // What needs dY alone, in one launch: dB in workgroups [0, y_groups), which run
-// longest, dS in the rest. Both wait for memory more than they compute, and what one reads of dY the
-// other finds in the caches.
+// longest, dS in the rest. Both wait for memory more than they compute, and what one
+// reads of dY the other finds in the caches. 60 us at 16384 x 1152, rank 64 (75 MB
+// of dY; dS first instead of dB: 99 against 88 us before both went to bf16).
 template <typename WT, int RT, int MT>
 __global__ __launch_bounds__(kOuterThreads) void k_lora_grad_y(DsArgs d, OuterArgs y, int y_groups) {
   __shared__ __align__(16) union Lds {
@@ -1133,7 +1159,9 @@ __global__ __launch_bounds__(kOuterThreads) void k_lora_grad_x(OuterArgs x) {
 }
 
 // ---------------------------------------------------------------- slot sum ----
-// dW[a][e] = scale_a * the sum of the slots of adapter a, in the slots' order.
+// dW[a][e] = scale_a * the sum of the slots of adapter a, in the slots' order. Bound
+// by memory (75 MB of slots in 16 us at 16384 rows, rank 64): eight loads at a time,
+// 4.5 us for 32 slots of 92160 values where one after another took 9.
 template <typename WT>
 __global__ __launch_bounds__(256) void k_lora_slot_sum(SlotSumArgs p, SlotSumArgs s, int p_groups) {
   const bool second = (int)blockIdx.x >= p_groups;
@@ -1198,15 +1226,19 @@ hipError_t forward_run(ForwardArgs a, hipStream_t s) {
                     (!a.base || (reinterpret_cast<uintptr_t>(a.base) % 16 == 0 && a.ldb % 4 == 0));
   const bool bvec = reinterpret_cast<uintptr_t>(a.B) % 16 == 0 && a.rank % (16 / sizeof(WT)) == 0;
   if (two_launches(a.q.rows, a.N)) {
-    constexpr int NW = RT * H >= 8 ? 4 : 8;  // the waves' sums fit LDS
+    // S by 32 rows a workgroup reads A half as often as by 16; used where registers
+    // and LDS hold it and the tiles fill the chip. Measured by 32 / 16 rows on 16384
+    // rows: K 2048, N 8192, rank 64, bf16 238 / 254 us; K 1152, N 4608, rank 32 135.5 /
+    // 137.7 us, rank 16, fp32 129.7 / 129.7 us.
+    constexpr bool kTall = RT * H <= 4;
     const int tiles = expand_tiles(a.q.rows, a.q.n);
     int4* table = reinterpret_cast<int4*>(a.ws);
     v4f* s_rows = reinterpret_cast<v4f*>(table + tiles);
-    if (tiles < 512)
-      hipLaunchKernelGGL((k_lora_s<XT, WT, RT, 1, H, 8>), dim3(2 * tiles), dim3(512), 0, s, a, xvec,
-                         s_rows, table);
+    if (kTall && tiles >= 512)
+      hipLaunchKernelGGL((k_lora_s<XT, WT, RT, kTall ? 2 : 1, H, 8>), dim3(tiles), dim3(512), 0, s, a,
+                         xvec, s_rows, table);
     else
-      hipLaunchKernelGGL((k_lora_s<XT, WT, RT, 2, H, NW>), dim3(tiles), dim3(64 * NW), 0, s, a, xvec,
+      hipLaunchKernelGGL((k_lora_s<XT, WT, RT, 1, H, 8>), dim3(2 * tiles), dim3(512), 0, s, a, xvec,
                          s_rows, table);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -1313,12 +1345,10 @@ int lora_ds_splits(int rows, int n_req, int N) {
 }
 
 // Row ranges: about `groups` workgroups, none with fewer than 64 rows.
-#ifndef QL_GX
-#define QL_GX 768
-#endif
-#ifndef QL_GY
-#define QL_GY 256
-#endif
+// Measured at 16384 rows, rank 64: 512 / 768 / 1152 groups on the X side 202.5 / 199.3 /
+// 203.7 us for the whole gradient; 128 / 256 / 512 on the dY side 200 / 203 / 211 us,
+// and 41.4 / 40.5 / 43.3 us at 2048 rows, rank 16, fp32.
+constexpr int kXGroups = 768, kYGroups = 256;
 static int outer_splits(int rows, int D, int groups) {
   const int chunks = (D + kOuterCols - 1) / kOuterCols;
   int64_t s = (groups + chunks - 1) / chunks;
@@ -1326,8 +1356,8 @@ static int outer_splits(int rows, int D, int groups) {
   s = s < cap ? s : cap;
   return (int)(s < 1 ? 1 : s);
 }
-int lora_x_splits(int rows, int K) { return outer_splits(rows, K, QL_GX); }
-int lora_y_splits(int rows, int N) { return outer_splits(rows, N, QL_GY); }
+int lora_x_splits(int rows, int K) { return outer_splits(rows, K, kXGroups); }
+int lora_y_splits(int rows, int N) { return outer_splits(rows, N, kYGroups); }
 
 int64_t lora_forward_ws(int rows, int n_req, int N, int rank, bool w_bf16) {
   if (!two_launches(rows, N)) return 0;
