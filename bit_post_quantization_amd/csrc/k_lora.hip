@@ -56,30 +56,42 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
   return v;
 }
 
+// A lane looks at four requests, so that one trip to memory covers 256 of them.
 __device__ bool find_tile(const Requests& q, int T, int t, Tile& out) {
+  constexpr int kEach = 4;
   const int lane = threadIdx.x & (kWave - 1);
   int done = 0;
-  for (int base = 0; base < q.n; base += kWave) {
-    const int i = base + lane;
-    int b = 0, e = 0, id = -1;
-    if (i < q.n) {
-      id = q.ids[i];  // of every request looked at: one trip to memory, not two
-      b = clampi(q.off[i], 0, q.rows);
-      e = clampi(q.off[i + 1], b, q.rows);
+  for (int base = 0; base < q.n; base += kEach * kWave) {
+    int off[kEach + 1], id[kEach];
+#pragma unroll
+    for (int k = 0; k <= kEach; ++k) off[k] = q.off[min(base + lane * kEach + k, q.n)];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) id[k] = q.ids[min(base + lane * kEach + k, q.n - 1)];
+    int begin[kEach], end[kEach], tiles[kEach], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      begin[k] = clampi(off[k], 0, q.rows);
+      end[k] = clampi(off[k + 1], begin[k], q.rows);
+      tiles[k] = base + lane * kEach + k < q.n ? (end[k] - begin[k] + T - 1) / T : 0;
+      sum += tiles[k];
     }
-    const int nt = (e - b + T - 1) / T;
-    const int incl = wave_scan(nt, lane);
+    const int incl = wave_scan(sum, lane);
     const int total = __builtin_amdgcn_readlane(incl, kWave - 1);
     if (t < done + total) {
       const int src = __ffsll((unsigned long long)__ballot(done + incl > t)) - 1;
-      const int first = done + __builtin_amdgcn_readlane(incl - nt, src);
-      const int rb = __builtin_amdgcn_readlane(b, src);
-      const int re = __builtin_amdgcn_readlane(e, src);
-      out.row0 = rb + (t - first) * T;
-      out.rows = min(T, re - out.row0);
-      id = __builtin_amdgcn_readlane(id, src);
-      out.adapter = id >= 0 && id < q.n_adapters ? id : -1;
-      return true;
+      int first = done + __builtin_amdgcn_readlane(incl - sum, src);  // tiles before request k
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const int nt = __builtin_amdgcn_readlane(tiles[k], src);
+        if (t < first + nt) {
+          out.row0 = __builtin_amdgcn_readlane(begin[k], src) + (t - first) * T;
+          out.rows = min(T, __builtin_amdgcn_readlane(end[k], src) - out.row0);
+          const int a = __builtin_amdgcn_readlane(id[k], src);
+          out.adapter = a >= 0 && a < q.n_adapters ? a : -1;
+          return true;
+        }
+        first += nt;
+      }
     }
     done += total;
   }
@@ -1358,6 +1370,19 @@ static int outer_splits(int rows, int D, int groups) {
 }
 int lora_x_splits(int rows, int K) { return outer_splits(rows, K, kXGroups); }
 int lora_y_splits(int rows, int N) { return outer_splits(rows, N, kYGroups); }
+
+// A launch holds fewer than 2^32 threads along its grid.
+bool lora_fits(int rows, int n_req, int N, bool grad) {
+  Requests q{};
+  q.rows = rows;
+  q.n = n_req;
+  int64_t threads = ((int64_t)max_tiles(q, 16) + 512) * 512;
+  if (!grad && two_launches(rows, N)) {
+    const int64_t shares = ((int64_t)N + kExpandCols - 1) / kExpandCols;
+    threads = expand_tiles(rows, n_req) * (shares > 4 ? shares : 4) * 256;
+  }
+  return threads < (int64_t)1 << 32;
+}
 
 int64_t lora_forward_ws(int rows, int n_req, int N, int rank, bool w_bf16) {
   if (!two_launches(rows, N)) return 0;

@@ -98,6 +98,8 @@ struct SlotSumArgs {
 
 // Workspace of a forward call with `rows` output rows.
 int64_t lora_forward_ws(int rows, int n_req, int N, int rank, bool w_bf16);
+// Whether the call's launches stay within the grid's limit.
+bool lora_fits(int rows, int n_req, int N, bool grad);
 hipError_t launch_lora_forward(const ForwardArgs& a, hipStream_t s);
 bool lora_ds_tall(int rows, int n_req);
 int lora_ds_splits(int rows, int n_req, int N);

@@ -51,6 +51,12 @@ constexpr int kMaxRank = 128;
 constexpr int kMaxAdapters = 65535;
 constexpr int kMaxRows = 1 << 23;
 
+ql_status check_grid(const ql_lora* d, int rows, int32_t n_requests, bool grad) {
+  if (ql::lora_fits(rows, n_requests, d->N, grad)) return QL_OK;
+  return fail(QL_ERR_UNSUPPORTED, "%d rows of %d requests with N = %d exceed one launch", rows,
+              n_requests, d->N);
+}
+
 ql_status check_lora(const ql_lora* d, int32_t M, int32_t n_requests) {
   if (!d) return fail(QL_ERR_ARG, "adapter descriptor is NULL");
   if (d->N < 1) return fail(QL_ERR_ARG, "N = %d must be >= 1", d->N);
@@ -69,6 +75,8 @@ ql_status check_lora(const ql_lora* d, int32_t M, int32_t n_requests) {
   if (n_requests < 1) return fail(QL_ERR_ARG, "n_requests = %d must be >= 1", n_requests);
   if (n_requests > kMaxRows)
     return fail(QL_ERR_UNSUPPORTED, "n_requests = %d exceeds %d", n_requests, kMaxRows);
+  if ((int64_t)d->N * d->rank >= (int64_t)1 << 31)
+    return fail(QL_ERR_UNSUPPORTED, "B_a of 2^31 elements or more (N = %d, rank = %d)", d->N, d->rank);
   return QL_OK;
 }
 
@@ -127,6 +135,8 @@ ql_status check_norm(const ql_norm* d) {
   if (!d) return fail(QL_ERR_ARG, "norm descriptor is NULL");
   if (d->batch < 0 || d->positions < 0)
     return fail(QL_ERR_ARG, "batch = %d and positions = %d must be >= 0", d->batch, d->positions);
+  if (d->positions > 1 << 30)
+    return fail(QL_ERR_UNSUPPORTED, "positions = %d: at most 1073741824", d->positions);
   if (d->channels < 1 || d->groups < 1 || d->channels % d->groups != 0)
     return fail(QL_ERR_ARG, "channels = %d must be a positive multiple of groups = %d", d->channels,
                 d->groups);
@@ -205,6 +215,7 @@ ql_status qlinear_lora_workspace(const ql_lora* d, int32_t M, int32_t n_requests
   if (!bytes) return fail(QL_ERR_ARG, "bytes is NULL");
   if (cfg != 0 && cfg != 1) return fail(QL_ERR_ARG, "cfg = %d must be 0 or 1", cfg);
   if (grad != 0 && grad != 1) return fail(QL_ERR_ARG, "grad = %d must be 0 or 1", grad);
+  QL_CHECK(check_grid(d, cfg && !grad ? M / 2 : M, n_requests, grad != 0));
   *bytes = grad ? grad_ws(d, M, n_requests).total
                 : ql::lora_forward_ws(cfg ? M / 2 : M, n_requests, d->N, d->rank,
                                       d->w_dtype == QL_BF16);
@@ -235,6 +246,7 @@ ql_status qlinear_lora(const ql_lora* d, const void* X, int64_t ldx, int32_t M,
   ql::ForwardArgs a{};
   a.halves = cfg ? 2 : 1;
   a.q = requests(d, q, M / a.halves);
+  QL_CHECK(check_grid(d, a.q.rows, q->n_requests, false));
   QL_CHECK(check_workspace(workspace, workspace_bytes,
                            ql::lora_forward_ws(a.q.rows, q->n_requests, d->N, d->rank,
                                                d->w_dtype == QL_BF16)));
@@ -279,6 +291,7 @@ ql_status qlinear_lora_grad(const ql_lora* d, const void* X, int64_t ldx, int32_
       return fail(QL_ERR_ARG, "ldx = %lld, lddy = %lld or lddx = %lld is less than its row",
                   (long long)ldx, (long long)lddy, (long long)lddx);
   }
+  QL_CHECK(check_grid(d, M, q->n_requests, true));
   const GradWs w = grad_ws(d, M, q->n_requests);
   if (M > 0) QL_CHECK(check_workspace(workspace, workspace_bytes, w.total));
   char* ws = reinterpret_cast<char*>(workspace);

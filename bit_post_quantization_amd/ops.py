@@ -137,7 +137,8 @@ class LoraAdapters:
     """Adapters A [n, rank, K], B [n, N, rank] (f32 or bf16) of one projection.
 
     ``scales`` f32 [n] (None: 1) and ``ranks`` int32 [n] (None: all of the
-    stored rank) are device tensors. The rows of a call belong to requests:
+    stored rank) are device tensors. All of them are used where they are: update
+    them in place. The rows of a call belong to requests:
     request i owns rows [row_offsets[i], row_offsets[i+1]) and runs adapter
     ``adapter[i]`` (-1: none); both are int32 device tensors."""
 

@@ -364,7 +364,10 @@ typedef struct {
 
 /* Workspace bytes (HOST out, may be 0) of qlinear_lora (grad = 0) or
  * qlinear_lora_grad (grad = 1, cfg ignored) with M rows and n_requests requests.
- * The pointers in d are not looked at. */
+ * The pointers in d are not looked at. The gradient's grows by (N + K) * rank * 4
+ * bytes a request: neighbouring requests of one adapter are best given as one.
+ * QL_ERR_UNSUPPORTED: M or n_requests above 2^23, N * rank of 2^31 or more, or
+ * more tiles of rows and columns than one launch holds. */
 ql_status qlinear_lora_workspace(const ql_lora* d, int32_t M, int32_t n_requests, int32_t cfg,
                                  int32_t grad, int64_t* bytes);
 
@@ -412,7 +415,7 @@ ql_status qlinear_lora_grad(const ql_lora* d, const void* X, int64_t ldx, int32_
  */
 typedef enum { QL_ACT_NONE = 0, QL_ACT_SILU = 1 } ql_act;
 typedef struct {
-  int32_t batch, positions;   /* >= 0; batch <= 65535 */
+  int32_t batch, positions;   /* >= 0; batch <= 65535, positions <= 2^30 */
   int32_t channels, groups;   /* 1 .. 8192 channels, a multiple of groups; groups <= 2048,
                                  batch * groups <= 2^22 */
   ql_dtype x_dtype;           /* x, y, dy, dx */

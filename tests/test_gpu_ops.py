@@ -140,6 +140,10 @@ LORA = [
     ([300], [0], 176, 200, 16, "f32", "bf16", None, False),
     ([1] * 70 + [9] * 70, list(range(5)) * 28, 32, 20, 8, "bf16", "bf16", (8, 3), False),
     ([7] * 3, [99, -7, 1], 32, 20, 8, "f32", "f32", None, False),
+    ([1] * 300 + [0] * 250 + [2, 40] * 60, list(range(-1, 4)) * 134, 32, 24, 8, "f32", "bf16", None, False),
+    ([2049], [1], 64, 4112, 16, "bf16", "f32", (7, 16), False),          # two launches, an odd tail
+    ([700, 0, 1500], [0, 1, -1], 96, 4100, 40, "f32", "bf16", None, True),
+    ([600, 1537, 1], [2, 0, 1], 80, 4099, 70, "bf16", "bf16", (70, 3), False),
 ]
 
 

@@ -35,6 +35,7 @@ def _msg():
     (dict(rank=129), _lib.QL_ERR_UNSUPPORTED, "rank = 129"),
     (dict(n_adapters=0), _lib.QL_ERR_ARG, "n_adapters"),
     (dict(n_adapters=65536), _lib.QL_ERR_UNSUPPORTED, "n_adapters"),
+    (dict(N=1 << 28), _lib.QL_ERR_UNSUPPORTED, "2^31"),
     (dict(x_dtype=2), _lib.QL_ERR_ARG, "x_dtype"),
     (dict(w_dtype=-1), _lib.QL_ERR_ARG, "w_dtype"),
 ])
@@ -63,6 +64,11 @@ def test_lora_workspace_query():
     assert query(ctypes.byref(d), 16, 1, 0, 0, U) == _lib.QL_ERR_ARG
     assert query(ctypes.byref(d), (1 << 23) + 1, 1, 0, 0, ctypes.byref(n)) == \
         _lib.QL_ERR_UNSUPPORTED
+    for M, reqs, N, grad in ((1 << 23, 1 << 23, 100, 0), (1 << 23, 1 << 23, 100, 1),
+                             (1 << 23, 1 << 16, 1 << 20, 0)):  # past the grid's limit
+        assert query(ctypes.byref(_lora(N=N)), M, reqs, 0, grad, ctypes.byref(n)) == \
+            _lib.QL_ERR_UNSUPPORTED
+        assert "one launch" in _msg()
     for M, grad, least in ((16, 0, 0), (16, 1, 16 * 8 * 4), (1 << 20, 0, (1 << 20) * 8 * 4)):
         assert query(ctypes.byref(d), M, 1, 0, grad, ctypes.byref(n)) == _lib.QL_OK
         assert n.value >= least
@@ -150,6 +156,7 @@ def _norm(**kw):
     (dict(batch=65536), _lib.QL_ERR_UNSUPPORTED, "batch"),
     (dict(channels=8200), _lib.QL_ERR_UNSUPPORTED, "8192"),
     (dict(channels=4098, groups=2049), _lib.QL_ERR_UNSUPPORTED, "2048"),
+    (dict(positions=(1 << 30) + 1), _lib.QL_ERR_UNSUPPORTED, "positions"),
     (dict(batch=2049, channels=2048, groups=2048), _lib.QL_ERR_UNSUPPORTED, "4194304"),
     (dict(x_dtype=3), _lib.QL_ERR_ARG, "x_dtype"),
     (dict(w_dtype=3), _lib.QL_ERR_ARG, "w_dtype"),
