@@ -21,12 +21,12 @@
 // to bf16's 8 anyway. Where both are fp32, v_mfma_f32_16x16x4_f32.
 //
 // Measured per call (MI355X; what a copy of the same bytes would take in brackets):
-//   8 rows, K 1152, N 6912, rank 16, bf16, 8 adapters: 6.4 us of kernel, 7.7 us a call
-//   1003 rows of 23 requests, N 1001, rank 12: 11.5 us
-//   guided 4096 rows, K 1152, N 4608, rank 16, fp32: 24.4 us (17)
+//   8 rows, K 1152, N 6912, rank 16, bf16, 8 adapters: 6.5 us of kernel, 7.6 us a call
+//   1003 rows of 23 requests, N 1001, rank 12: 11.8 us
+//   guided 4096 rows, K 1152, N 4608, rank 16, fp32: 24.6 us (17)
 //   16384 rows, K 2048, N 8192, rank 64, bf16: 239 us, 4.8 TB/s (212)
-//   gradients of 2048 rows, K 1152, N 4608, rank 16, fp32: 38.7 us (11)
-//   gradients of 16384 rows, K 4608, N 1152, rank 64, bf16: 177 us (72)
+//   gradients of 2048 rows, K 1152, N 4608, rank 16, fp32: 38.9 us (11)
+//   gradients of 16384 rows, K 4608, N 1152, rank 64, bf16: 182 us (72)
 #include "ql_device.h"
 #include "ql_ops.h"
 
