@@ -817,7 +817,7 @@ __device__ void ds_body(const DsArgs& a, int tile, int split, DsLds<RT, MT, NW>&
 // addresses side by side: split in registers for bf16 results, as it is for fp32.
 //
 // Measured at 16384 rows, K 4608, rank 64, bf16: 112 us for 302 MB of X and dX and 58
-// MB of slots, 3.2 TB/s; bound by the rows' latency between barriers (matrix cores
+// MB of slots, 3.2 TB/s, with 774 workgroups; bound by the rows' latency between barriers (matrix cores
 // 15 %, LDS 15 % busy). Four waves of 64 columns instead of eight of 32: 268 instead
 // of 231 us for the whole gradient; 256 threads and 128 columns: 260 instead of 200.
 constexpr int kOuterRows = 32, kOuterThreads = 512;
@@ -1356,20 +1356,28 @@ int lora_ds_splits(int rows, int n_req, int N) {
   return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
 }
 
-// Row ranges: about `groups` workgroups, none with fewer than 64 rows.
-// Measured at 16384 rows, rank 64: 512 / 768 / 1152 groups on the X side 202.5 / 199.3 /
-// 203.7 us for the whole gradient; 128 / 256 / 512 on the dY side 200 / 203 / 211 us,
-// and 41.4 / 40.5 / 43.3 us at 2048 rows, rank 16, fp32.
-constexpr int kXGroups = 768, kYGroups = 256;
+// Row ranges: at most `groups` workgroups, none with fewer than 64 rows. Workgroups
+// here take long and alike, so they are counted to fill the chip evenly: two a compute
+// unit are resident. On the X side 504 of them instead of 774 took 164 instead of 181 us
+// for the whole gradient at 16384 rows, rank 64 (1008: 186). On the dY side dB gets what
+// dS leaves of the next multiple of 256 (96 at least): 16384 rows 157 us against 164
+// with 255 of them, 2048 rows, N 4608, rank 16, fp32 37.9 against 40.7.
+constexpr int kXGroups = 512;
 static int outer_splits(int rows, int D, int groups) {
   const int chunks = (D + kOuterCols - 1) / kOuterCols;
-  int64_t s = (groups + chunks - 1) / chunks;
+  int64_t s = groups / chunks;
   const int64_t cap = (rows + 63) / 64;
   s = s < cap ? s : cap;
   return (int)(s < 1 ? 1 : s);
 }
 int lora_x_splits(int rows, int K) { return outer_splits(rows, K, kXGroups); }
-int lora_y_splits(int rows, int N) { return outer_splits(rows, N, kYGroups); }
+int lora_y_splits(int rows, int n_req, int N) {
+  const int64_t ds = lora_ds_tall(rows, n_req)
+                         ? (int64_t)rows / 32 + n_req
+                         : ((int64_t)rows / 16 + n_req) * lora_ds_splits(rows, n_req, N);
+  const int64_t all = (ds + 96 + 255) / 256 * 256;
+  return outer_splits(rows, N, (int)(all - ds));
+}
 
 // A launch holds fewer than 2^32 threads along its grid.
 bool lora_fits(int rows, int n_req, int N, bool grad) {

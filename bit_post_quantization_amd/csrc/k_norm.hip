@@ -786,6 +786,9 @@ hipError_t norm_grad_run(const NormArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Tensors that go by slabs with vectors narrower than 16 bytes too.
+bool small_tensor(int B, int L, int C, int es) { return (int64_t)B * L * C * es <= 24 << 20; }
+
 // Vectors a thread holds when one workgroup takes a slab, 0 where it does not fit.
 template <typename T, int V>
 int slab_vectors(const NormArgs& a) {
@@ -876,7 +879,7 @@ hipError_t norm_dispatch(const NormArgs& a, bool grad, hipStream_t st) {
   // (4 bytes, 42 MB) 50.8 / 37.5; 2x500x224 bf16 (2 bytes, 0.4 MB) 12.9 / 17.9;
   // gradients of 2x500x224 bf16 15.3 / 23.7 and of 16x2048x320 fp32 (8 bytes, 42 MB)
   // 52.1 / 44.3.
-  const bool small = (int64_t)a.B * a.L * a.C * es <= 24 << 20;
+  const bool small = small_tensor(a.B, a.L, a.C, es);
   if (aligned(16) && slab_vectors<T, V>(a)) return norm_width<T, W, V>(a, true, grad, st);
   if (small && aligned(8) && cpg % (V / 2) == 0 && slab_vectors<T, V / 2>(a))
     return norm_width<T, W, V / 2>(a, true, grad, st);
@@ -895,7 +898,13 @@ hipError_t norm_types(const NormArgs& a, bool grad, hipStream_t s) {
 
 }  // namespace
 
-int64_t norm_ws_bytes(int B, int L, int C, int G, bool grad) {
+int64_t norm_ws_bytes(int B, int L, int C, int G, int es, bool grad) {
+  // Small tensors whose slabs fit even element by element go by slabs at any
+  // alignment: the gradient's per-channel sums are all they put through memory.
+  const int cpg = C / G;
+  if (small_tensor(B, L, C, es) && cpg <= kNormThreads &&
+      ((int64_t)L + kNormThreads / cpg - 1) / (kNormThreads / cpg) <= slab_most(es))
+    return grad && B > 1 ? (int64_t)B * C * (int64_t)sizeof(float2) : 0;
   int64_t chunks = 0;  // the most of any vector width
   for (int V : {1, 2, 4, 8}) {
     if (C % V) continue;

@@ -105,7 +105,7 @@ bool lora_ds_tall(int rows, int n_req);
 int lora_ds_splits(int rows, int n_req, int N);
 // Row ranges of dA's and dB's sums.
 int lora_x_splits(int rows, int K);
-int lora_y_splits(int rows, int N);
+int lora_y_splits(int rows, int n_req, int N);
 // dS and dB.
 hipError_t launch_lora_grad_y(const DsArgs& d, const OuterArgs& y, hipStream_t s);
 // dA and dX.
@@ -134,7 +134,8 @@ struct NormArgs {
   void* ws;
   bool x_bf16, w_bf16;
 };
-int64_t norm_ws_bytes(int B, int L, int C, int G, bool grad);
+// es: bytes of an element.
+int64_t norm_ws_bytes(int B, int L, int C, int G, int es, bool grad);
 hipError_t launch_group_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_group_norm_grad(const NormArgs& a, hipStream_t s);
 

@@ -107,7 +107,7 @@ GradWs grad_ws(const ql_lora* d, int32_t M, int32_t n) {
   GradWs w;
   w.s_splits = ql::lora_ds_splits(M, n, d->N);
   w.x_splits = ql::lora_x_splits(M, d->K);
-  w.y_splits = ql::lora_y_splits(M, d->N);
+  w.y_splits = ql::lora_y_splits(M, n, d->N);
   w.x_slots = w.x_splits + n - 1;
   w.y_slots = w.y_splits + n - 1;
   int64_t at = 0;
@@ -166,6 +166,11 @@ ql_status check_image(const ql_norm* d, const char* name, const void* p, int64_t
                 d->channels);
   if (batch < 0) return fail(QL_ERR_ARG, "%s: batch stride %lld is negative", name, (long long)batch);
   return QL_OK;
+}
+
+int64_t norm_ws(const ql_norm* d, bool grad) {
+  return ql::norm_ws_bytes(d->batch, d->positions, d->channels, d->groups,
+                           (int)size_of(d->x_dtype), grad);
 }
 
 ql::NormArgs norm_args(const ql_norm* d) {
@@ -371,7 +376,7 @@ ql_status qlinear_group_norm_workspace(const ql_norm* d, int32_t grad, int64_t* 
   if (!bytes) return fail(QL_ERR_ARG, "bytes is NULL");
   if (grad != 0 && grad != 1) return fail(QL_ERR_ARG, "grad = %d must be 0 or 1", grad);
   const bool empty = d->batch == 0 || d->positions == 0;
-  *bytes = empty ? 0 : ql::norm_ws_bytes(d->batch, d->positions, d->channels, d->groups, grad != 0);
+  *bytes = empty ? 0 : norm_ws(d, grad != 0);
   return ok();
 }
 
@@ -387,7 +392,7 @@ ql_status qlinear_group_norm(const ql_norm* d, const void* x, int64_t x_batch, i
   if (x == y && (x_batch != y_batch || x_row != y_row))
     return fail(QL_ERR_ARG, "y is x with other strides");
   QL_CHECK(check_workspace(workspace, workspace_bytes,
-                           ql::norm_ws_bytes(d->batch, d->positions, d->channels, d->groups, false)));
+                           norm_ws(d, false)));
   ql::NormArgs a = norm_args(d);
   a.x = x;
   a.xb = x_batch;
@@ -426,7 +431,7 @@ ql_status qlinear_group_norm_grad(const ql_norm* d, const void* dy, int64_t dy_b
         (dx == x && (dx_batch != x_batch || dx_row != x_row)))
       return fail(QL_ERR_ARG, "dx is dy or x with other strides");
     QL_CHECK(check_workspace(workspace, workspace_bytes,
-                             ql::norm_ws_bytes(d->batch, d->positions, d->channels, d->groups, true)));
+                             norm_ws(d, true)));
   }
   a.dy = dy;
   a.dyb = dy_batch;

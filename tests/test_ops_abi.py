@@ -191,7 +191,8 @@ def test_norm_descriptor(kw, status, frag):
 def test_norm_refusals(kw, frag):
     a = dict(x=A, xb=216, xr=24, y=A + 4096, yb=216, yr=24, mean=U, rstd=U, ws=A, nb=1 << 30)
     a.update(kw)
-    st = _lib.load().qlinear_group_norm(ctypes.byref(_norm()), a["x"], a["xb"], a["xr"], a["y"],
+    # positions enough that the call takes a workspace
+    st = _lib.load().qlinear_group_norm(ctypes.byref(_norm(positions=100000)), a["x"], a["xb"], a["xr"], a["y"],
                                         a["yb"], a["yr"], a["mean"], a["rstd"], a["ws"], a["nb"], U)
     assert st == _lib.QL_ERR_ARG
     assert frag in _msg()
