@@ -22,11 +22,11 @@
 //
 // Measured per call (MI355X; what a copy of the same bytes would take in brackets):
 //   8 rows, K 1152, N 6912, rank 16, bf16, 8 adapters: 6.5 us of kernel, 7.6 us a call
-//   1003 rows of 23 requests, N 1001, rank 12: 11.8 us
+//   1003 rows of 23 requests, N 1001, rank 12: 12.0 us
 //   guided 4096 rows, K 1152, N 4608, rank 16, fp32: 24.6 us (17)
 //   16384 rows, K 2048, N 8192, rank 64, bf16: 239 us, 4.8 TB/s (212)
-//   gradients of 2048 rows, K 1152, N 4608, rank 16, fp32: 38.9 us (11)
-//   gradients of 16384 rows, K 4608, N 1152, rank 64, bf16: 182 us (72)
+//   gradients of 2048 rows, K 1152, N 4608, rank 16, fp32: 36 us (11)
+//   gradients of 16384 rows, K 4608, N 1152, rank 64, bf16: 156 us (72)
 #include "ql_device.h"
 #include "ql_ops.h"
 
@@ -816,10 +816,10 @@ __device__ void ds_body(const DsArgs& a, int tile, int split, DsLds<RT, MT, NW>&
 // of column c). fp32 P comes element by element from memory, lanes side by side at
 // addresses side by side: split in registers for bf16 results, as it is for fp32.
 //
-// Measured at 16384 rows, K 4608, rank 64, bf16: 112 us for 302 MB of X and dX and 58
-// MB of slots, 3.2 TB/s, with 774 workgroups; bound by the rows' latency between barriers (matrix cores
-// 15 %, LDS 15 % busy). Four waves of 64 columns instead of eight of 32: 268 instead
-// of 231 us for the whole gradient; 256 threads and 128 columns: 260 instead of 200.
+// Measured at 16384 rows, K 4608, rank 64, bf16: 97 us for 302 MB of X and dX and 40
+// MB of slots, 3.5 TB/s; bound by the rows' latency between barriers (matrix cores and
+// LDS busy 20 % at most). Four waves of 64 columns instead of eight of 32: 268 instead
+// of 231 us for the whole gradient then; 256 threads and 128 columns: 260 instead of 200.
 constexpr int kOuterRows = 32, kOuterThreads = 512;
 constexpr int kOuterU = 2;  // 16-column tiles of a wave
 constexpr int kOuterCols = kOuterThreads / 64 * 16 * kOuterU;
@@ -1146,7 +1146,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
 
 // What needs dY alone, in one launch: dB in workgroups [0, y_groups), which run
 // longest, dS in the rest. Both wait for memory more than they compute, and what one
-// reads of dY the other finds in the caches. 60 us at 16384 x 1152, rank 64 (75 MB
+// reads of dY the other finds in the caches. 55 us at 16384 x 1152, rank 64 (75 MB
 // of dY; dS first instead of dB: 99 against 88 us before both went to bf16).
 template <typename WT, int RT, int MT>
 __global__ __launch_bounds__(kOuterThreads) void k_lora_grad_y(DsArgs d, OuterArgs y, int y_groups) {
@@ -1172,7 +1172,7 @@ __global__ __launch_bounds__(kOuterThreads) void k_lora_grad_x(OuterArgs x) {
 
 // ---------------------------------------------------------------- slot sum ----
 // dW[a][e] = scale_a * the sum of the slots of adapter a, in the slots' order. Bound
-// by memory (75 MB of slots in 16 us at 16384 rows, rank 64): eight loads at a time,
+// by memory (55 MB of slots in 13 us at 16384 rows, rank 64): eight loads at a time,
 // 4.5 us for 32 slots of 92160 values where one after another took 9.
 template <typename WT>
 __global__ __launch_bounds__(256) void k_lora_slot_sum(SlotSumArgs p, SlotSumArgs s, int p_groups) {

@@ -18,11 +18,11 @@
 // zero costs no digits of the variance.
 //
 // Measured per call (MI355X; a copy of the bytes read and written once in brackets):
-//   2x256x1280 bf16: 6.5 us of kernel, 8.6 us a call; latency: load, two sums over the
+//   2x256x1280 bf16: 6.5 us of kernel, 7.7 us a call; latency: load, two sums over the
 //     workgroup, store
 //   8x16384x320 bf16 (84 MB): 65 us (31): 17 us of sums at 4.9 TB/s, 33 us of writing
 //     at 5.1 TB/s, read again from the last-level cache
-//   gradient of 4x1024x640 fp32 (31 MB): 16.7 us (6): 128 slabs for 256 compute units,
+//   gradient of 4x1024x640 fp32 (31 MB): 16.4 us (6): 128 slabs for 256 compute units,
 //     bound by the arithmetic of a SiLU's gradient
 //   gradient of 4x16383x256 bf16 (101 MB): 46 us (19): 17 us of sums and 26 of writing,
 //     4.0 TB/s
