@@ -25,7 +25,6 @@ namespace {
 typedef __bf16 bf16;
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef bf16 v8h __attribute__((ext_vector_type(8)));
-typedef bf16 v4h __attribute__((ext_vector_type(4)));
 constexpr int kUnit = QL_GRAD_UNIT;
 constexpr int kParts = QL_GRAD_PARTIALS;
 constexpr int kThreads = 512;

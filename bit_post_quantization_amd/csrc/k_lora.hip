@@ -37,7 +37,6 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16;
 typedef bf16 v8h __attribute__((ext_vector_type(8)));
-typedef bf16 v4h __attribute__((ext_vector_type(4)));
 
 // Request and rows of tile t when every request's rows are cut into tiles of
 // T. Uniform over the wave; false past the last tile.

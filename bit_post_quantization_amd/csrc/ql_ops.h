@@ -61,7 +61,8 @@ struct ForwardArgs {
 };
 
 // Row ranges s = 0 .. splits-1 of row_len rows each. For every range and the
-// requests i in it, slot s + i of `out` receives the sum over the common rows
+// requests i in it, slot s + i of `out` receives the sum over the common rows (those
+// of neighbouring requests of one adapter together, in the last one's slot)
 // of Q[row][j] * P[row][d] ([j][d] for dA, [d][j] for dB);
 // slot_id[s + i] says which adapter it belongs to (-1: nothing was written).
 // With dX, dX[row][d] = sum_j Q[row][j] * A_a[j][d] too (zero for rows without
