@@ -16,9 +16,9 @@
 // no atomics and in a fixed order, so a call gives the same bits every time.
 //
 // Products: where both operands are bf16, v_mfma_f32_16x16x32_bf16. An fp32 operand
-// beside a bf16 one is split into bf16 terms (v = h + m + l holds fp32's 24 bits):
-// three terms where the result stays fp32, two (16 bits) where the result is rounded
-// to bf16's 8 anyway. Where both are fp32, v_mfma_f32_16x16x4_f32.
+// beside a bf16 one is split into three bf16 terms (v = h + m + l holds fp32's 24 bits),
+// also where the result is rounded to bf16: sums that cancel show every bit. Where
+// both are fp32, v_mfma_f32_16x16x4_f32, or both split where the sums run over rows.
 //
 // Measured per call (MI355X; what a copy of the same bytes would take in brackets):
 //   8 rows, K 1152, N 6912, rank 16, bf16, 8 adapters: 6.5 us of kernel, 7.6 us a call
@@ -26,7 +26,7 @@
 //   guided 4096 rows, K 1152, N 4608, rank 16, fp32: 24.6 us (17)
 //   16384 rows, K 2048, N 8192, rank 64, bf16: 239 us, 4.8 TB/s (212)
 //   gradients of 2048 rows, K 1152, N 4608, rank 16, fp32: 36 us (11)
-//   gradients of 16384 rows, K 4608, N 1152, rank 64, bf16: 156 us (72)
+//   gradients of 16384 rows, K 4608, N 1152, rank 64, bf16: 173 us (72)
 #include "ql_device.h"
 #include "ql_ops.h"
 
@@ -841,13 +841,9 @@ struct OuterLds {
   static constexpr bool PB = sizeof(PT) == 2;  // bf16 products for Q^T P, P through LDS
   static constexpr bool PS = !PB && sizeof(WT) == 2;  // the same, fp32 P split in registers
   static constexpr bool XB = DX && sizeof(WT) == 2;  // bf16 products for dX
-  // Terms of Q: all three (24 bits) where the result is fp32, two (16 bits) where
-  // it is rounded to bf16's 8.
-  static constexpr int kTermsA = PB || PS ? (sizeof(WT) == 2 ? 2 : 3) : 0;
-  static constexpr int kTermsX = XB ? (sizeof(PT) == 2 ? 2 : 3) : 0;
-  static constexpr int kTerms = kTermsA > kTermsX ? kTermsA : kTermsX;
+  static constexpr bool kSplit = PB || PS || XB;  // bf16 products read Q's three terms
   static constexpr bool kFloat = (!PB && !PS) || (DX && !XB);  // fp32 products read Q itself
-  static constexpr int kPlanes = RT == 1 && kTermsX == 3 ? 4 : kTerms;
+  static constexpr int kPlanes = !kSplit ? 0 : RT == 1 && XB ? 4 : 3;
   struct Tile {
     float q[kFloat ? kOuterRows : 1][FLD];
     bf16 x[PB ? kOuterRows : 1][XLD];
@@ -859,7 +855,7 @@ struct OuterLds {
 template <typename PT, typename WT, int RT, bool DX, bool TR>
 __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, WT, RT, DX>& lds) {
   typedef OuterLds<PT, WT, RT, DX> L;
-  constexpr int R = RT * 16, U = kOuterU, kTermsA = L::kTermsA, kTermsX = L::kTermsX;
+  constexpr int R = RT * 16, U = kOuterU;
   constexpr bool PB = L::PB, PS = L::PS, XB = L::XB;
   constexpr int t_xld = L::XLD, t_qld = L::QLD, t_fld = L::FLD;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
@@ -966,7 +962,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
 #pragma unroll
           for (int k = 0; k < QN; ++k) t.q[qm][qj + k] = qz[k];
         }
-        if constexpr (L::kTerms > 0) {
+        if constexpr (L::kSplit) {
           typedef bf16 vt __attribute__((ext_vector_type(QN < 8 ? QN : 8)));
           constexpr int W = QN < 8 ? QN : 8;
 #pragma unroll
@@ -982,9 +978,8 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
             }
             *reinterpret_cast<vt*>(&t.h[0][qm][qj + c * W]) = h;
             *reinterpret_cast<vt*>(&t.h[1][qm][qj + c * W]) = mi;
-            if constexpr (L::kTerms == 3)
-              *reinterpret_cast<vt*>(&t.h[2][qm][qj + c * W]) = l;
-            if constexpr (RT == 1 && kTermsX == 3) *reinterpret_cast<vt*>(&t.h[3][qm][qj]) = vt(0.0f);
+            *reinterpret_cast<vt*>(&t.h[2][qm][qj + c * W]) = l;
+            if constexpr (RT == 1 && XB) *reinterpret_cast<vt*>(&t.h[3][qm][qj]) = vt(0.0f);
           }
         }
         if constexpr (PB) {
@@ -1025,13 +1020,13 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
 #pragma unroll
           for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int k = 0; k < kTermsA; ++k) {
+            for (int k = 0; k < 3; ++k) {
               const v8h qt = read_transposed(&t.h[k][0][16 * r], t_qld, r16, g);
 #pragma unroll
               for (int u = 0; u < U; ++u) acc[r][u] = mfma_bf16(qt, xt[u], acc[r][u]);
             }
         } else if constexpr (PS) {
-          v8h ph[U], pm[U];
+          v8h ph[U], pm[U], pl[U];
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -1040,19 +1035,25 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
               split3(pc[k][u], h, m, l);
               ph[u][k] = h;
               pm[u][k] = m;
+              pl[u][k] = l;
             }
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
             const v8h qh = read_transposed(&t.h[0][0][16 * r], t_qld, r16, g);
             const v8h qm = read_transposed(&t.h[1][0][16 * r], t_qld, r16, g);
+            const v8h ql = read_transposed(&t.h[2][0][16 * r], t_qld, r16, g);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               auto add = [&](const v8h& q, const v8h& p) {
                 acc[r][u] = TR ? mfma_bf16(q, p, acc[r][u]) : mfma_bf16(p, q, acc[r][u]);
               };
+              // all but the products below 2^-24 of the first
               add(qh, ph[u]);
               add(qm, ph[u]);
               add(qh, pm[u]);
+              add(qm, pm[u]);
+              add(ql, ph[u]);
+              add(qh, pl[u]);
             }
           }
         } else {
@@ -1076,7 +1077,6 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
               for (int u = 0; u < U; ++u) y[u] = v4f{0, 0, 0, 0};
 #pragma unroll
               for (int k = 0; k < KS; ++k) {
-                if (kTermsX == 2 && (RT == 1 ? k == 1 : k % 3 == 2)) continue;
                 const int plane = RT == 1 ? 2 * k + g / 2 : k % 3;
                 const int j = RT == 1 ? 8 * (g & 1) : 32 * (k / 3) + 8 * g;
                 const v8h sv = *reinterpret_cast<const v8h*>(&t.h[plane][m * 16 + r16][j]);
