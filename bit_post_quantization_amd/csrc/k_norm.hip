@@ -106,6 +106,9 @@ struct Affine {
   }
 };
 
+// A variance that roundings took below zero is zero; a NaN stays one (fmax would drop it).
+__device__ __forceinline__ double variance(double v) { return v < 0.0 ? 0.0 : v; }
+
 constexpr int kAhead = 4;  // positions whose loads a thread has in flight
 
 // Position p of image b is chunk-local; thread (tx, ty) of a workgroup takes
@@ -211,7 +214,7 @@ __global__ __launch_bounds__(256) void k_norm_stats_join(const double2* part, St
     Q += __shfl_xor(Q, d);
   }
   if (lane != 0) return;
-  const double n = (double)s.L * s.cpg, m = S / n, var = fmax(Q / n - m * m, 0.0);
+  const double n = (double)s.L * s.cpg, m = S / n, var = variance(Q / n - m * m);
   const float2 r{(float)m, (float)(1.0 / sqrt(var + (double)o.eps))};
   o.stats[id] = r;
   if (o.mean) o.mean[id] = r.x;
@@ -581,7 +584,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_slab(SlabK a) {
       }
     }
   const double off = md - (double)m;  // squares about m, not about md
-  const double var = fmax(slab_sum2(q, 0.0f, red).x / n - off * off, 0.0);
+  const double var = variance(slab_sum2(q, 0.0f, red).x / n - off * off);
   const float r = (float)(1.0 / sqrt(var + (double)a.eps));
   if (threadIdx.x == 0) {
     if (a.mean) a.mean[b * a.G + g] = m;

@@ -98,3 +98,50 @@ def test_lora_gradient_ranks_that_cancel(torch, x, rank):
         ref, mag = dS @ A[0].double(), dS.abs() @ A[0].double().abs()
         _within(dX, ref, (16 + 4 * math.sqrt(N + 3)) * EPS * mag + _round(torch, ref, dX.dtype),
                 f"dX, ranks {3 * k}..")
+
+
+# -------------------------------------------------------------- group norm ----
+
+def _affine(t, C, w="f32", seed=0):
+    g = t.Generator(device="cuda")
+    g.manual_seed(seed)
+    n = lambda: t.empty(C, device="cuda").normal_(generator=g)  # noqa: E731
+    return (1 + 0.3 * n()).to(_dt(t, w)), (0.3 * n()).to(_dt(t, w))
+
+
+# B, L, C, G: one workgroup a group; two readings; two readings element by element
+# (the rows of 65 channels lie at odd multiples of 4 bytes)
+FORMS = [(2, 300, 16, 4), (2, 9001, 64, 4), (2, 60001, 65, 5)]
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", FORMS, ids=str)
+def test_group_norm_statistics_of_non_finite_groups(torch, shape, dtype, act):
+    # A NaN or an infinity anywhere in a group leaves it no variance: rstd is NaN
+    # and with it every output of that group; the others are what they are alone.
+    from bit_post_quantization_amd import GroupNormAct
+    say(f"[norm non-finite] {shape} {dtype} {act}")
+    B, L, C, G = shape
+    cpg = C // G
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.empty(shape[:3], device="cuda").normal_(generator=g).to(_dt(torch, dtype))
+    ga, be = _affine(torch, C)
+    ga[1] = -ga[1].abs()
+    op = GroupNormAct(ga, be, G, act=act)
+    want = op.forward(x, stats=True)
+    bad = x.clone()
+    inf = float("inf")
+    for b, l, grp, c, v in ((0, 7, 0, 1, float("nan")), (0, 5, 1, 0, inf), (1, 0, 2, 0, -inf),
+                            (1, L - 1, 3, cpg - 1, inf), (1, 0, 0, 0, float("nan"))):
+        bad[b, l, grp * cpg + c] = v
+    y, mean, rstd = op.forward(bad, stats=True)
+    hit = torch.zeros(B, G, dtype=torch.bool, device="cuda")
+    for b, grp in ((0, 0), (0, 1), (1, 2), (1, 3), (1, 0)):
+        hit[b, grp] = True
+    assert bool(torch.isnan(rstd[hit]).all()) and not bool(torch.isfinite(mean[hit]).any())
+    yg, wg = (t.view(B, L, G, cpg).transpose(1, 2) for t in (y, want[0]))
+    assert bool(torch.isnan(yg[hit]).all())
+    assert torch.equal(yg[~hit], wg[~hit])
+    assert torch.equal(mean[~hit], want[1][~hit]) and torch.equal(rstd[~hit], want[2][~hit])
