@@ -164,7 +164,9 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_stats(StatsK a) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float md = s1[i] * inv;
-        lds2[ty * s.C + v * V + i] = float2{k[i] + md, s2[i] - s1[i] * md};
+        // in fp64, so that squares past fp32 stay infinite and are not inf - inf
+        const double m2 = (double)s2[i] - (double)s1[i] * (double)md;
+        lds2[ty * s.C + v * V + i] = float2{k[i] + md, (float)m2};
       }
     }
   }

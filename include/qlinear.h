@@ -433,7 +433,9 @@ ql_status qlinear_group_norm_workspace(const ql_norm* d, int32_t grad, int64_t* 
 /*
  * z = (x - mean) rstd gamma + beta with the mean and 1 / sqrt(variance + eps)
  * of the image's group (biased variance); y = z, or z / (1 + exp(-z)) (SILU).
- * Statistics are joined in fp64. y may be x itself with the same strides.
+ * Statistics are joined in fp64; squares are taken in fp32, so values more than
+ * 1.8e19 apart can make a group's variance infinite and its rstd 0. A group with
+ * a NaN or an infinity has rstd NaN. y may be x itself with the same strides.
  *   mean, rstd : NULL, or DEVICE fp32 out [batch, groups] for the gradient.
  */
 ql_status qlinear_group_norm(const ql_norm* d, const void* x, int64_t x_batch, int64_t x_row,

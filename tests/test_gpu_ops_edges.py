@@ -145,3 +145,18 @@ def test_group_norm_statistics_of_non_finite_groups(torch, shape, dtype, act):
     assert bool(torch.isnan(yg[hit]).all())
     assert torch.equal(yg[~hit], wg[~hit])
     assert torch.equal(mean[~hit], want[1][~hit]) and torch.equal(rstd[~hit], want[2][~hit])
+
+
+@pytest.mark.parametrize("shape", FORMS, ids=str)
+def test_group_norm_squares_past_fp32(torch, shape):
+    # deviations whose squares pass fp32: an infinite variance in every form, so
+    # rstd is 0 and y = beta (not the quotient by sqrt(eps) of a variance lost)
+    from bit_post_quantization_amd import GroupNormAct
+    B, L, C, G = shape
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    x = torch.empty((B, L, C), device="cuda").normal_(generator=g) * 3e19
+    ga, be = _affine(torch, C)
+    y, mean, rstd = GroupNormAct(ga, be, G, act="none").forward(x, stats=True)
+    assert not bool(rstd.any()) and bool(torch.isfinite(mean).all())
+    assert torch.equal(y, be.expand(B, L, C))
