@@ -335,7 +335,7 @@ class GradSet:
 
     Made once for gradients that stay where they are (the set holds the tensors
     and a device table of their addresses); make a new one when a tensor is
-    replaced."""
+    replaced, and keep the set while a captured graph with its calls is replayed."""
 
     def __init__(self, grads: Sequence, out: Optional[Sequence] = None):
         self.grads = list(grads)
@@ -354,12 +354,17 @@ class GradSet:
             unit += -(-n // _lib.QL_GRAD_UNIT)
         self.units = unit
         self.device = torch.device("cuda", dev)
+        self._made_on = _stream(dev)
         self.table = torch.tensor(rows, dtype=torch.int64).reshape(-1, 5).to(self.device)
 
     def _ready(self) -> int:
+        """The current stream's handle, on which the table may be read from now on."""
         dev = _device()
         _need(dev == self.device.index, "the set's tensors are not on the current device")
-        return dev
+        s = _stream(dev)
+        if s != self._made_on:  # the table's memory outlives the set until this stream is done
+            self.table.record_stream(torch.cuda.current_stream(dev))
+        return s
 
     def partials(self, stream=None):
         """f64 [QL_GRAD_PARTIALS], adding up to the squared norm. Gradients sharded
@@ -367,10 +372,9 @@ class GradSet:
         if stream is not None:
             with _on(stream):
                 return self.partials()
-        dev = self._ready()
+        s = self._ready()
         p = torch.empty(_lib.QL_GRAD_PARTIALS, dtype=_F64, device=self.device)
-        qlinear_grad_norm(self.table.data_ptr(), len(self.grads), self.units, p.data_ptr(),
-                          _stream(dev))
+        qlinear_grad_norm(self.table.data_ptr(), len(self.grads), self.units, p.data_ptr(), s)
         return p
 
     def clip(self, max_norm: float, partials=None, stream=None):
@@ -378,10 +382,10 @@ class GradSet:
         if stream is not None:
             with _on(stream):
                 return self.clip(max_norm, partials)
-        dev = self._ready()
+        s = self._ready()
         p = self.partials() if partials is None else partials
-        at = _flat(p, "partials", dev, _F64, (_lib.QL_GRAD_PARTIALS,))
+        at = _flat(p, "partials", self.device.index, _F64, (_lib.QL_GRAD_PARTIALS,))
         norm = torch.empty((), dtype=_F32, device=self.device)
         qlinear_grad_clip(self.table.data_ptr(), len(self.grads), self.units, at, max_norm,
-                          norm.data_ptr(), _stream(dev))
+                          norm.data_ptr(), s)
         return norm
