@@ -168,6 +168,26 @@ ql_status check_image(const ql_norm* d, const char* name, const void* p, int64_t
   return QL_OK;
 }
 
+// Two images of an output must not share an element: workgroups of both would
+// write it. They share one where d batch strides and some row strides, d < batch,
+// come within `channels` of each other.
+ql_status check_apart(const ql_norm* d, const char* name, int64_t batch, int64_t row) {
+  typedef __int128 wide;
+  const wide last = d->positions - 1;
+  bool apart = d->batch == 1 || (wide)batch >= last * row + d->channels ||  // one after another
+               (batch >= d->channels && row >= (wide)(d->batch - 1) * batch + d->channels);
+  if (!apart && batch >= d->channels) {  // neither contains the other: image by image
+    apart = true;
+    for (int32_t i = 1; apart && i < d->batch; ++i) {
+      const wide q = (wide)i * batch / row, r = (wide)i * batch % row;
+      apart = !(q <= last && r < d->channels) && !(q + 1 <= last && row - r < d->channels);
+    }
+  }
+  if (apart) return QL_OK;
+  return fail(QL_ERR_ARG, "%s: images overlap (batch stride %lld, row stride %lld)", name,
+              (long long)batch, (long long)row);
+}
+
 int64_t norm_ws(const ql_norm* d, bool grad) {
   return ql::norm_ws_bytes(d->batch, d->positions, d->channels, d->groups,
                            (int)size_of(d->x_dtype), grad);
@@ -393,6 +413,7 @@ ql_status qlinear_group_norm(const ql_norm* d, const void* x, int64_t x_batch, i
     return fail(QL_ERR_ARG, "y is x with other strides");
   QL_CHECK(check_workspace(workspace, workspace_bytes,
                            norm_ws(d, false)));
+  QL_CHECK(check_apart(d, "y", y_batch, y_row));
   ql::NormArgs a = norm_args(d);
   a.x = x;
   a.xb = x_batch;
@@ -432,6 +453,7 @@ ql_status qlinear_group_norm_grad(const ql_norm* d, const void* dy, int64_t dy_b
       return fail(QL_ERR_ARG, "dx is dy or x with other strides");
     QL_CHECK(check_workspace(workspace, workspace_bytes,
                              norm_ws(d, true)));
+    QL_CHECK(check_apart(d, "dx", dx_batch, dx_row));
   }
   a.dy = dy;
   a.dyb = dy_batch;

@@ -412,6 +412,8 @@ ql_status qlinear_lora_grad(const ql_lora* d, const void* X, int64_t ldx, int32_
  * An image is [positions, channels]; element (b, l, c) of x lies at
  * b * batch stride + l * row stride + c (strides in elements, row stride >=
  * channels), so an NHWC tensor or a slice of its channels is taken as it is.
+ * Images of an input may overlap (a batch stride of 0 repeats one); those of an
+ * output may not.
  */
 typedef enum { QL_ACT_NONE = 0, QL_ACT_SILU = 1 } ql_act;
 typedef struct {

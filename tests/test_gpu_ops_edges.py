@@ -11,7 +11,7 @@ import math
 import pytest
 
 from tests.parity import say
-from tests.test_gpu_ops import EPS, _dt, _round, _within
+from tests.test_gpu_ops import EPS, _dt, _norm_ref, _round, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -160,6 +160,34 @@ def test_group_norm_squares_past_fp32(torch, shape):
     y, mean, rstd = GroupNormAct(ga, be, G, act="none").forward(x, stats=True)
     assert not bool(rstd.any()) and bool(torch.isfinite(mean).all())
     assert torch.equal(y, be.expand(B, L, C))
+
+
+def test_group_norm_output_strides(torch):
+    # outputs whose images do not overlap are taken in any order: positions first,
+    # images between one another's rows, gaps; repeated images as input
+    from bit_post_quantization_amd import GroupNormAct, QLError
+    B, L, C, G = 3, 41, 24, 4
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.empty((B, L, C), device="cuda").normal_(generator=g)
+    ga, be = _affine(torch, C)
+    op = GroupNormAct(ga, be, G)
+    ref, tol, _, _ = _norm_ref(torch, x, ga, be, G, 1e-5, "silu")
+    tol = tol + _round(torch, ref, x.dtype)
+    for yb, yr in ((C, B * C), (C + 1, 4 * C), (L * C, C), (L * (C + 4), C + 4), (3 * C, 2 * C * L),
+                   (5 * C, 4 * C)):
+        buf = torch.full((B * yb + L * yr,), 7.0, device="cuda")
+        out = buf.as_strided((B, L, C), (yb, yr, 1))
+        op.forward(x, out=out)
+        _within(out, ref, tol, f"strides {yb}, {yr}")
+        out.fill_(7.0)
+        assert bool((buf == 7.0).all())
+    one = x[:1].expand(B, L, C)
+    _within(op.forward(one), ref[:1].expand(B, L, C), tol[:1].expand(B, L, C), "one image repeated")
+    for out in (torch.empty((1, L, C), device="cuda").expand(B, L, C),
+                torch.empty(B * L * C, device="cuda").as_strided((B, L, C), (L * C - 1, C, 1))):
+        with pytest.raises(QLError):
+            op.forward(x, out=out)
 
 
 # ---------------------------------------------------------------- clipping ----

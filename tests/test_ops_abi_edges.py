@@ -1,0 +1,35 @@
+"""More host-side argument checks of the operators beside the layer, on the CPU: as in
+test_ops_abi, every refusal is decided before anything is enqueued. (No call here may
+be one that is accepted: its addresses lead nowhere.)"""
+import ctypes
+
+import pytest
+
+from bit_post_quantization_amd import _lib
+from tests.test_ops_abi import A, U, _msg, _norm
+
+
+def _overlap(batch, positions, channels, yb, yr):
+    at = [b * yb + r * yr + c for b in range(batch) for r in range(positions)
+          for c in range(channels)]
+    return len(set(at)) < len(at)
+
+
+@pytest.mark.parametrize("batch,positions,channels,yb,yr", [
+    (2, 9, 4, 0, 4),     # an expanded tensor
+    (2, 1, 4, 3, 4),     # one position an image
+    (3, 9, 4, 35, 4),    # the last position of an image is the next one's first
+    (2, 5, 4, 7, 8),     # a row of one image reaches into a row of the other
+    (5, 4, 4, 6, 25),    # an image's rows leave room for four others, not for five
+    (4, 7, 2, 3, 8),     # only the fourth image meets the first one's next row but one
+])
+def test_norm_refuses_overlapping_images_of_an_output(batch, positions, channels, yb, yr):
+    assert _overlap(batch, positions, channels, yb, yr)
+    L = _lib.load()
+    d = ctypes.byref(_norm(batch=batch, positions=positions, channels=channels, groups=1))
+    xb = positions * channels
+    st = L.qlinear_group_norm(d, A, xb, channels, 2 * A, yb, yr, U, U, A, 1 << 30, U)
+    assert st == _lib.QL_ERR_ARG and "y: images overlap" in _msg()
+    st = L.qlinear_group_norm_grad(d, A, xb, channels, A, xb, channels, A, A, 2 * A, yb, yr, A, A,
+                                   A, 1 << 30, U)
+    assert st == _lib.QL_ERR_ARG and "dx: images overlap" in _msg()
