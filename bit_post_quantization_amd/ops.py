@@ -329,9 +329,21 @@ class GroupNormAct:
 
 # ---------------------------------------------------------------- clipping ----
 
+def _order(t):
+    """The strides of a tensor that fills its storage's span without gaps or
+    repeats (channels last, transposed, ...), None for any other."""
+    n = 1
+    for stride, size in sorted((s, k) for s, k in zip(t.stride(), t.shape) if k != 1):
+        if stride != n:
+            return None
+        n *= size
+    return [s for s, k in zip(t.stride(), t.shape) if k != 1]
+
+
 class GradSet:
     """Gradients to be clipped by their global norm, in place or into ``out``
-    (tensors of the same sizes, f32 or bf16 each).
+    (tensors of the same sizes, f32 or bf16 each). They may lie in any dense order
+    (channels last, transposed); an ``out`` lies in its gradient's order.
 
     Made once for gradients that stay where they are (the set holds the tensors
     and a device table of their addresses); make a new one when a tensor is
@@ -343,11 +355,17 @@ class GradSet:
         _need(len(self.grads) == len(self.out), "out must list one tensor for each gradient")
         dev, rows, unit = _device(), [], 0
         for g, o in zip(self.grads, self.out):
+            n, plain = g.numel(), True
             for t, name in ((g, "gradient"), (o, "out")):
                 _need(t.dtype in _DT, f"{name} is {t.dtype}: f32 or bf16 only")
-                _flat(t, name, dev, t.dtype, t.shape)
-            n = g.numel()
+                if t.get_device() != dev:
+                    _refuse(t, name, dev, t.dtype, t.shape)
+                if not t.is_contiguous():
+                    plain = False
+                    _need(_order(t) is not None, f"{name} is not dense")
             _need(o.numel() == n, "out and its gradient differ in size")
+            _need(plain or o is g or (o.shape == g.shape and _order(o) == _order(g)),
+                  "out lies in another order than its gradient")
             _need(_ptr(g) != _ptr(o) or g.dtype == o.dtype or n == 0,
                   "out is its gradient with another type")
             rows.append((_ptr(g), _ptr(o), n, unit, _DT[g.dtype] | _DT[o.dtype] << 32))

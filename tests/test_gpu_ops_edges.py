@@ -211,3 +211,38 @@ def test_clip_table_outlives_its_set_on_another_stream(torch):
     assert abs(float(norm) - want) <= 2 * EPS * want
     _within(a, torch.full((5000,), 2.0 / (want + 1e-6), dtype=torch.float64, device="cuda"),
             2.0 / want * 4 * EPS, "clipped")
+
+
+def test_clip_of_dense_gradients_in_any_order(torch):
+    # the norm and the scaling need no order: channels-last images' and transposed
+    # gradients go as they are, an out in the same order
+    from bit_post_quantization_amd import GradSet, QLError
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+
+    def make():
+        a = torch.empty((48, 33, 3, 5), device="cuda").normal_(generator=g)
+        return [a.to(memory_format=torch.channels_last),
+                torch.empty((70, 131), device="cuda").normal_(generator=g).bfloat16().t(),
+                torch.empty((6, 1, 9, 4), device="cuda").normal_(generator=g).permute(3, 1, 0, 2),
+                torch.empty((5, 7), device="cuda").normal_(generator=g)]
+
+    grads = make()
+    was = [t.double() for t in grads]
+    assert not any(t.is_contiguous() for t in grads[:3])
+    norm = math.sqrt(sum(float(t.square().sum()) for t in was))
+    outs = [torch.empty_like(t, dtype=torch.float32) for t in grads]
+    assert [o.stride() for o in outs] == [t.stride() for t in grads]
+    assert abs(float(GradSet(grads, out=outs).clip(2.0)) - norm) <= 2 * EPS * norm
+    GradSet(grads).clip(2.0)
+    for got in (outs, grads):
+        for a, b in zip(got, was):
+            r = b * (2.0 / (norm + 1e-6))
+            _within(a, r, 4 * EPS * r.abs() + _round(torch, r, a.dtype), "clipped")
+    for bad in (lambda: GradSet([grads[0]], out=[grads[0].contiguous()]),
+                lambda: GradSet([grads[1].contiguous()], out=[grads[1]]),
+                lambda: GradSet([grads[3].expand(2, 5, 7)]),
+                lambda: GradSet([grads[3][:, ::2]]),
+                lambda: GradSet([grads[0][:, 1:]])):
+        with pytest.raises(QLError):
+            bad()
