@@ -343,7 +343,9 @@ def _order(t):
 class GradSet:
     """Gradients to be clipped by their global norm, in place or into ``out``
     (tensors of the same sizes, f32 or bf16 each). They may lie in any dense order
-    (channels last, transposed); an ``out`` lies in its gradient's order.
+    (channels last, transposed); an ``out`` lies in its gradient's order. What is
+    written overlaps nothing else that is listed: a gradient that two parameters
+    share is listed once.
 
     Made once for gradients that stay where they are (the set holds the tensors
     and a device table of their addresses); make a new one when a tensor is
@@ -353,7 +355,7 @@ class GradSet:
         self.grads = list(grads)
         self.out = self.grads if out is None else list(out)
         _need(len(self.grads) == len(self.out), "out must list one tensor for each gradient")
-        dev, rows, unit = _device(), [], 0
+        dev, rows, unit, spans = _device(), [], 0, []
         for g, o in zip(self.grads, self.out):
             n, plain = g.numel(), True
             for t, name in ((g, "gradient"), (o, "out")):
@@ -368,8 +370,19 @@ class GradSet:
                   "out lies in another order than its gradient")
             _need(_ptr(g) != _ptr(o) or g.dtype == o.dtype or n == 0,
                   "out is its gradient with another type")
-            rows.append((_ptr(g), _ptr(o), n, unit, _DT[g.dtype] | _DT[o.dtype] << 32))
+            at, to = _ptr(g), _ptr(o)
+            rows.append((at, to, n, unit, _DT[g.dtype] | _DT[o.dtype] << 32))
+            if n:
+                spans.append((to, to + n * o.element_size(), True))
+                if at != to:
+                    spans.append((at, at + n * g.element_size(), False))
             unit += -(-n // _lib.QL_GRAD_UNIT)
+        # Different workgroups write what they write and read what they read.
+        read = written = 0  # ends of what lies before
+        for lo, hi, out in sorted(spans):
+            _need(lo >= (max(read, written) if out else written),
+                  "an out overlaps another one or another gradient (or a gradient is listed twice)")
+            read, written = (read, max(written, hi)) if out else (max(read, hi), written)
         self.units = unit
         self.device = torch.device("cuda", dev)
         self._made_on = _stream(dev)

@@ -465,7 +465,8 @@ ql_status qlinear_group_norm_grad(const ql_norm* d, const void* dy, int64_t dy_b
 #define QL_GRAD_PARTIALS 1024
 typedef struct {
   const void* src;    /* contiguous, aligned to its element; NULL is skipped */
-  void* dst;          /* qlinear_grad_clip: out; src itself (same dtype) for in place */
+  void* dst;          /* qlinear_grad_clip: out; src itself (same dtype) for in place, else it
+                         overlaps nothing else that is listed */
   int64_t n;          /* elements, >= 0 */
   int64_t start;      /* first unit */
   int32_t src_dtype, dst_dtype; /* ql_dtype */

@@ -246,3 +246,28 @@ def test_clip_of_dense_gradients_in_any_order(torch):
                 lambda: GradSet([grads[0][:, 1:]])):
         with pytest.raises(QLError):
             bad()
+
+
+def test_clip_refuses_overlapping_outputs(torch):
+    from bit_post_quantization_amd import GradSet, QLError
+    buf = torch.zeros(9000, device="cuda")
+    a, b, c = buf[:4000], buf[3999:6000], buf[6000:]
+    bad = [
+        lambda: GradSet([a, a]),                              # would be scaled twice, or once
+        lambda: GradSet([a, b]),
+        lambda: GradSet([c, a], out=[b, torch.empty_like(a)]),  # an out over another's gradient
+        lambda: GradSet([a.clone(), c.clone()], out=[buf[:4000], buf[1000:4000]]),
+        lambda: GradSet([a], out=[buf[1:4001]]),              # over its own, shifted
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(QLError):
+            f()
+            pytest.fail(f"case {i} was accepted")
+    e = torch.empty(0, device="cuda")
+    out = torch.empty(8000, device="cuda")
+    a.fill_(3.0)
+    # neighbours, empty ones, and one gradient read twice into two places are fine
+    s = GradSet([a, a, e, e], out=[out[:4000], out[4000:], e, e])
+    want = 3.0 * math.sqrt(8000)
+    assert abs(float(s.clip(1e9)) - want) <= 2 * EPS * want and bool((out == 3.0).all())
+    GradSet([buf[:4000], buf[4000:]]).clip(1.0)
