@@ -200,19 +200,26 @@ class LoraAdapters:
                      ldy, _ptr(S), _ptr(ws), nb, _stream(dev))
         return (out, S) if save else out
 
-    def grad(self, X, row_offsets, adapter, S, dY, need_dx: bool = True, stream=None):
+    def grad(self, X, row_offsets, adapter, S, dY, need_dx: bool = True, stream=None, out=None):
         """(dX, dA, dB) of :meth:`apply` (cfg = 0): dX is the adapters' part only
-        (None without ``need_dx``); dA, dB in the adapters' type."""
+        (None without ``need_dx``); dA, dB in the adapters' type, written into the
+        pair ``out`` where it is given (every element, so that one :class:`GradSet`
+        serves all steps)."""
         if stream is not None:
             with _on(stream):
-                return self.grad(X, row_offsets, adapter, S, dY, need_dx)
+                return self.grad(X, row_offsets, adapter, S, dY, need_dx, out=out)
         dev, M = _device(), X.shape[0]
         ldx = _rows(X, "X", dev, self.x_dtype, (M, self.K))
         lddy = _rows(dY, "dY", dev, _F32, (M, self.N))
         s_ptr = _flat(S, "S", dev, _F32, (M, self.rank))
         q = self._requests(dev, row_offsets, adapter)
         dX = torch.empty((M, self.K), dtype=self.x_dtype, device=X.device) if need_dx else None
-        dA, dB = torch.empty_like(self.A), torch.empty_like(self.B)
+        if out is None:
+            dA, dB = torch.empty_like(self.A), torch.empty_like(self.B)
+        else:
+            dA, dB = out
+            _flat(dA, "dA", dev, self.A.dtype, self.A.shape)
+            _flat(dB, "dB", dev, self.B.dtype, self.B.shape)
         nb = self._workspace_bytes(M, q.n_requests, 0, 1)
         ws = torch.empty(nb, dtype=torch.uint8, device=X.device)
         qlinear_lora_grad(self.desc, X.data_ptr(), ldx, M, q, s_ptr, dY.data_ptr(), lddy, _ptr(dX),
@@ -305,12 +312,12 @@ class GroupNormAct:
                            _ptr(ws), nb, _stream(dev))
         return (out, mean, rstd) if stats else out
 
-    def grad(self, dy, x, mean, rstd, stream=None):
+    def grad(self, dy, x, mean, rstd, stream=None, out=None):
         """(dx, dgamma, dbeta); the last two in gamma's type, None where the
-        parameter is."""
+        parameter is, written into the pair ``out`` where it is given."""
         if stream is not None:
             with _on(stream):
-                return self.grad(dy, x, mean, rstd)
+                return self.grad(dy, x, mean, rstd, out=out)
         dev, dt, shape = _device(), x.dtype, x.shape
         _need(dt in _DT, f"x is {dt}: f32 or bf16 only")
         B, L, C, xb, xr = _image(x, "x", dev, dt, shape)
@@ -319,8 +326,15 @@ class GroupNormAct:
         m = _flat(mean, "mean", dev, _F32, (B, self.groups))
         r = _flat(rstd, "rstd", dev, _F32, (B, self.groups))
         dx = _like(x)
-        dgamma = None if self.gamma is None else torch.empty_like(self.gamma)
-        dbeta = None if self.beta is None else torch.empty_like(self.beta)
+        if out is None:
+            dgamma = None if self.gamma is None else torch.empty_like(self.gamma)
+            dbeta = None if self.beta is None else torch.empty_like(self.beta)
+        else:
+            dgamma, dbeta = out
+            for t, p, name in ((dgamma, self.gamma, "dgamma"), (dbeta, self.beta, "dbeta")):
+                _need((t is None) == (p is None), f"{name} is given without its parameter, or not")
+                if t is not None:
+                    _flat(t, name, dev, p.dtype, p.shape)
         ws = torch.empty(nb, dtype=torch.uint8, device=x.device) if nb else None
         qlinear_group_norm_grad(d, dy.data_ptr(), db, dr, x.data_ptr(), xb, xr, m, r, dx.data_ptr(),
                                 L * C, C, _ptr(dgamma), _ptr(dbeta), _ptr(ws), nb, _stream(dev))

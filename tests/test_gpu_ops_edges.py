@@ -271,3 +271,43 @@ def test_clip_refuses_overlapping_outputs(torch):
     want = 3.0 * math.sqrt(8000)
     assert abs(float(s.clip(1e9)) - want) <= 2 * EPS * want and bool((out == 3.0).all())
     GradSet([buf[:4000], buf[4000:]]).clip(1.0)
+
+
+# ---------------------------------------------------------- kept gradients ----
+
+def test_gradients_into_given_tensors(torch):
+    # parameters' gradients that stay where they are, so that a set of them is made
+    # once: the same bits as in new tensors, every element written
+    from bit_post_quantization_amd import GradSet, GroupNormAct, QLError
+    from tests.test_gpu_ops import Case
+    c = Case(torch, [20, 0, 31], [0, 1, 2], 64, 40, 8, "f32", "bf16", ranks=(8, 3), seed=9)
+    L = c.layer()
+    _, S = L.apply(c.X, c.off, c.d_ids, c.base, save=True)
+    want = L.grad(c.X, c.off, c.d_ids, S, c.dY)
+    x = torch.randn(2, 50, 16, device="cuda")
+    ga, be = _affine(torch, 16)
+    op = GroupNormAct(ga, be, 4)
+    _, mean, rstd = op.forward(x, stats=True)
+    nwant = op.grad(x, x, mean, rstd)
+    kept = [torch.full_like(t, float("nan")) for t in (*want[1:], *nwant[1:])]
+    s = GradSet(kept)
+    st = torch.cuda.Stream()
+    for k in range(3):
+        stream = st if k == 2 else None
+        st.wait_stream(torch.cuda.current_stream())
+        dX, dA, dB = L.grad(c.X, c.off, c.d_ids, S, c.dY, out=kept[:2], stream=stream)
+        dx, dg, db = op.grad(x, x, mean, rstd, out=kept[2:], stream=stream)
+        torch.cuda.synchronize()
+        assert dA is kept[0] and dB is kept[1] and dg is kept[2] and db is kept[3]
+        assert torch.equal(dX, want[0]) and torch.equal(dx, nwant[0])
+        assert all(torch.equal(a, b) for a, b in zip(kept, (*want[1:], *nwant[1:])))
+        norm = math.sqrt(sum(float(t.double().square().sum()) for t in kept))
+        assert abs(float(s.clip(0.5 * norm)) - norm) <= 2 * EPS * norm
+    for bad in (lambda: L.grad(c.X, c.off, c.d_ids, S, c.dY, out=(kept[1], kept[0])),
+                lambda: L.grad(c.X, c.off, c.d_ids, S, c.dY, out=(kept[0].float(), kept[1])),
+                lambda: L.grad(c.X, c.off, c.d_ids, S, c.dY, out=(kept[0].cpu(), kept[1])),
+                lambda: op.grad(x, x, mean, rstd, out=(kept[2], None)),
+                lambda: op.grad(x, x, mean, rstd, out=(kept[2][:8], kept[3])),
+                lambda: GroupNormAct(ga, None, 4).grad(x, x, mean, rstd, out=(kept[2], kept[3]))):
+        with pytest.raises(QLError):
+            bad()

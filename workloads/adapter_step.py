@@ -46,6 +46,10 @@ class AdapterLayer:
         self.scales = torch.full((adapters,), 2.0, device="cuda")
         self.norm = GroupNormAct(self.gamma, self.beta, groups, act="silu")
         self.lora = LoraAdapters(self.A, self.B, scales=self.scales)
+        # The parameters' gradients stay where they are, so that their clipping is
+        # set up once.
+        self.grads = [torch.empty_like(p) for p in self.parameters()]
+        self.clipping = GradSet(self.grads)
 
     def parameters(self):
         return [self.A, self.B, self.gamma, self.beta]
@@ -61,12 +65,12 @@ class AdapterLayer:
         return (out[0], (image, rows, mean, rstd, out[1])) if save else out
 
     def backward(self, dY, saved, row_offsets, adapter):
-        """Gradients of :meth:`parameters`."""
+        """Gradients of :meth:`parameters`: ``self.grads``, written anew."""
         image, rows, mean, rstd, S = saved
-        dx, dA, dB = self.lora.grad(rows, row_offsets, adapter, S, dY)
+        dx, _, _ = self.lora.grad(rows, row_offsets, adapter, S, dY, out=self.grads[:2])
         dx.addmm_(dY, self.W_deq)  # through the frozen linear
-        _, dgamma, dbeta = self.norm.grad(dx.view_as(image), image, mean, rstd)
-        return [dA, dB, dgamma, dbeta]
+        self.norm.grad(dx.view_as(image), image, mean, rstd, out=self.grads[2:])
+        return self.grads
 
 
 def train(steps: int = 20, batch: int = 4, positions: int = 256, N: int = 1152, K: int = 1152,
@@ -87,7 +91,7 @@ def train(steps: int = 20, batch: int = 4, positions: int = 256, N: int = 1152, 
         diff = Y - target
         losses.append(float(diff.square().mean()))
         grads = layer.backward(diff * (2.0 / diff.shape[0]), saved, off, ids)
-        GradSet(grads).clip(max_norm)
+        layer.clipping.clip(max_norm)
         for p, d in zip(layer.parameters(), grads):
             p.sub_(d, alpha=lr)
     return losses
