@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_stats(StatsK a) {
 
 // mean and rstd of every image's group from its chunks: one wave a group.
 struct StatsOut {
-  float2* stats;  // [B][G]: mean, rstd
+  float2* stats;  // [B][G]: mean, rstd; or nullptr
   float* mean;    // the caller's, or nullptr
   float* rstd;
   float eps;
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(256) void k_norm_stats_join(const double2* part, St
   if (lane != 0) return;
   const double n = (double)s.L * s.cpg, m = S / n, var = variance(Q / n - m * m);
   const float2 r{(float)m, (float)(1.0 / sqrt(var + (double)o.eps))};
-  o.stats[id] = r;
+  if (o.stats) o.stats[id] = r;
   if (o.mean) o.mean[id] = r.x;
   if (o.rstd) o.rstd[id] = r.y;
 }
@@ -921,7 +921,16 @@ int64_t norm_ws_bytes(int B, int L, int C, int G, int es, bool grad) {
   return ((int64_t)B * C + (int64_t)B * G + (int64_t)B * chunks * C) * (int64_t)sizeof(float2);
 }
 
-hipError_t launch_group_norm(const NormArgs& a, hipStream_t s) { return norm_types(a, false, s); }
+hipError_t launch_group_norm(const NormArgs& a, hipStream_t s) {
+  if (a.L > 0) return norm_types(a, false, s);
+  Shape e{};  // no positions: 0 / 0 for the statistics, no outputs
+  e.B = a.B;
+  e.G = a.G;
+  e.cpg = a.C / a.G;
+  hipLaunchKernelGGL(k_norm_stats_join, dim3((a.B * a.G + 3) / 4), dim3(256), 0, s, nullptr,
+                     StatsOut{nullptr, a.mean, a.rstd, a.eps}, e);
+  return hipGetLastError();
+}
 
 hipError_t launch_group_norm_grad(const NormArgs& a, hipStream_t s) {
   return norm_types(a, true, s);

@@ -404,16 +404,21 @@ ql_status qlinear_group_norm(const ql_norm* d, const void* x, int64_t x_batch, i
                              void* y, int64_t y_batch, int64_t y_row, float* mean, float* rstd,
                              void* workspace, int64_t workspace_bytes, void* stream) {
   QL_CHECK(check_norm(d));
-  if (d->batch == 0 || d->positions == 0) return ok();  // empty tensors may carry NULL pointers
-  QL_CHECK(check_image(d, "x", x, x_batch, x_row));
-  QL_CHECK(check_image(d, "y", y, y_batch, y_row));
+  if (d->batch == 0) return ok();
+  if (d->positions > 0) {  // empty tensors may carry NULL pointers
+    QL_CHECK(check_image(d, "x", x, x_batch, x_row));
+    QL_CHECK(check_image(d, "y", y, y_batch, y_row));
+  }
   if (!aligned(mean, 4) || !aligned(rstd, 4))
     return fail(QL_ERR_ARG, "mean and rstd must be 4-byte aligned");
-  if (x == y && (x_batch != y_batch || x_row != y_row))
-    return fail(QL_ERR_ARG, "y is x with other strides");
-  QL_CHECK(check_workspace(workspace, workspace_bytes,
-                           norm_ws(d, false)));
-  QL_CHECK(check_apart(d, "y", y_batch, y_row));
+  if (d->positions > 0) {
+    if (x == y && (x_batch != y_batch || x_row != y_row))
+      return fail(QL_ERR_ARG, "y is x with other strides");
+    QL_CHECK(check_workspace(workspace, workspace_bytes, norm_ws(d, false)));
+    QL_CHECK(check_apart(d, "y", y_batch, y_row));
+  } else if (!mean && !rstd) {
+    return ok();
+  }
   ql::NormArgs a = norm_args(d);
   a.x = x;
   a.xb = x_batch;
@@ -451,8 +456,7 @@ ql_status qlinear_group_norm_grad(const ql_norm* d, const void* dy, int64_t dy_b
     if ((dx == dy && (dx_batch != dy_batch || dx_row != dy_row)) ||
         (dx == x && (dx_batch != x_batch || dx_row != x_row)))
       return fail(QL_ERR_ARG, "dx is dy or x with other strides");
-    QL_CHECK(check_workspace(workspace, workspace_bytes,
-                             norm_ws(d, true)));
+    QL_CHECK(check_workspace(workspace, workspace_bytes, norm_ws(d, true)));
     QL_CHECK(check_apart(d, "dx", dx_batch, dx_row));
   }
   a.dy = dy;

@@ -438,7 +438,8 @@ ql_status qlinear_group_norm_workspace(const ql_norm* d, int32_t grad, int64_t* 
  * Statistics are joined in fp64; squares are taken in fp32, so values more than
  * 1.8e19 apart can make a group's variance infinite and its rstd 0. A group with
  * a NaN or an infinity has rstd NaN. y may be x itself with the same strides.
- *   mean, rstd : NULL, or DEVICE fp32 out [batch, groups] for the gradient.
+ *   mean, rstd : NULL, or DEVICE fp32 out [batch, groups] for the gradient (NaN
+ *                where there are no positions).
  */
 ql_status qlinear_group_norm(const ql_norm* d, const void* x, int64_t x_batch, int64_t x_row,
                              void* y, int64_t y_batch, int64_t y_row, float* mean, float* rstd,

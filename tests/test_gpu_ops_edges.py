@@ -190,6 +190,24 @@ def test_group_norm_output_strides(torch):
             op.forward(x, out=out)
 
 
+def test_group_norm_statistics_without_positions(torch):
+    # 0 / 0: written as NaN, not left as they were
+    from bit_post_quantization_amd import GroupNormAct, ops
+    op = GroupNormAct(None, None, 2, channels=8)
+    d, nb = op._of(torch.float32, 3, 0, 8, 0)
+    assert nb == 0
+    for which in ((True, True), (True, False), (False, True)):
+        st = torch.full((2, 3, 2), 7.0, device="cuda")
+        at = [t.data_ptr() if w else None for t, w in zip(st, which)]
+        ops.qlinear_group_norm(d, None, 0, 8, None, 0, 8, *at, None, 0,
+                               torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        for t, w in zip(st, which):
+            assert bool(torch.isnan(t).all()) if w else bool((t == 7.0).all())
+    y, mean, rstd = op.forward(torch.empty((3, 0, 8), device="cuda"), stats=True)
+    assert y.shape == (3, 0, 8) and bool(torch.isnan(mean).all()) and bool(torch.isnan(rstd).all())
+
+
 # ---------------------------------------------------------------- clipping ----
 
 def test_clip_table_outlives_its_set_on_another_stream(torch):
