@@ -1378,12 +1378,15 @@ int lora_y_splits(int rows, int n_req, int N) {
   return outer_splits(rows, N, (int)(all - ds));
 }
 
-// A launch holds fewer than 2^32 threads along its grid.
+// A launch holds fewer than 2^32 threads along its grid. The gradient's dY side has
+// a workgroup for every tile of rows (or at most 256) and, beside them, 352 at most or
+// one for every chunk of N.
 bool lora_fits(int rows, int n_req, int N, bool grad) {
   Requests q{};
   q.rows = rows;
   q.n = n_req;
-  int64_t threads = ((int64_t)max_tiles(q, 16) + 512) * 512;
+  const int64_t chunks = ((int64_t)N + kOuterCols - 1) / kOuterCols + 256;
+  int64_t threads = ((int64_t)max_tiles(q, 16) + (grad && chunks > 512 ? chunks : 512)) * 512;
   if (!grad && two_launches(rows, N)) {
     const int64_t shares = ((int64_t)N + kExpandCols - 1) / kExpandCols;
     threads = expand_tiles(rows, n_req) * (shares > 4 ? shares : 4) * 256;

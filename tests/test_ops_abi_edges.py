@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from bit_post_quantization_amd import _lib
-from tests.test_ops_abi import A, U, _msg, _norm
+from tests.test_ops_abi import A, U, _lora, _msg, _norm, _req
 
 
 def _overlap(batch, positions, channels, yb, yr):
@@ -33,3 +33,18 @@ def test_norm_refuses_overlapping_images_of_an_output(batch, positions, channels
     st = L.qlinear_group_norm_grad(d, A, xb, channels, A, xb, channels, A, A, 2 * A, yb, yr, A, A,
                                    A, 1 << 30, U)
     assert st == _lib.QL_ERR_ARG and "dx: images overlap" in _msg()
+
+
+@pytest.mark.parametrize("N", [(1 << 31) - 1, (1 << 31) - 600, (1 << 31) - 65792])
+def test_lora_gradient_counts_the_chunks_of_n(N):
+    # a grid (and, at the end, 32-bit column numbers) that wide outputs alone pass
+    L = _lib.load()
+    n = ctypes.c_int64()
+    d = ctypes.byref(_lora(N=N, rank=1))
+    assert L.qlinear_lora_workspace(d, 1, 1, 0, 1, ctypes.byref(n)) == _lib.QL_ERR_UNSUPPORTED
+    assert "one launch" in _msg()
+    assert L.qlinear_lora_grad(d, A, 64, 1, ctypes.byref(_req()), A, A, N, A, 64, A, A, A, 1 << 62,
+                               U) == _lib.QL_ERR_UNSUPPORTED
+    # the largest that stays below it
+    d = ctypes.byref(_lora(N=(1 << 31) - 66560, rank=1))
+    assert L.qlinear_lora_workspace(d, 1, 1, 0, 1, ctypes.byref(n)) == _lib.QL_OK
