@@ -72,7 +72,8 @@ ql_status check_lora(const ql_lora* d, int32_t M, int32_t n_requests) {
   if (!dtype_ok(d->w_dtype)) return fail(QL_ERR_ARG, "bad w_dtype %d", (int)d->w_dtype);
   if (M < 0) return fail(QL_ERR_ARG, "M = %d must be >= 0", M);
   if (M > kMaxRows) return fail(QL_ERR_UNSUPPORTED, "M = %d exceeds %d rows", M, kMaxRows);
-  if (n_requests < 1) return fail(QL_ERR_ARG, "n_requests = %d must be >= 1", n_requests);
+  if (n_requests < (M > 0 ? 1 : 0))  // a batch without rows may be one without requests
+    return fail(QL_ERR_ARG, "n_requests = %d must be >= %d", n_requests, M > 0 ? 1 : 0);
   if (n_requests > kMaxRows)
     return fail(QL_ERR_UNSUPPORTED, "n_requests = %d exceeds %d", n_requests, kMaxRows);
   if ((int64_t)d->N * d->rank >= (int64_t)1 << 31)
@@ -105,6 +106,7 @@ struct GradWs {
 };
 GradWs grad_ws(const ql_lora* d, int32_t M, int32_t n) {
   GradWs w;
+  if (n < 1) n = 1;
   w.s_splits = ql::lora_ds_splits(M, n, d->N);
   w.x_splits = ql::lora_x_splits(M, d->K);
   w.y_splits = ql::lora_y_splits(M, n, d->N);

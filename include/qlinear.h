@@ -357,7 +357,7 @@ typedef struct {
  * empty); others are clamped, never followed out of the tensors, and the rows
  * they leave out are unspecified. */
 typedef struct {
-  int32_t n_requests;          /* >= 1 */
+  int32_t n_requests;          /* >= 1; 0 with M = 0 */
   const int32_t* row_offsets;  /* DEVICE [n_requests + 1] */
   const int32_t* adapter;      /* DEVICE [n_requests] */
 } ql_requests;

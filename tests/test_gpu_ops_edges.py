@@ -100,6 +100,20 @@ def test_lora_gradient_ranks_that_cancel(torch, x, rank):
                 f"dX, ranks {3 * k}..")
 
 
+def test_lora_batch_without_requests(torch):
+    from bit_post_quantization_amd import LoraAdapters
+    A, B = torch.randn(2, 4, 32, device="cuda"), torch.randn(2, 24, 4, device="cuda")
+    L = LoraAdapters(A, B)
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    off = torch.zeros(1, dtype=torch.int32, device="cuda")
+    X, dY = torch.empty(0, 32, device="cuda"), torch.empty(0, 24, device="cuda")
+    for cfg in (0, 1):
+        Y, S = L.apply(X, off, none, cfg=cfg, save=True)
+        assert Y.shape == (0, 24) and S.shape == (0, 4)
+    dX, dA, dB = L.grad(X, off, none, S, dY)
+    assert dX.shape == (0, 32) and not bool(dA.any()) and not bool(dB.any())
+
+
 # -------------------------------------------------------------- group norm ----
 
 def _affine(t, C, w="f32", seed=0):

@@ -48,3 +48,17 @@ def test_lora_gradient_counts_the_chunks_of_n(N):
     # the largest that stays below it
     d = ctypes.byref(_lora(N=(1 << 31) - 66560, rank=1))
     assert L.qlinear_lora_workspace(d, 1, 1, 0, 1, ctypes.byref(n)) == _lib.QL_OK
+
+
+def test_lora_requests_may_be_none_without_rows():
+    L = _lib.load()
+    n = ctypes.c_int64()
+    d = ctypes.byref(_lora())
+    for grad in (0, 1):
+        assert L.qlinear_lora_workspace(d, 0, 0, 0, grad, ctypes.byref(n)) == _lib.QL_OK
+        assert L.qlinear_lora_workspace(d, 1, 0, 0, grad, ctypes.byref(n)) == _lib.QL_ERR_ARG
+        assert L.qlinear_lora_workspace(d, 0, -1, 0, grad, ctypes.byref(n)) == _lib.QL_ERR_ARG
+    q = ctypes.byref(_req(n_requests=0, row_offsets=U, adapter=U))
+    assert L.qlinear_lora(d, U, 64, 0, q, 0, 1.0, U, 100, U, 100, U, U, 0, U) == _lib.QL_OK
+    assert L.qlinear_lora(d, A, 64, 1, ctypes.byref(_req(n_requests=0)), 0, 1.0, A, 100, A + 64, 100,
+                          U, A, 1 << 30, U) == _lib.QL_ERR_ARG
