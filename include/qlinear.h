@@ -338,6 +338,9 @@ ql_status qlinear_probe_mfma(const void* operands, int32_t iters, int32_t waves_
  * weight with its adapter is W + B A; here scale_a B_a A_a, and many adapters
  * at once). Adapter a is A_a [rank, K] and B_a [N, rank]; only its first
  * ranks[a] rank rows / columns are used (the storage past them is not).
+ * Infinities and NaN make non-finite what their products enter and nothing else; an
+ * infinity may come out as NaN there (an fp32 operand beside a bf16 one is
+ * multiplied in three bf16 parts, two of which may have the other sign).
  */
 typedef struct {
   int32_t N, K;          /* as in ql_desc: 1 <= N, K % 16 == 0, 16 <= K <= 65536 */

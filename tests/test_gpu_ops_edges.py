@@ -114,6 +114,36 @@ def test_lora_batch_without_requests(torch):
     assert dX.shape == (0, 32) and not bool(dA.any()) and not bool(dB.any())
 
 
+@pytest.mark.parametrize("x,w", [("f32", "f32"), ("f32", "bf16"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rank", [1, 16, 30, 70])
+def test_lora_non_finite_values_reach_their_products_only(torch, rank, x, w):
+    # one infinity or NaN in one operand at a time: what the formula has non-finite
+    # is non-finite, everything else is what it is without it, to the last bit
+    from tests.test_gpu_ops import Case
+    say(f"[lora non-finite] rank {rank} x {x} w {w}")
+    for v in (float("inf"), float("-inf"), float("nan")):
+        for what, at in (("X", (9, 17)), ("A", (1, rank - 1, 40)), ("B", (1, 33, rank // 2)),
+                         ("dY", (70, 5)), ("S", (44, 0))):
+            c = Case(torch, [40, 41, 7], [0, 1, 0], 80, 50, rank, x, w, seed=8)
+            L = c.layer()
+            want, S = L.apply(c.X, c.off, c.d_ids, c.base, save=True)
+            grads = L.grad(c.X, c.off, c.d_ids, S, c.dY)
+            if what == "S":
+                S[at] = v
+            else:
+                getattr(c, what)[at] = v
+            if what not in ("S", "dY"):
+                got = L.apply(c.X, c.off, c.d_ids, c.base)
+                hit = ~torch.isfinite(c.forward()[0])
+                assert torch.equal(~torch.isfinite(got), hit), (what, v)
+                assert torch.equal(got[~hit], want[~hit]), (what, v)
+            for name, g, r, u in zip(("dX", "dA", "dB"), L.grad(c.X, c.off, c.d_ids, S, c.dY),
+                                     c.grads(S)[0], grads):
+                hit = ~torch.isfinite(r)
+                assert torch.equal(~torch.isfinite(g), hit), (what, v, name)
+                assert torch.equal(g[~hit], u[~hit]), (what, v, name)
+
+
 # -------------------------------------------------------------- group norm ----
 
 def _affine(t, C, w="f32", seed=0):
