@@ -144,6 +144,86 @@ def test_lora_non_finite_values_reach_their_products_only(torch, rank, x, w):
                 assert torch.equal(g[~hit], u[~hit]), (what, v, name)
 
 
+# Large outputs, S of 32 rows a workgroup (512 tiles of 32 rows or more, and rank 64 at
+# most, guided 32), and what is next to it: rank above, rows just short of it.
+TALL = [
+    ([16001, 0, 403], [0, 1, 2], 48, 521, 12, "f32", "f32", (12, 5), False),
+    ([5000, 1, 11399], [2, -1, 0], 80, 520, 30, "bf16", "bf16", None, False),
+    ([16395, 7], [1, 0], 64, 516, 64, "f32", "bf16", (64, 33), False),
+    ([9, 16400], [0, 2], 144, 513, 64, "bf16", "f32", None, False),
+    ([300] * 55, list(range(-1, 4)) * 11, 48, 512, 16, "bf16", "bf16", (16, 3), False),
+    ([16400], [0], 32, 513, 100, "bf16", "bf16", None, False),
+    ([16401, 30], [1, 0], 48, 512, 16, "f32", "f32", None, True),
+    ([8200, 8205], [0, 2], 48, 520, 32, "bf16", "bf16", (32, 9), True),
+    ([16300, 101], [1, -1], 32, 519, 48, "f32", "bf16", None, True),
+    ([16300], [0], 48, 520, 16, "f32", "f32", None, False),
+]
+
+
+@pytest.mark.parametrize("case", TALL, ids=range(len(TALL)))
+def test_lora_forward_of_many_rows(torch, case):
+    from tests.test_gpu_ops import Case
+    say(f"[lora tall] {case}")
+    assert sum(case[0]) * case[3] >= 1 << 23
+    c = Case(torch, *case, seed=10)
+    kw = dict(cfg=int(c.cfg), w=c.w)
+    ref, tol, S_ref = c.forward()
+    got, S = c.layer().apply(c.X, c.off, c.d_ids, c.base, save=True, **kw)
+    torch.cuda.synchronize()
+    _within(got, ref, tol + 2 * EPS * ref.abs(), "Y")
+    mag = c.X.double().abs().sum(1, keepdim=True) * float(c.A.nan_to_num(0.0).abs().max())
+    _within(S, S_ref, (16 + 4 * math.sqrt(c.K)) * EPS * mag.expand_as(S_ref), "S")
+    Y = c.base.clone()
+    assert c.layer().apply(c.X, c.off, c.d_ids, Y, out=Y, **kw) is Y and torch.equal(Y, got)
+    ref, tol, _ = c.forward(base=False)
+    _within(c.layer().apply(c.X, c.off, c.d_ids, **kw), ref, tol + 2 * EPS * ref.abs(), "no base")
+
+
+# dS by 32 rows (rows / 32 + requests of 256 and more), and dS split over the columns
+# (few rows beside a wide output; two, three, seven and eight parts).
+TALL_GRAD = [
+    ([8000, 0, 333], [0, 1, 2], 48, 75, 30, "f32", "f32", None, False),
+    ([4100, 1, 4203], [2, -1, 0], 80, 45, 30, "bf16", "bf16", (30, 7), False),
+    ([8300, 9], [1, 1], 48, 101, 64, "f32", "bf16", None, False),
+    ([17, 8250], [0, 2], 272, 33, 64, "bf16", "f32", (64, 40), False),
+    ([8291], [0], 32, 70, 12, "f32", "f32", None, False),
+    ([8200], [1], 32, 70, 100, "bf16", "bf16", None, False),
+    ([31] * 270, list(range(-1, 4)) * 54, 32, 50, 64, "bf16", "bf16", (64, 1), False),
+]
+SPLIT_GRAD = [
+    ([40], [0], 48, 4099, 4, "f32", "f32", None, False),
+    ([33, 1, 62], [1, -1, 0], 64, 1100, 31, "bf16", "bf16", (31, 7), False),
+    ([17, 0, 19], [0, 1, 2], 48, 3599, 64, "f32", "bf16", None, False),
+    ([5], [2], 48, 1633, 128, "bf16", "f32", (128, 3), False),
+    ([300, 300], [0, 1], 32, 4097, 16, "f32", "bf16", None, False),
+    ([1], [0], 32, 1024, 1, "bf16", "bf16", None, False),
+]
+
+
+@pytest.mark.parametrize("case", TALL_GRAD + SPLIT_GRAD,
+                         ids=range(len(TALL_GRAD) + len(SPLIT_GRAD)))
+def test_lora_gradient_tall_and_split(torch, case):
+    from tests.test_gpu_ops import Case
+    say(f"[lora grad tall / split] {case}")
+    lens, N = case[0], case[3]
+    if case in TALL_GRAD:
+        assert sum(lens) // 32 + len(lens) >= 256
+    else:
+        assert 256 // (sum(lens) // 16 + len(lens)) >= 2 and N >= 1024
+    c = Case(torch, *case, seed=11)
+    L = c.layer()
+    _, S = L.apply(c.X, c.off, c.d_ids, c.base, save=True)
+    got = L.grad(c.X, c.off, c.d_ids, S, c.dY)
+    torch.cuda.synchronize()
+    ref, tol = c.grads(S)
+    for name, g, r, b in zip(("dX", "dA", "dB"), got, ref, tol):
+        _within(g, r, b + _round(torch, r, g.dtype), name)
+    again = L.grad(c.X, c.off, c.d_ids, S, c.dY)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    none, dA, dB = L.grad(c.X, c.off, c.d_ids, S, c.dY, need_dx=False)
+    assert none is None and torch.equal(dA, got[1]) and torch.equal(dB, got[2])
+
+
 # -------------------------------------------------------------- group norm ----
 
 def _affine(t, C, w="f32", seed=0):
@@ -250,6 +330,80 @@ def test_group_norm_statistics_without_positions(torch):
             assert bool(torch.isnan(t).all()) if w else bool((t == 7.0).all())
     y, mean, rstd = op.forward(torch.empty((3, 0, 8), device="cuda"), stats=True)
     assert y.shape == (3, 0, 8) and bool(torch.isnan(mean).all()) and bool(torch.isnan(rstd).all())
+
+
+# B, L, C, G, x, w, act, columns of a wider image before and after
+TWO_READINGS = [
+    (1, 9001, 64, 2, "f32", "f32", "silu", (3, 2)),      # odd offset: element by element
+    (2, 9001, 64, 2, "bf16", "bf16", "none", (1, 0)),
+    (1, 5001, 525, 1, "f32", "bf16", "silu", (0, 0)),    # odd rows, more channels than threads
+    (2, 3001, 525, 1, "bf16", "f32", "silu", (0, 0)),
+    (1, 2000, 8192, 8, "f32", "f32", "silu", (0, 0)),    # more vectors a row than threads
+    (1, 1500, 8192, 4, "bf16", "f32", "none", (0, 0)),
+    (3, 4099, 1040, 2, "bf16", "f32", "silu", (8, 8)),   # a slice whose vectors are aligned
+    (2, 4099, 260, 4, "f32", "f32", "none", (0, 0)),
+    (1, 30011, 24, 3, "bf16", "f32", "silu", (0, 0)),
+]
+
+
+def _image_case(torch, case):
+    B, L, C, G, dt, w, act, (before, after) = case
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+    normal = lambda *s: torch.empty(s, device="cuda").normal_(generator=g)  # noqa: E731
+    wide = torch.zeros((B, L, before + C + after), device="cuda").to(_dt(torch, dt))
+    x = wide[:, :, before:before + C]
+    x.copy_(normal(B, L, C) * (0.5 + normal(C).abs()) + 0.3)
+    return x, *_affine(torch, C, w, seed=13), normal(B, L, C).to(_dt(torch, dt))
+
+
+@pytest.mark.parametrize("case", TWO_READINGS, ids=str)
+def test_group_norm_in_two_readings(torch, case):
+    from bit_post_quantization_amd import GroupNormAct
+    from tests.test_gpu_ops import _norm_grad_ref
+    say(f"[norm two readings] {case}")
+    B, L, C, G, _, _, act, _ = case
+    x, ga, be, dy = _image_case(torch, case)
+    op = GroupNormAct(ga, be, G, act=act)
+    y, mean, rstd = op.forward(x, stats=True)
+    torch.cuda.synchronize()
+    xc = x.contiguous()
+    ref, tol, m, r = _norm_ref(torch, xc, ga, be, G, 1e-5, act)
+    _within(y, ref, tol + _round(torch, ref, x.dtype), "y")
+    _within(mean, m, 2 * EPS * m.abs() + 16 * EPS / r, "mean")
+    _within(rstd, r, r * (16 * EPS + 4 * (EPS * (m.abs() + 1) * r) ** 2), "rstd")
+    got = op.grad(dy, x, mean, rstd)
+    ref, tol = _norm_grad_ref(torch, dy, xc, ga, be, G, 1e-5, act)
+    for name, a, r, b in zip(("dx", "dgamma", "dbeta"), got, ref, tol):
+        _within(a, r, b + _round(torch, r, a.dtype) + 1e-30, name)
+    assert all(torch.equal(a, b) for a, b in zip(got, op.grad(dy, x, mean, rstd)))
+    want = y.clone()
+    assert torch.equal(op.forward(x, out=x), want)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("given", [(True, False), (False, True), (False, False)], ids=str)
+@pytest.mark.parametrize("shape", [(2, 300, 16, 4), (1, 77, 40, 8), (2, 9001, 64, 4),
+                                   (2, 60001, 65, 5)], ids=str)
+def test_group_norm_gradient_without_parameters(torch, shape, given, act):
+    # gamma or beta or both absent: 1 and 0, and no gradient of them
+    from bit_post_quantization_amd import GroupNormAct
+    from tests.test_gpu_ops import _norm_grad_ref
+    say(f"[norm grad] {shape} gamma, beta {given} {act}")
+    B, L, C, G = shape
+    x, ga, be, dy = _image_case(torch, (*shape, "f32", "f32", act, (0, 0)))
+    ga, be = (t if k else None for t, k in zip((ga, be), given))
+    op = GroupNormAct(ga, be, G, act=act, channels=C)
+    y, mean, rstd = op.forward(x, stats=True)
+    ref, tol, _, _ = _norm_ref(torch, x, ga, be, G, 1e-5, act)
+    _within(y, ref, tol + _round(torch, ref, x.dtype), "y")
+    got = op.grad(dy, x, mean, rstd)
+    ref, tol = _norm_grad_ref(torch, dy, x, torch.ones(C, device="cuda") if ga is None else ga,
+                              torch.zeros(C, device="cuda") if be is None else be, G, 1e-5, act)
+    for name, a, r, b, k in zip(("dx", "dgamma", "dbeta"), got, ref, tol, (True, *given)):
+        assert (a is not None) == k
+        if k:
+            _within(a, r, b + _round(torch, r, a.dtype) + 1e-30, name)
 
 
 # ---------------------------------------------------------------- clipping ----
