@@ -101,32 +101,16 @@ __device__ __forceinline__ int rank_of(const int32_t* ranks, int a, int rank) {
   return ranks ? clampi(ranks[a], 0, rank) : rank;
 }
 
-// NE (4 or 8) consecutive elements as fp32; `valid` of them exist (the rest
-// are zero and not read). vec: p is aligned to NE elements of bf16 / 4 of f32.
-template <int NE>
-__device__ __forceinline__ void load_n(const float* p, int valid, bool vec, float (&v)[NE]) {
-  if (vec && valid >= NE) {
+// Four consecutive elements; `valid` of them exist (the rest are zero and not
+// read). vec: p is 16-byte aligned.
+__device__ __forceinline__ void load_4(const float* p, int valid, bool vec, float (&v)[4]) {
+  if (vec && valid >= 4) {
+    const v4f x = *reinterpret_cast<const v4f*>(p);
 #pragma unroll
-    for (int c = 0; c < NE / 4; ++c) {
-      const v4f x = *reinterpret_cast<const v4f*>(p + 4 * c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[4 * c + e] = x[e];
-    }
+    for (int e = 0; e < 4; ++e) v[e] = x[e];
   } else {
 #pragma unroll
-    for (int e = 0; e < NE; ++e) v[e] = e < valid ? p[e] : 0.0f;
-  }
-}
-template <int NE>
-__device__ __forceinline__ void load_n(const bf16* p, int valid, bool vec, float (&v)[NE]) {
-  if (vec && valid >= NE) {
-    typedef bf16 vh __attribute__((ext_vector_type(NE)));
-    const vh x = *reinterpret_cast<const vh*>(p);
-#pragma unroll
-    for (int e = 0; e < NE; ++e) v[e] = (float)x[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < NE; ++e) v[e] = e < valid ? (float)p[e] : 0.0f;
+    for (int e = 0; e < 4; ++e) v[e] = e < valid ? p[e] : 0.0f;
   }
 }
 
@@ -254,7 +238,7 @@ struct BFrag<float, RT> {
   float b[RT][4];
   __device__ __forceinline__ void load(const float* row, int ra, bool vec, int g) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) load_n<4>(row + r * 16 + 4 * g, ra - r * 16 - 4 * g, vec, b[r]);
+    for (int r = 0; r < RT; ++r) load_4(row + r * 16 + 4 * g, ra - r * 16 - 4 * g, vec, b[r]);
   }
   // The same from a column of A: element j at p[j * ld].
   __device__ __forceinline__ void load_column(const float* p, int64_t ld, int ra, int g) {
