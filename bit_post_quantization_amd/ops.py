@@ -9,6 +9,10 @@ Tensors must be on the current device. Every call is asynchronous on the
 current stream, or on ``stream``; what a call allocates belongs to the stream
 that it runs on. Arguments that do not fit raise QLError before anything is
 enqueued.
+
+As with the layer itself, autograd sees none of the calls: results carry no
+graph, also where an argument requires grad, and the gradients are the classes'
+``grad`` methods.
 """
 from __future__ import annotations
 
@@ -73,6 +77,16 @@ def _rows(t, name: str, dev: int, dtype, shape) -> int:
 
 def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
+
+
+_MOST_SIZES = 4096  # sizes of calls whose workspace a layer remembers
+
+
+def _remember(sizes: dict, key, value):
+    if len(sizes) >= _MOST_SIZES:
+        sizes.clear()
+    sizes[key] = value
+    return value
 
 
 def _on(stream):
@@ -167,7 +181,7 @@ class LoraAdapters:
     def _workspace_bytes(self, *size) -> int:
         n = self._bytes.get(size)
         if n is None:
-            n = self._bytes[size] = qlinear_lora_workspace(self.desc, *size)
+            n = _remember(self._bytes, size, qlinear_lora_workspace(self.desc, *size))
         return n
 
     @staticmethod
@@ -285,7 +299,8 @@ class GroupNormAct:
         if d is None:
             d = QlNorm.from_buffer_copy(self.desc)
             d.batch, d.positions, d.x_dtype = B, L, _DT[dtype]
-            d = self._sizes[dtype, B, L, grad] = d, qlinear_group_norm_workspace(d, grad)
+            d = _remember(self._sizes, (dtype, B, L, grad),
+                          (d, qlinear_group_norm_workspace(d, grad)))
         _need(C == self.C, f"x has {C} channels, not {self.C}")
         return d
 

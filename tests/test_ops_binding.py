@@ -48,3 +48,23 @@ def test_grad_table_is_lent_to_the_stream_that_reads_it(grad_set):
     now[0] = 11
     s.clip(1.0, partials=torch.zeros(_lib.QL_GRAD_PARTIALS, dtype=torch.float64))
     assert s.table.lent == [9, 11]
+
+
+def test_sizes_remembered_are_bounded(monkeypatch):
+    # a server's batches differ in rows and requests from call to call: what is
+    # remembered of them does not grow without end
+    lora = object.__new__(ops.LoraAdapters)
+    lora.desc = _lib.QlLora(N=64, K=32, rank=8, n_adapters=2, x_dtype=0, w_dtype=0, A=0x1000,
+                            B=0x1000)
+    lora._bytes = {}
+    norm = object.__new__(ops.GroupNormAct)
+    norm.C = 16
+    norm.desc = _lib.QlNorm(batch=0, positions=0, channels=16, groups=4, x_dtype=0, w_dtype=0, act=0,
+                            eps=1e-5)
+    norm._sizes = {}
+    for m in range(1, 6000):
+        n = lora._workspace_bytes(m, 1, 0, 1)
+        assert n == lora._workspace_bytes(m, 1, 0, 1) == ops.qlinear_lora_workspace(lora.desc, m, 1, 0, 1)
+        d, nb = norm._of(torch.float32, 2, m, 16, 1)
+        assert d.positions == m and nb == ops.qlinear_group_norm_workspace(d, 1)
+    assert len(lora._bytes) <= 4096 and len(norm._sizes) <= 4096
