@@ -647,7 +647,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(ForwardArgs a, bool bvec, c
 // products, and join their sums in LDS. Lane l of a step has columns
 // 8 (l / 16) .. + 7 of row l % 16 of dY, and rank l % 16 of the same rows of B.
 // With bf16 B, dY goes in three bf16 terms: 16384 x 1152 at rank 64 with dB beside it
-// took 88 us with fp32 instructions, 71 so.
+// took 88 us with fp32 instructions, 71 so (dB still in fp32 ones then).
 //
 // A single element of B as it is held until its use: bf16 in a register of its own
 // (loads into register halves would wait for one another).
@@ -799,10 +799,11 @@ __device__ void ds_body(const DsArgs& a, int tile, int split, DsLds<RT, MT, NW>&
 // of column c). fp32 P comes element by element from memory, lanes side by side at
 // addresses side by side: split in registers for bf16 results, as it is for fp32.
 //
-// Measured at 16384 rows, K 4608, rank 64, bf16: 97 us for 302 MB of X and dX and 40
-// MB of slots, 3.5 TB/s; bound by the rows' latency between barriers (matrix cores and
-// LDS busy 20 % at most). Four waves of 64 columns instead of eight of 32: 268 instead
-// of 231 us for the whole gradient then; 256 threads and 128 columns: 260 instead of 200.
+// Measured at 16384 rows, K 4608, rank 64, bf16: 109-118 us for 302 MB of X and dX and
+// 40 MB of slots, 3 TB/s (with 16 bits of dS instead of 24 it was 97); bound by the rows'
+// latency between barriers, with one workgroup a compute unit to wait for them. Four
+// waves of 64 columns instead of eight of 32: 268 instead of 231 us for the whole
+// gradient then; 256 threads and 128 columns: 260 instead of 200.
 constexpr int kOuterRows = 32, kOuterThreads = 512;
 constexpr int kOuterU = 2;  // 16-column tiles of a wave
 constexpr int kOuterCols = kOuterThreads / 64 * 16 * kOuterU;
@@ -1129,7 +1130,7 @@ __device__ void outer_body(const OuterArgs& a, int chunk, int sp, OuterLds<PT, W
 
 // What needs dY alone, in one launch: dB in workgroups [0, y_groups), which run
 // longest, dS in the rest. Both wait for memory more than they compute, and what one
-// reads of dY the other finds in the caches. 55 us at 16384 x 1152, rank 64 (75 MB
+// reads of dY the other finds in the caches. 60-64 us at 16384 x 1152, rank 64 (75 MB
 // of dY; dS first instead of dB: 99 against 88 us before both went to bf16).
 template <typename WT, int RT, int MT>
 __global__ __launch_bounds__(kOuterThreads) void k_lora_grad_y(DsArgs d, OuterArgs y, int y_groups) {
@@ -1340,11 +1341,12 @@ int lora_ds_splits(int rows, int n_req, int N) {
 }
 
 // Row ranges: at most `groups` workgroups, none with fewer than 64 rows. Workgroups
-// here take long and alike, so they are counted to fill the chip evenly: two a compute
-// unit are resident. On the X side 504 of them instead of 774 took 164 instead of 181 us
-// for the whole gradient at 16384 rows, rank 64 (1008: 186). On the dY side dB gets what
-// dS leaves of the next multiple of 256 (96 at least): 16384 rows 157 us against 164
-// with 255 of them, 2048 rows, N 4608, rank 16, fp32 37.9 against 40.7.
+// here take long and alike, so they are counted to fill the chip evenly, in whole
+// rounds: two a compute unit are resident up to rank 16, one at rank 64 (222 registers
+// on the X side, 186 on the dY side). On the X side 504 of them instead of 774 took 171
+// instead of 195 us for the whole gradient at 16384 rows, rank 64 (1008: 192). On the
+// dY side dB gets what dS leaves of the next multiple of 256 (96 at least): 16384 rows
+// 171 us against 178 with 256 of them, 2048 rows, N 4608, rank 16, fp32 35.9 against 39.0.
 constexpr int kXGroups = 512;
 static int outer_splits(int rows, int D, int groups) {
   const int chunks = (D + kOuterCols - 1) / kOuterCols;

@@ -20,12 +20,13 @@
 // Measured per call (MI355X; a copy of the bytes read and written once in brackets):
 //   2x256x1280 bf16: 6.5 us of kernel, 7.7 us a call; latency: load, two sums over the
 //     workgroup, store
-//   8x16384x320 bf16 (84 MB): 65 us (31): 17 us of sums at 4.9 TB/s, 33 us of writing
-//     at 5.1 TB/s, read again from the last-level cache
+//   8x16384x320 bf16 (84 MB): 65 us (31): 17 us of sums at 4.9 TB/s, 4.5 of joining
+//     them, 33 of writing at 5.1 TB/s, read again from the last-level cache, and 10
+//     between the three launches
 //   gradient of 4x1024x640 fp32 (31 MB): 16.4 us (6): 128 slabs for 256 compute units,
 //     bound by the arithmetic of a SiLU's gradient
-//   gradient of 4x16383x256 bf16 (101 MB): 46 us (19): 17 us of sums and 26 of writing,
-//     4.0 TB/s
+//   gradient of 4x16383x256 bf16 (101 MB): 46 us (19): 17 us of sums, 4 of joining them
+//     and 26 of writing, 4.0 TB/s
 #include "ql_device.h"
 #include "ql_ops.h"
 
@@ -729,7 +730,8 @@ Shape shape_of(int B, int L, int C, int G, int V, int groups) {
   s.chunks = (L + s.rows - 1) / s.rows;
   return s;
 }
-// Workgroups of the summing and of the writing launch. Measured on 8x16384x320 bf16
+// Workgroups of the summing and of the writing launch. Measured (on one input again and
+// again, which leaves more of it in the last-level cache) on 8x16384x320 bf16
 // and on the gradient of 4x16383x256 bf16: summing with 256 / 512 / 1024: 61.6 / 61.8
 // / 63.2 and 48.1 / 49.9 / 56.3 us; writing with 1024 / 2048 / 4096: 60.6 / 61.8 / 75.8
 // and 50.1 / 49.9 / 49.9 us. Two and eight positions ahead instead of four: 67.2, 73.3

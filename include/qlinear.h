@@ -484,7 +484,8 @@ ql_status qlinear_grad_norm(const ql_grad* table, int32_t n, int64_t units, doub
                             void* stream);
 
 /* norm (DEVICE fp32 out [1]) = sqrt(sum of partials); dst = src * coef with
- * coef = min(1, max_norm / (norm + 1e-6)), rounded once to dst's type. An
+ * coef = min(1, max_norm / (norm + 1e-6)) rounded to fp32: the product in fp32,
+ * which a bf16 dst rounds again. An
  * infinite norm gives coef 0 (infinite elements become NaN), a NaN norm makes
  * every element NaN. In place with coef = 1 nothing is written. */
 ql_status qlinear_grad_clip(const ql_grad* table, int32_t n, int64_t units, const double* partials,
