@@ -412,16 +412,15 @@ def test_clip_table_outlives_its_set_on_another_stream(torch):
     from bit_post_quantization_amd import GradSet
     a = torch.full((5000,), 2.0, device="cuda")
     st = torch.cuda.Stream()
-    st.wait_stream(torch.cuda.current_stream())
-    with torch.cuda.stream(st):
-        torch.cuda._sleep(20_000_000)  # some milliseconds of work ahead of the call
     s = GradSet([a])
     at = s.table.data_ptr()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)  # some milliseconds of work ahead of the call
     norm = s.clip(1.0, stream=st)
-    busy = not st.query()
     del s
     taken = [torch.empty((1, 5), dtype=torch.int64, device="cuda") for _ in range(4)]
-    assert not busy or at not in [t.data_ptr() for t in taken]
+    assert st.query() or at not in [t.data_ptr() for t in taken]
     st.synchronize()
     want = 2.0 * math.sqrt(5000)
     assert abs(float(norm) - want) <= 2 * EPS * want
