@@ -320,7 +320,11 @@ ql_status qlinear_lora_grad(const ql_lora* d, const void* X, int64_t ldx, int32_
   }
   QL_CHECK(check_grid(d, M, q->n_requests, true));
   const GradWs w = grad_ws(d, M, q->n_requests);
-  if (M > 0) QL_CHECK(check_workspace(workspace, workspace_bytes, w.total));
+  if (M > 0) {
+    QL_CHECK(check_workspace(workspace, workspace_bytes, w.total));
+    if ((dA && (dA == dB || dA == dX)) || (dB && dB == dX))
+      return fail(QL_ERR_ARG, "dX, dA and dB must differ");
+  }
   char* ws = reinterpret_cast<char*>(workspace);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const bool w_bf16 = d->w_dtype == QL_BF16;
@@ -460,6 +464,10 @@ ql_status qlinear_group_norm_grad(const ql_norm* d, const void* dy, int64_t dy_b
       return fail(QL_ERR_ARG, "dx is dy or x with other strides");
     QL_CHECK(check_workspace(workspace, workspace_bytes, norm_ws(d, true)));
     QL_CHECK(check_apart(d, "dx", dx_batch, dx_row));
+    // some workgroups write them while others still read gamma and beta
+    if ((dgamma && (dgamma == dbeta || dgamma == d->gamma || dgamma == d->beta)) ||
+        (dbeta && (dbeta == d->gamma || dbeta == d->beta)))
+      return fail(QL_ERR_ARG, "dgamma and dbeta must differ from each other, gamma and beta");
   }
   a.dy = dy;
   a.dyb = dy_batch;

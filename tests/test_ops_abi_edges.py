@@ -62,3 +62,18 @@ def test_lora_requests_may_be_none_without_rows():
     assert L.qlinear_lora(d, U, 64, 0, q, 0, 1.0, U, 100, U, 100, U, U, 0, U) == _lib.QL_OK
     assert L.qlinear_lora(d, A, 64, 1, ctypes.byref(_req(n_requests=0)), 0, 1.0, A, 100, A + 64, 100,
                           U, A, 1 << 30, U) == _lib.QL_ERR_ARG
+
+
+def test_gradients_of_parameters_must_differ():
+    # given tensors: one for both, or the parameter itself, would be a silent race
+    L = _lib.load()
+    q = ctypes.byref(_req())
+    for dX, dA, dB in ((A, 2 * A, 2 * A), (A, A, 2 * A), (A, 2 * A, A), (U, A, A)):
+        assert L.qlinear_lora_grad(ctypes.byref(_lora()), 4 * A, 64, 16, q, A, A, 100, dX, 64, dA, dB, A,
+                                   1 << 30, U) == _lib.QL_ERR_ARG
+        assert "must differ" in _msg()
+    for dg, db in ((3 * A, 3 * A), (A, 3 * A), (3 * A, 2 * A), (U, A), (2 * A, U)):
+        d = ctypes.byref(_norm(gamma=A, beta=2 * A))
+        assert L.qlinear_group_norm_grad(d, 5 * A, 216, 24, 6 * A, 216, 24, A, A, 7 * A, 216, 24, dg, db,
+                                         A, 1 << 30, U) == _lib.QL_ERR_ARG
+        assert "must differ" in _msg()
