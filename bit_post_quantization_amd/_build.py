@@ -14,7 +14,8 @@ ARCH = "gfx950"
 
 SOURCES = ["k_quant.hip", "k_gemm.hip", "k_gemm1.hip", "k_misc.hip", "k_probe.hip",
            "k_lora.hip", "k_norm.hip", "k_clip.hip",
-           "qlinear_api.cpp", "qlinear_ops.cpp", "gamp.cpp"]
+           "k_rows4.hip", "k_heads.hip", "k_attn.hip",
+           "qlinear_api.cpp", "qlinear_ops.cpp", "qlinear_block.cpp", "gamp.cpp"]
 
 # -ffp-contract=off: the epilogue's multiply-then-add order is part of the
 # numerics (no fused multiply-add). Correctly rounded fp32 division is the
@@ -37,9 +38,12 @@ def hipcc() -> str:
 EXTRA = {"k_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 # k_gemm1.hip is compiled once per (4-bit activations, symmetric scales)
-# pair, so its instantiations build in parallel.
+# pair and k_attn.hip once per (type, 16-channel blocks of a head), so their
+# instantiations build in parallel.
 VARIANTS = {"k_gemm1.hip": [(f"k_gemm1_a{a}_s{s}", [f"-DQL_G1_A4={a}", f"-DQL_G1_SYM={s}"])
-                            for a in (0, 1) for s in (0, 1)]}
+                            for a in (0, 1) for s in (0, 1)],
+            "k_attn.hip": [(f"k_attn_{t}_{d}", [f"-DQL_AT_T={t}", f"-DQL_AT_DC={d}"])
+                           for t in ("f32", "bf16") for d in (2, 4, 5, 6, 8, 10)]}
 
 
 def units():

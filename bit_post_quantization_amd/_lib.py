@@ -18,6 +18,10 @@ QL_F32, QL_BF16 = 0, 1
 QL_WSCALE_PER_TENSOR, QL_WSCALE_PER_SEGMENT, QL_WSCALE_PER_CHANNEL = 0, 1, 2
 QL_ASCALE_DUAL, QL_ASCALE_SYMMETRIC = 0, 1
 QL_ACT_NONE, QL_ACT_SILU = 0, 1
+QL_HEADS_NONE, QL_HEADS_RMS = 0, 1
+QL_PAIRS_ADJACENT, QL_PAIRS_HALVES = 0, 1
+QL_POS_I32, QL_POS_F32 = 0, 1
+QL_MAX_AXES = 4
 QL_GRAD_UNIT, QL_GRAD_PARTIALS = 4096, 1024
 
 EXPORTS = (
@@ -28,6 +32,10 @@ EXPORTS = (
     "qlinear_lora_workspace", "qlinear_lora", "qlinear_lora_grad",
     "qlinear_group_norm_workspace", "qlinear_group_norm", "qlinear_group_norm_grad",
     "qlinear_grad_norm", "qlinear_grad_clip",
+    "qlinear_rows4_bytes", "qlinear_rows4_pack", "qlinear_rows4_quantize", "qlinear_rows4_unpack",
+    "qlinear_rows4_workspace", "qlinear_rows4",
+    "qlinear_heads_workspace", "qlinear_heads", "qlinear_heads_grad",
+    "qlinear_attention_workspace", "qlinear_attention", "qlinear_attention_grad",
 )
 
 
@@ -66,6 +74,40 @@ class QlNorm(ctypes.Structure):
     ]
 
 
+class QlRows4(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int), ("s_dtype", ctypes.c_int), ("act", ctypes.c_int),
+        ("packed", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+    ]
+
+
+class QlHeadsView(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("batch", ctypes.c_int64), ("row", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
+
+
+class QlHeads(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("positions", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+        ("k_heads", ctypes.c_int32), ("v_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
+        ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("gamma_q", ctypes.c_void_p),
+        ("gamma_k", ctypes.c_void_p), ("n_axes", ctypes.c_int32),
+        ("axis_dims", ctypes.c_int32 * QL_MAX_AXES), ("pairs", ctypes.c_int),
+        ("freqs", ctypes.c_void_p), ("pos_dtype", ctypes.c_int),
+    ]
+
+
+class QlAttn(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("q_len", ctypes.c_int32), ("k_len", ctypes.c_int32),
+        ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("k_lens", ctypes.c_void_p),
+        ("k_mask", ctypes.c_void_p), ("mask_batch", ctypes.c_int64),
+    ]
+
+
 class QLError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"qlinear status {status}: {msg}")
@@ -86,6 +128,8 @@ def load() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     LORA, REQ, NORM = (ctypes.POINTER(t) for t in (QlLora, QlRequests, QlNorm))
+    ROWS4, HEADS, ATTN, VIEW, SIZE = (ctypes.POINTER(t) for t in (QlRows4, QlHeads, QlAttn,
+                                                                  QlHeadsView, I64))
     sig = {
         "qlinear_plan": ([ctypes.POINTER(QlDesc), P, P, ctypes.POINTER(P)], ctypes.c_int),
         "qlinear_plan_destroy": ([P], ctypes.c_int),
@@ -109,6 +153,20 @@ def load() -> ctypes.CDLL:
                                      I64, P], ctypes.c_int),
         "qlinear_grad_norm": ([P, I32, I64, P, P], ctypes.c_int),
         "qlinear_grad_clip": ([P, I32, I64, P, F32, P, P], ctypes.c_int),
+        "qlinear_rows4_bytes": ([ROWS4, SIZE], ctypes.c_int),
+        "qlinear_rows4_pack": ([ROWS4, P, P, P, P], ctypes.c_int),
+        "qlinear_rows4_quantize": ([ROWS4, P, ctypes.c_int, P, P], ctypes.c_int),
+        "qlinear_rows4_unpack": ([ROWS4, P, P, P], ctypes.c_int),
+        "qlinear_rows4_workspace": ([ROWS4, I32, SIZE], ctypes.c_int),
+        "qlinear_rows4": ([ROWS4, P, I64, I32, P, I64, P, I64, P], ctypes.c_int),
+        "qlinear_heads_workspace": ([HEADS, SIZE], ctypes.c_int),
+        "qlinear_heads": ([HEADS, P, I64, I64, P, I64, VIEW, VIEW, VIEW, P], ctypes.c_int),
+        "qlinear_heads_grad": ([HEADS, VIEW, VIEW, VIEW, P, I64, I64, P, I64, P, I64, I64, P, P, P,
+                                I64, P], ctypes.c_int),
+        "qlinear_attention_workspace": ([ATTN, I32, SIZE], ctypes.c_int),
+        "qlinear_attention": ([ATTN, VIEW, VIEW, VIEW, VIEW, P, P, I64, P], ctypes.c_int),
+        "qlinear_attention_grad": ([ATTN, VIEW, VIEW, VIEW, VIEW, VIEW, P, VIEW, VIEW, VIEW, P,
+                                    I64, P], ctypes.c_int),
         "qlinear_last_error": ([], ctypes.c_char_p),
         "qlinear_version": ([], ctypes.c_char_p),
     }

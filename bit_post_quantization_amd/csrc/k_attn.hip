@@ -1,0 +1,807 @@
+// Attention of queries to the states of another sequence, forward and backward.
+//
+//   forward   S = scale Q K^T,  P = softmax(S),  O = P V
+//   backward  P = exp(S - lse),  delta = rowsum(dO O),  dS = P (dO V^T - delta),
+//             dQ = scale dS K  (k_attn_dq),  dV = P^T dO and dK = scale dS^T Q (k_attn_dkv)
+//
+// A wave owns 32 rows (queries; in k_attn_dkv 32 keys), one a lane of each half
+// wave, and walks over tiles of the other side in LDS. Every product is taken so that
+// what the wave owns is the column of the matrix instruction (32x32x16 bf16, or eight
+// 32x32x2 fp32): S^T = K Q^T leaves a lane 16 scores of its own query for 32 keys,
+//   C[4 h + 8 (i / 4) + i % 4][lane % 32], h = lane / 32, i < 16,
+// so row maxima and sums stay in the lane but for one exchange between the halves, and
+// the scores, rounded, already are the operand of the next product (O^T += V^T P^T,
+// dQ^T += K^T dS^T): its 16 keys of step s are the lane's values 8 s .. 8 s + 7, and V^T is
+// read from LDS in that order (ds_read_b64_tr_b16 for bf16, single words for fp32). No
+// score goes through LDS, nothing is exchanged between waves until the end.
+//
+// The softmax runs in base 2 (scale2 = scale log2 e), one pass, with the running
+// maximum and sum in fp32; O is rescaled only where a maximum of the wave rose.
+// Roundings: bf16 tensors give bf16 weights P and, in the gradient, bf16 dS (both
+// 2^-9 of themselves, below what the rounding of the result adds); fp32 tensors stay
+// fp32 throughout.
+//
+// This file is compiled once for each type and number DC of 16-channel blocks
+// of a head (QL_AT_T, QL_AT_DC); heads of other sizes are padded with zeros in LDS.
+#include "ql_block.h"
+#include "ql_device.h"
+
+namespace ql {
+
+namespace {
+
+typedef __bf16 bf16;
+typedef float f32;
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v8f __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef bf16 v8h __attribute__((ext_vector_type(8)));
+typedef bf16 v4h __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s* lds_v4s;
+
+typedef QL_AT_T T;
+constexpr int DC = QL_AT_DC;
+constexpr int kChunk = 16 / sizeof(T);        // elements of a 16-byte piece
+constexpr int kD = 16 * DC;                   // padded channels
+constexpr int kOB = (DC + 1) / 2;             // 32-channel blocks of a result
+constexpr int kCPR = kD / kChunk;             // pieces of a padded row
+constexpr int kThreads = 256;
+
+// Eight elements of one row: an operand's part of a lane.
+template <typename E> struct Frag;
+template <> struct Frag<bf16> { typedef v8h t; };
+template <> struct Frag<f32> { typedef v8f t; };
+typedef Frag<T>::t frag;
+
+template <typename V>
+__device__ __forceinline__ v16f mma(const V& a, const V& b, v16f c) {
+  if constexpr (sizeof(V) == 16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+}
+
+// Values 8 s .. 8 s + 7 of a result as an operand of the next product.
+__device__ __forceinline__ frag operand(const v16f& c, int s) {
+  frag f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = (T)c[8 * s + e];
+  return f;
+}
+
+// LDS rows, in elements. Reads of whole rows by neighbouring lanes want an odd number
+// of 16-byte pieces (every lane of sixteen on its own banks), transposed reads of four
+// rows by 32 channels 16 words more than a multiple of 64.
+constexpr int kRowLd = (kCPR | 1) * kChunk;
+constexpr int tr_ld() {
+  if (sizeof(T) == 4) return kOB * 32;  // lanes read neighbouring words of one row
+  int words = kOB * 16;                 // as many channels as the result's blocks read
+  while (words % 64 != 16 && words % 64 != 48) words += 4;
+  return words * 2;
+}
+constexpr int kTrLd = tr_ld();
+// Read both ways: padded to whole blocks, then an odd number of pieces.
+constexpr int kBothLd = ((kOB * 32 / kChunk) | 1) * kChunk;
+
+// Operand of rows: row lane % 32 of p, channels 16 kb + 8 h .. + 7.
+__device__ __forceinline__ frag row_frag(const T* p, int ld, int kb, int r32, int h) {
+  return *reinterpret_cast<const frag*>(p + r32 * ld + 16 * kb + 8 * h);
+}
+
+// Operand of columns: channel c0 + lane % 32, rows 4 h .. + 3 and 8 + 4 h .. + 3 of p.
+template <typename E>
+__device__ __forceinline__ typename Frag<E>::t col_frag(const E* p, int ld, int c0, int lane) {
+  if constexpr (sizeof(E) == 2) {
+    const int i = lane & 15;
+    const E* a = p + (4 * (lane >> 5) + i / 4) * ld + c0 + 16 * ((lane >> 4) & 1) + 4 * (i % 4);
+    const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(a));
+    const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(a + 8 * ld));
+    return __builtin_bit_cast(v8h, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+  } else {
+    const E* a = p + 4 * (lane >> 5) * ld + c0 + (lane & 31);
+    v8f f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = a[e * ld];
+      f[4 + e] = a[(8 + e) * ld];
+    }
+    return f;
+  }
+}
+
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+__device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Workgroup `id` of n in an order that gives each of the 8 XCDs (workgroups are dealt to
+// them in turn) a run of neighbours, so that the tiles of one head meet in one L2.
+__device__ __forceinline__ int by_xcd(int id, int n) {
+  const int x = id % 8, q = n / 8, r = n % 8;
+  return x * q + min(x, r) + id / 8;
+}
+
+__device__ __forceinline__ void split_row(const AttnArgs& a, int r, int& l, int& g) {
+  l = a.G == 1 ? r : r / a.G;
+  g = a.G == 1 ? 0 : r - l * a.G;
+}
+
+__device__ __forceinline__ const T* row_of(const AttnArgs& a, const ql_heads_view& t, int b, int hk,
+                                           int r) {
+  int l, g;
+  split_row(a, r, l, g);
+  return reinterpret_cast<const T*>(t.p) + b * t.batch + l * t.row + (int64_t)(hk * a.G + g) * t.head;
+}
+
+// Place of row r in a [B, H, Lq] array.
+__device__ __forceinline__ int64_t stat_at(const AttnArgs& a, int b, int hk, int r) {
+  int l, g;
+  split_row(a, r, l, g);
+  return ((int64_t)b * a.H + hk * a.G + g) * a.Lq + l;
+}
+
+// Eight channels of a row in memory, zero past D.
+__device__ __forceinline__ frag load_frag(const T* row, int c, int D) {
+  frag f;
+  if (c < D) {
+    f = *reinterpret_cast<const frag*>(row + c);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = (T)0.0f;
+  }
+  return f;
+}
+
+// Four consecutive channels of a result (values 4 j .. 4 j + 3 of block c) to memory.
+__device__ __forceinline__ void store4(T* p, const v16f& c, int j, float f) {
+  if constexpr (sizeof(T) == 2) {
+    v4h o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = (T)(c[4 * j + e] * f);
+    *reinterpret_cast<v4h*>(p) = o;
+  } else {
+    v4f o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = c[4 * j + e] * f;
+    *reinterpret_cast<v4f*>(p) = o;
+  }
+}
+__device__ __forceinline__ void store4f(float* p, const v16f& c, int j, float f) {
+  v4f o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = c[4 * j + e] * f;
+  *reinterpret_cast<v4f*>(p) = o;
+}
+
+__device__ __forceinline__ v16f zero16() {
+  v16f z;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) z[e] = 0.0f;
+  return z;
+}
+
+// Which of the keys of a tile of 32 W count: a bit each, the same in all lanes.
+template <int W>
+struct KeyBits {
+  uint32_t w[W];
+  __device__ __forceinline__ void look(const AttnArgs& a, int b, int key0, int len, int lane) {
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+      const int key = key0 + 32 * i + lane;
+      bool ok = key < len;
+      if (a.mask && ok) ok = a.mask[b * a.mask_batch + key] != 0;
+      const uint64_t m = __ballot(ok);
+      w[i] = (uint32_t)m;
+      if (i + 1 < W) w[i + 1] = (uint32_t)(m >> 32);
+    }
+  }
+  __device__ __forceinline__ bool all() const {
+    uint32_t x = w[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) x &= w[i];
+    return x == 0xffffffffu;
+  }
+  __device__ __forceinline__ bool none() const {
+    uint32_t x = w[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) x |= w[i];
+    return x == 0;
+  }
+};
+
+__device__ __forceinline__ int key_len(const AttnArgs& a, int b) {
+  if (!a.lens) return a.Lk;
+  const int n = a.lens[b];
+  return n < 0 ? 0 : n > a.Lk ? a.Lk : n;
+}
+
+// A tile of KT rows of one tensor on its way from memory through registers to LDS.
+template <int KT>
+struct Stage {
+  static constexpr int N = (KT * kCPR + kThreads - 1) / kThreads;
+  v4u r[N];
+  // row(i): the address of row i of the tile (any valid one past the end)
+  template <typename F>
+  __device__ __forceinline__ void fetch(int tid, int D, F row) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = tid + i * kThreads, at = idx / kCPR, c = idx % kCPR;
+      r[i] = v4u{0, 0, 0, 0};
+      if ((KT * kCPR % kThreads == 0 || at < KT) && (c + 1) * kChunk <= D)
+        r[i] = *reinterpret_cast<const v4u*>(row(at) + c * kChunk);
+    }
+  }
+  // keep(i): whether row i of the tile is kept (else zero)
+  template <bool ALL, typename F>
+  __device__ __forceinline__ void put(T* lds, int ld, int tid, F keep) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = tid + i * kThreads, at = idx / kCPR, c = idx % kCPR;
+      v4u x = r[i];
+      if constexpr (!ALL) {
+        if (!keep(at)) x = v4u{0, 0, 0, 0};
+      }
+      if (KT * kCPR % kThreads == 0 || at < KT)
+        *reinterpret_cast<v4u*>(lds + at * ld + c * kChunk) = x;
+    }
+  }
+};
+
+template <int W>
+__device__ __forceinline__ bool bit_of(const KeyBits<W>& k, int i) {
+  uint32_t x = k.w[0];
+#pragma unroll
+  for (int j = 1; j < W; ++j) x = (i >> 5) == j ? k.w[j] : x;
+  return (x >> (i & 31)) & 1;
+}
+
+// ----------------------------------------------------------------- forward ----
+
+// WK waves of a workgroup share its keys, 4 / WK its rows: one for many rows; all
+// four (two in fp32, whose tiles fill LDS) for few of them.
+template <int WK>
+struct Fwd {
+  static constexpr int WQ = 4 / WK, kRows = 32 * WQ;
+  static constexpr int SUB = WK == 1 ? 2 : 1;  // 32-key pieces of a wave in a tile
+  static constexpr int KT = 32 * WK * SUB;
+  static constexpr int NB = WK == 1 && sizeof(T) * kD <= 320 ? 2 : 1;  // tiles in LDS
+  static constexpr int kTile = KT * (kRowLd + kTrLd);
+  static constexpr int kJoin = WK > 1 ? (WK - 1) * WQ * 32 * (kOB * 32 + 2) * 4 : 0;
+  static constexpr int kLds = NB * kTile * (int)sizeof(T) > kJoin ? NB * kTile * (int)sizeof(T)
+                                                                 : kJoin;
+};
+
+template <int WK>
+__global__ __launch_bounds__(kThreads) void k_attn_forward(AttnArgs a) {
+  typedef Fwd<WK> P;
+  constexpr int KT = P::KT, SUB = P::SUB, W = KT / 32;
+  __shared__ __attribute__((aligned(16))) char smem[P::kLds];
+  T* const lds = reinterpret_cast<T*>(smem);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wq = wave / WK, wk = wave % WK, r32 = lane & 31, h = lane >> 5;
+  int id = by_xcd(blockIdx.x, gridDim.x);
+  const int sp = id % a.splits;
+  id /= a.splits;
+  const int rt = id % a.row_tiles;
+  id /= a.row_tiles;
+  const int hk = id % a.Hk, b = id / a.Hk;
+  const int len = key_len(a, b);
+  const int tiles = (len + KT - 1) / KT, per = (tiles + a.splits - 1) / a.splits;
+  const int t0 = sp * per, t1 = min(tiles, t0 + per);
+  const int row = rt * P::kRows + wq * 32 + r32, rr = min(row, a.R - 1);
+
+  frag q[DC];
+  {
+    const T* p = row_of(a, a.q, b, hk, rr);
+#pragma unroll
+    for (int kb = 0; kb < DC; ++kb) q[kb] = load_frag(p, 16 * kb + 8 * h, a.D);
+  }
+  const T* const kp = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
+  const T* const vp = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
+  v16f o[kOB];
+#pragma unroll
+  for (int i = 0; i < kOB; ++i) o[i] = zero16();
+  float m = -INFINITY, l = 0.0f;
+
+  Stage<KT> ks, vs;
+  KeyBits<W> bits, next;
+  const auto fetch = [&](int t) {
+    ks.fetch(tid, a.D, [&](int i) { return kp + (int64_t)min(t * KT + i, a.Lk - 1) * a.k.row; });
+    vs.fetch(tid, a.D, [&](int i) { return vp + (int64_t)min(t * KT + i, a.Lk - 1) * a.v.row; });
+    next.look(a, b, t * KT, len, lane);
+  };
+  const auto put = [&](T* at) {
+    const auto keep = [&](int i) { return bit_of(next, i); };
+    ks.template put<true>(at, kRowLd, tid, keep);  // scores of other keys are not looked at
+    if (next.all())
+      vs.template put<true>(at + KT * kRowLd, kTrLd, tid, keep);
+    else
+      vs.template put<false>(at + KT * kRowLd, kTrLd, tid, keep);
+  };
+  if (t0 < t1) {
+    fetch(t0);
+    put(lds);
+  }
+  bits = next;
+  __syncthreads();
+  for (int t = t0; t < t1; ++t) {
+    const T* const kt = lds + ((t - t0) % P::NB) * P::kTile;
+    const T* const vt = kt + KT * kRowLd;
+    if (t + 1 < t1) fetch(t + 1);
+    if (!bits.none()) {
+      v16f s[SUB];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        s[u] = zero16();
+        const T* p = kt + (wk * SUB + u) * 32 * kRowLd;
+#pragma unroll
+        for (int kb = 0; kb < DC; ++kb) s[u] = mma(row_frag(p, kRowLd, kb, r32, h), q[kb], s[u]);
+      }
+      if (!bits.all()) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          uint32_t w = 0;  // wk is uniform: a select of the words
+#pragma unroll
+          for (int j = 0; j < W; ++j) w = j == wk * SUB + u ? bits.w[j] : w;
+          w >>= 4 * h;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (!((w >> (8 * (i / 4) + i % 4)) & 1)) s[u][i] = -INFINITY;
+        }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+      top = fmaxf(top, other_half(top)) * a.scale2;
+      const float m_new = fmaxf(m, top);
+      if (__any(m_new > m)) {
+        const float f = exp2_fast(m - (m_new == -INFINITY ? 0.0f : m_new));
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < kOB; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[i][e] *= f;
+        m = m_new;
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      float sum = 0.0f;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[u][i] = exp2_fast(__builtin_fmaf(s[u][i], a.scale2, -base));
+          sum += s[u][i];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const frag p = operand(s[u], i);
+          const T* v0 = vt + ((wk * SUB + u) * 32 + 16 * i) * kTrLd;
+#pragma unroll
+          for (int c = 0; c < kOB; ++c) o[c] = mma(col_frag(v0, kTrLd, 32 * c, lane), p, o[c]);
+        }
+      }
+      l += sum;
+    }
+    if constexpr (P::NB == 1) __syncthreads();
+    if (t + 1 < t1) put(lds + ((t + 1 - t0) % P::NB) * P::kTile);
+    bits = next;
+    __syncthreads();
+  }
+  l += other_half(l);
+
+  if constexpr (WK > 1) {  // the waves of other keys hand over what they have
+    float* const box = reinterpret_cast<float*>(smem);
+    constexpr int kLd = kOB * 32 + 2;
+    if (wk > 0) {
+      float* p = box + ((wk - 1) * P::WQ + wq) * 32 * kLd + r32 * kLd;
+#pragma unroll
+      for (int c = 0; c < kOB; ++c)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[32 * c + 8 * (e / 4) + 4 * h + e % 4] = o[c][e];
+      if (h == 0) {
+        p[kOB * 32] = m;
+        p[kOB * 32 + 1] = l;
+      }
+    }
+    __syncthreads();
+    if (wk > 0) return;
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < WK - 1; ++j)
+      top = fmaxf(top, box[((j * P::WQ + wq) * 32 + r32) * kLd + kOB * 32]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const float f = exp2_fast(m - base);
+    l *= f;
+#pragma unroll
+    for (int c = 0; c < kOB; ++c)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[c][e] *= f;
+#pragma unroll
+    for (int j = 0; j < WK - 1; ++j) {
+      const float* p = box + ((j * P::WQ + wq) * 32 + r32) * kLd;
+      const float g = exp2_fast(p[kOB * 32] - base);
+      l = __builtin_fmaf(g, p[kOB * 32 + 1], l);
+#pragma unroll
+      for (int c = 0; c < kOB; ++c)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          o[c][e] = __builtin_fmaf(g, p[32 * c + 8 * (e / 4) + 4 * h + e % 4], o[c][e]);
+    }
+    m = top;
+  }
+  if (row >= a.R) return;
+  const bool empty = m == -INFINITY && l == 0.0f;
+  const float inv = empty ? 0.0f : 1.0f / l;
+  const float lse2 = empty ? -INFINITY : m + __log2f(l);
+  const int64_t at = stat_at(a, b, hk, row);
+  if (a.splits > 1) {
+    const int64_t n = (int64_t)a.B * a.H * a.Lq;
+    float* p = a.part + (sp * n + at) * a.D;
+    if (h == 0) a.part_lse[sp * n + at] = lse2;
+#pragma unroll
+    for (int c = 0; c < kOB; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = 32 * c + 8 * j + 4 * h;
+        if (d < a.D) store4f(p + d, o[c], j, inv);
+      }
+    return;
+  }
+  T* p = const_cast<T*>(row_of(a, a.o, b, hk, row));
+  if (a.lse && h == 0) a.lse[at] = lse2 * kLn2;
+#pragma unroll
+  for (int c = 0; c < kOB; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int d = 32 * c + 8 * j + 4 * h;
+      if (d < a.D) store4(p + d, o[c], j, inv);
+    }
+}
+
+// One wave a row: the parts of its splits weighted by their share of the sum.
+__global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
+  const int64_t n = (int64_t)a.B * a.H * a.Lq;
+  const int64_t at = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (at >= n) return;
+  const int lane = threadIdx.x & 63;
+  float top = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * n + at]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  float total = 0.0f, acc[3] = {0.0f, 0.0f, 0.0f};
+  for (int s = 0; s < a.splits; ++s) {
+    const float f = exp2_fast(a.part_lse[s * n + at] - base);
+    total += f;
+    const float* p = a.part + (s * n + at) * a.D;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (lane + 64 * i < a.D) acc[i] = __builtin_fmaf(f, p[lane + 64 * i], acc[i]);
+  }
+  const bool empty = total == 0.0f;
+  const float inv = empty ? 0.0f : 1.0f / total;
+  const int l = (int)(at % a.Lq);
+  const int64_t bh = at / a.Lq;
+  T* p = reinterpret_cast<T*>(a.o.p) + bh / a.H * a.o.batch + l * a.o.row + bh % a.H * a.o.head;
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (lane + 64 * i < a.D) p[lane + 64 * i] = (T)(acc[i] * inv);
+  if (a.lse && lane == 0) a.lse[at] = empty ? -INFINITY : (top + __log2f(total)) * kLn2;
+}
+
+// ---------------------------------------------------------------- backward ----
+
+constexpr int kBackRows = 32;  // rows or keys of a tile in LDS
+
+// dQ, and delta for k_attn_dkv. Keys that do not count are zero in LDS and have P = 0.
+__global__ __launch_bounds__(kThreads) void k_attn_dq(AttnArgs a) {
+  constexpr int KT = 64, W = 2, kTile = KT * (kBothLd + kRowLd);
+  constexpr int NB = 2 * kTile * (int)sizeof(T) <= 81920 ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) T lds[NB * kTile];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, h = lane >> 5;
+  int id = by_xcd(blockIdx.x, gridDim.x);
+  const int rt = id % a.row_tiles;
+  id /= a.row_tiles;
+  const int hk = id % a.Hk, b = id / a.Hk;
+  const int len = key_len(a, b), tiles = (len + KT - 1) / KT;
+  const int row = rt * 128 + wave * 32 + r32, rr = min(row, a.R - 1);
+  const int64_t at = stat_at(a, b, hk, rr);
+
+  frag q[DC], g[DC];
+  float delta = 0.0f;
+  {
+    const T* pq = row_of(a, a.q, b, hk, rr);
+    const T* pg = row_of(a, a.dout, b, hk, rr);
+    const T* po = row_of(a, a.o, b, hk, rr);
+#pragma unroll
+    for (int kb = 0; kb < DC; ++kb) {
+      q[kb] = load_frag(pq, 16 * kb + 8 * h, a.D);
+      g[kb] = load_frag(pg, 16 * kb + 8 * h, a.D);
+      const frag o = load_frag(po, 16 * kb + 8 * h, a.D);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta = __builtin_fmaf((float)g[kb][e], (float)o[e], delta);
+    }
+    delta += other_half(delta);
+    if (h == 0 && row < a.R) a.delta[at] = delta;
+  }
+  float lse2 = a.lse[at] * kLog2e;
+  if (lse2 == -INFINITY) lse2 = INFINITY;  // no key counts: P = 0
+  const T* const kp = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
+  const T* const vp = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
+  v16f dq[kOB];
+#pragma unroll
+  for (int i = 0; i < kOB; ++i) dq[i] = zero16();
+
+  Stage<KT> ks, vs;
+  KeyBits<W> bits, next;
+  const auto fetch = [&](int t) {
+    ks.fetch(tid, a.D, [&](int i) { return kp + (int64_t)min(t * KT + i, a.Lk - 1) * a.k.row; });
+    vs.fetch(tid, a.D, [&](int i) { return vp + (int64_t)min(t * KT + i, a.Lk - 1) * a.v.row; });
+    next.look(a, b, t * KT, len, lane);
+  };
+  const auto put = [&](T* to) {
+    const auto keep = [&](int i) { return bit_of(next, i); };
+    if (next.all()) {
+      ks.template put<true>(to, kBothLd, tid, keep);
+      vs.template put<true>(to + KT * kBothLd, kRowLd, tid, keep);
+    } else {
+      ks.template put<false>(to, kBothLd, tid, keep);
+      vs.template put<false>(to + KT * kBothLd, kRowLd, tid, keep);
+    }
+  };
+  if (tiles > 0) {
+    fetch(0);
+    put(lds);
+  }
+  bits = next;
+  __syncthreads();
+  for (int t = 0; t < tiles; ++t) {
+    const T* const kt = lds + (t % NB) * kTile;
+    const T* const vt = kt + KT * kBothLd;
+    if (t + 1 < tiles) fetch(t + 1);
+    if (!bits.none()) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        v16f s = zero16(), dp = zero16();
+#pragma unroll
+        for (int kb = 0; kb < DC; ++kb) {
+          s = mma(row_frag(kt + 32 * u * kBothLd, kBothLd, kb, r32, h), q[kb], s);
+          dp = mma(row_frag(vt + 32 * u * kRowLd, kRowLd, kb, r32, h), g[kb], dp);
+        }
+        const uint32_t w = bits.w[u] >> (4 * h);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p = exp2_fast(__builtin_fmaf(s[i], a.scale2, -lse2));
+          s[i] = p * (dp[i] - delta);
+        }
+        if (bits.w[u] != 0xffffffffu) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (!((w >> (8 * (i / 4) + i % 4)) & 1)) s[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const frag ds = operand(s, i);
+          const T* k0 = kt + (32 * u + 16 * i) * kBothLd;
+#pragma unroll
+          for (int c = 0; c < kOB; ++c) dq[c] = mma(col_frag(k0, kBothLd, 32 * c, lane), ds, dq[c]);
+        }
+      }
+    }
+    if constexpr (NB == 1) __syncthreads();
+    if (t + 1 < tiles) put(lds + ((t + 1) % NB) * kTile);
+    bits = next;
+    __syncthreads();
+  }
+  if (row >= a.R) return;
+  T* p = const_cast<T*>(row_of(a, a.dq, b, hk, row));
+#pragma unroll
+  for (int c = 0; c < kOB; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int d = 32 * c + 8 * j + 4 * h;
+      if (d < a.D) store4(p + d, dq[c], j, a.scale);
+    }
+}
+
+// dK and dV of 128 keys from a range of the rows; a lane has one key.
+__global__ __launch_bounds__(kThreads) void k_attn_dkv(AttnArgs a) {
+  constexpr int RT = kBackRows, kTile = RT * 2 * kBothLd;
+  constexpr int NB = 2;
+  __shared__ __attribute__((aligned(16))) T lds[NB * kTile];
+  __shared__ __attribute__((aligned(16))) float stats[NB][2][RT];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, h = lane >> 5;
+  int id = by_xcd(blockIdx.x, gridDim.x);
+  const int sp = id % a.splits;
+  id /= a.splits;
+  const int kt = id % a.key_tiles;
+  id /= a.key_tiles;
+  const int hk = id % a.Hk, b = id / a.Hk;
+  const int len = key_len(a, b);
+  const int key = kt * 128 + wave * 32 + r32, kk = min(key, a.Lk - 1);
+  bool counts = key < len;
+  if (a.mask && counts) counts = a.mask[b * a.mask_batch + key] != 0;
+  const int tiles = (a.R + RT - 1) / RT, per = (tiles + a.splits - 1) / a.splits;
+  const int t0 = sp * per, t1 = kt * 128 < len ? min(tiles, t0 + per) : 0;
+
+  frag k[DC], v[DC];
+  {
+    const T* pk = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + kk * a.k.row + hk * a.k.head;
+    const T* pv = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + kk * a.v.row + hk * a.v.head;
+#pragma unroll
+    for (int kb = 0; kb < DC; ++kb) {
+      k[kb] = load_frag(pk, 16 * kb + 8 * h, a.D);
+      v[kb] = load_frag(pv, 16 * kb + 8 * h, a.D);
+    }
+  }
+  v16f dk[kOB], dv[kOB];
+#pragma unroll
+  for (int i = 0; i < kOB; ++i) dk[i] = dv[i] = zero16();
+
+  Stage<RT> qs, gs;
+  float stat = 0.0f;  // of thread t < RT lse of row t, of t < 2 RT delta of row t - RT
+  const auto fetch = [&](int t) {
+    qs.fetch(tid, a.D, [&](int i) { return row_of(a, a.q, b, hk, min(t * RT + i, a.R - 1)); });
+    gs.fetch(tid, a.D, [&](int i) { return row_of(a, a.dout, b, hk, min(t * RT + i, a.R - 1)); });
+    if (tid < 2 * RT) {
+      const int r = t * RT + tid % RT;
+      const int64_t at = stat_at(a, b, hk, min(r, a.R - 1));
+      if (tid < RT) {
+        stat = a.lse[at] * kLog2e;
+        if (stat == -INFINITY || r >= a.R) stat = INFINITY;  // P = 0
+      } else {
+        stat = r < a.R ? a.delta[at] : 0.0f;
+      }
+    }
+  };
+  const auto put = [&](int t) {
+    const int n = a.R - t * RT, at = (t - t0) % NB;
+    T* to = lds + at * kTile;
+    const auto keep = [&](int i) { return i < n; };
+    if (n >= RT) {
+      qs.template put<true>(to, kBothLd, tid, keep);
+      gs.template put<true>(to + RT * kBothLd, kBothLd, tid, keep);
+    } else {
+      qs.template put<false>(to, kBothLd, tid, keep);
+      gs.template put<false>(to + RT * kBothLd, kBothLd, tid, keep);
+    }
+    if (tid < 2 * RT) stats[at][tid / RT][tid % RT] = stat;
+  };
+  if (t0 < t1) {
+    fetch(t0);
+    put(t0);
+  }
+  __syncthreads();
+  for (int t = t0; t < t1; ++t) {
+    const int at = (t - t0) % NB;
+    const T* const qt = lds + at * kTile;
+    const T* const gt = qt + RT * kBothLd;
+    if (t + 1 < t1) fetch(t + 1);
+    v16f s = zero16(), dp = zero16();
+#pragma unroll
+    for (int kb = 0; kb < DC; ++kb) {
+      s = mma(row_frag(qt, kBothLd, kb, r32, h), k[kb], s);
+      dp = mma(row_frag(gt, kBothLd, kb, r32, h), v[kb], dp);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const v4f lse2 = *reinterpret_cast<const v4f*>(&stats[at][0][8 * j + 4 * h]);
+      const v4f delta = *reinterpret_cast<const v4f*>(&stats[at][1][8 * j + 4 * h]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = exp2_fast(__builtin_fmaf(s[4 * j + e], a.scale2, -lse2[e]));
+        s[4 * j + e] = p;
+        dp[4 * j + e] = p * (dp[4 * j + e] - delta[e]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const frag p = operand(s, i), ds = operand(dp, i);
+#pragma unroll
+      for (int c = 0; c < kOB; ++c) {
+        dv[c] = mma(col_frag(gt + 16 * i * kBothLd, kBothLd, 32 * c, lane), p, dv[c]);
+        dk[c] = mma(col_frag(qt + 16 * i * kBothLd, kBothLd, 32 * c, lane), ds, dk[c]);
+      }
+    }
+    if (t + 1 < t1) put(t + 1);
+    __syncthreads();
+  }
+  if (key >= a.Lk) return;
+  if (!counts) {  // whatever their columns hold
+#pragma unroll
+    for (int i = 0; i < kOB; ++i) dk[i] = dv[i] = zero16();
+  }
+  if (a.splits > 1) {
+    const int64_t n = (int64_t)a.B * a.Lk * a.Hk * a.D;
+    float* p = a.part + sp * 2 * n + (((int64_t)b * a.Lk + key) * a.Hk + hk) * a.D;
+#pragma unroll
+    for (int c = 0; c < kOB; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = 32 * c + 8 * j + 4 * h;
+        if (d < a.D) {
+          store4f(p + d, dk[c], j, a.scale);
+          store4f(p + n + d, dv[c], j, 1.0f);
+        }
+      }
+    return;
+  }
+  T* pk = reinterpret_cast<T*>(a.dk.p) + b * a.dk.batch + key * a.dk.row + hk * a.dk.head;
+  T* pv = reinterpret_cast<T*>(a.dv.p) + b * a.dv.batch + key * a.dv.row + hk * a.dv.head;
+#pragma unroll
+  for (int c = 0; c < kOB; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int d = 32 * c + 8 * j + 4 * h;
+      if (d < a.D) {
+        store4(pk + d, dk[c], j, a.scale);
+        store4(pv + d, dv[c], j, 1.0f);
+      }
+    }
+}
+
+// dK (blockIdx.y 0) and dV (1): the sum of the row ranges' parts, four channels a thread.
+__global__ __launch_bounds__(kThreads) void k_attn_dkv_sum(AttnArgs a) {
+  const int64_t n = (int64_t)a.B * a.Lk * a.Hk * a.D;
+  const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (e >= n) return;
+  const float* p = a.part + blockIdx.y * n + e;
+  v4f sum = {0, 0, 0, 0};
+  for (int s = 0; s < a.splits; ++s) sum += *reinterpret_cast<const v4f*>(p + s * 2 * n);
+  const ql_heads_view& t = blockIdx.y ? a.dv : a.dk;
+  const int64_t row = e / a.D, lh = row / a.Hk;
+  T* to = reinterpret_cast<T*>(t.p) + lh / a.Lk * t.batch + lh % a.Lk * t.row + row % a.Hk * t.head +
+          e % a.D;
+  if constexpr (sizeof(T) == 2) {
+    v4h o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (T)sum[i];
+    *reinterpret_cast<v4h*>(to) = o;
+  } else {
+    *reinterpret_cast<v4f*>(to) = sum;
+  }
+}
+
+constexpr int kNarrow = sizeof(T) == 2 ? 4 : 2;
+
+}  // namespace
+
+#define QL_CAT3(a, b, c, d) a##b##c##d
+#define QL_NAME(f, t, d) QL_CAT3(f, t, _, d)
+
+hipError_t QL_NAME(attn_forward_, QL_AT_T, QL_AT_DC)(const AttnArgs& a, bool narrow, hipStream_t s) {
+  const int grid = a.B * a.Hk * a.row_tiles * a.splits;
+  if (narrow)
+    k_attn_forward<kNarrow><<<grid, kThreads, 0, s>>>(a);
+  else
+    k_attn_forward<1><<<grid, kThreads, 0, s>>>(a);
+  if (a.splits > 1) {
+    const int64_t n = (int64_t)a.B * a.H * a.Lq;
+    k_attn_join<<<(int)((n + 3) / 4), kThreads, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t QL_NAME(attn_grad_, QL_AT_T, QL_AT_DC)(const AttnArgs& args, const AttnPlan& p,
+                                                  hipStream_t s) {
+  AttnArgs a = args;
+  a.row_tiles = p.q_tiles;
+  a.key_tiles = p.key_tiles;
+  a.splits = p.k_splits;
+  if (a.R > 0) k_attn_dq<<<a.B * a.Hk * a.row_tiles, kThreads, 0, s>>>(a);
+  if (a.Lk > 0) {
+    k_attn_dkv<<<a.B * a.Hk * a.key_tiles * a.splits, kThreads, 0, s>>>(a);
+    if (a.splits > 1) {
+      const int64_t n = (int64_t)a.B * a.Lk * a.Hk * a.D;
+      k_attn_dkv_sum<<<dim3((int)((n / 4 + kThreads - 1) / kThreads), 2), kThreads, 0, s>>>(a);
+    }
+  }
+  return hipGetLastError();
+}
+
+}  // namespace ql

@@ -1,0 +1,112 @@
+// Internal interface between the C ABI of a conditioned block's operators
+// (qlinear_block.cpp) and their kernels (k_rows4.hip, k_heads.hip, k_attn.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/qlinear.h"
+
+namespace ql {
+
+// -------------------------------------------------------------- 4-bit rows ----
+
+// Weights as the kernel reads them: tiles of 16 output channels by steps of 32 input
+// channels, tile after tile. A step is 64 words, word 16 q + i holding the codes of
+// channel 16 tile + i at inputs 8 q .. 8 q + 7 (nibble j: input 8 q + j). Behind the
+// codes the scales, [tile][group][16].
+struct Rows4Layout {
+  int tiles, steps, groups;
+  int64_t scales, bytes;  // offset of the scales, bytes in all
+};
+Rows4Layout rows4_layout(const ql_rows4& d);
+
+struct Rows4Args {
+  const uint32_t* codes;
+  const void* scales;
+  const float* bias;
+  const void* X;
+  int64_t ldx;
+  float* Y;
+  int64_t ldy;
+  float* part;  // [splits][M][tiles * 16], splits > 1
+  int M, N, K, steps, tiles, groups, group_steps;  // steps of a group
+  int splits;
+  bool x_bf16, s_bf16, silu;
+};
+int rows4_splits(int M, int N, int K);
+hipError_t launch_rows4(const Rows4Args& a, hipStream_t s);
+hipError_t launch_rows4_pack(const ql_rows4& d, const int8_t* codes, const void* scales,
+                             void* packed, hipStream_t s);
+hipError_t launch_rows4_quantize(const ql_rows4& d, const void* W, bool w_bf16, void* packed,
+                                 hipStream_t s);
+hipError_t launch_rows4_unpack(const ql_rows4& d, int8_t* codes, void* scales, hipStream_t s);
+
+// ------------------------------------------------------------- norms, turns ----
+
+struct HeadsArgs {
+  const void* x;
+  int64_t xb, xr;
+  const void* pos;
+  int64_t pb;
+  ql_heads_view y[3];  // q, k, v; in the gradient dq, dk, dv
+  void* dx;
+  int64_t db, dr;
+  const void* gamma[2];
+  const double* freqs;
+  int heads[3];
+  int B, L, D, n_axes, half[QL_MAX_AXES];  // half: pairs of an axis
+  float eps;
+  bool rms, halves, pos_f32, x_bf16, y_bf16, w_bf16;
+  bool vec;       // rows of x and y can be read and written in vectors
+  int tokens;     // tokens a workgroup turns at once (set by the launch)
+  void* dgamma[2];
+  float* part;    // [workgroups][2][D]
+  int groups;     // workgroups of the gradient
+};
+// Workgroups of the gradient call (each has a row of partial sums).
+int heads_grad_groups(int64_t tokens, int heads);
+hipError_t launch_heads(const HeadsArgs& a, hipStream_t s);
+hipError_t launch_heads_grad(const HeadsArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------- attention ----
+
+// Queries of the G = H / Hk heads that share a key head are rows of one matrix, row
+// r = l * G + g, so shared heads need no care in the kernels: they read a key once for
+// all of its rows, and the gradients of keys sum over all of them.
+struct AttnArgs {
+  ql_heads_view q, k, v, o, dout, dq, dk, dv;
+  float* lse;    // [B, H, Lq]; forward: may be nullptr
+  float* delta;  // [B, H, Lq]
+  const int32_t* lens;
+  const uint8_t* mask;
+  int64_t mask_batch;
+  int B, H, Hk, G, Lq, Lk, D, R;  // R = Lq * G
+  float scale, scale2;            // scale2 = scale * log2(e)
+  int row_tiles, key_tiles;
+  int splits;       // of the keys (forward), of the rows (dk and dv)
+  float* part;      // forward [splits][B, H, Lq][D]; dk, dv: [splits][2][B, Lk, Hk][D]
+  float* part_lse;  // [splits][B, H, Lq], base 2
+  bool bf16;
+};
+struct AttnPlan {
+  bool narrow;
+  int row_tiles, splits;          // forward
+  int q_tiles, key_tiles, k_splits;  // gradient
+  int64_t forward_bytes, grad_bytes;
+};
+AttnPlan attn_plan(const ql_attn& d);
+hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
+hipError_t launch_attn_grad(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
+
+// One object file for each head size and type defines its own; DC = 16-channel blocks.
+#define QL_ATTN_UNIT(T, DC)                                                        \
+  hipError_t attn_forward_##T##_##DC(const AttnArgs& a, bool narrow, hipStream_t); \
+  hipError_t attn_grad_##T##_##DC(const AttnArgs& a, const AttnPlan& p, hipStream_t);
+#define QL_ATTN_UNITS(X) \
+  X(f32, 2) X(f32, 4) X(f32, 5) X(f32, 6) X(f32, 8) X(f32, 10) \
+  X(bf16, 2) X(bf16, 4) X(bf16, 5) X(bf16, 6) X(bf16, 8) X(bf16, 10)
+#define QL_ATTN_DECL(T, DC) QL_ATTN_UNIT(T, DC)
+QL_ATTN_UNITS(QL_ATTN_DECL)
+
+}  // namespace ql

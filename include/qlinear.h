@@ -491,6 +491,175 @@ ql_status qlinear_grad_norm(const ql_grad* table, int32_t n, int64_t units, doub
 ql_status qlinear_grad_clip(const ql_grad* table, int32_t n, int64_t units, const double* partials,
                             float max_norm, float* norm, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a conditioned transformer block: what it computes between its
+ * quantized linears. The rules of the operators beside the layer hold for them too:
+ * no handle, no atomics, the caller's workspace, calls on any stream.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Few rows against 4-bit weights with a scale for each group of input channels:
+ * the modulation linear, which reads one conditioning vector an image. Weights
+ * are W[n,k] = scale[n, k / group] * code[n,k], codes in [-8, 7], laid out once by
+ * qlinear_rows4_pack or qlinear_rows4_quantize.
+ */
+typedef struct {
+  int32_t N, K;        /* 1 <= N <= 2^22; K % 16 == 0, 16 <= K <= 65536; N * K < 2^34 */
+  int32_t group;       /* 32, 64 or 128; the last group of a row may be short */
+  ql_dtype x_dtype;    /* X */
+  ql_dtype s_dtype;    /* scales */
+  ql_act act;          /* applied to X, in fp32 */
+  const void* packed;  /* DEVICE, 16-byte aligned, qlinear_rows4_bytes() bytes */
+  const float* bias;   /* DEVICE [N], or NULL */
+} ql_rows4;
+
+/* Bytes (HOST out) of the packed weights. The pointers in d are not looked at. */
+ql_status qlinear_rows4_bytes(const ql_rows4* d, int64_t* bytes);
+
+/* packed (DEVICE out, as d->packed will be) from codes (DEVICE int8 [N,K], their low
+ * four bits are kept) and scales (DEVICE s_dtype [N, ceil(K / group)]). */
+ql_status qlinear_rows4_pack(const ql_rows4* d, const int8_t* codes, const void* scales,
+                             void* packed, void* stream);
+
+/* The same from weights W (DEVICE w_dtype [N,K]): scale = absmax of the group / 7
+ * rounded to s_dtype, code = W / scale rounded half to even within [-7, 7] (0 where the
+ * scale is 0). W must be finite. */
+ql_status qlinear_rows4_quantize(const ql_rows4* d, const void* W, ql_dtype w_dtype, void* packed,
+                                 void* stream);
+
+/* codes (DEVICE int8 out [N,K]) and scales (DEVICE s_dtype out) of d->packed; either
+ * may be NULL. */
+ql_status qlinear_rows4_unpack(const ql_rows4* d, int8_t* codes, void* scales, void* stream);
+
+/* Workspace bytes (HOST out, may be 0) of qlinear_rows4 with M rows. */
+ql_status qlinear_rows4_workspace(const ql_rows4* d, int32_t M, int64_t* bytes);
+
+/*
+ * Y[m,n] = bias[n] + sum over groups g of scale[n,g] * sum over k in g of
+ * code[n,k] act(X[m,k]), sums in fp32.
+ *   X : DEVICE [M,K] of x_dtype, row stride ldx >= K elements, M <= 2^20.
+ *   Y : DEVICE fp32 out [M,N], row stride ldy >= N; overlaps nothing else.
+ * act(X) is multiplied in three bf16 parts that hold its 24 bits (a bf16 X without an
+ * activation in one); an infinity in X may come out as NaN. Meant for few rows: the
+ * weights are read again for every 48 rows. M = 0 enqueues nothing.
+ */
+ql_status qlinear_rows4(const ql_rows4* d, const void* X, int64_t ldx, int32_t M, float* Y,
+                        int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Element (b, l, h, c) of a tensor by heads lies at p + b * batch + l * row +
+ * h * head + c (strides in elements): [B, L, H, D], [B, H, L, D], or a slice of a wider
+ * row. p is DEVICE. Strides of an input are >= 0 and may repeat elements; those of an
+ * output may not. */
+typedef struct {
+  void* p;
+  int64_t batch, row, head;
+} ql_heads_view;
+
+/*
+ * Norms of queries and keys for each head and their rotation by positions of several
+ * axes (time, height, width), in one pass over the rows of a qkv linear. A row
+ * of x is q_heads + k_heads + v_heads heads of dim channels; queries and keys are
+ * normed and rotated, values only change their type. The first axis_dims[0]
+ * channels of a head turn with axis 0, the next axis_dims[1] with axis 1, ...;
+ * the rest do not turn.
+ */
+typedef enum { QL_HEADS_NONE = 0, QL_HEADS_RMS = 1 } ql_heads_norm;
+typedef enum { QL_PAIRS_ADJACENT = 0, QL_PAIRS_HALVES = 1 } ql_pairs;
+typedef enum { QL_POS_I32 = 0, QL_POS_F32 = 1 } ql_pos;
+#define QL_MAX_AXES 4
+typedef struct {
+  int32_t batch, positions;           /* >= 0; batch * positions < 2^24 */
+  int32_t q_heads, k_heads, v_heads;  /* >= 0, one at least > 0, together <= 4096 */
+  int32_t dim;                        /* 8 .. 160, a multiple of 8 */
+  ql_dtype x_dtype;                   /* x, dx */
+  ql_dtype y_dtype;                   /* q, k, v and their gradients */
+  ql_dtype w_dtype;                   /* gammas and their gradients */
+  ql_heads_norm norm;                 /* none, or x / sqrt(mean of squares + eps) * gamma */
+  float eps;                          /* > 0 */
+  const void* gamma_q;                /* DEVICE [dim], or NULL for 1 */
+  const void* gamma_k;
+  int32_t n_axes;                     /* 0 (no rotation) .. QL_MAX_AXES */
+  int32_t axis_dims[QL_MAX_AXES];     /* even, >= 2, together <= dim */
+  ql_pairs pairs;                     /* pair i of an axis at its channel c0 with d channels:
+                                         (c0 + 2 i, c0 + 2 i + 1) or (c0 + i, c0 + d / 2 + i) */
+  const double* freqs;                /* DEVICE [sum of axis_dims / 2], axis by axis: turns (of
+                                         2 pi) of each pair for one unit of position */
+  ql_pos pos_dtype;
+} ql_heads;
+
+/* Workspace bytes (HOST out) of qlinear_heads_grad. The pointers in d are not looked at. */
+ql_status qlinear_heads_workspace(const ql_heads* d, int64_t* bytes);
+
+/*
+ * q, k, v (y_dtype; a part of 0 heads is not looked at) from x. A pair (a, b) becomes
+ * (a cos - b sin, a sin + b cos) of its angle; angles are formed in fp64 and reduced
+ * there, so far positions keep their accuracy; statistics are fp32.
+ *   x   : DEVICE [batch, positions, heads * dim], strides in elements, row >= heads * dim.
+ *   pos : DEVICE pos_dtype, n_axes values a position (dense), batch stride pos_batch
+ *         elements (0: all images share them). NULL with n_axes = 0.
+ * The outputs overlap nothing else.
+ */
+ql_status qlinear_heads(const ql_heads* d, const void* x, int64_t x_batch, int64_t x_row,
+                        const void* pos, int64_t pos_batch, const ql_heads_view* q,
+                        const ql_heads_view* k, const ql_heads_view* v, void* stream);
+
+/*
+ * Gradients for dq, dk, dv: dx (x_dtype; strides as x; overlaps nothing else) and
+ * dgamma_q, dgamma_k [dim] of w_dtype (either may be NULL), summed in fp32 and joined
+ * in fp64, every element written.
+ */
+ql_status qlinear_heads_grad(const ql_heads* d, const ql_heads_view* dq, const ql_heads_view* dk,
+                             const ql_heads_view* dv, const void* x, int64_t x_batch,
+                             int64_t x_row, const void* pos, int64_t pos_batch, void* dx,
+                             int64_t dx_batch, int64_t dx_row, void* dgamma_q, void* dgamma_k,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Attention of q_len queries to the k_len states of another sequence (or the same):
+ * O = softmax(scale Q K^T) V by head; query head h reads key head h / (heads /
+ * kv_heads). Keys that do not count (past k_lens[b], or with k_mask 0) take no part:
+ * nothing of them is multiplied, so infinities and NaN there do no harm. A query
+ * without any key that counts gets O = 0 and lse = -infinity.
+ */
+typedef struct {
+  int32_t batch, q_len, k_len;  /* >= 0; batch * heads * q_len and batch * kv_heads * k_len < 2^31 */
+  int32_t heads, kv_heads;      /* heads a positive multiple of kv_heads */
+  int32_t dim;                  /* 8 .. 160, a multiple of 8 */
+  ql_dtype dtype;               /* of all tensors by heads */
+  float scale;                  /* > 0, finite */
+  const int32_t* k_lens;        /* DEVICE [batch], clamped to [0, k_len], or NULL for k_len */
+  const uint8_t* k_mask;        /* DEVICE [batch, k_len], 0: does not count; or NULL */
+  int64_t mask_batch;           /* batch stride of k_mask in bytes */
+} ql_attn;
+
+/* Workspace bytes (HOST out, may be 0) of qlinear_attention (grad = 0) or
+ * qlinear_attention_grad (grad = 1). The pointers in d are not looked at. */
+ql_status qlinear_attention_workspace(const ql_attn* d, int32_t grad, int64_t* bytes);
+
+/*
+ * out from q [batch, q_len, heads, dim] and k, v [batch, k_len, kv_heads, dim]; views
+ * start at multiples of 16 bytes and so do their strides. Products and sums
+ * run in fp32 on the matrix cores; with bf16 tensors the softmax's weights are
+ * rounded to bf16 before they meet v, its statistics stay fp32.
+ *   lse : NULL, or DEVICE fp32 out [batch, heads, q_len]: log of the sum of
+ *         exp(scale q k), which the gradient takes.
+ */
+ql_status qlinear_attention(const ql_attn* d, const ql_heads_view* q, const ql_heads_view* k,
+                            const ql_heads_view* v, const ql_heads_view* out, float* lse,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Gradients for dout: dq, dk, dv (dtype; a key head's are summed over the queries' heads
+ * that share it; zero for keys that do not count), from out and lse as the forward call
+ * gave them. All elements of the three are written.
+ */
+ql_status qlinear_attention_grad(const ql_attn* d, const ql_heads_view* dout,
+                                 const ql_heads_view* q, const ql_heads_view* k,
+                                 const ql_heads_view* v, const ql_heads_view* out,
+                                 const float* lse, const ql_heads_view* dq,
+                                 const ql_heads_view* dk, const ql_heads_view* dv, void* workspace,
+                                 int64_t workspace_bytes, void* stream);
+
 /* Message for the last non-OK status on this thread ("" if none). */
 const char* qlinear_last_error(void);
 
