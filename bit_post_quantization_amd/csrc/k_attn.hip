@@ -276,8 +276,17 @@ struct Fwd {
                                                                  : kJoin;
 };
 
+#ifndef FW
+#define FW 1
+#endif
+#ifndef QW
+#define QW 1
+#endif
+#ifndef KW
+#define KW 1
+#endif
 template <int WK>
-__global__ __launch_bounds__(kThreads) void k_attn_forward(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
   typedef Fwd<WK> P;
   constexpr int KT = P::KT, SUB = P::SUB, W = KT / 32;
   __shared__ __attribute__((aligned(16))) char smem[P::kLds];
@@ -499,7 +508,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
 constexpr int kBackRows = 32;  // rows or keys of a tile in LDS
 
 // dQ, and delta for k_attn_dkv. Keys that do not count are zero in LDS and have P = 0.
-__global__ __launch_bounds__(kThreads) void k_attn_dq(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
   constexpr int KT = 64, W = 2, kTile = KT * (kBothLd + kRowLd);
   constexpr int NB = 2 * kTile * (int)sizeof(T) <= 81920 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) T lds[NB * kTile];
@@ -610,7 +619,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_dq(AttnArgs a) {
 }
 
 // dK and dV of 128 keys from a range of the rows; a lane has one key.
-__global__ __launch_bounds__(kThreads) void k_attn_dkv(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
   constexpr int RT = kBackRows, kTile = RT * 2 * kBothLd;
   constexpr int NB = 2;
   __shared__ __attribute__((aligned(16))) T lds[NB * kTile];

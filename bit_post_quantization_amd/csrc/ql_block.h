@@ -11,30 +11,38 @@ namespace ql {
 
 // -------------------------------------------------------------- 4-bit rows ----
 
-// Weights as the kernel reads them: tiles of 16 output channels by steps of 32 input
-// channels, tile after tile. A step is 64 words, word 16 q + i holding the codes of
-// channel 16 tile + i at inputs 8 q .. 8 q + 7 (nibble j: input 8 q + j). Behind the
-// codes the scales, [tile][group][16].
+// Weights as the kernel reads them: tiles of 16 output channels by units of 128 input
+// channels, tile after tile. A unit is 64 pieces of 16 bytes, word s of piece 16 q + i
+// holding the codes of channel 16 tile + i at inputs 32 s + 8 q .. + 7 (nibble j: input
+// j of the eight). Behind the codes the scales, [tile][group][16], with groups up to the
+// end of the last unit.
 struct Rows4Layout {
-  int tiles, steps, groups;
-  int64_t scales, bytes;  // offset of the scales, bytes in all
+  int tiles, units, groups, spots;  // spots: groups with those past K
+  int64_t scales, bytes;            // offset of the scales, bytes in all
 };
 Rows4Layout rows4_layout(const ql_rows4& d);
 
+typedef uint32_t Rows4Piece __attribute__((ext_vector_type(4)));
 struct Rows4Args {
-  const uint32_t* codes;
+  const Rows4Piece* codes;
   const void* scales;
   const float* bias;
   const void* X;
   int64_t ldx;
   float* Y;
   int64_t ldy;
-  float* part;  // [splits][M][tiles * 16], splits > 1
-  int M, N, K, steps, tiles, groups, group_steps;  // steps of a group
-  int splits;
+  char* digits;   // workspace: act(X) in fixed point
+  float* worths;  // workspace: [M][units]
+  float* part;    // workspace: [splits][M][N], splits > 1
+  int M, N, K, units, tiles, group;
+  int splits;     // workgroups that share a tile's inputs (set by the launch)
   bool x_bf16, s_bf16, silu;
+  bool x_vec;     // rows of X are 16-byte aligned
 };
-int rows4_splits(int M, int N, int K);
+struct Rows4Ws {
+  int64_t worths, part, bytes;  // offsets, and bytes in all
+};
+Rows4Ws rows4_ws(const ql_rows4& d, int M);
 hipError_t launch_rows4(const Rows4Args& a, hipStream_t s);
 hipError_t launch_rows4_pack(const ql_rows4& d, const int8_t* codes, const void* scales,
                              void* packed, hipStream_t s);

@@ -74,11 +74,6 @@ ql_status check_few_rows(int32_t M) {
   return QL_OK;
 }
 
-int64_t rows4_ws(const ql_rows4* d, int32_t M) {
-  const int n = M > 0 ? ql::rows4_splits(M, d->N, d->K) : 1;
-  return n > 1 ? (int64_t)n * M * d->N * 4 : 0;
-}
-
 ql_status check_packed(const ql_rows4* d, const void* packed) {
   if (!packed) return fail(QL_ERR_ARG, "packed is NULL");
   if (!aligned(packed, 16)) return fail(QL_ERR_ARG, "packed must be 16-byte aligned");
@@ -436,7 +431,7 @@ ql_status qlinear_rows4_workspace(const ql_rows4* d, int32_t M, int64_t* bytes) 
   QL_CHECK(check_rows4(d));
   QL_CHECK(check_few_rows(M));
   if (!bytes) return fail(QL_ERR_ARG, "bytes is NULL");
-  *bytes = rows4_ws(d, M);
+  *bytes = ql::rows4_ws(*d, M).bytes;
   return ok();
 }
 
@@ -454,28 +449,30 @@ ql_status qlinear_rows4(const ql_rows4* d, const void* X, int64_t ldx, int32_t M
     return fail(QL_ERR_ARG, "ldx = %lld or ldy = %lld is less than its row", (long long)ldx,
                 (long long)ldy);
   if (X == Y) return fail(QL_ERR_ARG, "Y is X");
-  QL_CHECK(check_workspace(workspace, workspace_bytes, rows4_ws(d, M)));
+  const ql::Rows4Ws w = ql::rows4_ws(*d, M);
+  QL_CHECK(check_workspace(workspace, workspace_bytes, w.bytes));
   const ql::Rows4Layout l = ql::rows4_layout(*d);
   ql::Rows4Args a{};
-  a.codes = reinterpret_cast<const uint32_t*>(d->packed);
+  a.codes = reinterpret_cast<const ql::Rows4Piece*>(d->packed);
   a.scales = reinterpret_cast<const char*>(d->packed) + l.scales;
   a.bias = d->bias;
   a.X = X;
   a.ldx = ldx;
   a.Y = Y;
   a.ldy = ldy;
-  a.part = reinterpret_cast<float*>(workspace);
+  a.digits = reinterpret_cast<char*>(workspace);
+  a.worths = reinterpret_cast<float*>(a.digits + w.worths);
+  a.part = reinterpret_cast<float*>(a.digits + w.part);
   a.M = M;
   a.N = d->N;
   a.K = d->K;
-  a.steps = l.steps;
+  a.units = l.units;
   a.tiles = l.tiles;
-  a.groups = l.groups;
-  a.group_steps = d->group / 32;
-  a.splits = ql::rows4_splits(M, d->N, d->K);
+  a.group = d->group;
   a.x_bf16 = d->x_dtype == QL_BF16;
   a.s_bf16 = d->s_dtype == QL_BF16;
   a.silu = d->act == QL_ACT_SILU;
+  a.x_vec = aligned(X, 16) && ldx * size_of(d->x_dtype) % 16 == 0;
   QL_LAUNCH(ql::launch_rows4(a, reinterpret_cast<hipStream_t>(stream)), "launching 4-bit rows");
   return ok();
 }
