@@ -199,10 +199,13 @@ class GroupLinear4:
 
 # --------------------------------------------------------------- norms, turns ----
 
-def _view(t, name: str, dev: int, dtype, shape) -> QlHeadsView:
-    """A [B, L, H, D] tensor, whose channels are contiguous, as the C ABI takes it."""
+def _view(t, name: str, dev: int, dtype, shape, dense) -> QlHeadsView:
+    """A [B, L, H, D] tensor, whose channels are contiguous, as the C ABI takes it; `dense`
+    are the strides of a packed one."""
     if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
         _refuse(t, name, dev, dtype, shape)
+    if t.is_contiguous():
+        return QlHeadsView(t.data_ptr(), *dense)
     sb, sl, sh, sd = t.stride()
     _need(sd == 1, f"{name}: channels are not contiguous")
     return QlHeadsView(t.data_ptr(), sb, sl, sh)
@@ -254,41 +257,58 @@ class HeadNormRope:
                                   device=torch.device("cuda", dev)) if axes else None
         self.desc.freqs = _ptr(self.freqs)
         self._dev, self._made_on = dev, _stream(dev)
-        self._sizes = {}  # descriptor and workspace bytes by size of call
+        self._alike = self.heads[0] == self.heads[1] == self.heads[2]
+        self._sizes = {}  # what :meth:`_size` makes, by size of call
 
     def _call(self, x, pos):
-        """(device, stream, descriptor, workspace bytes, x's batch and row stride,
-        positions' address and batch stride) of a call."""
+        """(device, stream, size, x's batch and row stride, positions' address and batch
+        stride) of a call; a size is (descriptor, workspace bytes, shapes of q, k and v,
+        their dense strides)."""
         dev, dt, shape = _device(), x.dtype, x.shape
-        _need(dt in _DT, f"x is {dt}: f32 or bf16 only")
-        _need(dev == self._dev, "the layer was made on another device")
-        _need(len(shape) == 3 and shape[2] == sum(self.heads) * self.dim,
-              f"x is {tuple(shape)}, not [B, L, {sum(self.heads) * self.dim}]")
-        if x.get_device() != dev:
+        if x.get_device() != dev or dev != self._dev:
+            _need(dev == self._dev, "the layer was made on another device")
             _refuse(x, "x", dev, dt, shape)
-        B, L, n = shape
-        xb, xr, xc = x.stride()
-        _need(xc == 1 or n == 1, "x: channels are not contiguous")
-        at, pb, kind = None, 0, _lib.QL_POS_I32
+        kind, own = None, False
         if self.axes:
             _need(isinstance(pos, torch.Tensor) and pos.dtype in _POS,
                   "pos must be an int32 or f32 tensor")
-            kind = _POS[pos.dtype]
-            own = pos.dim() == 3
-            at = _flat(pos, "pos", dev, pos.dtype,
-                       (B, L, len(self.axes)) if own else (L, len(self.axes)))
-            pb = L * len(self.axes) if own else 0
-        key = (dt, B, L, kind)
-        size = self._sizes.get(key)
+            kind, own = pos.dtype, pos.dim() == 3
+        size = self._sizes.get((dt, shape, kind))
         if size is None:
-            d = QlHeads.from_buffer_copy(self.desc)
-            d.batch, d.positions, d.x_dtype, d.pos_dtype = B, L, _DT[dt], kind
-            size = _remember(self._sizes, key, (d, qlinear_heads_workspace(d)))
+            size = self._size(dt, shape, kind)
+        n = shape[2]
+        if x.is_contiguous():
+            xb, xr = shape[1] * n, n
+        else:
+            xb, xr, xc = x.stride()
+            _need(xc == 1 or n == 1, "x: channels are not contiguous")
+        at, pb = None, 0
+        if kind is not None:
+            want = (shape[1], len(self.axes))
+            at = _flat(pos, "pos", dev, kind, (shape[0], *want) if own else want)
+            pb = want[0] * want[1] if own else 0
         s = _stream(dev)
         if s != self._made_on and self.freqs is not None:
             # the table's memory outlives the layer until this stream is done
             self.freqs.record_stream(torch.cuda.current_stream(dev))
-        return dev, s, size[0], size[1], xb, xr, at, pb
+        return dev, s, size, xb, xr, at, pb
+
+    def _size(self, dt, shape, kind):
+        _need(dt in _DT, f"x is {dt}: f32 or bf16 only")
+        n = sum(self.heads) * self.dim
+        _need(len(shape) == 3 and shape[2] == n, f"x is {tuple(shape)}, not [B, L, {n}]")
+        d = QlHeads.from_buffer_copy(self.desc)
+        d.batch, d.positions, d.x_dtype = shape[0], shape[1], _DT[dt]
+        d.pos_dtype = _lib.QL_POS_I32 if kind is None else _POS[kind]
+        parts = [(shape[0], shape[1], h, self.dim) if h else None for h in self.heads]
+        dense = [(shape[1] * h * self.dim, h * self.dim, self.dim) for h in self.heads]
+        return _remember(self._sizes, (dt, shape, kind),
+                         (d, qlinear_heads_workspace(d), parts, dense))
+
+    def _views(self, tensors, names, dev, size):
+        """Views of a triple as the C ABI takes them, None for a part without heads."""
+        return [None if shape is None else _view(t, name, dev, self.y_dtype, shape, strides)
+                for t, name, shape, strides in zip(tensors, names, size[2], size[3])]
 
     def forward(self, x, pos=None, out=None, stream=None):
         """(q, k, v) from x [B, L, heads * dim] (f32 or bf16): [B, L, heads, dim] each, None
@@ -298,20 +318,20 @@ class HeadNormRope:
         if stream is not None:
             with _on(stream):
                 return self.forward(x, pos, out)
-        dev, s, d, _, xb, xr, at, pb = self._call(x, pos)
-        B, L, _ = x.shape
-        given = (None, None, None) if out is None else out
-        outs, views = [], []
-        for t, h, name in zip(given, self.heads, ("q", "k", "v")):
-            shape = (B, L, h, self.dim)
-            if h == 0:
-                t = None
-            elif out is None:
-                t = torch.empty(shape, dtype=self.y_dtype, device=x.device)
-            outs.append(t)
-            views.append(_view(t, name, dev, self.y_dtype, shape) if h else None)
-        qlinear_heads(d, x.data_ptr(), xb, xr, at, pb, *views, s)
-        return tuple(outs)
+        dev, s, size, xb, xr, at, pb = self._call(x, pos)
+        if out is None:
+            if self._alike:  # one allocation for all three: an allocation takes the host 1 us
+                out = torch.empty((3, *size[2][0]), dtype=self.y_dtype, device=x.device).unbind(0)
+            else:
+                out = [None if shape is None else
+                       torch.empty(shape, dtype=self.y_dtype, device=x.device) for shape in size[2]]
+            views = [None if t is None else QlHeadsView(t.data_ptr(), *dense)
+                     for t, dense in zip(out, size[3])]
+        else:
+            out = [None if shape is None else t for t, shape in zip(out, size[2])]
+            views = self._views(out, ("q", "k", "v"), dev, size)
+        qlinear_heads(size[0], x.data_ptr(), xb, xr, at, pb, *views, s)
+        return tuple(out)
 
     def grad(self, dy, x, pos=None, out=None, stream=None):
         """(dx, dgamma_q, dgamma_k) for dy = (dq, dk, dv) of :meth:`forward` (None for a
@@ -320,11 +340,11 @@ class HeadNormRope:
         if stream is not None:
             with _on(stream):
                 return self.grad(dy, x, pos, out)
-        dev, s, d, nb, xb, xr, at, pb = self._call(x, pos)
-        B, L, n = x.shape
-        views = [_view(t, name, dev, self.y_dtype, (B, L, h, self.dim)) if h else None
-                 for t, h, name in zip(dy, self.heads, ("dq", "dk", "dv"))]
-        dx = torch.empty((B, L, n), dtype=x.dtype, device=x.device)
+        dev, s, size, xb, xr, at, pb = self._call(x, pos)
+        d, nb = size[:2]
+        _, L, n = x.shape
+        views = self._views(dy, ("dq", "dk", "dv"), dev, size)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         gammas = (self.gamma_q, self.gamma_k)
         if out is None:
             out = [None if g is None else torch.empty_like(g) for g in gammas]
@@ -362,26 +382,34 @@ class CrossAttention:
         self._sizes = {}  # descriptor and workspace bytes by size of call
 
     def _call(self, dev, q, k, lens, mask, grad):
-        """(descriptor, workspace bytes, shapes of queries and keys) of a call."""
-        dt, qs, ks = q.dtype, q.shape, k.shape
-        _need(len(qs) == 4 and len(ks) == 4, "q and k must be [B, L, heads, dim]")
-        key = (dt, qs[0], qs[1], ks[1], grad)
+        """(descriptor, workspace bytes, shapes of queries and keys, their dense strides)
+        of a call."""
+        key = (q.dtype, q.shape, k.shape, grad)
         size = self._sizes.get(key)
         if size is None:
-            _need(dt in _DT, f"q is {dt}: f32 or bf16 only")
-            d = QlAttn.from_buffer_copy(self.desc)
-            d.batch, d.q_len, d.k_len, d.dtype = qs[0], qs[1], ks[1], _DT[dt]
-            size = _remember(self._sizes, key, (d, qlinear_attention_workspace(d, grad)))
-        d, nb = size
-        if lens is not None or mask is not None:
-            d = QlAttn.from_buffer_copy(d)
-            if lens is not None:
-                d.k_lens = _flat(lens, "lens", dev, _I32, (qs[0],))
-            if mask is not None:
-                _need(mask.dtype in (torch.bool, torch.uint8), f"mask is {mask.dtype}, not bool")
-                d.mask_batch = _rows(mask, "mask", dev, mask.dtype, (qs[0], ks[1]))
-                d.k_mask = mask.data_ptr()
-        return d, nb, (qs[0], qs[1], self.heads, self.dim), (qs[0], ks[1], self.kv_heads, self.dim)
+            size = self._size(key, q, k, grad)
+        if lens is None and mask is None:
+            return size
+        d = QlAttn.from_buffer_copy(size[0])
+        if lens is not None:
+            d.k_lens = _flat(lens, "lens", dev, _I32, (d.batch,))
+        if mask is not None:
+            _need(mask.dtype in (torch.bool, torch.uint8), f"mask is {mask.dtype}, not bool")
+            d.mask_batch = _rows(mask, "mask", dev, mask.dtype, (d.batch, d.k_len))
+            d.k_mask = mask.data_ptr()
+        return (d, *size[1:])
+
+    def _size(self, key, q, k, grad):
+        _need(q.dim() == 4 and k.dim() == 4, "q and k must be [B, L, heads, dim]")
+        _need(q.dtype in _DT, f"q is {q.dtype}: f32 or bf16 only")
+        d = QlAttn.from_buffer_copy(self.desc)
+        d.batch, d.q_len, d.k_len, d.dtype = q.shape[0], q.shape[1], k.shape[1], _DT[q.dtype]
+        D, shapes, dense = self.dim, [], []
+        for L, h in ((d.q_len, self.heads), (d.k_len, self.kv_heads)):
+            shapes.append((d.batch, L, h, D))
+            dense.append((L * h * D, h * D, D))
+        return _remember(self._sizes, key,
+                         (d, qlinear_attention_workspace(d, grad), *shapes, *dense))
 
     def forward(self, q, k, v, lens=None, mask=None, out=None, save: bool = False, stream=None):
         """softmax(scale q k^T) v in q's type and shape; with ``save`` returns (out, lse),
@@ -390,12 +418,14 @@ class CrossAttention:
             with _on(stream):
                 return self.forward(q, k, v, lens, mask, out, save)
         dev, dt = _device(), q.dtype
-        d, nb, qs, ks = self._call(dev, q, k, lens, mask, 0)
-        vq, vk = _view(q, "q", dev, dt, qs), _view(k, "k", dev, dt, ks)
-        vv = _view(v, "v", dev, dt, ks)
+        d, nb, qs, ks, qd, kd = self._call(dev, q, k, lens, mask, 0)
+        vq, vk = _view(q, "q", dev, dt, qs, qd), _view(k, "k", dev, dt, ks, kd)
+        vv = _view(v, "v", dev, dt, ks, kd)
         if out is None:
             out = torch.empty(qs, dtype=dt, device=q.device)
-        vo = _view(out, "out", dev, dt, qs)
+            vo = QlHeadsView(out.data_ptr(), *qd)
+        else:
+            vo = _view(out, "out", dev, dt, qs, qd)
         lse = torch.empty((qs[0], qs[2], qs[1]), dtype=_F32, device=q.device) if save else None
         ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
         qlinear_attention(d, vq, vk, vv, vo, _ptr(lse), _ptr(ws), nb, _stream(dev))
@@ -409,15 +439,15 @@ class CrossAttention:
             with _on(stream):
                 return self.grad(dout, q, k, v, out, lse, lens, mask, into)
         dev, dt = _device(), q.dtype
-        d, nb, qs, ks = self._call(dev, q, k, lens, mask, 1)
-        vq, vk = _view(q, "q", dev, dt, qs), _view(k, "k", dev, dt, ks)
-        vv, vd = _view(v, "v", dev, dt, ks), _view(dout, "dout", dev, dt, qs)
-        vo = _view(out, "out", dev, dt, qs)
+        d, nb, qs, ks, qd, kd = self._call(dev, q, k, lens, mask, 1)
+        vq, vk = _view(q, "q", dev, dt, qs, qd), _view(k, "k", dev, dt, ks, kd)
+        vv, vd = _view(v, "v", dev, dt, ks, kd), _view(dout, "dout", dev, dt, qs, qd)
+        vo = _view(out, "out", dev, dt, qs, qd)
         at = _flat(lse, "lse", dev, _F32, (qs[0], qs[2], qs[1]))
         if into is None:
             into = [torch.empty(s, dtype=dt, device=q.device) for s in (qs, ks, ks)]
-        views = [_view(t, name, dev, dt, s)
-                 for t, name, s in zip(into, ("dq", "dk", "dv"), (qs, ks, ks))]
+        views = [_view(t, name, dev, dt, s, n) for t, name, s, n in
+                 zip(into, ("dq", "dk", "dv"), (qs, ks, ks), (qd, kd, kd))]
         ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
         qlinear_attention_grad(d, vd, vq, vk, vv, vo, at, *views, _ptr(ws), nb, _stream(dev))
         return tuple(into)

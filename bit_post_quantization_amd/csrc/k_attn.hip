@@ -276,14 +276,15 @@ struct Fwd {
                                                                  : kJoin;
 };
 
+// Waves a SIMD that the registers are to allow.
 #ifndef FW
-#define FW 1
+#define FW (sizeof(T) == 2 ? 2 : 1)
 #endif
 #ifndef QW
-#define QW 1
+#define QW (sizeof(T) == 2 ? 2 : 1)
 #endif
 #ifndef KW
-#define KW 1
+#define KW (sizeof(T) == 2 && DC <= 6 ? 2 : 1)
 #endif
 template <int WK>
 __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
@@ -474,23 +475,33 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
     }
 }
 
-// One wave a row: the parts of its splits weighted by their share of the sum.
+// One wave a row: the parts of its splits weighted by their share of the sum. Lane s
+// has split s's share; the parts' loads wait for nothing.
 __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
   const int64_t n = (int64_t)a.B * a.H * a.Lq;
   const int64_t at = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
   if (at >= n) return;
   const int lane = threadIdx.x & 63;
-  float top = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * n + at]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  float total = 0.0f, acc[3] = {0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float f = exp2_fast(a.part_lse[s * n + at] - base);
-    total += f;
-    const float* p = a.part + (s * n + at) * a.D;
+  const float mine = lane < a.splits ? a.part_lse[lane * n + at] : -INFINITY;  // splits <= 64
+  float acc[3] = {0.0f, 0.0f, 0.0f}, top = mine;
+  for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
+  const float share = exp2_fast(mine - (top == -INFINITY ? 0.0f : top));
+  float total = share;
+  for (int i = 1; i < 64; i *= 2) total += __shfl_xor(total, i);
+  for (int s0 = 0; s0 < a.splits; s0 += 8) {
+    float p[8][3];
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (lane + 64 * i < a.D) acc[i] = __builtin_fmaf(f, p[lane + 64 * i], acc[i]);
+    for (int j = 0; j < 8; ++j) {
+      const float* from = a.part + (min(s0 + j, a.splits - 1) * n + at) * a.D;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) p[j][i] = lane + 64 * i < a.D ? from[lane + 64 * i] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = s0 + j < a.splits ? __shfl(share, s0 + j) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) acc[i] = __builtin_fmaf(f, p[j][i], acc[i]);
+    }
   }
   const bool empty = total == 0.0f;
   const float inv = empty ? 0.0f : 1.0f / total;

@@ -54,7 +54,6 @@ enum { kAdjacent = 0, kHalves = 1, kScattered = 2 };
 
 template <typename XT> struct Geo {
   static constexpr int V = 16 / sizeof(XT), P = V / 2;  // channels and pairs of a piece
-  static constexpr int G = sizeof(XT) == 4 ? 8 : 4;     // lanes of a head
 };
 
 // Where the pieces of a lane lie in a head, in pair order.
@@ -155,7 +154,8 @@ template <int G>
 __device__ __forceinline__ float head_sum(float v) {
   v += xor_lane<1>(v);
   v += xor_lane<2>(v);
-  if constexpr (G == 8) v += xor_lane<4>(v);
+  if constexpr (G >= 8) v += xor_lane<4>(v);
+  if constexpr (G >= 16) v += xor_lane<8>(v);
   return v;
 }
 
@@ -168,9 +168,8 @@ __device__ __forceinline__ void form_turns(const HeadsArgs& a, float2* turn, int
     const int axis = pair_channels(a, p, c1, c2);
     float2 cs = make_float2(1.0f, 0.0f);
     if (axis < a.n_axes) {
-      const int64_t tok = tok0 + t;
-      const int b = (int)(tok / a.L);
-      const int64_t at = b * a.pb + (tok - (int64_t)b * a.L) * a.n_axes + axis;
+      const int tok = (int)tok0 + t, b = tok / a.L;
+      const int64_t at = b * a.pb + (int64_t)(tok - b * a.L) * a.n_axes + axis;
       const double x = a.pos_f32 ? (double)reinterpret_cast<const float*>(a.pos)[at]
                                  : (double)reinterpret_cast<const int32_t*>(a.pos)[at];
       const double turns = x * a.freqs[p];
@@ -178,6 +177,22 @@ __device__ __forceinline__ void form_turns(const HeadsArgs& a, float2* turn, int
       sincospif(2.0f * part, &cs.y, &cs.x);
     }
     turn[i] = cs;
+  }
+}
+
+// Where the tokens' rows start, in elements: x and dx, and the outputs or their gradients.
+struct Starts {
+  int64_t x, dx, y[3];
+};
+__device__ __forceinline__ void find_starts(const HeadsArgs& a, Starts* out, int64_t tok0, int n) {
+  for (int t = threadIdx.x; t < n; t += kThreads) {
+    const int tok = (int)tok0 + t, b = tok / a.L, l = tok - b * a.L;
+    Starts s;
+    s.x = b * a.xb + l * a.xr;
+    s.dx = b * a.db + l * a.dr;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) s.y[i] = b * a.y[i].batch + l * a.y[i].row;
+    out[t] = s;
   }
 }
 
@@ -195,23 +210,23 @@ __device__ __forceinline__ void fetch_gammas(const HeadsArgs& a, float (*out)[2 
 
 // ----------------------------------------------------------------- forward ----
 
-template <typename XT, typename YT, int C, int MODE>
+template <typename XT, typename YT, int G, int C, int MODE>
 __global__ __launch_bounds__(kThreads) void k_heads(HeadsArgs a) {
-  constexpr int P = Geo<XT>::P, G = Geo<XT>::G, kGroups = kThreads / G;
+  constexpr int P = Geo<XT>::P, kGroups = kThreads / G;
   __shared__ float gamma[2][2 * kMaxPairs];
+  __shared__ Starts starts[kMaxTokens];
   extern __shared__ float2 turn[];  // [tokens][D / 2]
   const int tid = threadIdx.x, group = tid / G;
   const int64_t all = (int64_t)a.B * a.L, tok0 = (int64_t)blockIdx.x * a.tokens;
   const int n = (int)(all - tok0 < a.tokens ? all - tok0 : a.tokens);
   const int heads = a.heads[0] + a.heads[1] + a.heads[2], rows = n * heads;
+  find_starts(a, starts, tok0, n);
   Places<C, P, MODE> at;
   at.template find<G>(a, tid % G);
+  __syncthreads();
   const auto row_in = [&](int r) {
     const int t = r / heads;
-    const int64_t tok = tok0 + t;
-    const int b = (int)(tok / a.L);
-    return reinterpret_cast<const XT*>(a.x) + b * a.xb + (tok - (int64_t)b * a.L) * a.xr +
-           (int64_t)(r - t * heads) * a.D;
+    return reinterpret_cast<const XT*>(a.x) + starts[t].x + (r - t * heads) * a.D;
   };
   Vals<C, P> v, next;
   load<XT, C, P, G, MODE>(row_in(min(group, rows - 1)), at, group < rows, next);
@@ -255,11 +270,8 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadsArgs a) {
         }
       }
     }
-    const ql_heads_view& y = a.y[part];
-    const int64_t tok = tok0 + t;
-    const int b = (int)(tok / a.L);
-    store<YT, C, P, G, MODE>(reinterpret_cast<YT*>(y.p) + b * y.batch +
-                                 (tok - (int64_t)b * a.L) * y.row + hd * y.head,
+    store<YT, C, P, G, MODE>(reinterpret_cast<YT*>(a.y[part].p) + starts[t].y[part] +
+                                 hd * a.y[part].head,
                              at, v);
   }
 }
@@ -268,11 +280,12 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadsArgs a) {
 
 // blockIdx.y says which part (q, k, v) a workgroup works for, so that a lane keeps
 // one sum of dgamma; it walks over the tokens in steps of gridDim.x tiles.
-template <typename XT, typename YT, int C, int MODE>
+template <typename XT, typename YT, int G, int C, int MODE>
 __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
-  constexpr int P = Geo<XT>::P, G = Geo<XT>::G, kGroups = kThreads / G;
+  constexpr int P = Geo<XT>::P, kGroups = kThreads / G;
   __shared__ float gamma[2][2 * kMaxPairs];
   __shared__ float sums[kThreads / 64][2 * kMaxPairs];
+  __shared__ Starts starts[kMaxTokens];
   extern __shared__ float2 turn[];
   const int tid = threadIdx.x, group = tid / G, part = blockIdx.y, heads = a.heads[part];
   const int64_t all = (int64_t)a.B * a.L;
@@ -290,20 +303,18 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
   for (int64_t tok0 = (int64_t)blockIdx.x * a.tokens; tok0 < all && heads > 0; tok0 += step) {
     const int n = (int)(all - tok0 < a.tokens ? all - tok0 : a.tokens), rows = n * heads;
     __syncthreads();  // the turns before have been read
+    find_starts(a, starts, tok0, n);
     if (part < 2) form_turns(a, turn, tok0, n);
     __syncthreads();
     for (int r = group; r < rows; r += kGroups) {
       const int t = r / heads, hd = r - t * heads;
-      const int64_t tok = tok0 + t;
-      const int b = (int)(tok / a.L);
-      const int64_t l = tok - (int64_t)b * a.L;
       Vals<C, P> x, d;
-      load<YT, C, P, G, MODE>(reinterpret_cast<const YT*>(y.p) + b * y.batch + l * y.row +
-                                  hd * y.head, at, true, d);
+      load<YT, C, P, G, MODE>(reinterpret_cast<const YT*>(y.p) + starts[t].y[part] + hd * y.head, at,
+                              true, d);
       if (part < 2) {
         if (a.rms)
-          load<XT, C, P, G, MODE>(reinterpret_cast<const XT*>(a.x) + b * a.xb + l * a.xr +
-                                      (int64_t)(head0 + hd) * a.D, at, true, x);
+          load<XT, C, P, G, MODE>(reinterpret_cast<const XT*>(a.x) + starts[t].x +
+                                      (head0 + hd) * a.D, at, true, x);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           const int p0 = min(at.j + c * G, at.pieces - 1) * P;
@@ -347,8 +358,7 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
           }
         }
       }
-      store<XT, C, P, G, MODE>(reinterpret_cast<XT*>(a.dx) + b * a.db + l * a.dr +
-                                   (int64_t)(head0 + hd) * a.D, at, d);
+      store<XT, C, P, G, MODE>(reinterpret_cast<XT*>(a.dx) + starts[t].dx + (head0 + hd) * a.D, at, d);
     }
   }
   if (!a.part || part == 2) return;
@@ -360,8 +370,8 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float v = dg.p[c][i][e];
-        if constexpr (G == 4) v += __shfl_xor(v, 4);
-        v += __shfl_xor(v, 8);
+        if constexpr (G <= 4) v += __shfl_xor(v, 4);
+        if constexpr (G <= 8) v += __shfl_xor(v, 8);
         v += __shfl_xor(v, 16);
         v += __shfl_xor(v, 32);
         if ((tid & 63) < G && at.j + c * G < at.pieces)
@@ -376,19 +386,33 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
   }
 }
 
-// dgamma of part blockIdx.y, 32 channels a workgroup, from the workgroups' sums.
-__global__ __launch_bounds__(kThreads) void k_heads_gamma(HeadsArgs a) {
-  __shared__ double box[8][32];
-  const int part = blockIdx.y, i = blockIdx.x * 32 + threadIdx.x % 32, strip = threadIdx.x / 32;
+// dgamma of part blockIdx.y, 32 channels a workgroup, from the workgroups' sums: 32 strips
+// of them, eight loads in flight.
+__global__ __launch_bounds__(1024) void k_heads_gamma(HeadsArgs a) {
+  __shared__ double box[16][32];
+  const int part = blockIdx.y, col = threadIdx.x % 32, i = blockIdx.x * 32 + col;
+  const int strip = threadIdx.x / 32;
+  if (!a.dgamma[part]) return;
   double sum = 0.0;
-  if (i < a.D)
-    for (int g = strip; g < a.groups; g += 8)
-      sum += (double)a.part[((int64_t)part * a.groups + g) * a.D + i];
-  box[strip][threadIdx.x % 32] = sum;
-  __syncthreads();
-  if (strip != 0 || i >= a.D || !a.dgamma[part]) return;
+  if (i < a.D) {
+    const float* p = a.part + (int64_t)part * a.groups * a.D + i;
+    for (int g = strip; g < a.groups; g += 256) {
+      float v[8];
 #pragma unroll
-  for (int s = 1; s < 8; ++s) sum += box[s][threadIdx.x];
+      for (int j = 0; j < 8; ++j) v[j] = g + 32 * j < a.groups ? p[(int64_t)(g + 32 * j) * a.D] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += (double)v[j];
+    }
+  }
+  sum += __shfl_xor(sum, 32);  // two strips a wave
+  if (strip % 2 == 0) box[strip / 2][col] = sum;
+  __syncthreads();
+  if (strip > 1) return;
+  sum = 0.0;
+#pragma unroll
+  for (int s = 0; s < 8; ++s) sum += box[8 * strip + s][col];
+  sum += __shfl_xor(sum, 32);
+  if (strip != 0 || i >= a.D) return;
   int c1, c2;
   pair_channels(a, i / 2, c1, c2);
   const int c = i % 2 ? c2 : c1;
@@ -412,16 +436,16 @@ int mode_of(const HeadsArgs& a) {
   return rest % Geo<XT>::P ? kScattered : kHalves;
 }
 
-template <typename XT, typename YT, int C>
+template <typename XT, typename YT, int G, int C>
 hipError_t run(const HeadsArgs& a, bool grad, dim3 grid, hipStream_t s) {
   const size_t lds = (size_t)a.tokens * (a.D / 2) * sizeof(float2);
   const int mode = mode_of<XT>(a);
 #define QL_HEADS_MODE(M)                                      \
   if (mode == M) {                                            \
     if (grad)                                                 \
-      k_heads_grad<XT, YT, C, M><<<grid, kThreads, lds, s>>>(a); \
+      k_heads_grad<XT, YT, G, C, M><<<grid, kThreads, lds, s>>>(a); \
     else                                                      \
-      k_heads<XT, YT, C, M><<<grid, kThreads, lds, s>>>(a);   \
+      k_heads<XT, YT, G, C, M><<<grid, kThreads, lds, s>>>(a);   \
   }
   QL_HEADS_MODE(kAdjacent)
   QL_HEADS_MODE(kHalves)
@@ -430,14 +454,22 @@ hipError_t run(const HeadsArgs& a, bool grad, dim3 grid, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Lanes of a head: as few as keep a lane's values in registers with room for other waves,
+// twice as many where the pieces still fill them.
+template <typename XT>
+int lanes_of(int D) { return (D % 64 == 0 ? 2 : 1) * (sizeof(XT) == 4 ? 8 : 4); }
+
 template <typename XT, typename YT>
 hipError_t pick(const HeadsArgs& a, bool grad, dim3 grid, hipStream_t s) {
+  constexpr int G = sizeof(XT) == 4 ? 8 : 4;
+  if (a.D == 64) return run<XT, YT, 2 * G, 1>(a, grad, grid, s);
+  if (a.D == 128) return run<XT, YT, 2 * G, 2>(a, grad, grid, s);
   switch ((a.D + 31) / 32) {
-    case 1: return run<XT, YT, 1>(a, grad, grid, s);
-    case 2: return run<XT, YT, 2>(a, grad, grid, s);
-    case 3: return run<XT, YT, 3>(a, grad, grid, s);
-    case 4: return run<XT, YT, 4>(a, grad, grid, s);
-    default: return run<XT, YT, 5>(a, grad, grid, s);
+    case 1: return run<XT, YT, G, 1>(a, grad, grid, s);
+    case 2: return run<XT, YT, G, 2>(a, grad, grid, s);
+    case 3: return run<XT, YT, G, 3>(a, grad, grid, s);
+    case 4: return run<XT, YT, G, 4>(a, grad, grid, s);
+    default: return run<XT, YT, G, 5>(a, grad, grid, s);
   }
 }
 
@@ -449,8 +481,8 @@ hipError_t go(const HeadsArgs& a, bool grad, dim3 grid, hipStream_t s) {
 
 // Tokens of a workgroup: enough rows for four passes of its lanes, unless that
 // leaves fewer workgroups than fill the chip.
-int tokens_of(int64_t all, int heads, bool x_bf16) {
-  const int groups = kThreads / (x_bf16 ? 4 : 8);
+int tokens_of(int64_t all, int heads, int D, bool x_bf16) {
+  const int groups = kThreads / (x_bf16 ? lanes_of<bf16>(D) : lanes_of<float>(D));
   int t = 1;
   while (t < kMaxTokens && t * heads < 4 * groups &&
          (t * heads < groups || all / (2 * t) >= 1024))
@@ -468,7 +500,7 @@ int heads_grad_groups(int64_t tokens, int heads) {
 hipError_t launch_heads(const HeadsArgs& args, hipStream_t s) {
   HeadsArgs a = args;
   const int64_t all = (int64_t)a.B * a.L;
-  a.tokens = tokens_of(all, a.heads[0] + a.heads[1] + a.heads[2], a.x_bf16);
+  a.tokens = tokens_of(all, a.heads[0] + a.heads[1] + a.heads[2], a.D, a.x_bf16);
   return go(a, false, dim3((unsigned)((all + a.tokens - 1) / a.tokens)), s);
 }
 
@@ -477,13 +509,13 @@ hipError_t launch_heads_grad(const HeadsArgs& args, hipStream_t s) {
   const int64_t all = (int64_t)a.B * a.L;
   if (all > 0) {
     const int most = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
-    a.tokens = tokens_of(all, most > a.heads[2] ? most : a.heads[2], a.x_bf16);
+    a.tokens = tokens_of(all, most > a.heads[2] ? most : a.heads[2], a.D, a.x_bf16);
     const hipError_t e = go(a, true, dim3((unsigned)a.groups, 3), s);
     if (e != hipSuccess) return e;
   }
   if (!a.dgamma[0] && !a.dgamma[1]) return hipSuccess;
   if (all == 0) a.groups = 0;
-  k_heads_gamma<<<dim3((a.D + 31) / 32, 2), kThreads, 0, s>>>(a);
+  k_heads_gamma<<<dim3((a.D + 31) / 32, 2), 1024, 0, s>>>(a);
   return hipGetLastError();
 }
 
