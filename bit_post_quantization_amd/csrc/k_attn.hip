@@ -74,41 +74,61 @@ __device__ __forceinline__ frag operand(const v16f& c, int s) {
   return f;
 }
 
-// LDS rows, in elements. Reads of whole rows by neighbouring lanes want an odd number
-// of 16-byte pieces (every lane of sixteen on its own banks), transposed reads of four
-// rows by 32 channels 16 words more than a multiple of 64.
-constexpr int kRowLd = (kCPR | 1) * kChunk;
-constexpr int tr_ld() {
-  if (sizeof(T) == 4) return kOB * 32;  // lanes read neighbouring words of one row
-  int words = kOB * 16;                 // as many channels as the result's blocks read
-  while (words % 64 != 16 && words % 64 != 48) words += 4;
-  return words * 2;
+// A tile's rows in LDS are read both ways: whole rows by neighbouring lanes, 16 bytes each,
+// and, for bf16, four rows by 32 channels transposed. Both meet every bank once if the
+// 16-byte piece c of row r lies at c ^ turn(r), turn() going through all of 0 .. 7 in eight
+// rows and through four even or four odd values in four: no padding, no conflicts (odd
+// row lengths instead cost the gradients 45 % of their LDS time). fp32 rows, whose columns
+// are read by words, are an odd number of pieces long.
+constexpr bool kTurned = sizeof(T) == 2;
+constexpr int kPitch = kTurned ? (kOB * 32 * 2 + 127) / 128 * 64 : ((kOB * 32 / kChunk) | 1) * kChunk;
+__device__ __forceinline__ int turn(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+__device__ __forceinline__ int place(int r, int c) {
+  return r * kPitch + (kTurned ? (c ^ turn(r)) : c) * kChunk;
 }
-constexpr int kTrLd = tr_ld();
-// Read both ways: padded to whole blocks, then an odd number of pieces.
-constexpr int kBothLd = ((kOB * 32 / kChunk) | 1) * kChunk;
+
+// A lane's places in a tile.
+struct Spots {
+  int row[kTurned ? 4 : 1], col[kTurned ? 2 : 1];
+  __device__ __forceinline__ void find(int lane) {
+    const int r32 = lane & 31, h = lane >> 5, i = lane & 15;
+    if constexpr (kTurned) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) row[k] = place(r32, 2 * k + h);
+      const int r = 4 * h + i / 4, c = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+      col[0] = place(r, c) + 4 * (i & 1);
+      col[1] = place(r, c ^ 4) + 4 * (i & 1);
+    } else {
+      row[0] = r32 * kPitch + 8 * h;
+      col[0] = 4 * h * kPitch + r32;
+    }
+  }
+};
 
 // Operand of rows: row lane % 32 of p, channels 16 kb + 8 h .. + 7.
-__device__ __forceinline__ frag row_frag(const T* p, int ld, int kb, int r32, int h) {
-  return *reinterpret_cast<const frag*>(p + r32 * ld + 16 * kb + 8 * h);
+template <typename E>
+__device__ __forceinline__ typename Frag<E>::t row_frag(const E* p, const Spots& s, int kb) {
+  if constexpr (sizeof(E) == 2)
+    return *reinterpret_cast<const v8h*>(p + s.row[kb & 3] + (kb >> 2) * 64);
+  else
+    return *reinterpret_cast<const v8f*>(p + s.row[0] + 16 * kb);
 }
 
-// Operand of columns: channel c0 + lane % 32, rows 4 h .. + 3 and 8 + 4 h .. + 3 of p.
+// Operand of columns: channel 32 c + lane % 32, rows 4 h .. + 3 and 8 + 4 h .. + 3 of p.
 template <typename E>
-__device__ __forceinline__ typename Frag<E>::t col_frag(const E* p, int ld, int c0, int lane) {
+__device__ __forceinline__ typename Frag<E>::t col_frag(const E* p, const Spots& s, int c) {
   if constexpr (sizeof(E) == 2) {
-    const int i = lane & 15;
-    const E* a = p + (4 * (lane >> 5) + i / 4) * ld + c0 + 16 * ((lane >> 4) & 1) + 4 * (i % 4);
+    const E* a = p + s.col[c & 1] + (c >> 1) * 64;
     const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(a));
-    const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(a + 8 * ld));
+    const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(a + 8 * kPitch));
     return __builtin_bit_cast(v8h, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
-    const E* a = p + 4 * (lane >> 5) * ld + c0 + (lane & 31);
+    const E* a = p + s.col[0] + 32 * c;
     v8f f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      f[e] = a[e * ld];
-      f[4 + e] = a[(8 + e) * ld];
+      f[e] = a[e * kPitch];
+      f[4 + e] = a[(8 + e) * kPitch];
     }
     return f;
   }
@@ -117,6 +137,7 @@ __device__ __forceinline__ typename Frag<E>::t col_frag(const E* p, int ld, int 
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
+constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Workgroup `id` of n in an order that gives each of the 8 XCDs (workgroups are dealt to
@@ -190,6 +211,11 @@ template <int W>
 struct KeyBits {
   uint32_t w[W];
   __device__ __forceinline__ void look(const AttnArgs& a, int b, int key0, int len, int lane) {
+    if (!a.mask && key0 + 32 * W <= len) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = 0xffffffffu;
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < W; i += 2) {
       const int key = key0 + 32 * i + lane;
@@ -220,34 +246,52 @@ __device__ __forceinline__ int key_len(const AttnArgs& a, int b) {
   return n < 0 ? 0 : n > a.Lk ? a.Lk : n;
 }
 
-// A tile of KT rows of one tensor on its way from memory through registers to LDS.
+// A tile of KT rows of one tensor on its way from memory through registers to LDS. Where
+// rows lie evenly (row i of a tile, i = u G + g, at u steps and g heads from the tile's
+// start) and near, a piece's address is the tile's, which is the same for all lanes, and
+// an offset formed once; else it is formed for each tile.
 template <int KT>
 struct Stage {
   static constexpr int N = (KT * kCPR + kThreads - 1) / kThreads;
+  static constexpr bool kWhole = KT * kCPR % kThreads == 0;
   v4u r[N];
-  // row(i): the address of row i of the tile (any valid one past the end)
-  template <typename F>
-  __device__ __forceinline__ void fetch(int tid, int D, F row) {
+  uint32_t off[N];
+  int to[N];
+  static __device__ __forceinline__ int row(int tid, int i) { return min((tid + i * kThreads) / kCPR, KT - 1); }
+  static __device__ __forceinline__ int piece(int tid, int i, int D) {
+    return min((tid + i * kThreads) % kCPR, D / kChunk - 1);
+  }
+  __device__ __forceinline__ void find(int tid, int D, int G, int64_t step, int64_t head) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int idx = tid + i * kThreads, at = idx / kCPR, c = idx % kCPR;
-      r[i] = v4u{0, 0, 0, 0};
-      if ((KT * kCPR % kThreads == 0 || at < KT) && (c + 1) * kChunk <= D)
-        r[i] = *reinterpret_cast<const v4u*>(row(at) + c * kChunk);
+      const int at = row(tid, i), u = G == 1 ? at : at / G, g = G == 1 ? 0 : at - u * G;
+      off[i] = (uint32_t)(u * step + g * head) * (uint32_t)sizeof(T) + 16 * piece(tid, i, D);
+      to[i] = place(at, (tid + i * kThreads) % kCPR);
     }
   }
-  // keep(i): whether row i of the tile is kept (else zero)
+  __device__ __forceinline__ void fetch(const T* tile) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      r[i] = *reinterpret_cast<const v4u*>(reinterpret_cast<const char*>(tile) + off[i]);
+  }
+  // row(i): the address of row i of the tile (any valid one past the end)
+  template <typename F>
+  __device__ __forceinline__ void fetch_by(int tid, int D, F address) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      r[i] = *reinterpret_cast<const v4u*>(address(row(tid, i)) + piece(tid, i, D) * kChunk);
+  }
+  // keep(i): whether row i of the tile is kept (else zero); channels past D are zero
   template <bool ALL, typename F>
-  __device__ __forceinline__ void put(T* lds, int ld, int tid, F keep) const {
+  __device__ __forceinline__ void put(T* lds, int tid, int D, F keep) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int idx = tid + i * kThreads, at = idx / kCPR, c = idx % kCPR;
       v4u x = r[i];
+      if (D < kD && (tid + i * kThreads) % kCPR * kChunk >= D) x = v4u{0, 0, 0, 0};
       if constexpr (!ALL) {
-        if (!keep(at)) x = v4u{0, 0, 0, 0};
+        if (!keep(row(tid, i))) x = v4u{0, 0, 0, 0};
       }
-      if (KT * kCPR % kThreads == 0 || at < KT)
-        *reinterpret_cast<v4u*>(lds + at * ld + c * kChunk) = x;
+      if (kWhole || tid + i * kThreads < KT * kCPR) *reinterpret_cast<v4u*>(lds + to[i]) = x;
     }
   }
 };
@@ -270,7 +314,7 @@ struct Fwd {
   static constexpr int SUB = WK == 1 ? 2 : 1;  // 32-key pieces of a wave in a tile
   static constexpr int KT = 32 * WK * SUB;
   static constexpr int NB = WK == 1 && sizeof(T) * kD <= 320 ? 2 : 1;  // tiles in LDS
-  static constexpr int kTile = KT * (kRowLd + kTrLd);
+  static constexpr int kTile = KT * 2 * kPitch;
   static constexpr int kJoin = WK > 1 ? (WK - 1) * WQ * 32 * (kOB * 32 + 2) * 4 : 0;
   static constexpr int kLds = NB * kTile * (int)sizeof(T) > kJoin ? NB * kTile * (int)sizeof(T)
                                                                  : kJoin;
@@ -284,7 +328,7 @@ struct Fwd {
 #define QW (sizeof(T) == 2 ? 2 : 1)
 #endif
 #ifndef KW
-#define KW (sizeof(T) == 2 && DC <= 6 ? 2 : 1)
+#define KW (sizeof(T) == 2 && DC <= 8 ? 2 : 1)
 #endif
 template <int WK>
 __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
@@ -319,19 +363,28 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
   float m = -INFINITY, l = 0.0f;
 
   Stage<KT> ks, vs;
+  ks.find(tid, a.D, 1, a.k.row, 0);
+  vs.find(tid, a.D, 1, a.v.row, 0);
+  Spots spots;
+  spots.find(lane);
   KeyBits<W> bits, next;
   const auto fetch = [&](int t) {
-    ks.fetch(tid, a.D, [&](int i) { return kp + (int64_t)min(t * KT + i, a.Lk - 1) * a.k.row; });
-    vs.fetch(tid, a.D, [&](int i) { return vp + (int64_t)min(t * KT + i, a.Lk - 1) * a.v.row; });
+    if (a.near_keys && (t + 1) * KT <= a.Lk) {
+      ks.fetch(kp + (int64_t)t * KT * a.k.row);
+      vs.fetch(vp + (int64_t)t * KT * a.v.row);
+    } else {
+      ks.fetch_by(tid, a.D, [&](int i) { return kp + (int64_t)min(t * KT + i, a.Lk - 1) * a.k.row; });
+      vs.fetch_by(tid, a.D, [&](int i) { return vp + (int64_t)min(t * KT + i, a.Lk - 1) * a.v.row; });
+    }
     next.look(a, b, t * KT, len, lane);
   };
   const auto put = [&](T* at) {
     const auto keep = [&](int i) { return bit_of(next, i); };
-    ks.template put<true>(at, kRowLd, tid, keep);  // scores of other keys are not looked at
+    ks.template put<true>(at, tid, a.D, keep);  // scores of other keys are not looked at
     if (next.all())
-      vs.template put<true>(at + KT * kRowLd, kTrLd, tid, keep);
+      vs.template put<true>(at + KT * kPitch, tid, a.D, keep);
     else
-      vs.template put<false>(at + KT * kRowLd, kTrLd, tid, keep);
+      vs.template put<false>(at + KT * kPitch, tid, a.D, keep);
   };
   if (t0 < t1) {
     fetch(t0);
@@ -341,16 +394,16 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
   __syncthreads();
   for (int t = t0; t < t1; ++t) {
     const T* const kt = lds + ((t - t0) % P::NB) * P::kTile;
-    const T* const vt = kt + KT * kRowLd;
+    const T* const vt = kt + KT * kPitch;
     if (t + 1 < t1) fetch(t + 1);
     if (!bits.none()) {
       v16f s[SUB];
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
         s[u] = zero16();
-        const T* p = kt + (wk * SUB + u) * 32 * kRowLd;
+        const T* p = kt + (wk * SUB + u) * 32 * kPitch;
 #pragma unroll
-        for (int kb = 0; kb < DC; ++kb) s[u] = mma(row_frag(p, kRowLd, kb, r32, h), q[kb], s[u]);
+        for (int kb = 0; kb < DC; ++kb) s[u] = mma(row_frag(p, spots, kb), q[kb], s[u]);
       }
       if (!bits.all()) {
 #pragma unroll
@@ -370,8 +423,10 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
       top = fmaxf(top, other_half(top)) * a.scale2;
+      // Weights stay within 2^8 of what the true maximum would make them: O and l are only
+      // rescaled where one rose further (the first of them starts from -infinity).
       const float m_new = fmaxf(m, top);
-      if (__any(m_new > m)) {
+      if (__any(m_new > m + kSlack)) {
         const float f = exp2_fast(m - (m_new == -INFINITY ? 0.0f : m_new));
         l *= f;
 #pragma unroll
@@ -392,9 +447,9 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const frag p = operand(s[u], i);
-          const T* v0 = vt + ((wk * SUB + u) * 32 + 16 * i) * kTrLd;
+          const T* v0 = vt + ((wk * SUB + u) * 32 + 16 * i) * kPitch;
 #pragma unroll
-          for (int c = 0; c < kOB; ++c) o[c] = mma(col_frag(v0, kTrLd, 32 * c, lane), p, o[c]);
+          for (int c = 0; c < kOB; ++c) o[c] = mma(col_frag(v0, spots, c), p, o[c]);
         }
       }
       l += sum;
@@ -520,7 +575,7 @@ constexpr int kBackRows = 32;  // rows or keys of a tile in LDS
 
 // dQ, and delta for k_attn_dkv. Keys that do not count are zero in LDS and have P = 0.
 __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
-  constexpr int KT = 64, W = 2, kTile = KT * (kBothLd + kRowLd);
+  constexpr int KT = 64, W = 2, kTile = KT * 2 * kPitch;
   constexpr int NB = 2 * kTile * (int)sizeof(T) <= 81920 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) T lds[NB * kTile];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, h = lane >> 5;
@@ -558,20 +613,29 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
   for (int i = 0; i < kOB; ++i) dq[i] = zero16();
 
   Stage<KT> ks, vs;
+  ks.find(tid, a.D, 1, a.k.row, 0);
+  vs.find(tid, a.D, 1, a.v.row, 0);
+  Spots spots;
+  spots.find(lane);
   KeyBits<W> bits, next;
   const auto fetch = [&](int t) {
-    ks.fetch(tid, a.D, [&](int i) { return kp + (int64_t)min(t * KT + i, a.Lk - 1) * a.k.row; });
-    vs.fetch(tid, a.D, [&](int i) { return vp + (int64_t)min(t * KT + i, a.Lk - 1) * a.v.row; });
+    if (a.near_keys && (t + 1) * KT <= a.Lk) {
+      ks.fetch(kp + (int64_t)t * KT * a.k.row);
+      vs.fetch(vp + (int64_t)t * KT * a.v.row);
+    } else {
+      ks.fetch_by(tid, a.D, [&](int i) { return kp + (int64_t)min(t * KT + i, a.Lk - 1) * a.k.row; });
+      vs.fetch_by(tid, a.D, [&](int i) { return vp + (int64_t)min(t * KT + i, a.Lk - 1) * a.v.row; });
+    }
     next.look(a, b, t * KT, len, lane);
   };
   const auto put = [&](T* to) {
     const auto keep = [&](int i) { return bit_of(next, i); };
     if (next.all()) {
-      ks.template put<true>(to, kBothLd, tid, keep);
-      vs.template put<true>(to + KT * kBothLd, kRowLd, tid, keep);
+      ks.template put<true>(to, tid, a.D, keep);
+      vs.template put<true>(to + KT * kPitch, tid, a.D, keep);
     } else {
-      ks.template put<false>(to, kBothLd, tid, keep);
-      vs.template put<false>(to + KT * kBothLd, kRowLd, tid, keep);
+      ks.template put<false>(to, tid, a.D, keep);
+      vs.template put<false>(to + KT * kPitch, tid, a.D, keep);
     }
   };
   if (tiles > 0) {
@@ -582,7 +646,7 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
   __syncthreads();
   for (int t = 0; t < tiles; ++t) {
     const T* const kt = lds + (t % NB) * kTile;
-    const T* const vt = kt + KT * kBothLd;
+    const T* const vt = kt + KT * kPitch;
     if (t + 1 < tiles) fetch(t + 1);
     if (!bits.none()) {
 #pragma unroll
@@ -590,8 +654,8 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
         v16f s = zero16(), dp = zero16();
 #pragma unroll
         for (int kb = 0; kb < DC; ++kb) {
-          s = mma(row_frag(kt + 32 * u * kBothLd, kBothLd, kb, r32, h), q[kb], s);
-          dp = mma(row_frag(vt + 32 * u * kRowLd, kRowLd, kb, r32, h), g[kb], dp);
+          s = mma(row_frag(kt + 32 * u * kPitch, spots, kb), q[kb], s);
+          dp = mma(row_frag(vt + 32 * u * kPitch, spots, kb), g[kb], dp);
         }
         const uint32_t w = bits.w[u] >> (4 * h);
 #pragma unroll
@@ -607,9 +671,9 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const frag ds = operand(s, i);
-          const T* k0 = kt + (32 * u + 16 * i) * kBothLd;
+          const T* k0 = kt + (32 * u + 16 * i) * kPitch;
 #pragma unroll
-          for (int c = 0; c < kOB; ++c) dq[c] = mma(col_frag(k0, kBothLd, 32 * c, lane), ds, dq[c]);
+          for (int c = 0; c < kOB; ++c) dq[c] = mma(col_frag(k0, spots, c), ds, dq[c]);
         }
       }
     }
@@ -629,13 +693,19 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
     }
 }
 
-// dK and dV of 128 keys from a range of the rows; a lane has one key.
+#ifndef VL
+#define VL (sizeof(T) == 2 && DC >= 8)
+#endif
+// dK and dV of 128 keys from a range of the rows; a lane has one key. With long heads V
+// stays in LDS, so that the registers leave room for two waves a SIMD.
 __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
-  constexpr int RT = kBackRows, kTile = RT * 2 * kBothLd;
+  constexpr int RT = kBackRows, kTile = RT * 2 * kPitch;
   constexpr int NB = 2;
   __shared__ __attribute__((aligned(16))) T lds[NB * kTile];
   __shared__ __attribute__((aligned(16))) float stats[NB][2][RT];
+  __shared__ __attribute__((aligned(16))) T v_rows[VL ? 128 * kPitch : 8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, h = lane >> 5;
+  T* const my_v = v_rows + (VL ? wave * 32 * kPitch : 0);
   int id = by_xcd(blockIdx.x, gridDim.x);
   const int sp = id % a.splits;
   id /= a.splits;
@@ -646,17 +716,24 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
   const int key = kt * 128 + wave * 32 + r32, kk = min(key, a.Lk - 1);
   bool counts = key < len;
   if (a.mask && counts) counts = a.mask[b * a.mask_batch + key] != 0;
+  const bool busy = __any(counts);  // else this wave only helps to fill the tiles
   const int tiles = (a.R + RT - 1) / RT, per = (tiles + a.splits - 1) / a.splits;
   const int t0 = sp * per, t1 = kt * 128 < len ? min(tiles, t0 + per) : 0;
 
-  frag k[DC], v[DC];
+  Spots spots;
+  spots.find(lane);
+  frag k[DC], v[VL ? 1 : DC];
   {
     const T* pk = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + kk * a.k.row + hk * a.k.head;
     const T* pv = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + kk * a.v.row + hk * a.v.head;
 #pragma unroll
     for (int kb = 0; kb < DC; ++kb) {
       k[kb] = load_frag(pk, 16 * kb + 8 * h, a.D);
-      v[kb] = load_frag(pv, 16 * kb + 8 * h, a.D);
+      const frag x = load_frag(pv, 16 * kb + 8 * h, a.D);
+      if constexpr (VL)
+        *reinterpret_cast<frag*>(my_v + spots.row[kb & 3] + (kb >> 2) * 64) = x;
+      else
+        v[kb] = x;
     }
   }
   v16f dk[kOB], dv[kOB];
@@ -664,10 +741,17 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
   for (int i = 0; i < kOB; ++i) dk[i] = dv[i] = zero16();
 
   Stage<RT> qs, gs;
+  qs.find(tid, a.D, a.G, a.q.row, a.q.head);
+  gs.find(tid, a.D, a.G, a.dout.row, a.dout.head);
   float stat = 0.0f;  // of thread t < RT lse of row t, of t < 2 RT delta of row t - RT
   const auto fetch = [&](int t) {
-    qs.fetch(tid, a.D, [&](int i) { return row_of(a, a.q, b, hk, min(t * RT + i, a.R - 1)); });
-    gs.fetch(tid, a.D, [&](int i) { return row_of(a, a.dout, b, hk, min(t * RT + i, a.R - 1)); });
+    if (a.near_rows && (t + 1) * RT <= a.R) {
+      qs.fetch(row_of(a, a.q, b, hk, t * RT));
+      gs.fetch(row_of(a, a.dout, b, hk, t * RT));
+    } else {
+      qs.fetch_by(tid, a.D, [&](int i) { return row_of(a, a.q, b, hk, min(t * RT + i, a.R - 1)); });
+      gs.fetch_by(tid, a.D, [&](int i) { return row_of(a, a.dout, b, hk, min(t * RT + i, a.R - 1)); });
+    }
     if (tid < 2 * RT) {
       const int r = t * RT + tid % RT;
       const int64_t at = stat_at(a, b, hk, min(r, a.R - 1));
@@ -684,11 +768,11 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
     T* to = lds + at * kTile;
     const auto keep = [&](int i) { return i < n; };
     if (n >= RT) {
-      qs.template put<true>(to, kBothLd, tid, keep);
-      gs.template put<true>(to + RT * kBothLd, kBothLd, tid, keep);
+      qs.template put<true>(to, tid, a.D, keep);
+      gs.template put<true>(to + RT * kPitch, tid, a.D, keep);
     } else {
-      qs.template put<false>(to, kBothLd, tid, keep);
-      gs.template put<false>(to + RT * kBothLd, kBothLd, tid, keep);
+      qs.template put<false>(to, tid, a.D, keep);
+      gs.template put<false>(to + RT * kPitch, tid, a.D, keep);
     }
     if (tid < 2 * RT) stats[at][tid / RT][tid % RT] = stat;
   };
@@ -700,13 +784,14 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
   for (int t = t0; t < t1; ++t) {
     const int at = (t - t0) % NB;
     const T* const qt = lds + at * kTile;
-    const T* const gt = qt + RT * kBothLd;
+    const T* const gt = qt + RT * kPitch;
     if (t + 1 < t1) fetch(t + 1);
+    if (busy) {
     v16f s = zero16(), dp = zero16();
 #pragma unroll
     for (int kb = 0; kb < DC; ++kb) {
-      s = mma(row_frag(qt, kBothLd, kb, r32, h), k[kb], s);
-      dp = mma(row_frag(gt, kBothLd, kb, r32, h), v[kb], dp);
+      s = mma(row_frag(qt, spots, kb), k[kb], s);
+      dp = mma(row_frag(gt, spots, kb), VL ? row_frag(my_v, spots, kb) : v[VL ? 0 : kb], dp);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -724,14 +809,15 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
       const frag p = operand(s, i), ds = operand(dp, i);
 #pragma unroll
       for (int c = 0; c < kOB; ++c) {
-        dv[c] = mma(col_frag(gt + 16 * i * kBothLd, kBothLd, 32 * c, lane), p, dv[c]);
-        dk[c] = mma(col_frag(qt + 16 * i * kBothLd, kBothLd, 32 * c, lane), ds, dk[c]);
+        dv[c] = mma(col_frag(gt + 16 * i * kPitch, spots, c), p, dv[c]);
+        dk[c] = mma(col_frag(qt + 16 * i * kPitch, spots, c), ds, dk[c]);
       }
+    }
     }
     if (t + 1 < t1) put(t + 1);
     __syncthreads();
   }
-  if (key >= a.Lk) return;
+  if (key >= a.Lk || (a.splits > 1 && !counts)) return;  // k_attn_dkv_sum knows them too
   if (!counts) {  // whatever their columns hold
 #pragma unroll
     for (int i = 0; i < kOB; ++i) dk[i] = dv[i] = zero16();
@@ -771,10 +857,23 @@ __global__ __launch_bounds__(kThreads) void k_attn_dkv_sum(AttnArgs a) {
   const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
   if (e >= n) return;
   const float* p = a.part + blockIdx.y * n + e;
-  v4f sum = {0, 0, 0, 0};
-  for (int s = 0; s < a.splits; ++s) sum += *reinterpret_cast<const v4f*>(p + s * 2 * n);
   const ql_heads_view& t = blockIdx.y ? a.dv : a.dk;
   const int64_t row = e / a.D, lh = row / a.Hk;
+  const int b = (int)(lh / a.Lk), key = (int)(lh - (int64_t)b * a.Lk);
+  bool counts = key < key_len(a, b);
+  if (a.mask && counts) counts = a.mask[b * a.mask_batch + key] != 0;
+  v4f sum = {0, 0, 0, 0};
+  if (counts) {
+    for (int s0 = 0; s0 < a.splits; s0 += 8) {
+      v4f x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = *reinterpret_cast<const v4f*>(p + min(s0 + j, a.splits - 1) * 2 * n);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (s0 + j < a.splits) sum += x[j];
+    }
+  }
   T* to = reinterpret_cast<T*>(t.p) + lh / a.Lk * t.batch + lh % a.Lk * t.row + row % a.Hk * t.head +
           e % a.D;
   if constexpr (sizeof(T) == 2) {

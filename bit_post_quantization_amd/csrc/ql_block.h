@@ -96,6 +96,8 @@ struct AttnArgs {
   float* part;      // forward [splits][B, H, Lq][D]; dk, dv: [splits][2][B, Lk, Hk][D]
   float* part_lse;  // [splits][B, H, Lq], base 2
   bool bf16;
+  bool near_keys;   // 128 rows of k and of v lie within 32-bit offsets
+  bool near_rows;   // 32 rows of q and of dout lie evenly and within 32-bit offsets
 };
 struct AttnPlan {
   bool narrow;

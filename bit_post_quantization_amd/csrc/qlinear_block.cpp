@@ -311,6 +311,11 @@ ql::AttnArgs attn_args(const ql_attn* d) {
   return a;
 }
 
+// Whether n rows of a tensor lie within 32-bit offsets of the first, g heads side by side.
+bool near(const ql_heads_view& t, int64_t n, int64_t g, int64_t size) {
+  return t.row * size * (n / g) + t.head * size * g < (int64_t)1 << 32;
+}
+
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 }  // namespace
@@ -576,6 +581,8 @@ ql_status qlinear_attention(const ql_attn* d, const ql_heads_view* q, const ql_h
   a.v = view(v);
   a.o = view(out);
   a.lse = lse;
+  const int64_t size = size_of(d->dtype);
+  a.near_keys = near(a.k, 128, 1, size) && near(a.v, 128, 1, size);
   a.row_tiles = p.row_tiles;
   a.splits = p.splits;
   if (p.splits > 1) {
@@ -631,6 +638,9 @@ ql_status qlinear_attention_grad(const ql_attn* d, const ql_heads_view* dout,
   a.dq = view(dq);
   a.dk = view(dk);
   a.dv = view(dv);
+  const int64_t size = size_of(d->dtype);
+  a.near_keys = near(a.k, 128, 1, size) && near(a.v, 128, 1, size);
+  a.near_rows = 32 % a.G == 0 && near(a.q, 32, a.G, size) && near(a.dout, 32, a.G, size);
   a.delta = reinterpret_cast<float*>(workspace);
   a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) +
                                     up16((int64_t)d->batch * d->heads * d->q_len * 4));
