@@ -74,56 +74,68 @@ __device__ __forceinline__ frag operand(const v16f& c, int s) {
   return f;
 }
 
-// A tile's rows in LDS are read both ways: whole rows by neighbouring lanes, 16 bytes each,
-// and, for bf16, four rows by 32 channels transposed. Both meet every bank once if the
-// 16-byte piece c of row r lies at c ^ turn(r), turn() going through all of 0 .. 7 in eight
-// rows and through four even or four odd values in four: no padding, no conflicts (odd
-// row lengths instead cost the gradients 45 % of their LDS time). fp32 rows, whose columns
-// are read by words, are an odd number of pieces long.
+// A tile's rows in LDS are read both ways: whole rows by neighbouring lanes, 16 bytes each
+// (sixteen lanes meet all 64 banks once), and, for bf16, four rows by 32 channels
+// transposed. Both are free of conflicts if the 16-byte piece c of row r lies at
+// c ^ turn(r): rows of 256 bytes need all of 0 .. 15 in sixteen rows and four unlike upper
+// halves in four; rows of 128 or 384, which alternate between the halves of the banks,
+// the same of 0 .. 7 in every other row. (Rows padded to an odd number of pieces cost the
+// gradients 45 % of their LDS time.) fp32 rows, whose columns are read by words, are an
+// odd number of pieces long.
 constexpr bool kTurned = sizeof(T) == 2;
 constexpr int kPitch = kTurned ? (kOB * 32 * 2 + 127) / 128 * 64 : ((kOB * 32 / kChunk) | 1) * kChunk;
-__device__ __forceinline__ int turn(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+constexpr int kTurn = kPitch == 128 ? 128 : 64;  // elements that trade places
+__device__ __forceinline__ int turn(int r) {
+  return ((kTurn == 128 ? r & 3 : (r >> 1) & 1) << 2) | ((r >> 2) & 3);
+}
 __device__ __forceinline__ int place(int r, int c) {
   return r * kPitch + (kTurned ? (c ^ turn(r)) : c) * kChunk;
+}
+// From the place of a row's first channels to that of the channels `by` further on, a
+// multiple of 16.
+__device__ __forceinline__ int further(int at, int by) {
+  return (at ^ (by & (kTurn - 1))) + (by & ~(kTurn - 1));
 }
 
 // A lane's places in a tile.
 struct Spots {
-  int row[kTurned ? 4 : 1], col[kTurned ? 2 : 1];
+  int row, col;
   __device__ __forceinline__ void find(int lane) {
     const int r32 = lane & 31, h = lane >> 5, i = lane & 15;
     if constexpr (kTurned) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) row[k] = place(r32, 2 * k + h);
-      const int r = 4 * h + i / 4, c = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-      col[0] = place(r, c) + 4 * (i & 1);
-      col[1] = place(r, c ^ 4) + 4 * (i & 1);
+      row = place(r32, h);
+      col = place(4 * h + i / 4, 2 * ((lane >> 4) & 1) + ((i & 3) >> 1)) + 4 * (i & 1);
     } else {
-      row[0] = r32 * kPitch + 8 * h;
-      col[0] = 4 * h * kPitch + r32;
+      row = r32 * kPitch + 8 * h;
+      col = 4 * h * kPitch + r32;
     }
   }
 };
+
+// The places of a tile's operands are formed from two registers for each tile: kept over the
+// loop they would take sixteen, and spill.
+__device__ __forceinline__ void form_anew(Spots& s) { asm volatile("" : "+v"(s.row), "+v"(s.col)); }
 
 // Operand of rows: row lane % 32 of p, channels 16 kb + 8 h .. + 7.
 template <typename E>
 __device__ __forceinline__ typename Frag<E>::t row_frag(const E* p, const Spots& s, int kb) {
   if constexpr (sizeof(E) == 2)
-    return *reinterpret_cast<const v8h*>(p + s.row[kb & 3] + (kb >> 2) * 64);
+    return *reinterpret_cast<const v8h*>(p + further(s.row, 16 * kb));
   else
-    return *reinterpret_cast<const v8f*>(p + s.row[0] + 16 * kb);
+    return *reinterpret_cast<const v8f*>(p + s.row + 16 * kb);
 }
 
 // Operand of columns: channel 32 c + lane % 32, rows 4 h .. + 3 and 8 + 4 h .. + 3 of p.
 template <typename E>
 __device__ __forceinline__ typename Frag<E>::t col_frag(const E* p, const Spots& s, int c) {
   if constexpr (sizeof(E) == 2) {
-    const E* a = p + s.col[c & 1] + (c >> 1) * 64;
-    const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(a));
-    const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(a + 8 * kPitch));
+    // eight rows on, turn() differs by 2: 16 channels
+    const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p + further(s.col, 32 * c)));
+    const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_v4s)(p + further(s.col ^ 16, 32 * c) + 8 * kPitch));
     return __builtin_bit_cast(v8h, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
-    const E* a = p + s.col[0] + 32 * c;
+    const E* a = p + s.col + 32 * c;
     v8f f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -396,6 +408,7 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
     const T* const kt = lds + ((t - t0) % P::NB) * P::kTile;
     const T* const vt = kt + KT * kPitch;
     if (t + 1 < t1) fetch(t + 1);
+    form_anew(spots);
     if (!bits.none()) {
       v16f s[SUB];
 #pragma unroll
@@ -648,6 +661,7 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
     const T* const kt = lds + (t % NB) * kTile;
     const T* const vt = kt + KT * kPitch;
     if (t + 1 < tiles) fetch(t + 1);
+    form_anew(spots);
     if (!bits.none()) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -731,7 +745,7 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
       k[kb] = load_frag(pk, 16 * kb + 8 * h, a.D);
       const frag x = load_frag(pv, 16 * kb + 8 * h, a.D);
       if constexpr (VL)
-        *reinterpret_cast<frag*>(my_v + spots.row[kb & 3] + (kb >> 2) * 64) = x;
+        *reinterpret_cast<frag*>(my_v + further(spots.row, 16 * kb)) = x;
       else
         v[kb] = x;
     }
@@ -786,6 +800,7 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
     const T* const qt = lds + at * kTile;
     const T* const gt = qt + RT * kPitch;
     if (t + 1 < t1) fetch(t + 1);
+    form_anew(spots);
     if (busy) {
     v16f s = zero16(), dp = zero16();
 #pragma unroll
