@@ -38,8 +38,16 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef bf16 v8h __attribute__((ext_vector_type(8)));
 typedef bf16 v4h __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s* lds_v4s;
+
+#define QL_AT_F32_f32 1
+#define QL_AT_F32_bf16 0
+#define QL_AT_IS_F32_(t) QL_AT_F32_##t
+#define QL_AT_IS_F32(t) QL_AT_IS_F32_(t)
+// 128 keys in LDS: all but the longest heads in fp32.
+#define QL_AT_SHORT (!QL_AT_IS_F32(QL_AT_T) || QL_AT_DC <= 8)
 
 typedef QL_AT_T T;
 constexpr int DC = QL_AT_DC;
@@ -93,7 +101,7 @@ __device__ __forceinline__ int place(int r, int c) {
 }
 // From the place of a row's first channels to that of the channels `by` further on, a
 // multiple of 16.
-__device__ __forceinline__ int further(int at, int by) {
+__device__ __forceinline__ constexpr int further(int at, int by) {
   return (at ^ (by & (kTurn - 1))) + (by & ~(kTurn - 1));
 }
 
@@ -190,25 +198,38 @@ __device__ __forceinline__ frag load_frag(const T* row, int c, int D) {
   return f;
 }
 
-// Four consecutive channels of a result (values 4 j .. 4 j + 3 of block c) to memory.
-__device__ __forceinline__ void store4(T* p, const v16f& c, int j, float f) {
-  if constexpr (sizeof(T) == 2) {
-    v4h o;
+// A row of a result, times f, to memory. A lane has four channels in eight; in bf16 the
+// halves of the wave trade two such pieces, so that each stores eight in one piece.
+template <typename E>
+__device__ __forceinline__ void store_row(E* p, const v16f (&c)[kOB], float f, int D, int h) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = (T)(c[4 * j + e] * f);
-    *reinterpret_cast<v4h*>(p) = o;
-  } else {
-    v4f o;
+  for (int i = 0; i < kOB; ++i) {
+    if constexpr (sizeof(E) == 2) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = c[4 * j + e] * f;
-    *reinterpret_cast<v4f*>(p) = o;
+      for (int j = 0; j < 4; j += 2) {
+        v4h x, y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = (E)(c[i][4 * j + e] * f);
+          y[e] = (E)(c[i][4 * j + 4 + e] * f);
+        }
+        const v2u u = __builtin_bit_cast(v2u, x), v = __builtin_bit_cast(v2u, y);
+        const auto lo = __builtin_amdgcn_permlane32_swap(u[0], v[0], false, false);
+        const auto hi = __builtin_amdgcn_permlane32_swap(u[1], v[1], false, false);
+        const int d = 32 * i + 8 * j + 8 * h;
+        if (d < D) *reinterpret_cast<v4u*>(p + d) = v4u{lo[0], hi[0], lo[1], hi[1]};
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = 32 * i + 8 * j + 4 * h;
+        v4f o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = c[i][4 * j + e] * f;
+        if (d < D) *reinterpret_cast<v4f*>(p + d) = o;
+      }
+    }
   }
-}
-__device__ __forceinline__ void store4f(float* p, const v16f& c, int j, float f) {
-  v4f o;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = c[4 * j + e] * f;
-  *reinterpret_cast<v4f*>(p) = o;
 }
 
 __device__ __forceinline__ v16f zero16() {
@@ -316,7 +337,156 @@ __device__ __forceinline__ bool bit_of(const KeyBits<W>& k, int i) {
   return (x >> (i & 31)) & 1;
 }
 
+// Waves a SIMD that the registers are to allow.
+#ifndef FW
+#define FW (sizeof(T) == 2 ? 2 : 1)
+#endif
+#ifndef QW
+#define QW (sizeof(T) == 2 ? 2 : 1)
+#endif
+#ifndef KW
+#define KW (sizeof(T) == 2 && DC <= 8 ? 2 : 1)
+#endif
 // ----------------------------------------------------------------- forward ----
+
+// SUB pieces of 32 keys for a wave's rows: scores, the running maximum m and sum l, and
+// O += weights times values. words: the keys of each piece that count.
+template <int SUB>
+__device__ __forceinline__ void attend(const T* kt, const T* vt, const Spots& spots, float scale2,
+                                       const uint32_t (&words)[SUB], const frag (&q)[DC],
+                                       v16f (&o)[kOB], float& m, float& l, int h) {
+  v16f s[SUB];
+  uint32_t every = 0xffffffffu;
+#pragma unroll
+  for (int u = 0; u < SUB; ++u) {
+    s[u] = zero16();
+    every &= words[u];
+#pragma unroll
+    for (int kb = 0; kb < DC; ++kb) s[u] = mma(row_frag(kt + 32 * u * kPitch, spots, kb), q[kb], s[u]);
+  }
+  if (every != 0xffffffffu) {
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      const uint32_t w = words[u] >> (4 * h);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (!((w >> (8 * (i / 4) + i % 4)) & 1)) s[u][i] = -INFINITY;
+    }
+  }
+  float top = s[0][0];
+#pragma unroll
+  for (int u = 0; u < SUB; ++u)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+  // Weights stay within 2^8 of what the true maximum would make them: O and l are only
+  // rescaled where one rose further (the first of them starts from -infinity).
+  const float m_new = fmaxf(m, fmaxf(top, other_half(top)) * scale2);
+  if (__any(m_new > m + kSlack)) {
+    const float f = exp2_fast(m - (m_new == -INFINITY ? 0.0f : m_new));
+    l *= f;
+#pragma unroll
+    for (int i = 0; i < kOB; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[i][e] *= f;
+    m = m_new;
+  }
+  const float base = m == -INFINITY ? 0.0f : m;
+  float sum = 0.0f;
+#pragma unroll
+  for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[u][i] = exp2_fast(__builtin_fmaf(s[u][i], scale2, -base));
+      sum += s[u][i];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const frag p = operand(s[u], i);
+      const T* v0 = vt + (32 * u + 16 * i) * kPitch;
+#pragma unroll
+      for (int c = 0; c < kOB; ++c) o[c] = mma(col_frag(v0, spots, c), p, o[c]);
+    }
+  }
+  l += sum;
+}
+
+// O and lse of a row, l being the whole sum.
+__device__ __forceinline__ void finish(const AttnArgs& a, int b, int hk, int row, const v16f (&o)[kOB],
+                                       float m, float l, int h) {
+  const bool empty = m == -INFINITY && l == 0.0f;
+  const float inv = empty ? 0.0f : 1.0f / l;
+  if (a.lse && h == 0)
+    a.lse[stat_at(a, b, hk, row)] = empty ? -INFINITY : (m + __log2f(l)) * kLn2;
+  T* p = const_cast<T*>(row_of(a, a.o, b, hk, row));
+  store_row(p, o, inv, a.D, h);
+}
+
+// Few keys (a prompt's): all of them stay in LDS while a workgroup goes through `per_group`
+// tiles of rows, its waves on their own after the one barrier, the next rows' queries under
+// way.
+#if QL_AT_SHORT
+__global__ __launch_bounds__(kThreads, FW) void k_attn_short(AttnArgs a) {
+  constexpr int KT = 64, kTile = KT * 2 * kPitch;
+  __shared__ __attribute__((aligned(16))) T lds[2 * kTile];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r32 = lane & 31, h = lane >> 5;
+  int id = by_xcd(blockIdx.x, gridDim.x);
+  const int groups = (a.row_tiles + a.per_group - 1) / a.per_group;
+  const int rt0 = id % groups * a.per_group, rt1 = min(rt0 + a.per_group, a.row_tiles);
+  id /= groups;
+  const int hk = id % a.Hk, b = id / a.Hk;
+  const int len = key_len(a, b), tiles = (len + KT - 1) / KT;
+  const T* const kp = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
+  const T* const vp = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
+  frag next[DC];
+  const auto ask = [&](int rt) {
+    const T* p = row_of(a, a.q, b, hk, min(rt * 128 + wave * 32 + r32, a.R - 1));
+#pragma unroll
+    for (int kb = 0; kb < DC; ++kb) next[kb] = load_frag(p, 16 * kb + 8 * h, a.D);
+  };
+  ask(rt0);
+  KeyBits<2> bits[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    bits[t].look(a, b, t * KT, len, lane);
+    if (t < tiles) {
+      Stage<KT> ks, vs;
+      ks.find(tid, a.D, 1, 0, 0);
+      vs.find(tid, a.D, 1, 0, 0);
+      ks.fetch_by(tid, a.D, [&](int i) { return kp + (int64_t)min(t * KT + i, a.Lk - 1) * a.k.row; });
+      vs.fetch_by(tid, a.D, [&](int i) { return vp + (int64_t)min(t * KT + i, a.Lk - 1) * a.v.row; });
+      const auto keep = [&](int i) { return bit_of(bits[t], i); };
+      ks.template put<true>(lds + t * kTile, tid, a.D, keep);
+      vs.template put<false>(lds + t * kTile + KT * kPitch, tid, a.D, keep);
+    }
+  }
+  Spots spots;
+  spots.find(lane);
+  __syncthreads();
+  for (int rt = rt0; rt < rt1; ++rt) {
+    frag q[DC];
+#pragma unroll
+    for (int kb = 0; kb < DC; ++kb) q[kb] = next[kb];
+    if (rt + 1 < rt1) ask(rt + 1);
+    v16f o[kOB];
+#pragma unroll
+    for (int i = 0; i < kOB; ++i) o[i] = zero16();
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      form_anew(spots);
+      const T* const kt = lds + t * kTile;
+      if (bits[t].w[1])
+        attend<2>(kt, kt + KT * kPitch, spots, a.scale2, bits[t].w, q, o, m, l, h);
+      else if (bits[t].w[0])
+        attend<1>(kt, kt + KT * kPitch, spots, a.scale2, {bits[t].w[0]}, q, o, m, l, h);
+    }
+    const int row = rt * 128 + wave * 32 + r32;
+    l += other_half(l);
+    if (row < a.R) finish(a, b, hk, row, o, m, l, h);
+  }
+}
+#endif
 
 // WK waves of a workgroup share its keys, 4 / WK its rows: one for many rows; all
 // four (two in fp32, whose tiles fill LDS) for few of them.
@@ -332,16 +502,6 @@ struct Fwd {
                                                                  : kJoin;
 };
 
-// Waves a SIMD that the registers are to allow.
-#ifndef FW
-#define FW (sizeof(T) == 2 ? 2 : 1)
-#endif
-#ifndef QW
-#define QW (sizeof(T) == 2 ? 2 : 1)
-#endif
-#ifndef KW
-#define KW (sizeof(T) == 2 && DC <= 8 ? 2 : 1)
-#endif
 template <int WK>
 __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
   typedef Fwd<WK> P;
@@ -410,62 +570,15 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
     if (t + 1 < t1) fetch(t + 1);
     form_anew(spots);
     if (!bits.none()) {
-      v16f s[SUB];
+      uint32_t words[SUB];
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        s[u] = zero16();
-        const T* p = kt + (wk * SUB + u) * 32 * kPitch;
+        words[u] = 0;  // wk is uniform: a select of the words
 #pragma unroll
-        for (int kb = 0; kb < DC; ++kb) s[u] = mma(row_frag(p, spots, kb), q[kb], s[u]);
+        for (int j = 0; j < W; ++j) words[u] = j == wk * SUB + u ? bits.w[j] : words[u];
       }
-      if (!bits.all()) {
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          uint32_t w = 0;  // wk is uniform: a select of the words
-#pragma unroll
-          for (int j = 0; j < W; ++j) w = j == wk * SUB + u ? bits.w[j] : w;
-          w >>= 4 * h;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (!((w >> (8 * (i / 4) + i % 4)) & 1)) s[u][i] = -INFINITY;
-        }
-      }
-      float top = s[0][0];
-#pragma unroll
-      for (int u = 0; u < SUB; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-      top = fmaxf(top, other_half(top)) * a.scale2;
-      // Weights stay within 2^8 of what the true maximum would make them: O and l are only
-      // rescaled where one rose further (the first of them starts from -infinity).
-      const float m_new = fmaxf(m, top);
-      if (__any(m_new > m + kSlack)) {
-        const float f = exp2_fast(m - (m_new == -INFINITY ? 0.0f : m_new));
-        l *= f;
-#pragma unroll
-        for (int i = 0; i < kOB; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[i][e] *= f;
-        m = m_new;
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
-      float sum = 0.0f;
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[u][i] = exp2_fast(__builtin_fmaf(s[u][i], a.scale2, -base));
-          sum += s[u][i];
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const frag p = operand(s[u], i);
-          const T* v0 = vt + ((wk * SUB + u) * 32 + 16 * i) * kPitch;
-#pragma unroll
-          for (int c = 0; c < kOB; ++c) o[c] = mma(col_frag(v0, spots, c), p, o[c]);
-        }
-      }
-      l += sum;
+      const int at = wk * SUB * 32 * kPitch;
+      attend<SUB>(kt + at, vt + at, spots, a.scale2, words, q, o, m, l, h);
     }
     if constexpr (P::NB == 1) __syncthreads();
     if (t + 1 < t1) put(lds + ((t + 1 - t0) % P::NB) * P::kTile);
@@ -515,32 +628,13 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
     m = top;
   }
   if (row >= a.R) return;
+  if (a.splits == 1) return finish(a, b, hk, row, o, m, l, h);
   const bool empty = m == -INFINITY && l == 0.0f;
   const float inv = empty ? 0.0f : 1.0f / l;
-  const float lse2 = empty ? -INFINITY : m + __log2f(l);
-  const int64_t at = stat_at(a, b, hk, row);
-  if (a.splits > 1) {
-    const int64_t n = (int64_t)a.B * a.H * a.Lq;
-    float* p = a.part + (sp * n + at) * a.D;
-    if (h == 0) a.part_lse[sp * n + at] = lse2;
-#pragma unroll
-    for (int c = 0; c < kOB; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int d = 32 * c + 8 * j + 4 * h;
-        if (d < a.D) store4f(p + d, o[c], j, inv);
-      }
-    return;
-  }
-  T* p = const_cast<T*>(row_of(a, a.o, b, hk, row));
-  if (a.lse && h == 0) a.lse[at] = lse2 * kLn2;
-#pragma unroll
-  for (int c = 0; c < kOB; ++c)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int d = 32 * c + 8 * j + 4 * h;
-      if (d < a.D) store4(p + d, o[c], j, inv);
-    }
+  const int64_t n = (int64_t)a.B * a.H * a.Lq, at = stat_at(a, b, hk, row);
+  float* p = a.part + (sp * n + at) * a.D;
+  if (h == 0) a.part_lse[sp * n + at] = empty ? -INFINITY : m + __log2f(l);
+  store_row(p, o, inv, a.D, h);
 }
 
 // One wave a row: the parts of its splits weighted by their share of the sum. Lane s
@@ -665,6 +759,7 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
     if (!bits.none()) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        if (!bits.w[u]) continue;
         v16f s = zero16(), dp = zero16();
 #pragma unroll
         for (int kb = 0; kb < DC; ++kb) {
@@ -698,13 +793,7 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
   }
   if (row >= a.R) return;
   T* p = const_cast<T*>(row_of(a, a.dq, b, hk, row));
-#pragma unroll
-  for (int c = 0; c < kOB; ++c)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int d = 32 * c + 8 * j + 4 * h;
-      if (d < a.D) store4(p + d, dq[c], j, a.scale);
-    }
+  store_row(p, dq, a.scale, a.D, h);
 }
 
 #ifndef VL
@@ -840,30 +929,14 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
   if (a.splits > 1) {
     const int64_t n = (int64_t)a.B * a.Lk * a.Hk * a.D;
     float* p = a.part + sp * 2 * n + (((int64_t)b * a.Lk + key) * a.Hk + hk) * a.D;
-#pragma unroll
-    for (int c = 0; c < kOB; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int d = 32 * c + 8 * j + 4 * h;
-        if (d < a.D) {
-          store4f(p + d, dk[c], j, a.scale);
-          store4f(p + n + d, dv[c], j, 1.0f);
-        }
-      }
+    store_row(p, dk, a.scale, a.D, h);
+    store_row(p + n, dv, 1.0f, a.D, h);
     return;
   }
   T* pk = reinterpret_cast<T*>(a.dk.p) + b * a.dk.batch + key * a.dk.row + hk * a.dk.head;
   T* pv = reinterpret_cast<T*>(a.dv.p) + b * a.dv.batch + key * a.dv.row + hk * a.dv.head;
-#pragma unroll
-  for (int c = 0; c < kOB; ++c)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int d = 32 * c + 8 * j + 4 * h;
-      if (d < a.D) {
-        store4(pk + d, dk[c], j, a.scale);
-        store4(pv + d, dv[c], j, 1.0f);
-      }
-    }
+  store_row(pk, dk, a.scale, a.D, h);
+  store_row(pv, dv, 1.0f, a.D, h);
 }
 
 // dK (blockIdx.y 0) and dV (1): the sum of the row ranges' parts, four channels a thread.
@@ -908,9 +981,17 @@ constexpr int kNarrow = sizeof(T) == 2 ? 4 : 2;
 #define QL_CAT3(a, b, c, d) a##b##c##d
 #define QL_NAME(f, t, d) QL_CAT3(f, t, _, d)
 
-hipError_t QL_NAME(attn_forward_, QL_AT_T, QL_AT_DC)(const AttnArgs& a, bool narrow, hipStream_t s) {
+hipError_t QL_NAME(attn_forward_, QL_AT_T, QL_AT_DC)(const AttnArgs& a, const AttnPlan& p,
+                                                     hipStream_t s) {
   const int grid = a.B * a.Hk * a.row_tiles * a.splits;
-  if (narrow)
+#if QL_AT_SHORT
+  if (p.per_group > 0) {
+    const int groups = (a.row_tiles + a.per_group - 1) / a.per_group;
+    k_attn_short<<<a.B * a.Hk * groups, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+  }
+#endif
+  if (p.narrow)
     k_attn_forward<kNarrow><<<grid, kThreads, 0, s>>>(a);
   else
     k_attn_forward<1><<<grid, kThreads, 0, s>>>(a);

@@ -91,7 +91,7 @@ struct AttnArgs {
   int64_t mask_batch;
   int B, H, Hk, G, Lq, Lk, D, R;  // R = Lq * G
   float scale, scale2;            // scale2 = scale * log2(e)
-  int row_tiles, key_tiles;
+  int row_tiles, key_tiles, per_group;
   int splits;       // of the keys (forward), of the rows (dk and dv)
   float* part;      // forward [splits][B, H, Lq][D]; dk, dv: [splits][2][B, Lk, Hk][D]
   float* part_lse;  // [splits][B, H, Lq], base 2
@@ -101,6 +101,7 @@ struct AttnArgs {
 };
 struct AttnPlan {
   bool narrow;
+  int per_group;             // forward, few keys: tiles of rows of a workgroup, else 0
   int row_tiles, splits;          // forward
   int q_tiles, key_tiles, k_splits;  // gradient
   int64_t forward_bytes, grad_bytes;
@@ -111,7 +112,7 @@ hipError_t launch_attn_grad(const AttnArgs& a, const AttnPlan& p, hipStream_t s)
 
 // One object file for each head size and type defines its own; DC = 16-channel blocks.
 #define QL_ATTN_UNIT(T, DC)                                                        \
-  hipError_t attn_forward_##T##_##DC(const AttnArgs& a, bool narrow, hipStream_t); \
+  hipError_t attn_forward_##T##_##DC(const AttnArgs& a, const AttnPlan& p, hipStream_t); \
   hipError_t attn_grad_##T##_##DC(const AttnArgs& a, const AttnPlan& p, hipStream_t);
 #define QL_ATTN_UNITS(X) \
   X(f32, 2) X(f32, 4) X(f32, 5) X(f32, 6) X(f32, 8) X(f32, 10) \

@@ -320,6 +320,9 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 }  // namespace
 
+#ifndef SHORT_WGS
+#define SHORT_WGS 512
+#endif
 namespace ql {
 
 // Rows and keys by tiles, and how many workgroups share a long axis where few tiles of
@@ -337,13 +340,17 @@ AttnPlan attn_plan(const ql_attn& d) {
   const int64_t most = tiles / (p.narrow ? 2 : 4);
   s = s < most ? s : most;
   p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  if (!p.narrow && p.splits == 1 && d.k_len <= 128 && (bf16 || d.dim <= 128)) {
+    const int64_t each = base / SHORT_WGS;
+    p.per_group = (int)(each < 1 ? 1 : each > p.row_tiles ? p.row_tiles : each);
+  }
   p.forward_bytes = p.splits > 1 ? up16(p.splits * n * d.dim * 4) + up16(p.splits * n * 4) : 0;
 
   p.q_tiles = ceil_div(R, 128);
   p.key_tiles = ceil_div(d.k_len, 128);
   const int64_t kbase = bh * p.key_tiles;
   s = kbase > 0 ? 512 / kbase : 1;
-  const int64_t kmost = ceil_div(R, 32) / 8;
+  const int64_t kmost = ceil_div(R, 32) / (bf16 ? 8 : 2);
   s = s < kmost ? s : kmost;
   p.k_splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   p.grad_bytes = up16(n * 4);
@@ -362,7 +369,7 @@ int blocks16(int D) {
 hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const int dc = blocks16(a.D);
 #define QL_ATTN_GO(T, DC) \
-  if (dc == DC && a.bf16 == (sizeof(#T) == sizeof("bf16"))) return attn_forward_##T##_##DC(a, p.narrow, s);
+  if (dc == DC && a.bf16 == (sizeof(#T) == sizeof("bf16"))) return attn_forward_##T##_##DC(a, p, s);
   QL_ATTN_UNITS(QL_ATTN_GO)
 #undef QL_ATTN_GO
   return hipErrorInvalidValue;
@@ -584,6 +591,7 @@ ql_status qlinear_attention(const ql_attn* d, const ql_heads_view* q, const ql_h
   const int64_t size = size_of(d->dtype);
   a.near_keys = near(a.k, 128, 1, size) && near(a.v, 128, 1, size);
   a.row_tiles = p.row_tiles;
+  a.per_group = p.per_group;
   a.splits = p.splits;
   if (p.splits > 1) {
     const int64_t n = (int64_t)d->batch * d->heads * d->q_len;
