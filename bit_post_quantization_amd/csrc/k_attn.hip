@@ -160,11 +160,14 @@ __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_ex
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Workgroup `id` of n in an order that gives each of the 8 XCDs (workgroups are dealt to
-// them in turn) a run of neighbours, so that the tiles of one head meet in one L2.
-__device__ __forceinline__ int by_xcd(int id, int n) {
-  const int x = id % 8, q = n / 8, r = n % 8;
-  return x * q + min(x, r) + id / 8;
+// Workgroup `id` of B Hk runs of `per` (the tiles of one key head) in an order that keeps
+// `a.unit` neighbouring heads' runs in one L2: workgroups are dealt to the 8 XCDs in turn.
+// Neighbouring units go to unlike XCDs where they divide evenly.
+__device__ __forceinline__ int by_xcd(const AttnArgs& a, int id, int per) {
+  const int x = id % 8, j = id / 8, n = a.B * a.Hk * per;
+  per *= a.unit;
+  if (n / per % 8 == 0) return (j / per * 8 + x) * per + j % per;
+  return x * (n / 8) + min(x, n % 8) + j;
 }
 
 __device__ __forceinline__ void split_row(const AttnArgs& a, int r, int& l, int& g) {
@@ -430,8 +433,8 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_short(AttnArgs a) {
   __shared__ __attribute__((aligned(16))) T lds[2 * kTile];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r32 = lane & 31, h = lane >> 5;
-  int id = by_xcd(blockIdx.x, gridDim.x);
   const int groups = (a.row_tiles + a.per_group - 1) / a.per_group;
+  int id = by_xcd(a, blockIdx.x, groups);
   const int rt0 = id % groups * a.per_group, rt1 = min(rt0 + a.per_group, a.row_tiles);
   id /= groups;
   const int hk = id % a.Hk, b = id / a.Hk;
@@ -510,7 +513,7 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
   T* const lds = reinterpret_cast<T*>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wq = wave / WK, wk = wave % WK, r32 = lane & 31, h = lane >> 5;
-  int id = by_xcd(blockIdx.x, gridDim.x);
+  int id = by_xcd(a, blockIdx.x, a.row_tiles * a.splits);
   const int sp = id % a.splits;
   id /= a.splits;
   const int rt = id % a.row_tiles;
@@ -686,7 +689,7 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
   constexpr int NB = 2 * kTile * (int)sizeof(T) <= 81920 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) T lds[NB * kTile];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, h = lane >> 5;
-  int id = by_xcd(blockIdx.x, gridDim.x);
+  int id = by_xcd(a, blockIdx.x, a.row_tiles);
   const int rt = id % a.row_tiles;
   id /= a.row_tiles;
   const int hk = id % a.Hk, b = id / a.Hk;
@@ -809,7 +812,7 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
   __shared__ __attribute__((aligned(16))) T v_rows[VL ? 128 * kPitch : 8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, h = lane >> 5;
   T* const my_v = v_rows + (VL ? wave * 32 * kPitch : 0);
-  int id = by_xcd(blockIdx.x, gridDim.x);
+  int id = by_xcd(a, blockIdx.x, a.key_tiles * a.splits);
   const int sp = id % a.splits;
   id /= a.splits;
   const int kt = id % a.key_tiles;

@@ -90,6 +90,7 @@ struct AttnArgs {
   const uint8_t* mask;
   int64_t mask_batch;
   int B, H, Hk, G, Lq, Lk, D, R;  // R = Lq * G
+  int unit;      // neighbouring key heads that share an L2
   float scale, scale2;            // scale2 = scale * log2(e)
   int row_tiles, key_tiles, per_group;
   int splits;       // of the keys (forward), of the rows (dk and dv)

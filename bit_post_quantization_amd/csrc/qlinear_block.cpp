@@ -305,6 +305,12 @@ ql::AttnArgs attn_args(const ql_attn* d) {
   a.Lk = d->k_len;
   a.D = d->dim;
   a.R = a.Lq * a.G;
+  // Neighbouring heads lie in the same lines of memory; but sequences differ in length, and
+  // every XCD is to have its share of all of them: at least four units each.
+  a.unit = 1;
+  while (a.unit < 8 && a.Hk % (2 * a.unit) == 0 && (int64_t)a.B * a.Hk / (2 * a.unit) % 8 == 0 &&
+         (int64_t)a.B * a.Hk / (2 * a.unit) >= 32)
+    a.unit *= 2;
   a.scale = d->scale;
   a.scale2 = (float)((double)d->scale * 1.4426950408889634074);
   a.bf16 = d->dtype == QL_BF16;
@@ -320,9 +326,6 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 }  // namespace
 
-#ifndef SHORT_WGS
-#define SHORT_WGS 512
-#endif
 namespace ql {
 
 // Rows and keys by tiles, and how many workgroups share a long axis where few tiles of
@@ -336,12 +339,12 @@ AttnPlan attn_plan(const ql_attn& d) {
   p.row_tiles = ceil_div(R, p.narrow ? (bf16 ? 32 : 64) : 128);
   const int64_t tiles = ceil_div(d.k_len, p.narrow && bf16 ? 128 : 64);
   const int64_t base = bh * p.row_tiles;
-  int64_t s = base > 0 ? (p.narrow ? 1024 : 512) / base : 1;
+  int64_t s = base > 0 ? (p.narrow ? 768 : 512) / base : 1;
   const int64_t most = tiles / (p.narrow ? 2 : 4);
   s = s < most ? s : most;
   p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   if (!p.narrow && p.splits == 1 && d.k_len <= 128 && (bf16 || d.dim <= 128)) {
-    const int64_t each = base / SHORT_WGS;
+    const int64_t each = base / 512;
     p.per_group = (int)(each < 1 ? 1 : each > p.row_tiles ? p.row_tiles : each);
   }
   p.forward_bytes = p.splits > 1 ? up16(p.splits * n * d.dim * 4) + up16(p.splits * n * 4) : 0;
@@ -349,7 +352,7 @@ AttnPlan attn_plan(const ql_attn& d) {
   p.q_tiles = ceil_div(R, 128);
   p.key_tiles = ceil_div(d.k_len, 128);
   const int64_t kbase = bh * p.key_tiles;
-  s = kbase > 0 ? 512 / kbase : 1;
+  s = kbase > 0 ? (bf16 ? 512 : 256) / kbase : 1;
   const int64_t kmost = ceil_div(R, 32) / (bf16 ? 8 : 2);
   s = s < kmost ? s : kmost;
   p.k_splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
