@@ -8,9 +8,17 @@
 //
 // Bound by memory: some 10 operations an element that is read and written. G lanes
 // share a head, lane j taking the 16-byte pieces j, j + G, ... of it, so that neighbouring
-// lanes read neighbouring addresses and a head's sums cross two or three lanes. The
+// lanes read neighbouring addresses and a head's sums cross two to four lanes. The
 // angles are the same for all heads of a token: a workgroup forms the sines and
-// cosines of its tokens once, in LDS, a pair a thread (fp64 up to the fraction of a turn).
+// cosines of its tokens once, in LDS (fp64 up to the fraction of a turn), signed so that
+// every channel becomes n[c] cos + n[partner] sin. Adjacent partners are in the lane; any
+// others trade places in LDS (read and written in halves of pieces, with the
+// partners in one lane, the clip below takes 95 us where heads are cut at multiples of
+// four pairs, and element by element, as other heads would need, 213).
+//
+// Measured: one clip, 17550 tokens of 32 + 4 + 4 heads of 128, bf16: 98 us, 3.7 TB/s, for
+// pairs in halves, 78 (4.6) for neighbours; gradient, 18432 tokens of 3 x 16 heads of 128,
+// bf16: 131 us, 5.2 TB/s, and 5 for the sum of dgamma.
 #include "ql_block.h"
 #include "ql_device.h"
 
@@ -20,8 +28,8 @@ namespace {
 
 typedef __bf16 bf16;
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 64;
-constexpr int kMaxPairs = 80;
+constexpr int kMaxTokens = 32;  // their turns take up to 40 KB of LDS
+constexpr int kMaxDim = 160;
 
 template <typename T, int N>
 struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Vec {
@@ -35,116 +43,119 @@ __device__ __forceinline__ float read_w(const void* p, bool is_bf16, int i) {
 // Pairs are numbered axis by axis, then those that do not turn (numbered like one more
 // axis). Channels of pair p, and its axis (n_axes: does not turn).
 __device__ __forceinline__ int pair_channels(const HeadsArgs& a, int p, int& c1, int& c2) {
-  int axis = 0, first = 0, half = a.D / 2;
+  int axis = 0, first = 0;
 #pragma unroll
   for (int i = 0; i < QL_MAX_AXES; ++i)
     if (i < a.n_axes && axis == i && p - first >= a.half[i]) {
       first += a.half[i];
       axis = i + 1;
     }
-  half = axis < a.n_axes ? a.half[axis] : a.D / 2 - first;
+  const int half = axis < a.n_axes ? a.half[axis] : a.D / 2 - first;
   c1 = a.halves ? 2 * first + (p - first) : 2 * p;
   c2 = a.halves ? c1 + half : c1 + 1;
   return axis;
 }
 
-// How a lane's pairs lie: one vector of neighbouring pairs (a, b, a, b), one of first
-// and one of second members, or anyhow.
-enum { kAdjacent = 0, kHalves = 1, kScattered = 2 };
+// How partners meet and rows are read: pairs of neighbours, in vectors; any pairs, in
+// vectors; any pairs, element by element (rows that no vector is aligned to).
+enum { kAdjacent = 0, kApart = 1, kByElement = 2 };
 
-template <typename XT> struct Geo {
-  static constexpr int V = 16 / sizeof(XT), P = V / 2;  // channels and pairs of a piece
-};
+// Channels of a piece.
+template <typename XT> constexpr int kV = 16 / sizeof(XT);
 
-// Where the pieces of a lane lie in a head, in pair order.
-template <int C, int P, int MODE>
-struct Places {
-  int c1[MODE == kScattered ? C * P : C], c2[MODE == kScattered ? C * P : C];
-  int pieces, j;
-  template <int G>
-  __device__ __forceinline__ void find(const HeadsArgs& a, int lane_in_head) {
-    j = lane_in_head;
-    pieces = a.D / (2 * P);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int u = min(j + c * G, pieces - 1);
-      if constexpr (MODE == kScattered) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) pair_channels(a, u * P + i, c1[c * P + i], c2[c * P + i]);
-      } else {
-        pair_channels(a, u * P, c1[c], c2[c]);
-      }
-    }
-  }
-};
-
-// Values of a lane: pairs (p[.][.][0], p[.][.][1]); pieces past the head are zero.
-template <int C, int P>
+// Values of a lane: piece c has channels (j + c G) V .. + V - 1; those past the head are 0.
+template <int C, int V>
 struct Vals {
-  float p[C][P][2];
+  float v[C][V];
 };
 
-template <typename T, int C, int P, int G, int MODE>
-__device__ __forceinline__ void load(const T* row, const Places<C, P, MODE>& w, bool ok,
-                                     Vals<C, P>& v) {
+template <typename T, int C, int V, int G, int MODE>
+__device__ __forceinline__ void load(const T* row, int j, int pieces, bool ok, Vals<C, V>& x) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const bool in = ok && w.j + c * G < w.pieces;
+    const int u = j + c * G;
+    if (ok && u < pieces) {
+      if constexpr (MODE == kByElement) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) v.p[c][i][0] = v.p[c][i][1] = 0.0f;
-    if (!in) continue;
-    if constexpr (MODE == kAdjacent) {
-      const Vec<T, 2 * P> x = *reinterpret_cast<const Vec<T, 2 * P>*>(row + w.c1[c]);
+        for (int i = 0; i < V; ++i) x.v[c][i] = (float)row[u * V + i];
+      } else {
+        const Vec<T, V> y = *reinterpret_cast<const Vec<T, V>*>(row + u * V);
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        v.p[c][i][0] = (float)x.e[2 * i];
-        v.p[c][i][1] = (float)x.e[2 * i + 1];
-      }
-    } else if constexpr (MODE == kHalves) {
-      const Vec<T, P> x = *reinterpret_cast<const Vec<T, P>*>(row + w.c1[c]);
-      const Vec<T, P> y = *reinterpret_cast<const Vec<T, P>*>(row + w.c2[c]);
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        v.p[c][i][0] = (float)x.e[i];
-        v.p[c][i][1] = (float)y.e[i];
+        for (int i = 0; i < V; ++i) x.v[c][i] = (float)y.e[i];
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        v.p[c][i][0] = (float)row[w.c1[c * P + i]];
-        v.p[c][i][1] = (float)row[w.c2[c * P + i]];
-      }
+      for (int i = 0; i < V; ++i) x.v[c][i] = 0.0f;
     }
   }
 }
 
-template <typename T, int C, int P, int G, int MODE>
-__device__ __forceinline__ void store(T* row, const Places<C, P, MODE>& w, const Vals<C, P>& v) {
+template <typename T, int C, int V, int G, int MODE>
+__device__ __forceinline__ void store(T* row, int j, int pieces, const Vals<C, V>& x) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if (w.j + c * G >= w.pieces) continue;
-    if constexpr (MODE == kAdjacent) {
-      Vec<T, 2 * P> x;
+    const int u = j + c * G;
+    if (u >= pieces) continue;
+    if constexpr (MODE == kByElement) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        x.e[2 * i] = (T)v.p[c][i][0];
-        x.e[2 * i + 1] = (T)v.p[c][i][1];
-      }
-      *reinterpret_cast<Vec<T, 2 * P>*>(row + w.c1[c]) = x;
-    } else if constexpr (MODE == kHalves) {
-      Vec<T, P> x, y;
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        x.e[i] = (T)v.p[c][i][0];
-        y.e[i] = (T)v.p[c][i][1];
-      }
-      *reinterpret_cast<Vec<T, P>*>(row + w.c1[c]) = x;
-      *reinterpret_cast<Vec<T, P>*>(row + w.c2[c]) = y;
+      for (int i = 0; i < V; ++i) row[u * V + i] = (T)x.v[c][i];
     } else {
+      Vec<T, V> y;
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        row[w.c1[c * P + i]] = (T)v.p[c][i][0];
-        row[w.c2[c * P + i]] = (T)v.p[c][i][1];
+      for (int i = 0; i < V; ++i) y.e[i] = (T)x.v[c][i];
+      *reinterpret_cast<Vec<T, V>*>(row + u * V) = y;
+    }
+  }
+}
+
+// The partners of a lane's channels, a byte each.
+template <int C, int V>
+struct Partners {
+  uint32_t b[C * V / 4];
+  template <int G>
+  __device__ __forceinline__ void find(const uint8_t* partner, int j, int pieces) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < V; i += 4)
+        b[(c * V + i) / 4] = *reinterpret_cast<const uint32_t*>(partner + min(j + c * G, pieces - 1) * V + i);
+  }
+};
+
+// x[c] cos + x[partner] sin (with BACK - : turned back) for a head. In kApart and
+// kByElement `room` is the head's own D floats of LDS; its lanes are in one wave, whose
+// LDS operations are done in order.
+template <int C, int V, int G, int MODE, bool BACK>
+__device__ __forceinline__ void turn_head(const float2* cs, const Partners<C, V>& w, float* room,
+                                          int j, int pieces, Vals<C, V>& x) {
+  if constexpr (MODE != kAdjacent) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (j + c * G < pieces)
+#pragma unroll
+        for (int i = 0; i < V; ++i) room[(j + c * G) * V + i] = x.v[c][i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int at = min(j + c * G, pieces - 1) * V;
+    float y[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (MODE == kAdjacent)
+        y[i] = x.v[c][i ^ 1];
+      else
+        y[i] = room[(w.b[(c * V + i) / 4] >> (8 * (i % 4))) & 255];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (MODE == kAdjacent) {
+        const float2 t = cs[(at + i) / 2];
+        x.v[c][i] = __builtin_fmaf(x.v[c][i], t.x, (i % 2 == 0) != BACK ? -(y[i] * t.y) : y[i] * t.y);
+      } else {
+        const float2 t = cs[at + i];
+        x.v[c][i] = __builtin_fmaf(x.v[c][i], t.x, BACK ? -(y[i] * t.y) : y[i] * t.y);
       }
     }
   }
@@ -159,7 +170,9 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// Cosines and sines of `n` tokens from `tok0` on into turn[token][pair].
+// Cosines and sines of `n` tokens from `tok0` on into turn[token][pair], or signed into
+// turn[token][channel].
+template <int MODE>
 __device__ __forceinline__ void form_turns(const HeadsArgs& a, float2* turn, int64_t tok0, int n) {
   const int pairs = a.D / 2;
   for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
@@ -176,7 +189,12 @@ __device__ __forceinline__ void form_turns(const HeadsArgs& a, float2* turn, int
       const float part = (float)(turns - rint(turns));
       sincospif(2.0f * part, &cs.y, &cs.x);
     }
-    turn[i] = cs;
+    if constexpr (MODE == kAdjacent) {
+      turn[i] = cs;
+    } else {
+      turn[t * a.D + c1] = make_float2(cs.x, -cs.y);
+      turn[t * a.D + c2] = cs;
+    }
   }
 }
 
@@ -196,15 +214,18 @@ __device__ __forceinline__ void find_starts(const HeadsArgs& a, Starts* out, int
   }
 }
 
-// The gammas in pair order: out[part][2 pair + member].
-__device__ __forceinline__ void fetch_gammas(const HeadsArgs& a, float (*out)[2 * kMaxPairs]) {
-  for (int i = threadIdx.x; i < a.D; i += kThreads) {
-    const int part = i / (a.D / 2), p = i - part * (a.D / 2);
+// The gammas, and the partner of each channel.
+__device__ __forceinline__ void fetch_tables(const HeadsArgs& a, float (*gamma)[kMaxDim],
+                                             uint8_t* partner) {
+  for (int i = threadIdx.x; i < 2 * a.D; i += kThreads) {
+    const int part = i / a.D, c = i - part * a.D;
+    gamma[part][c] = a.gamma[part] ? read_w(a.gamma[part], a.w_bf16, c) : 1.0f;
+  }
+  for (int p = threadIdx.x; p < a.D / 2; p += kThreads) {
     int c1, c2;
     pair_channels(a, p, c1, c2);
-    const void* g = a.gamma[part];
-    out[part][2 * p] = g ? read_w(g, a.w_bf16, c1) : 1.0f;
-    out[part][2 * p + 1] = g ? read_w(g, a.w_bf16, c2) : 1.0f;
+    partner[c1] = c2;
+    partner[c2] = c1;
   }
 }
 
@@ -212,67 +233,61 @@ __device__ __forceinline__ void fetch_gammas(const HeadsArgs& a, float (*out)[2 
 
 template <typename XT, typename YT, int G, int C, int MODE>
 __global__ __launch_bounds__(kThreads) void k_heads(HeadsArgs a) {
-  constexpr int P = Geo<XT>::P, kGroups = kThreads / G;
-  __shared__ float gamma[2][2 * kMaxPairs];
+  constexpr int V = kV<XT>, kGroups = kThreads / G;
+  constexpr int kRoom = C * G * V + 1;  // an odd step from head to head: other banks
+  __shared__ __attribute__((aligned(16))) float gamma[2][kMaxDim];
+  __shared__ __attribute__((aligned(16))) float rooms[MODE == kAdjacent ? 4 : kGroups * kRoom];
+  __shared__ __attribute__((aligned(4))) uint8_t partner[kMaxDim];
   __shared__ Starts starts[kMaxTokens];
-  extern __shared__ float2 turn[];  // [tokens][D / 2]
-  const int tid = threadIdx.x, group = tid / G;
+  extern __shared__ __attribute__((aligned(16))) float2 turn[];  // [tokens][D]
+  const int tid = threadIdx.x, group = tid / G, j = tid % G, pieces = a.D / V;
+  const int turns = MODE == kAdjacent ? a.D / 2 : a.D;  // of a token
+  float* const room = rooms + (MODE == kAdjacent ? 0 : group * kRoom);
   const int64_t all = (int64_t)a.B * a.L, tok0 = (int64_t)blockIdx.x * a.tokens;
   const int n = (int)(all - tok0 < a.tokens ? all - tok0 : a.tokens);
   const int heads = a.heads[0] + a.heads[1] + a.heads[2], rows = n * heads;
   find_starts(a, starts, tok0, n);
-  Places<C, P, MODE> at;
-  at.template find<G>(a, tid % G);
   __syncthreads();
   const auto row_in = [&](int r) {
     const int t = r / heads;
     return reinterpret_cast<const XT*>(a.x) + starts[t].x + (r - t * heads) * a.D;
   };
-  Vals<C, P> v, next;
-  load<XT, C, P, G, MODE>(row_in(min(group, rows - 1)), at, group < rows, next);
-  fetch_gammas(a, gamma);
-  form_turns(a, turn, tok0, n);
+  Vals<C, V> v, next;
+  load<XT, C, V, G, MODE>(row_in(min(group, rows - 1)), j, pieces, group < rows, next);
+  fetch_tables(a, gamma, partner);
+  form_turns<MODE>(a, turn, tok0, n);
   __syncthreads();
+  Partners<C, V> with;
+  with.template find<G>(partner, j, pieces);
   for (int r = group; r < rows; r += kGroups) {
     v = next;
     const int rn = r + kGroups;
-    load<XT, C, P, G, MODE>(row_in(min(rn, rows - 1)), at, rn < rows, next);
+    load<XT, C, V, G, MODE>(row_in(min(rn, rows - 1)), j, pieces, rn < rows, next);
     const int t = r / heads;
     int hd = r - t * heads;
     const int part = hd < a.heads[0] ? 0 : hd < a.heads[0] + a.heads[1] ? 1 : 2;
     if (part == 1) hd -= a.heads[0];
     if (part == 2) hd -= a.heads[0] + a.heads[1];
     if (part < 2) {
-      float rstd = 1.0f;
       if (a.rms) {
         float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-          for (int i = 0; i < P; ++i)
-            sum = __builtin_fmaf(v.p[c][i][0], v.p[c][i][0],
-                                 __builtin_fmaf(v.p[c][i][1], v.p[c][i][1], sum));
-        rstd = rsqrtf(head_sum<G>(sum) / (float)a.D + a.eps);
-      }
+          for (int i = 0; i < V; ++i) sum = __builtin_fmaf(v.v[c][i], v.v[c][i], sum);
+        const float rstd = rsqrtf(head_sum<G>(sum) / (float)a.D + a.eps);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int p0 = min(at.j + c * G, at.pieces - 1) * P;
+        for (int c = 0; c < C; ++c) {
+          const int at = min(j + c * G, pieces - 1) * V;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const float2 cs = turn[t * (a.D / 2) + p0 + i];
-          float x = v.p[c][i][0], y = v.p[c][i][1];
-          if (a.rms) {
-            x *= rstd * gamma[part][2 * (p0 + i)];
-            y *= rstd * gamma[part][2 * (p0 + i) + 1];
-          }
-          v.p[c][i][0] = __builtin_fmaf(x, cs.x, -(y * cs.y));
-          v.p[c][i][1] = __builtin_fmaf(x, cs.y, y * cs.x);
+          for (int i = 0; i < V; ++i) v.v[c][i] *= rstd * gamma[part][at + i];
         }
       }
+      if (a.n_axes) turn_head<C, V, G, MODE, false>(turn + t * turns, with, room, j, pieces, v);
     }
-    store<YT, C, P, G, MODE>(reinterpret_cast<YT*>(a.y[part].p) + starts[t].y[part] +
+    store<YT, C, V, G, MODE>(reinterpret_cast<YT*>(a.y[part].p) + starts[t].y[part] +
                                  hd * a.y[part].head,
-                             at, v);
+                             j, pieces, v);
   }
 }
 
@@ -282,63 +297,57 @@ __global__ __launch_bounds__(kThreads) void k_heads(HeadsArgs a) {
 // one sum of dgamma; it walks over the tokens in steps of gridDim.x tiles.
 template <typename XT, typename YT, int G, int C, int MODE>
 __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
-  constexpr int P = Geo<XT>::P, kGroups = kThreads / G;
-  __shared__ float gamma[2][2 * kMaxPairs];
-  __shared__ float sums[kThreads / 64][2 * kMaxPairs];
+  constexpr int V = kV<XT>, kGroups = kThreads / G;
+  constexpr int kRoom = C * G * V + 1;  // an odd step from head to head: other banks
+  __shared__ __attribute__((aligned(16))) float gamma[2][kMaxDim];
+  __shared__ __attribute__((aligned(16))) float rooms[MODE == kAdjacent ? 4 : kGroups * kRoom];
+  __shared__ __attribute__((aligned(4))) uint8_t partner[kMaxDim];
+  __shared__ float sums[kThreads / 64][kMaxDim];
   __shared__ Starts starts[kMaxTokens];
-  extern __shared__ float2 turn[];
-  const int tid = threadIdx.x, group = tid / G, part = blockIdx.y, heads = a.heads[part];
+  extern __shared__ __attribute__((aligned(16))) float2 turn[];
+  const int tid = threadIdx.x, group = tid / G, j = tid % G, pieces = a.D / V;
+  const int turns = MODE == kAdjacent ? a.D / 2 : a.D;  // of a token
+  float* const room = rooms + (MODE == kAdjacent ? 0 : group * kRoom);
+  const int part = blockIdx.y, heads = a.heads[part];
   const int64_t all = (int64_t)a.B * a.L;
   const int head0 = part == 0 ? 0 : part == 1 ? a.heads[0] : a.heads[0] + a.heads[1];
-  Places<C, P, MODE> at;
-  at.template find<G>(a, tid % G);
-  fetch_gammas(a, gamma);
-  Vals<C, P> dg;
+  fetch_tables(a, gamma, partner);
+  __syncthreads();
+  Partners<C, V> with;
+  with.template find<G>(partner, j, pieces);
+  Vals<C, V> dg;
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < P; ++i) dg.p[c][i][0] = dg.p[c][i][1] = 0.0f;
+    for (int i = 0; i < V; ++i) dg.v[c][i] = 0.0f;
   const ql_heads_view& y = a.y[part];
   const int64_t step = (int64_t)gridDim.x * a.tokens;
   for (int64_t tok0 = (int64_t)blockIdx.x * a.tokens; tok0 < all && heads > 0; tok0 += step) {
     const int n = (int)(all - tok0 < a.tokens ? all - tok0 : a.tokens), rows = n * heads;
     __syncthreads();  // the turns before have been read
     find_starts(a, starts, tok0, n);
-    if (part < 2) form_turns(a, turn, tok0, n);
+    if (part < 2) form_turns<MODE>(a, turn, tok0, n);
     __syncthreads();
     for (int r = group; r < rows; r += kGroups) {
       const int t = r / heads, hd = r - t * heads;
-      Vals<C, P> x, d;
-      load<YT, C, P, G, MODE>(reinterpret_cast<const YT*>(y.p) + starts[t].y[part] + hd * y.head, at,
-                              true, d);
+      Vals<C, V> x, d;
+      load<YT, C, V, G, MODE>(reinterpret_cast<const YT*>(y.p) + starts[t].y[part] + hd * y.head, j,
+                              pieces, true, d);
       if (part < 2) {
         if (a.rms)
-          load<XT, C, P, G, MODE>(reinterpret_cast<const XT*>(a.x) + starts[t].x +
-                                      (head0 + hd) * a.D, at, true, x);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int p0 = min(at.j + c * G, at.pieces - 1) * P;
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const float2 cs = turn[t * (a.D / 2) + p0 + i];
-            const float da = d.p[c][i][0], db = d.p[c][i][1];
-            d.p[c][i][0] = __builtin_fmaf(da, cs.x, db * cs.y);
-            d.p[c][i][1] = __builtin_fmaf(db, cs.x, -(da * cs.y));
-          }
-        }
+          load<XT, C, V, G, MODE>(reinterpret_cast<const XT*>(a.x) + starts[t].x +
+                                      (head0 + hd) * a.D, j, pieces, true, x);
+        if (a.n_axes) turn_head<C, V, G, MODE, true>(turn + t * turns, with, room, j, pieces, d);
         if (a.rms) {
           float s2 = 0.0f, st = 0.0f;
 #pragma unroll
           for (int c = 0; c < C; ++c) {
-            const int p0 = min(at.j + c * G, at.pieces - 1) * P;
+            const int at = min(j + c * G, pieces - 1) * V;
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float xv = x.p[c][i][e];
-                s2 = __builtin_fmaf(xv, xv, s2);
-                st = __builtin_fmaf(d.p[c][i][e] * gamma[part][2 * (p0 + i) + e], xv, st);
-              }
+            for (int i = 0; i < V; ++i) {
+              s2 = __builtin_fmaf(x.v[c][i], x.v[c][i], s2);
+              st = __builtin_fmaf(d.v[c][i] * gamma[part][at + i], x.v[c][i], st);
+            }
           }
           s2 = head_sum<G>(s2);
           st = head_sum<G>(st);
@@ -346,19 +355,18 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
           const float f = rstd * rstd * (st / (float)a.D);
 #pragma unroll
           for (int c = 0; c < C; ++c) {
-            const int p0 = min(at.j + c * G, at.pieces - 1) * P;
+            const int at = min(j + c * G, pieces - 1) * V;
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float dn = d.p[c][i][e], xv = x.p[c][i][e];
-                dg.p[c][i][e] = __builtin_fmaf(dn, xv * rstd, dg.p[c][i][e]);
-                d.p[c][i][e] = rstd * __builtin_fmaf(dn, gamma[part][2 * (p0 + i) + e], -(xv * f));
-              }
+            for (int i = 0; i < V; ++i) {
+              const float dn = d.v[c][i], xv = x.v[c][i];
+              dg.v[c][i] = __builtin_fmaf(dn, xv * rstd, dg.v[c][i]);
+              d.v[c][i] = rstd * __builtin_fmaf(dn, gamma[part][at + i], -(xv * f));
+            }
           }
         }
       }
-      store<XT, C, P, G, MODE>(reinterpret_cast<XT*>(a.dx) + starts[t].dx + (head0 + hd) * a.D, at, d);
+      store<XT, C, V, G, MODE>(reinterpret_cast<XT*>(a.dx) + starts[t].dx + (head0 + hd) * a.D, j,
+                               pieces, d);
     }
   }
   if (!a.part || part == 2) return;
@@ -366,23 +374,20 @@ __global__ __launch_bounds__(kThreads) void k_heads_grad(HeadsArgs a) {
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = dg.p[c][i][e];
-        if constexpr (G <= 4) v += __shfl_xor(v, 4);
-        if constexpr (G <= 8) v += __shfl_xor(v, 8);
-        v += __shfl_xor(v, 16);
-        v += __shfl_xor(v, 32);
-        if ((tid & 63) < G && at.j + c * G < at.pieces)
-          sums[tid >> 6][2 * ((at.j + c * G) * P + i) + e] = v;
-      }
+    for (int i = 0; i < V; ++i) {
+      float v = dg.v[c][i];
+      if constexpr (G <= 4) v += __shfl_xor(v, 4);
+      if constexpr (G <= 8) v += __shfl_xor(v, 8);
+      v += __shfl_xor(v, 16);
+      v += __shfl_xor(v, 32);
+      if ((tid & 63) < G && j + c * G < pieces) sums[tid >> 6][(j + c * G) * V + i] = v;
+    }
   __syncthreads();
   for (int i = tid; i < a.D; i += kThreads) {
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kThreads / 64; ++w) v += sums[w][i];
-    a.part[((int64_t)part * gridDim.x + blockIdx.x) * a.D + i] = v;  // in pair order
+    a.part[((int64_t)part * gridDim.x + blockIdx.x) * a.D + i] = v;
   }
 }
 
@@ -413,33 +418,18 @@ __global__ __launch_bounds__(1024) void k_heads_gamma(HeadsArgs a) {
   for (int s = 0; s < 8; ++s) sum += box[8 * strip + s][col];
   sum += __shfl_xor(sum, 32);
   if (strip != 0 || i >= a.D) return;
-  int c1, c2;
-  pair_channels(a, i / 2, c1, c2);
-  const int c = i % 2 ? c2 : c1;
   if (a.w_bf16)
-    reinterpret_cast<bf16*>(a.dgamma[part])[c] = (bf16)(float)sum;
+    reinterpret_cast<bf16*>(a.dgamma[part])[i] = (bf16)(float)sum;
   else
-    reinterpret_cast<float*>(a.dgamma[part])[c] = (float)sum;
+    reinterpret_cast<float*>(a.dgamma[part])[i] = (float)sum;
 }
 
 // ------------------------------------------------------------------ launch ----
 
-template <typename XT>
-int mode_of(const HeadsArgs& a) {
-  if (!a.vec) return kScattered;
-  if (!a.halves) return kAdjacent;
-  int rest = a.D / 2;
-  for (int i = 0; i < a.n_axes; ++i) {
-    if (a.half[i] % Geo<XT>::P) return kScattered;
-    rest -= a.half[i];
-  }
-  return rest % Geo<XT>::P ? kScattered : kHalves;
-}
-
 template <typename XT, typename YT, int G, int C>
 hipError_t run(const HeadsArgs& a, bool grad, dim3 grid, hipStream_t s) {
-  const size_t lds = (size_t)a.tokens * (a.D / 2) * sizeof(float2);
-  const int mode = mode_of<XT>(a);
+  const int mode = !a.vec ? kByElement : a.halves && a.n_axes ? kApart : kAdjacent;
+  const size_t lds = (size_t)a.tokens * (mode == kAdjacent ? a.D / 2 : a.D) * sizeof(float2);
 #define QL_HEADS_MODE(M)                                      \
   if (mode == M) {                                            \
     if (grad)                                                 \
@@ -448,8 +438,8 @@ hipError_t run(const HeadsArgs& a, bool grad, dim3 grid, hipStream_t s) {
       k_heads<XT, YT, G, C, M><<<grid, kThreads, lds, s>>>(a);   \
   }
   QL_HEADS_MODE(kAdjacent)
-  QL_HEADS_MODE(kHalves)
-  QL_HEADS_MODE(kScattered)
+  QL_HEADS_MODE(kApart)
+  QL_HEADS_MODE(kByElement)
 #undef QL_HEADS_MODE
   return hipGetLastError();
 }
