@@ -84,17 +84,18 @@ __device__ __forceinline__ frag operand(const v16f& c, int s) {
 
 // A tile's rows in LDS are read both ways: whole rows by neighbouring lanes, 16 bytes each
 // (sixteen lanes meet all 64 banks once), and, for bf16, four rows by 32 channels
-// transposed. Both are free of conflicts if the 16-byte piece c of row r lies at
-// c ^ turn(r): rows of 256 bytes need all of 0 .. 15 in sixteen rows and four unlike upper
-// halves in four; rows of 128 or 384, which alternate between the halves of the banks,
-// the same of 0 .. 7 in every other row. (Rows padded to an odd number of pieces cost the
-// gradients 45 % of their LDS time.) fp32 rows, whose columns are read by words, are an
-// odd number of pieces long.
+// transposed. Both are free of conflicts, without padding, if the 16-byte piece c of row r
+// lies at c ^ turn(r). Rows are kOB times 64 bytes: an odd number of them spreads four rows
+// over all banks, and turn() needs four values for the rows four apart; rows of 128 bytes
+// alternate between two halves, and need eight; rows of 256 all start alike, and need
+// sixteen. (Rows padded to an odd number of pieces cost the gradients 45 % of their LDS
+// time.) fp32 rows, whose columns are read by words, are an odd number of pieces long.
 constexpr bool kTurned = sizeof(T) == 2;
-constexpr int kPitch = kTurned ? (kOB * 32 * 2 + 127) / 128 * 64 : ((kOB * 32 / kChunk) | 1) * kChunk;
-constexpr int kTurn = kPitch == 128 ? 128 : 64;  // elements that trade places
+constexpr int kPitch = kTurned ? kOB * 32 : ((kOB * 32 / kChunk) | 1) * kChunk;
+static_assert(kOB <= 5, "turn() for longer rows");
+constexpr int kTurn = kOB == 4 ? 128 : kOB == 2 ? 64 : 32;  // elements that trade places
 __device__ __forceinline__ int turn(int r) {
-  return ((kTurn == 128 ? r & 3 : (r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  return (kOB == 4 ? (r & 3) << 2 : kOB == 2 ? (r & 2) << 1 : 0) | ((r >> 2) & 3);
 }
 __device__ __forceinline__ int place(int r, int c) {
   return r * kPitch + (kTurned ? (c ^ turn(r)) : c) * kChunk;
@@ -200,6 +201,39 @@ __device__ __forceinline__ frag load_frag(const T* row, int c, int D) {
   }
   return f;
 }
+
+// The rows of a wave as operands, by way of LDS: neighbouring lanes load neighbouring
+// pieces of a row, which the load path takes four at a time, where the operand's own order,
+// a row a lane, goes piece by piece (two thirds of k_attn_dq's time for q, dO and O). `room`
+// is the wave's own, 32 kPitch elements.
+struct Rows {
+  static constexpr int N = (32 * kCPR + 63) / 64;
+  v4u r[N];
+  template <typename F>
+  __device__ __forceinline__ void fetch(int lane, int D, F address) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = lane + 64 * i;
+      r[i] = *reinterpret_cast<const v4u*>(address(min(at / kCPR, 31)) +
+                                           min(at % kCPR, D / kChunk - 1) * kChunk);
+    }
+  }
+  __device__ __forceinline__ void operands(T* room, const Spots& s, int lane, int D,
+                                           frag (&out)[DC]) const {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = lane + 64 * i;
+      v4u x = r[i];
+      if (D < kD && at % kCPR * kChunk >= D) x = v4u{0, 0, 0, 0};
+      if (32 * kCPR % 64 == 0 || at < 32 * kCPR)
+        *reinterpret_cast<v4u*>(room + place(at / kCPR, at % kCPR)) = x;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int kb = 0; kb < DC; ++kb) out[kb] = row_frag(room, s, kb);
+  }
+};
 
 // A row of a result, times f, to memory. A lane has four channels in eight; in bf16 the
 // halves of the wave trade two such pieces, so that each stores eight in one piece.
@@ -430,9 +464,12 @@ __device__ __forceinline__ void finish(const AttnArgs& a, int b, int hk, int row
 #if QL_AT_SHORT
 __global__ __launch_bounds__(kThreads, FW) void k_attn_short(AttnArgs a) {
   constexpr int KT = 64, kTile = KT * 2 * kPitch;
-  __shared__ __attribute__((aligned(16))) T lds[2 * kTile];
+  constexpr bool kRoom = (2 * kTile + 128 * kPitch) * sizeof(T) <= 81920;  // for two workgroups
+  __shared__ __attribute__((aligned(16))) T lds[2 * kTile + (kRoom ? 128 * kPitch : 0)];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r32 = lane & 31, h = lane >> 5;
+  Spots spots;
+  spots.find(lane);
   const int groups = (a.row_tiles + a.per_group - 1) / a.per_group;
   int id = by_xcd(a, blockIdx.x, groups);
   const int rt0 = id % groups * a.per_group, rt1 = min(rt0 + a.per_group, a.row_tiles);
@@ -441,11 +478,17 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_short(AttnArgs a) {
   const int len = key_len(a, b), tiles = (len + KT - 1) / KT;
   const T* const kp = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
   const T* const vp = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
-  frag next[DC];
+  frag next[kRoom ? 1 : DC];
+  Rows rows;
   const auto ask = [&](int rt) {
-    const T* p = row_of(a, a.q, b, hk, min(rt * 128 + wave * 32 + r32, a.R - 1));
+    const int r0 = rt * 128 + wave * 32;
+    if constexpr (kRoom) {
+      rows.fetch(lane, a.D, [&](int i) { return row_of(a, a.q, b, hk, min(r0 + i, a.R - 1)); });
+    } else {
+      const T* p = row_of(a, a.q, b, hk, min(r0 + r32, a.R - 1));
 #pragma unroll
-    for (int kb = 0; kb < DC; ++kb) next[kb] = load_frag(p, 16 * kb + 8 * h, a.D);
+      for (int kb = 0; kb < DC; ++kb) next[kb] = load_frag(p, 16 * kb + 8 * h, a.D);
+    }
   };
   ask(rt0);
   KeyBits<2> bits[2];
@@ -463,13 +506,15 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_short(AttnArgs a) {
       vs.template put<false>(lds + t * kTile + KT * kPitch, tid, a.D, keep);
     }
   }
-  Spots spots;
-  spots.find(lane);
   __syncthreads();
   for (int rt = rt0; rt < rt1; ++rt) {
     frag q[DC];
+    if constexpr (kRoom) {
+      rows.operands(lds + 2 * kTile + wave * 32 * kPitch, spots, lane, a.D, q);
+    } else {
 #pragma unroll
-    for (int kb = 0; kb < DC; ++kb) q[kb] = next[kb];
+      for (int kb = 0; kb < DC; ++kb) q[kb] = next[kb];
+    }
     if (rt + 1 < rt1) ask(rt + 1);
     v16f o[kOB];
 #pragma unroll
@@ -522,13 +567,15 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
   const int len = key_len(a, b);
   const int tiles = (len + KT - 1) / KT, per = (tiles + a.splits - 1) / a.splits;
   const int t0 = sp * per, t1 = min(tiles, t0 + per);
-  const int row = rt * P::kRows + wq * 32 + r32, rr = min(row, a.R - 1);
-
+  const int row0 = rt * P::kRows + wq * 32, row = row0 + r32;
+  Spots spots;
+  spots.find(lane);
   frag q[DC];
   {
-    const T* p = row_of(a, a.q, b, hk, rr);
-#pragma unroll
-    for (int kb = 0; kb < DC; ++kb) q[kb] = load_frag(p, 16 * kb + 8 * h, a.D);
+    Rows rows;
+    rows.fetch(lane, a.D, [&](int i) { return row_of(a, a.q, b, hk, min(row0 + i, a.R - 1)); });
+    rows.operands(lds + (P::NB - 1) * P::kTile + wave * 32 * kPitch, spots, lane, a.D, q);
+    if (P::NB == 1) __syncthreads();
   }
   const T* const kp = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
   const T* const vp = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
@@ -540,8 +587,6 @@ __global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
   Stage<KT> ks, vs;
   ks.find(tid, a.D, 1, a.k.row, 0);
   vs.find(tid, a.D, 1, a.v.row, 0);
-  Spots spots;
-  spots.find(lane);
   KeyBits<W> bits, next;
   const auto fetch = [&](int t) {
     if (a.near_keys && (t + 1) * KT <= a.Lk) {
@@ -694,25 +739,30 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
   id /= a.row_tiles;
   const int hk = id % a.Hk, b = id / a.Hk;
   const int len = key_len(a, b), tiles = (len + KT - 1) / KT;
-  const int row = rt * 128 + wave * 32 + r32, rr = min(row, a.R - 1);
-  const int64_t at = stat_at(a, b, hk, rr);
+  const int row0 = rt * 128 + wave * 32, row = row0 + r32;
+  const int64_t at = stat_at(a, b, hk, min(row, a.R - 1));
+  Spots spots;
+  spots.find(lane);
 
   frag q[DC], g[DC];
   float delta = 0.0f;
   {
-    const T* pq = row_of(a, a.q, b, hk, rr);
-    const T* pg = row_of(a, a.dout, b, hk, rr);
-    const T* po = row_of(a, a.o, b, hk, rr);
+    T* const room = lds + (NB - 1) * kTile + wave * 32 * kPitch;
+    Rows rq, rg, ro;
+    rq.fetch(lane, a.D, [&](int i) { return row_of(a, a.q, b, hk, min(row0 + i, a.R - 1)); });
+    rg.fetch(lane, a.D, [&](int i) { return row_of(a, a.dout, b, hk, min(row0 + i, a.R - 1)); });
+    ro.fetch(lane, a.D, [&](int i) { return row_of(a, a.o, b, hk, min(row0 + i, a.R - 1)); });
+    frag o[DC];
+    rq.operands(room, spots, lane, a.D, q);
+    rg.operands(room, spots, lane, a.D, g);
+    ro.operands(room, spots, lane, a.D, o);
 #pragma unroll
-    for (int kb = 0; kb < DC; ++kb) {
-      q[kb] = load_frag(pq, 16 * kb + 8 * h, a.D);
-      g[kb] = load_frag(pg, 16 * kb + 8 * h, a.D);
-      const frag o = load_frag(po, 16 * kb + 8 * h, a.D);
+    for (int kb = 0; kb < DC; ++kb)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) delta = __builtin_fmaf((float)g[kb][e], (float)o[e], delta);
-    }
+      for (int e = 0; e < 8; ++e) delta = __builtin_fmaf((float)g[kb][e], (float)o[kb][e], delta);
     delta += other_half(delta);
     if (h == 0 && row < a.R) a.delta[at] = delta;
+    if (NB == 1) __syncthreads();
   }
   float lse2 = a.lse[at] * kLog2e;
   if (lse2 == -INFINITY) lse2 = INFINITY;  // no key counts: P = 0
@@ -725,8 +775,6 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
   Stage<KT> ks, vs;
   ks.find(tid, a.D, 1, a.k.row, 0);
   vs.find(tid, a.D, 1, a.v.row, 0);
-  Spots spots;
-  spots.find(lane);
   KeyBits<W> bits, next;
   const auto fetch = [&](int t) {
     if (a.near_keys && (t + 1) * KT <= a.Lk) {
@@ -819,7 +867,7 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
   id /= a.key_tiles;
   const int hk = id % a.Hk, b = id / a.Hk;
   const int len = key_len(a, b);
-  const int key = kt * 128 + wave * 32 + r32, kk = min(key, a.Lk - 1);
+  const int key = kt * 128 + wave * 32 + r32;
   bool counts = key < len;
   if (a.mask && counts) counts = a.mask[b * a.mask_batch + key] != 0;
   const bool busy = __any(counts);  // else this wave only helps to fill the tiles
@@ -830,16 +878,20 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
   spots.find(lane);
   frag k[DC], v[VL ? 1 : DC];
   {
-    const T* pk = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + kk * a.k.row + hk * a.k.head;
-    const T* pv = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + kk * a.v.row + hk * a.v.head;
+    const int key0 = kt * 128 + wave * 32;
+    T* const room = VL ? my_v : lds + wave * (NB * kTile / 4);
+    const T* const kp = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
+    const T* const vp = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
+    Rows rk, rv;
+    rk.fetch(lane, a.D, [&](int i) { return kp + (int64_t)min(key0 + i, a.Lk - 1) * a.k.row; });
+    rv.fetch(lane, a.D, [&](int i) { return vp + (int64_t)min(key0 + i, a.Lk - 1) * a.v.row; });
+    rk.operands(room, spots, lane, a.D, k);
+    frag x[DC];
+    rv.operands(room, spots, lane, a.D, x);  // my_v: where V stays
+    if constexpr (!VL) {
 #pragma unroll
-    for (int kb = 0; kb < DC; ++kb) {
-      k[kb] = load_frag(pk, 16 * kb + 8 * h, a.D);
-      const frag x = load_frag(pv, 16 * kb + 8 * h, a.D);
-      if constexpr (VL)
-        *reinterpret_cast<frag*>(my_v + further(spots.row, 16 * kb)) = x;
-      else
-        v[kb] = x;
+      for (int kb = 0; kb < DC; ++kb) v[VL ? 0 : kb] = x[kb];
+      __syncthreads();
     }
   }
   v16f dk[kOB], dv[kOB];
