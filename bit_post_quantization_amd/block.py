@@ -111,7 +111,8 @@ class GroupLinear4:
 
     From weights W [N, K] (f32 or bf16) by the groups' largest values (scales of
     ``s_dtype``), or from codes that are there (:meth:`from_codes`). The packed weights are
-    made once, on the current stream."""
+    made once, on the current stream, which the constructor waits for; keep the layer
+    while a captured graph with its calls is replayed."""
 
     def __init__(self, W, group: int = 128, bias=None, act: str = "none", s_dtype: str = "f32",
                  stream=None):
@@ -151,6 +152,7 @@ class GroupLinear4:
         self.desc.packed = self.packed.data_ptr()
         self._made_on = _stream(_device())
         fill(self._made_on)
+        torch.cuda.current_stream().synchronize()  # other streams may use the layer at once
         self._sizes = {}  # descriptor and workspace bytes by type and rows of a call
 
     def _ready(self, dev: int) -> int:
@@ -222,7 +224,8 @@ class HeadNormRope:
     order; the rest do not turn. Pair i of an axis of d channels turns by position *
     theta ** (-2 i / d), or by ``freqs`` (a sequence, radians for one unit of position,
     all axes' pairs in order); its members are ``pairs`` "adjacent" (2 i, 2 i + 1) or
-    "halves" (i, d / 2 + i). Outputs are of ``y_dtype``."""
+    "halves" (i, d / 2 + i). Outputs are of ``y_dtype``. Keep the layer while a captured
+    graph with its calls is replayed (it holds the table of frequencies)."""
 
     def __init__(self, heads: Sequence[int], dim: int, gamma_q=None, gamma_k=None,
                  norm: str = "rms", axes: Sequence[int] = (), pairs: str = "adjacent",

@@ -374,16 +374,14 @@ __device__ __forceinline__ bool bit_of(const KeyBits<W>& k, int i) {
   return (x >> (i & 31)) & 1;
 }
 
-// Waves a SIMD that the registers are to allow.
-#ifndef FW
-#define FW (sizeof(T) == 2 ? 2 : 1)
-#endif
-#ifndef QW
-#define QW (sizeof(T) == 2 ? 2 : 1)
-#endif
-#ifndef KW
-#define KW (sizeof(T) == 2 && DC <= 8 ? 2 : 1)
-#endif
+// Waves a SIMD that the registers are to allow. Two wherever bf16 fits (forward at 128
+// channels: 709 us with one, 390 with two), but for the longest heads where few rows share
+// them among the keys' loads and in the gradients, which would spill (8 rows of 160 channels
+// over 4096 keys: 105 us with two, 72 with one). fp32 takes all there are.
+constexpr bool kPairs = sizeof(T) == 2;
+template <int WK> constexpr int kForwardWaves = kPairs && (WK == 1 || DC <= 8) ? 2 : 1;
+constexpr int kDqWaves = kPairs && DC <= 8 ? 2 : 1, kDkvWaves = kDqWaves;
+
 // ----------------------------------------------------------------- forward ----
 
 // SUB pieces of 32 keys for a wave's rows: scores, the running maximum m and sum l, and
@@ -462,7 +460,7 @@ __device__ __forceinline__ void finish(const AttnArgs& a, int b, int hk, int row
 // tiles of rows, its waves on their own after the one barrier, the next rows' queries under
 // way.
 #if QL_AT_SHORT
-__global__ __launch_bounds__(kThreads, FW) void k_attn_short(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, kForwardWaves<1>) void k_attn_short(AttnArgs a) {
   constexpr int KT = 64, kTile = KT * 2 * kPitch;
   constexpr bool kRoom = (2 * kTile + 128 * kPitch) * sizeof(T) <= 81920;  // for two workgroups
   __shared__ __attribute__((aligned(16))) T lds[2 * kTile + (kRoom ? 128 * kPitch : 0)];
@@ -551,7 +549,7 @@ struct Fwd {
 };
 
 template <int WK>
-__global__ __launch_bounds__(kThreads, FW) void k_attn_forward(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, kForwardWaves<WK>) void k_attn_forward(AttnArgs a) {
   typedef Fwd<WK> P;
   constexpr int KT = P::KT, SUB = P::SUB, W = KT / 32;
   __shared__ __attribute__((aligned(16))) char smem[P::kLds];
@@ -726,10 +724,11 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
 
 // ---------------------------------------------------------------- backward ----
 
-constexpr int kBackRows = 32;  // rows or keys of a tile in LDS
+constexpr int kBackRows = 32;  // rows of a tile in LDS of k_attn_dkv
+constexpr bool kKeepV = sizeof(T) == 2 && DC >= 8;
 
 // dQ, and delta for k_attn_dkv. Keys that do not count are zero in LDS and have P = 0.
-__global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, kDqWaves) void k_attn_dq(AttnArgs a) {
   constexpr int KT = 64, W = 2, kTile = KT * 2 * kPitch;
   constexpr int NB = 2 * kTile * (int)sizeof(T) <= 81920 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) T lds[NB * kTile];
@@ -847,19 +846,16 @@ __global__ __launch_bounds__(kThreads, QW) void k_attn_dq(AttnArgs a) {
   store_row(p, dq, a.scale, a.D, h);
 }
 
-#ifndef VL
-#define VL (sizeof(T) == 2 && DC >= 8)
-#endif
 // dK and dV of 128 keys from a range of the rows; a lane has one key. With long heads V
 // stays in LDS, so that the registers leave room for two waves a SIMD.
-__global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, kDkvWaves) void k_attn_dkv(AttnArgs a) {
   constexpr int RT = kBackRows, kTile = RT * 2 * kPitch;
   constexpr int NB = 2;
   __shared__ __attribute__((aligned(16))) T lds[NB * kTile];
   __shared__ __attribute__((aligned(16))) float stats[NB][2][RT];
-  __shared__ __attribute__((aligned(16))) T v_rows[VL ? 128 * kPitch : 8];
+  __shared__ __attribute__((aligned(16))) T v_rows[kKeepV ? 128 * kPitch : 8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, h = lane >> 5;
-  T* const my_v = v_rows + (VL ? wave * 32 * kPitch : 0);
+  T* const my_v = v_rows + (kKeepV ? wave * 32 * kPitch : 0);
   int id = by_xcd(a, blockIdx.x, a.key_tiles * a.splits);
   const int sp = id % a.splits;
   id /= a.splits;
@@ -876,10 +872,10 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
 
   Spots spots;
   spots.find(lane);
-  frag k[DC], v[VL ? 1 : DC];
+  frag k[DC], v[kKeepV ? 1 : DC];
   {
     const int key0 = kt * 128 + wave * 32;
-    T* const room = VL ? my_v : lds + wave * (NB * kTile / 4);
+    T* const room = kKeepV ? my_v : lds + wave * (NB * kTile / 4);
     const T* const kp = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
     const T* const vp = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
     Rows rk, rv;
@@ -888,9 +884,9 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
     rk.operands(room, spots, lane, a.D, k);
     frag x[DC];
     rv.operands(room, spots, lane, a.D, x);  // my_v: where V stays
-    if constexpr (!VL) {
+    if constexpr (!kKeepV) {
 #pragma unroll
-      for (int kb = 0; kb < DC; ++kb) v[VL ? 0 : kb] = x[kb];
+      for (int kb = 0; kb < DC; ++kb) v[kKeepV ? 0 : kb] = x[kb];
       __syncthreads();
     }
   }
@@ -950,7 +946,7 @@ __global__ __launch_bounds__(kThreads, KW) void k_attn_dkv(AttnArgs a) {
 #pragma unroll
     for (int kb = 0; kb < DC; ++kb) {
       s = mma(row_frag(qt, spots, kb), k[kb], s);
-      dp = mma(row_frag(gt, spots, kb), VL ? row_frag(my_v, spots, kb) : v[VL ? 0 : kb], dp);
+      dp = mma(row_frag(gt, spots, kb), kKeepV ? row_frag(my_v, spots, kb) : v[kKeepV ? 0 : kb], dp);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {

@@ -644,6 +644,7 @@ ql_status qlinear_attention_workspace(const ql_attn* d, int32_t grad, int64_t* b
  * rounded to bf16 before they meet v, its statistics stay fp32.
  *   lse : NULL, or DEVICE fp32 out [batch, heads, q_len]: log of the sum of
  *         exp(scale q k), which the gradient takes.
+ * out and lse overlap nothing else.
  */
 ql_status qlinear_attention(const ql_attn* d, const ql_heads_view* q, const ql_heads_view* k,
                             const ql_heads_view* v, const ql_heads_view* out, float* lse,
@@ -652,7 +653,9 @@ ql_status qlinear_attention(const ql_attn* d, const ql_heads_view* q, const ql_h
 /*
  * Gradients for dout: dq, dk, dv (dtype; a key head's are summed over the queries' heads
  * that share it; zero for keys that do not count), from out and lse as the forward call
- * gave them. All elements of the three are written.
+ * gave them for the same k_lens and k_mask. All elements of the three are written; they
+ * overlap nothing else. With bf16 tensors the weights and their gradients are rounded to
+ * bf16 before they meet the other operand of a product.
  */
 ql_status qlinear_attention_grad(const ql_attn* d, const ql_heads_view* dout,
                                  const ql_heads_view* q, const ql_heads_view* k,

@@ -53,7 +53,8 @@ def test_rows4_calls():
     assert L.qlinear_rows4_bytes(U, ref(n)) == ARG
     assert L.qlinear_rows4_bytes(ref(d), U) == ARG
     assert L.qlinear_rows4_bytes(ref(d), ref(n)) == OK
-    assert n.value == 7 * 2 * 256 + 7 * 2 * 64  # 7 tiles of 16 channels, 2 steps, 2 groups
+    # 7 tiles of 16 channels by one unit of 128 inputs, 4 scales of 32 a channel
+    assert n.value == 7 * 1024 + 7 * 16 * 4 * 4
     assert L.qlinear_rows4_workspace(ref(d), -1, ref(n)) == ARG
     assert L.qlinear_rows4_workspace(ref(d), (1 << 20) + 1, ref(n)) == UNSUP
     assert L.qlinear_rows4_workspace(ref(d), 4, U) == ARG
