@@ -846,6 +846,50 @@ __global__ __launch_bounds__(kThreads, kDqWaves) void k_attn_dq(AttnArgs a) {
   store_row(p, dq, a.scale, a.D, h);
 }
 
+// Where tiles of keys are shared out (a.splits > 1, at most 256 sequences), the workgroups
+// of a key head, B key_tiles splits of them, are dealt to the tiles that have a key
+// that counts, all sequences together and all tiles alike: sequences differ in length, and
+// a tile's rows should not wait while others' workgroups have nothing to do.
+struct Deal {
+  int share;          // workgroups of a tile; 0: there is no such tile
+  int b, tile, turn;  // workgroup w's: sequence, tile of its keys, which of the sharers
+};
+constexpr int kMostShared = 256;
+__device__ __forceinline__ int used_tiles(const AttnArgs& a, int b) {
+  return b < a.B ? (key_len(a, b) + 127) / 128 : 0;
+}
+__device__ __forceinline__ Deal deal(const AttnArgs& a, int w, int lane) {
+  constexpr int N = kMostShared / 64;
+  int used[N], upto[N], total = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    used[i] = used_tiles(a, 64 * i + lane);
+    int n = used[i];
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(n, d);
+      if (lane >= d) n += o;
+    }
+    upto[i] = total + n;
+    total += __builtin_amdgcn_readlane(n, 63);
+  }
+  Deal out = {total ? a.B * a.key_tiles * a.splits / total : 0, 0, 0, 0};
+  if (!out.share) return out;
+  const int t = w / out.share;
+  if (t >= total) return Deal{0, 0, 0, 0};  // what does not divide evenly
+  out.turn = w - t * out.share;
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) {
+    const uint64_t past = __ballot(upto[i] > t);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      out.b = 64 * i + l;
+      out.tile = t - (__builtin_amdgcn_readlane(upto[i], l) - __builtin_amdgcn_readlane(used[i], l));
+    }
+  }
+  return out;
+}
+
 // dK and dV of 128 keys from a range of the rows; a lane has one key. With long heads V
 // stays in LDS, so that the registers leave room for two waves a SIMD.
 __global__ __launch_bounds__(kThreads, kDkvWaves) void k_attn_dkv(AttnArgs a) {
@@ -856,18 +900,31 @@ __global__ __launch_bounds__(kThreads, kDkvWaves) void k_attn_dkv(AttnArgs a) {
   __shared__ __attribute__((aligned(16))) T v_rows[kKeepV ? 128 * kPitch : 8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, h = lane >> 5;
   T* const my_v = v_rows + (kKeepV ? wave * 32 * kPitch : 0);
-  int id = by_xcd(a, blockIdx.x, a.key_tiles * a.splits);
-  const int sp = id % a.splits;
-  id /= a.splits;
-  const int kt = id % a.key_tiles;
-  id /= a.key_tiles;
-  const int hk = id % a.Hk, b = id / a.Hk;
-  const int len = key_len(a, b);
-  const int key = kt * 128 + wave * 32 + r32;
+  int b, hk, kt, sp, share, place_of;
+  if (a.splits == 1) {
+    place_of = by_xcd(a, blockIdx.x, a.key_tiles);
+    kt = place_of % a.key_tiles;
+    hk = place_of / a.key_tiles % a.Hk;
+    b = place_of / a.key_tiles / a.Hk;
+    sp = 0;
+    share = 1;
+  } else {  // heads in runs, so that those whose number 8 divides keep to one L2
+    const int all = a.B * a.key_tiles * a.splits;
+    place_of = a.Hk % 8 == 0 ? (blockIdx.x / 8 / all * 8 + blockIdx.x % 8) * all + blockIdx.x / 8 % all
+                             : blockIdx.x;
+    hk = place_of / all;
+    const Deal d = deal(a, place_of % all, lane);
+    if (!d.share) return;
+    b = d.b;
+    kt = d.tile;
+    sp = d.turn;
+    share = d.share;
+  }
+  const int len = key_len(a, b), key = kt * 128 + wave * 32 + r32;
   bool counts = key < len;
   if (a.mask && counts) counts = a.mask[b * a.mask_batch + key] != 0;
   const bool busy = __any(counts);  // else this wave only helps to fill the tiles
-  const int tiles = (a.R + RT - 1) / RT, per = (tiles + a.splits - 1) / a.splits;
+  const int tiles = (a.R + RT - 1) / RT, per = (tiles + share - 1) / share;
   const int t0 = sp * per, t1 = kt * 128 < len ? min(tiles, t0 + per) : 0;
 
   Spots spots;
@@ -978,10 +1035,9 @@ __global__ __launch_bounds__(kThreads, kDkvWaves) void k_attn_dkv(AttnArgs a) {
     for (int i = 0; i < kOB; ++i) dk[i] = dv[i] = zero16();
   }
   if (a.splits > 1) {
-    const int64_t n = (int64_t)a.B * a.Lk * a.Hk * a.D;
-    float* p = a.part + sp * 2 * n + (((int64_t)b * a.Lk + key) * a.Hk + hk) * a.D;
+    float* p = a.part + ((int64_t)place_of * 256 + key % 128) * a.D;
     store_row(p, dk, a.scale, a.D, h);
-    store_row(p + n, dv, 1.0f, a.D, h);
+    store_row(p + 128 * a.D, dv, 1.0f, a.D, h);
     return;
   }
   T* pk = reinterpret_cast<T*>(a.dk.p) + b * a.dk.batch + key * a.dk.row + hk * a.dk.head;
@@ -992,25 +1048,47 @@ __global__ __launch_bounds__(kThreads, kDkvWaves) void k_attn_dkv(AttnArgs a) {
 
 // dK (blockIdx.y 0) and dV (1): the sum of the row ranges' parts, four channels a thread.
 __global__ __launch_bounds__(kThreads) void k_attn_dkv_sum(AttnArgs a) {
+  __shared__ int before[kMostShared + 1];  // tiles with keys that count of the sequences before
+  const int lane = threadIdx.x & 63;
+  if (threadIdx.x < 64) {
+    int base = 0;
+#pragma unroll
+    for (int i = 0; i < kMostShared / 64; ++i) {
+      int n = used_tiles(a, 64 * i + lane);
+      const int mine = n;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(n, d);
+        if (lane >= d) n += o;
+      }
+      before[64 * i + lane] = base + n - mine;
+      base += __builtin_amdgcn_readlane(n, 63);
+    }
+    if (lane == 0) before[kMostShared] = base;
+  }
+  __syncthreads();
   const int64_t n = (int64_t)a.B * a.Lk * a.Hk * a.D;
   const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
   if (e >= n) return;
-  const float* p = a.part + blockIdx.y * n + e;
   const ql_heads_view& t = blockIdx.y ? a.dv : a.dk;
   const int64_t row = e / a.D, lh = row / a.Hk;
-  const int b = (int)(lh / a.Lk), key = (int)(lh - (int64_t)b * a.Lk);
-  bool counts = key < key_len(a, b);
+  const int b = (int)(lh / a.Lk), key = (int)(lh - (int64_t)b * a.Lk), len = key_len(a, b);
+  const int all = a.B * a.key_tiles * a.splits, total = before[kMostShared];
+  const int share = total ? all / total : 0;
+  const int64_t first = row % a.Hk * all + (int64_t)(before[b] + key / 128) * share;
+  const float* p = a.part + (first * 256 + blockIdx.y * 128 + key % 128) * a.D + e % a.D;
+  bool counts = key < len;
   if (a.mask && counts) counts = a.mask[b * a.mask_batch + key] != 0;
   v4f sum = {0, 0, 0, 0};
   if (counts) {
-    for (int s0 = 0; s0 < a.splits; s0 += 8) {
+    for (int s0 = 0; s0 < share; s0 += 8) {
       v4f x[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        x[j] = *reinterpret_cast<const v4f*>(p + min(s0 + j, a.splits - 1) * 2 * n);
+        x[j] = *reinterpret_cast<const v4f*>(p + min(s0 + j, share - 1) * 256 * (int64_t)a.D);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (s0 + j < a.splits) sum += x[j];
+        if (s0 + j < share) sum += x[j];
     }
   }
   T* to = reinterpret_cast<T*>(t.p) + lh / a.Lk * t.batch + lh % a.Lk * t.row + row % a.Hk * t.head +

@@ -94,7 +94,7 @@ struct AttnArgs {
   float scale, scale2;            // scale2 = scale * log2(e)
   int row_tiles, key_tiles, per_group;
   int splits;       // of the keys (forward), of the rows (dk and dv)
-  float* part;      // forward [splits][B, H, Lq][D]; dk, dv: [splits][2][B, Lk, Hk][D]
+  float* part;      // forward [splits][B, H, Lq][D]; dk, dv: [workgroup][2][128 keys][D]
   float* part_lse;  // [splits][B, H, Lq], base 2
   bool bf16;
   bool near_keys;   // 128 rows of k and of v lie within 32-bit offsets

@@ -358,7 +358,7 @@ AttnPlan attn_plan(const ql_attn& d) {
   p.k_splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   p.grad_bytes = up16(n * 4);
   if (p.k_splits > 1)
-    p.grad_bytes += up16((int64_t)p.k_splits * 2 * d.batch * d.k_len * d.kv_heads * d.dim * 4);
+    p.grad_bytes += up16(kbase * p.k_splits * 256 * d.dim * 4);
   return p;
 }
 

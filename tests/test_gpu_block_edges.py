@@ -53,6 +53,9 @@ CUTS = [
     (1, 2049, 100, 2, 1, 96, "f32", "both"),
     (600, 1, 1, 1, 1, 32, "bf16", "none"),
     (2, 128, 512, 16, 16, 64, "bf16", "none"),
+    (3, 1100, 300, 8, 8, 64, "bf16", "lens"),     # tiles of unlike sequences shared out alike
+    (5, 1300, 130, 3, 3, 40, "f32", "lens"),
+    (90, 300, 20, 2, 2, 32, "bf16", "both"),
 ]
 
 
