@@ -16,19 +16,20 @@
 // score goes through LDS, nothing is exchanged between waves until the end.
 //
 // The softmax runs in base 2 (scale2 = scale log2 e), one pass, with the running
-// maximum and sum in fp32; O is rescaled only where a maximum of the wave rose.
-// Roundings: bf16 tensors give bf16 weights P and, in the gradient, bf16 dS (both
-// 2^-9 of themselves, below what the rounding of the result adds); fp32 tensors stay
+// maximum and sum in fp32; O is rescaled only where a maximum of the wave rose past 2^8.
+// Roundings: bf16 tensors give bf16 weights P and, in the gradient, bf16 dS (off by at
+// most 2^-8 of themselves, as the rounded result is); fp32 tensors stay
 // fp32 throughout.
 //
 // Measured per call (MI355X; bf16 unless said; the library's bf16 matrix product reaches
 // 1185 TFLOP/s here, its fp32 one 154, a copy 5.4 TB/s):
-//   2 x 4096 queries, 4608 keys, 16 heads of 128: 340-355 us, 880 TFLOP/s
+//   2 x 4096 queries, 4608 keys, 16 heads of 128: 335-355 us, 870-920 TFLOP/s
 //   16 x 1024 queries, prompts of up to 120 keys, 16 heads of 72: 24 us, 3.3 TB/s
-//   4 x 1 query over 4608 keys, 16 heads of 64: 24 us, 3.2 TB/s
-//   gradient, 2 x 8190 queries, prompts of 512 and 156, 16 heads on 8 of 128: 260-275 us,
-//     405 TFLOP/s of the five products that it takes (seven are done), 660 at 4096 x 4096
-//   gradient, 8 x 256 queries, 77 keys with holes, 16 heads of 72, fp32: 68 us
+//   4 x 1 query over 4608 keys, 16 heads of 64: 24-28 us, 2.7-3.2 TB/s
+//   gradient, 2 x 8190 queries, prompts of 512 and 156, 16 heads on 8 of 128: 257-277 us,
+//     400-430 TFLOP/s of the five products that it takes (seven are done), 680 for two
+//     sequences of 4096 x 4096 with 16 heads
+//   gradient, 8 x 256 queries, 77 keys with holes, 16 heads of 72, fp32: 66-70 us
 // What bounds the large ones: LDS gives one operand of 1 KB in the time of one 32x32x16
 // product, so the products wait for it whenever all SIMDs are at them (with operands from
 // registers instead the first case takes 239 us); 64 rows a wave, which would halve that,
@@ -389,11 +390,10 @@ __device__ __forceinline__ bool bit_of(const KeyBits<W>& k, int i) {
 }
 
 // Waves a SIMD that the registers are to allow. Two wherever bf16 fits (forward at 128
-// channels: 709 us with one, 390 with two), but for the longest heads where few rows share
-// them among the keys' loads and in the gradients, which would spill (8 rows of 160 channels
-// over 4096 keys: 105 us with two, 72 with one). fp32 takes all there are.
+// channels: 709 us with one, 390 with two), but for the longest heads in the gradients, which
+// would spill. fp32 takes all there are.
 constexpr bool kPairs = sizeof(T) == 2;
-template <int WK> constexpr int kForwardWaves = kPairs && (WK == 1 || DC <= 8) ? 2 : 1;
+constexpr int kForwardWaves = kPairs ? 2 : 1;
 constexpr int kDqWaves = kPairs && DC <= 8 ? 2 : 1, kDkvWaves = kDqWaves;
 
 // ----------------------------------------------------------------- forward ----
@@ -474,7 +474,7 @@ __device__ __forceinline__ void finish(const AttnArgs& a, int b, int hk, int row
 // tiles of rows, its waves on their own after the one barrier, the next rows' queries under
 // way.
 #if QL_AT_SHORT
-__global__ __launch_bounds__(kThreads, kForwardWaves<1>) void k_attn_short(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, kForwardWaves) void k_attn_short(AttnArgs a) {
   constexpr int KT = 64, kTile = KT * 2 * kPitch;
   constexpr bool kRoom = (2 * kTile + 128 * kPitch) * sizeof(T) <= 81920;  // for two workgroups
   __shared__ __attribute__((aligned(16))) T lds[2 * kTile + (kRoom ? 128 * kPitch : 0)];
@@ -548,8 +548,10 @@ __global__ __launch_bounds__(kThreads, kForwardWaves<1>) void k_attn_short(AttnA
 }
 #endif
 
-// WK waves of a workgroup share its keys, 4 / WK its rows: one for many rows; all
-// four (two in fp32, whose tiles fill LDS) for few of them.
+// WK waves of a workgroup share its keys, 4 / WK its rows: one, or two in fp32 for up to 64
+// rows (4 x 1 query over 4608 keys, 16 heads of 64: 65 us, 91 with one). In bf16 few rows
+// too are faster with one, the other waves helping to load (8 x 1 query of 32 heads on 8 of
+// 128, 4096 keys: 36 us; with four, 57): two tiles fit LDS.
 template <int WK>
 struct Fwd {
   static constexpr int WQ = 4 / WK, kRows = 32 * WQ;
@@ -563,7 +565,7 @@ struct Fwd {
 };
 
 template <int WK>
-__global__ __launch_bounds__(kThreads, kForwardWaves<WK>) void k_attn_forward(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, kForwardWaves) void k_attn_forward(AttnArgs a) {
   typedef Fwd<WK> P;
   constexpr int KT = P::KT, SUB = P::SUB, W = KT / 32;
   __shared__ __attribute__((aligned(16))) char smem[P::kLds];
@@ -580,6 +582,7 @@ __global__ __launch_bounds__(kThreads, kForwardWaves<WK>) void k_attn_forward(At
   const int tiles = (len + KT - 1) / KT, per = (tiles + a.splits - 1) / a.splits;
   const int t0 = sp * per, t1 = min(tiles, t0 + per);
   const int row0 = rt * P::kRows + wq * 32, row = row0 + r32;
+  const bool busy = row0 < a.R;  // else this wave only helps to fill the tiles
   Spots spots;
   spots.find(lane);
   frag q[DC];
@@ -629,7 +632,7 @@ __global__ __launch_bounds__(kThreads, kForwardWaves<WK>) void k_attn_forward(At
     const T* const vt = kt + KT * kPitch;
     if (t + 1 < t1) fetch(t + 1);
     form_anew(spots);
-    if (!bits.none()) {
+    if (busy && !bits.none()) {
       uint32_t words[SUB];
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
@@ -1117,8 +1120,6 @@ __global__ __launch_bounds__(kThreads) void k_attn_dkv_sum(AttnArgs a) {
   }
 }
 
-constexpr int kNarrow = sizeof(T) == 2 ? 4 : 2;
-
 }  // namespace
 
 #define QL_CAT3(a, b, c, d) a##b##c##d
@@ -1134,8 +1135,8 @@ hipError_t QL_NAME(attn_forward_, QL_AT_T, QL_AT_DC)(const AttnArgs& a, const At
     return hipGetLastError();
   }
 #endif
-  if (p.narrow)
-    k_attn_forward<kNarrow><<<grid, kThreads, 0, s>>>(a);
+  if (sizeof(T) == 4 && p.narrow)
+    k_attn_forward<sizeof(T) == 4 ? 2 : 1><<<grid, kThreads, 0, s>>>(a);
   else
     k_attn_forward<1><<<grid, kThreads, 0, s>>>(a);
   if (a.splits > 1) {

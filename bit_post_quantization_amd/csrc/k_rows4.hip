@@ -15,8 +15,8 @@
 // are joined in fp32 and scaled: 28 operations for 16 by 16 outputs.
 //
 // Measured: 2 rows, K 1152, N 6912: 5.8 us of kernel (latency); 8 rows, K 4096, N 24576:
-// 4.8 us of digits and 19.4 of products, 2.8 TB/s (adding up as many bytes takes 25); 77 rows,
-// K 4608, N 1151, groups of 32: 18 us, bound by the joining of its sums and latency.
+// 4 us of digits and 21 of products, 2.2-2.5 TB/s of the two (adding up as many bytes takes 25); 77 rows,
+// K 4608, N 1151, groups of 32: 4 and 15 us, bound by the joining of its sums and latency.
 //
 // The waves of a workgroup share out the units of its NT tiles of 16 channels and join
 // in LDS. The digits come from LDS where the rows fit: formed there by the workgroup, if

@@ -101,7 +101,7 @@ struct AttnArgs {
   bool near_rows;   // 32 rows of q and of dout lie evenly and within 32-bit offsets
 };
 struct AttnPlan {
-  bool narrow;
+  bool narrow;               // forward, fp32, few rows: waves share the keys
   int per_group;             // forward, few keys: tiles of rows of a workgroup, else 0
   int row_tiles, splits;          // forward
   int q_tiles, key_tiles, k_splits;  // gradient

@@ -329,15 +329,24 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 namespace ql {
 
 // Rows and keys by tiles, and how many workgroups share a long axis where few tiles of
-// the other one are there. The sizes are those of k_attn.hip's kernels.
+// the other one are there. The sizes are those of k_attn.hip's kernels. How many workgroups
+// splitting aims at is a compromise; us at each aim, heads of 128 in bf16 unless said:
+//   forward, 512: 8 x 1 query, 4096 keys, 32 heads on 8: 39 at 256, 36 at 512, 43 at 768;
+//     2 x 512 queries, 2048 keys, 16 heads of 72: 37 at 256, 34 at 512, 41 at 1024; but
+//     256 queries, 4608 keys, 16 heads: 28 at 256, 33 at 512, 40 at 1024
+//   few keys, workgroups that go through several tiles of rows, 512: 16 x 1024 queries, up to
+//     120 keys, 16 heads of 72: 35 at 256, 33 at 512, 37 at 768; with the kernel that does
+//     not keep the keys in LDS 38 (30 with it, later)
+//   gradient, bf16, 512: 2 x 8190 queries, 512 and 156 keys, 16 heads on 8: 377 at 256, 280
+//     at 512; fp32, 256: 8 x 256 queries, 77 keys, 16 heads of 72: 71 at 256, 78 at 512
 AttnPlan attn_plan(const ql_attn& d) {
   AttnPlan p{};
   const int64_t G = d.heads / d.kv_heads, R = d.q_len * G, bh = (int64_t)d.batch * d.kv_heads;
   const int64_t n = (int64_t)d.batch * d.heads * d.q_len;
   const bool bf16 = d.dtype == QL_BF16;
-  p.narrow = R <= (bf16 ? 32 : 64);
-  p.row_tiles = ceil_div(R, p.narrow ? (bf16 ? 32 : 64) : 128);
-  const int64_t tiles = ceil_div(d.k_len, p.narrow && bf16 ? 128 : 64);
+  p.narrow = !bf16 && R <= 64;
+  p.row_tiles = ceil_div(R, p.narrow ? 64 : 128);
+  const int64_t tiles = ceil_div(d.k_len, 64);
   const int64_t base = bh * p.row_tiles;
   int64_t s = base > 0 ? (p.narrow ? 768 : 512) / base : 1;
   const int64_t most = tiles / (p.narrow ? 2 : 4);
