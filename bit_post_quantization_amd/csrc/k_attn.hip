@@ -389,12 +389,13 @@ __device__ __forceinline__ bool bit_of(const KeyBits<W>& k, int i) {
   return (x >> (i & 31)) & 1;
 }
 
-// Waves a SIMD that the registers are to allow. Two wherever bf16 fits (forward at 128
-// channels: 709 us with one, 390 with two), but for the longest heads in the gradients, which
-// would spill. fp32 takes all there are.
+// Waves a SIMD that the registers are to allow: two wherever they fit without spills (us with
+// one and with two; bf16, forward, 128 channels: 709, 390; fp32, 2 x 2048 queries and keys:
+// forward, 8 heads of 96: 250, 224, 8 of 128: 325, 312 but one query a sequence 125, 158;
+// gradient, 16 heads of 64: 1112, 920, 8 of 96: 801, 906, 8 of 128: 1036, 1632).
 constexpr bool kPairs = sizeof(T) == 2;
-constexpr int kForwardWaves = kPairs ? 2 : 1;
-constexpr int kDqWaves = kPairs && DC <= 8 ? 2 : 1, kDkvWaves = kDqWaves;
+constexpr int kForwardWaves = kPairs || DC <= 6 ? 2 : 1;
+constexpr int kDqWaves = DC <= (kPairs ? 8 : 4) ? 2 : 1, kDkvWaves = kDqWaves;
 
 // ----------------------------------------------------------------- forward ----
 
