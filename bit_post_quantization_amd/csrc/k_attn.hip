@@ -389,10 +389,11 @@ __device__ __forceinline__ bool bit_of(const KeyBits<W>& k, int i) {
   return (x >> (i & 31)) & 1;
 }
 
-// Waves a SIMD that the registers are to allow: two wherever they fit without spills (us with
-// one and with two; bf16, forward, 128 channels: 709, 390; fp32, 2 x 2048 queries and keys:
-// forward, 8 heads of 96: 250, 224, 8 of 128: 325, 312 but one query a sequence 125, 158;
-// gradient, 16 heads of 64: 1112, 920, 8 of 96: 801, 906, 8 of 128: 1036, 1632).
+// Waves a SIMD that the registers are to allow: two where they fit, at most a few of them
+// spilled (us with one and with two; bf16, forward, 128 channels: 709, 390, 4 x 4096 queries
+// and keys, 8 heads of 160, nine spilled: 545, 371; fp32, 2 x 2048 queries and keys: forward, 8
+// heads of 96: 250, 224, 8 of 128: 325, 312 but one query a sequence 125, 158; gradient, 16
+// heads of 64: 1112, 920, 8 of 96: 801, 906, 8 of 128: 1036, 1632).
 constexpr bool kPairs = sizeof(T) == 2;
 constexpr int kForwardWaves = kPairs || DC <= 6 ? 2 : 1;
 constexpr int kDqWaves = DC <= (kPairs ? 8 : 4) ? 2 : 1, kDkvWaves = kDqWaves;
@@ -558,8 +559,10 @@ struct Fwd {
   static constexpr int WQ = 4 / WK, kRows = 32 * WQ;
   static constexpr int SUB = WK == 1 ? 2 : 1;  // 32-key pieces of a wave in a tile
   static constexpr int KT = 32 * WK * SUB;
-  static constexpr int NB = WK == 1 && sizeof(T) * kD <= 320 ? 2 : 1;  // tiles in LDS
   static constexpr int kTile = KT * 2 * kPitch;
+  // Tiles in LDS: two where two workgroups still fit (fp32, 2 x 2048 queries and keys, 16 heads
+  // of 72: 419 us with two, 373 with one; bf16, 8 of 160: 83 and 85).
+  static constexpr int NB = WK == 1 && 4 * kTile * (int)sizeof(T) <= 160 * 1024 ? 2 : 1;
   static constexpr int kJoin = WK > 1 ? (WK - 1) * WQ * 32 * (kOB * 32 + 2) * 4 : 0;
   static constexpr int kLds = NB * kTile * (int)sizeof(T) > kJoin ? NB * kTile * (int)sizeof(T)
                                                                  : kJoin;
