@@ -65,6 +65,55 @@ def test_attention_every_cut(torch, case):  # noqa: F811
     _attention(torch, Attn(torch, *case))
 
 
+SHARED_OUT = [
+    # B, Lq, Lk, heads, kv, dim, type, mask: tiles of keys of many sequences, rows shared out
+    (65, 600, 30, 1, 1, 32, "bf16", "lens"),      # one sequence past the first 64
+    (100, 600, 20, 1, 1, 32, "bf16", "both"),
+    (128, 130, 40, 1, 1, 64, "f32", "both"),
+    (120, 600, 200, 1, 1, 24, "bf16", "lens"),    # one or two tiles, or none
+    (256, 520, 33, 1, 1, 32, "bf16", "lens"),     # as many as are shared out
+    (257, 520, 33, 1, 1, 32, "bf16", "lens"),     # one more: they are not
+    (16, 520, 33, 16, 8, 32, "bf16", "holes"),    # heads by eight
+]
+
+
+@pytest.mark.parametrize("case", SHARED_OUT, ids=str)
+def test_attention_many_sequences(torch, case):  # noqa: F811
+    say(f"[attention, many sequences] {case}")
+    _attention(torch, Attn(torch, *case))
+
+
+@pytest.mark.parametrize("where", [None, 0, 63, 64, 199])
+def test_attention_keys_of_one_sequence_only(torch, where):  # noqa: F811
+    """All workgroups of a head go to one tile, or to none: more sharers than tiles of rows."""
+    c = Attn(torch, 200, 520, 20, 1, 1, 32, "bf16", "none")
+    c.lens = torch.zeros(200, dtype=torch.int32, device="cuda")
+    if where is not None:
+        c.lens[where] = 13
+    c.ok = torch.arange(20, device="cuda") < c.lens[:, None]
+    c.k[~c.ok], c.v[~c.ok] = float("nan"), float("inf")
+    _attention(torch, c)
+
+
+ONE_TOKEN = [
+    # B, Lq, Lk, heads, kv, dim, type, mask: rows that fill a part of one tile only
+    (8, 1, 77, 4, 4, 72, "bf16", "lens"),         # keys in LDS
+    (8, 1, 77, 8, 2, 160, "bf16", "both"),
+    (2, 1, 4096, 32, 8, 128, "bf16", "lens"),     # keys shared out
+    (3, 8, 2000, 8, 8, 160, "bf16", "holes"),
+    (2, 33, 1000, 2, 1, 64, "bf16", "both"),      # three waves with rows, one without
+    (2, 97, 1000, 2, 2, 64, "bf16", "none"),
+    (2, 1, 1000, 8, 4, 96, "f32", "lens"),
+    (2, 65, 1000, 2, 2, 72, "f32", "both"),
+]
+
+
+@pytest.mark.parametrize("case", ONE_TOKEN, ids=str)
+def test_attention_few_rows(torch, case):  # noqa: F811
+    say(f"[attention, few rows] {case}")
+    _attention(torch, Attn(torch, *case))
+
+
 def test_attention_first_keys_do_not_count(torch):  # noqa: F811
     """Whole tiles without a key before the first one that counts, for rows of any number."""
     for Lq, dt in ((2, "bf16"), (200, "bf16"), (200, "f32")):
