@@ -392,10 +392,11 @@ __device__ __forceinline__ bool bit_of(const KeyBits<W>& k, int i) {
 // Waves a SIMD that the registers are to allow: two where they fit, at most a few of them
 // spilled (us with one and with two; bf16, forward, 128 channels: 709, 390, 4 x 4096 queries
 // and keys, 8 heads of 160, nine spilled: 545, 371; fp32, 2 x 2048 queries and keys: forward, 8
-// heads of 96: 250, 224, 8 of 128: 325, 312 but one query a sequence 125, 158; gradient, 16
-// heads of 64: 1112, 920, 8 of 96: 801, 906, 8 of 128: 1036, 1632).
+// heads of 96: 250, 224, 8 of 128: 326, 286 (with tiles of 32 keys, below), but one query a
+// sequence and 4096 keys, 16 heads on 8 of 128: 125, 158; gradient, 16 heads of 64: 1112, 920,
+// 8 of 96: 801, 906, 8 of 128: 1036, 1632). Of 160 channels in fp32 LDS holds one workgroup.
 constexpr bool kPairs = sizeof(T) == 2;
-constexpr int kForwardWaves = kPairs || DC <= 6 ? 2 : 1;
+template <int WK> constexpr int kForwardWaves = kPairs || DC <= (WK == 1 ? 8 : 6) ? 2 : 1;
 constexpr int kDqWaves = DC <= (kPairs ? 8 : 4) ? 2 : 1, kDkvWaves = kDqWaves;
 
 // ----------------------------------------------------------------- forward ----
@@ -476,7 +477,7 @@ __device__ __forceinline__ void finish(const AttnArgs& a, int b, int hk, int row
 // tiles of rows, its waves on their own after the one barrier, the next rows' queries under
 // way.
 #if QL_AT_SHORT
-__global__ __launch_bounds__(kThreads, kForwardWaves) void k_attn_short(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, (kForwardWaves<1>)) void k_attn_short(AttnArgs a) {
   constexpr int KT = 64, kTile = KT * 2 * kPitch;
   constexpr bool kRoom = (2 * kTile + 128 * kPitch) * sizeof(T) <= 81920;  // for two workgroups
   __shared__ __attribute__((aligned(16))) T lds[2 * kTile + (kRoom ? 128 * kPitch : 0)];
@@ -557,19 +558,25 @@ __global__ __launch_bounds__(kThreads, kForwardWaves) void k_attn_short(AttnArgs
 template <int WK>
 struct Fwd {
   static constexpr int WQ = 4 / WK, kRows = 32 * WQ;
-  static constexpr int SUB = WK == 1 ? 2 : 1;  // 32-key pieces of a wave in a tile
+  // 32-key pieces of a wave in a tile. Long fp32 heads take one, whose way to LDS leaves the
+  // registers for a second wave (8 heads of 128: 326 us with two, 286 with one; of 160: 428,
+  // 403; of 96 no less with one).
+  static constexpr int SUB = WK == 1 && (kPairs || DC <= 6) ? 2 : 1;
   static constexpr int KT = 32 * WK * SUB;
   static constexpr int kTile = KT * 2 * kPitch;
   // Tiles in LDS: two where two workgroups still fit (fp32, 2 x 2048 queries and keys, 16 heads
   // of 72: 419 us with two, 373 with one; bf16, 8 of 160: 83 and 85).
-  static constexpr int NB = WK == 1 && 4 * kTile * (int)sizeof(T) <= 160 * 1024 ? 2 : 1;
+  static constexpr int NB = KT == 32 || (WK == 1 && 4 * kTile * (int)sizeof(T) <= 160 * 1024) ? 2 : 1;
   static constexpr int kJoin = WK > 1 ? (WK - 1) * WQ * 32 * (kOB * 32 + 2) * 4 : 0;
   static constexpr int kLds = NB * kTile * (int)sizeof(T) > kJoin ? NB * kTile * (int)sizeof(T)
                                                                  : kJoin;
+  // Where the 128 rows of the waves pass: behind the first tile, or over it.
+  static constexpr int kRowsAt = NB * kTile - 128 * kPitch;
+  static_assert(kRowsAt >= 0, "the waves' rows fit the tiles");
 };
 
 template <int WK>
-__global__ __launch_bounds__(kThreads, kForwardWaves) void k_attn_forward(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, kForwardWaves<WK>) void k_attn_forward(AttnArgs a) {
   typedef Fwd<WK> P;
   constexpr int KT = P::KT, SUB = P::SUB, W = KT / 32;
   __shared__ __attribute__((aligned(16))) char smem[P::kLds];
@@ -593,8 +600,8 @@ __global__ __launch_bounds__(kThreads, kForwardWaves) void k_attn_forward(AttnAr
   {
     Rows rows;
     rows.fetch(lane, a.D, [&](int i) { return row_of(a, a.q, b, hk, min(row0 + i, a.R - 1)); });
-    rows.operands(lds + (P::NB - 1) * P::kTile + wave * 32 * kPitch, spots, lane, a.D, q);
-    if (P::NB == 1) __syncthreads();
+    rows.operands(lds + P::kRowsAt + wave * 32 * kPitch, spots, lane, a.D, q);
+    if (P::kRowsAt < P::kTile) __syncthreads();  // the first tile goes there
   }
   const T* const kp = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
   const T* const vp = reinterpret_cast<const T*>(a.v.p) + b * a.v.batch + hk * a.v.head;
