@@ -394,10 +394,16 @@ __device__ __forceinline__ bool bit_of(const KeyBits<W>& k, int i) {
 // and keys, 8 heads of 160, nine spilled: 545, 371; fp32, 2 x 2048 queries and keys: forward, 8
 // heads of 96: 250, 224, 8 of 128: 326, 286 (with tiles of 32 keys, below), but one query a
 // sequence and 4096 keys, 16 heads on 8 of 128: 125, 158; gradient, 16 heads of 64: 1112, 920,
-// 8 of 96: 801, 906, 8 of 128: 1036, 1632). Of 160 channels in fp32 LDS holds one workgroup.
+// both kernels 8 of 96: 801, 906, 8 of 128: 1036, 1632). Of 160 channels in fp32 LDS holds
+// one workgroup.
 constexpr bool kPairs = sizeof(T) == 2;
 template <int WK> constexpr int kForwardWaves = kPairs || DC <= (WK == 1 ? 8 : 6) ? 2 : 1;
-constexpr int kDqWaves = DC <= (kPairs ? 8 : 4) ? 2 : 1, kDkvWaves = kDqWaves;
+constexpr int kDqWaves = DC <= (kPairs ? 8 : 6) ? 2 : 1, kDkvWaves = DC <= (kPairs ? 8 : 4) ? 2 : 1;
+// Keys of a tile of k_attn_dq; 32 leave long fp32 heads the registers that they need (the
+// gradient of 2 x 2048 queries and keys, us: 16 heads of 72: 1472 with 64, 1436 with 32, 8 of
+// 96: 795, 782, 8 of 128: 1026, 1039; 8 x 256 queries of 77 keys, 16 heads of 128: 99, 97, of
+// 160: 151, 141).
+constexpr int kDqKeys = kPairs || DC <= 4 ? 64 : 32;
 
 // ----------------------------------------------------------------- forward ----
 
@@ -757,8 +763,10 @@ constexpr bool kKeepV = sizeof(T) == 2 && DC >= 8;
 
 // dQ, and delta for k_attn_dkv. Keys that do not count are zero in LDS and have P = 0.
 __global__ __launch_bounds__(kThreads, kDqWaves) void k_attn_dq(AttnArgs a) {
-  constexpr int KT = 64, W = 2, kTile = KT * 2 * kPitch;
-  constexpr int NB = 2 * kTile * (int)sizeof(T) <= 81920 ? 2 : 1;
+  constexpr int KT = kDqKeys, W = KT / 32, kTile = KT * 2 * kPitch;
+  constexpr int NB = KT == 32 || 2 * kTile * (int)sizeof(T) <= 81920 ? 2 : 1;
+  constexpr int kRowsAt = NB * kTile - 128 * kPitch;  // where the 128 rows of the waves pass
+  static_assert(kRowsAt >= 0, "the waves' rows fit the tiles");
   __shared__ __attribute__((aligned(16))) T lds[NB * kTile];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, h = lane >> 5;
   int id = by_xcd(a, blockIdx.x, a.row_tiles);
@@ -767,6 +775,7 @@ __global__ __launch_bounds__(kThreads, kDqWaves) void k_attn_dq(AttnArgs a) {
   const int hk = id % a.Hk, b = id / a.Hk;
   const int len = key_len(a, b), tiles = (len + KT - 1) / KT;
   const int row0 = rt * 128 + wave * 32, row = row0 + r32;
+  const bool busy = row0 < a.R;  // else this wave only helps to fill the tiles
   const int64_t at = stat_at(a, b, hk, min(row, a.R - 1));
   Spots spots;
   spots.find(lane);
@@ -774,7 +783,7 @@ __global__ __launch_bounds__(kThreads, kDqWaves) void k_attn_dq(AttnArgs a) {
   frag q[DC], g[DC];
   float delta = 0.0f;
   {
-    T* const room = lds + (NB - 1) * kTile + wave * 32 * kPitch;
+    T* const room = lds + kRowsAt + wave * 32 * kPitch;
     Rows rq, rg, ro;
     rq.fetch(lane, a.D, [&](int i) { return row_of(a, a.q, b, hk, min(row0 + i, a.R - 1)); });
     rg.fetch(lane, a.D, [&](int i) { return row_of(a, a.dout, b, hk, min(row0 + i, a.R - 1)); });
@@ -789,7 +798,7 @@ __global__ __launch_bounds__(kThreads, kDqWaves) void k_attn_dq(AttnArgs a) {
       for (int e = 0; e < 8; ++e) delta = __builtin_fmaf((float)g[kb][e], (float)o[kb][e], delta);
     delta += other_half(delta);
     if (h == 0 && row < a.R) a.delta[at] = delta;
-    if (NB == 1) __syncthreads();
+    if (kRowsAt < kTile) __syncthreads();  // the first tile goes there
   }
   float lse2 = a.lse[at] * kLog2e;
   if (lse2 == -INFINITY) lse2 = INFINITY;  // no key counts: P = 0
@@ -834,9 +843,9 @@ __global__ __launch_bounds__(kThreads, kDqWaves) void k_attn_dq(AttnArgs a) {
     const T* const vt = kt + KT * kPitch;
     if (t + 1 < tiles) fetch(t + 1);
     form_anew(spots);
-    if (!bits.none()) {
+    if (busy && !bits.none()) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < W; ++u) {
         if (!bits.w[u]) continue;
         v16f s = zero16(), dp = zero16();
 #pragma unroll
