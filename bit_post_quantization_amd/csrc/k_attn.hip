@@ -23,9 +23,9 @@
 //
 // Measured per call (MI355X; bf16 unless said; the library's bf16 matrix product reaches
 // 1185 TFLOP/s here, its fp32 one 154, a copy 5.4 TB/s):
-//   2 x 4096 queries, 4608 keys, 16 heads of 128: 335-355 us, 870-920 TFLOP/s
+//   2 x 4096 queries, 4608 keys, 16 heads of 128: 335-355 us, 870-920 TFLOP/s (cards and runs differ)
 //   16 x 1024 queries, prompts of up to 120 keys, 16 heads of 72: 24 us, 3.3 TB/s
-//   4 x 1 query over 4608 keys, 16 heads of 64: 24-28 us, 2.7-3.2 TB/s
+//   4 x 1 query over 4608 keys, 16 heads of 64: 19 us, 3.9 TB/s
 //   gradient, 2 x 8190 queries, prompts of 512 and 156, 16 heads on 8 of 128: 257-277 us,
 //     400-430 TFLOP/s of the five products that it takes (seven are done), 680 for two
 //     sequences of 4096 x 4096 with 16 heads
