@@ -373,7 +373,8 @@ class CrossAttention:
 
     ``lens`` int32 [B] says how many keys of each batch entry count, ``mask`` bool (or
     uint8) [B, k_len] which ones; with both, those that both name. Others take no
-    part, whatever they hold. A query without any key that counts gets 0."""
+    part, whatever they hold. A query without any key that counts gets 0, one whose keys
+    count and all score -infinity NaN."""
 
     def __init__(self, heads: int, dim: int, kv_heads: Optional[int] = None,
                  scale: Optional[float] = None):

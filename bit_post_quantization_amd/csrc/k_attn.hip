@@ -331,6 +331,16 @@ __device__ __forceinline__ int key_len(const AttnArgs& a, int b) {
   return n < 0 ? 0 : n > a.Lk ? a.Lk : n;
 }
 
+// The sum of a row that has none, in all lanes of a wave alike: 0 where no key of the sequence
+// counts (its result is 0), NaN where keys count and all score -infinity (they have no
+// softmax). Looked up only where a row ends so; the loop over the tiles keeps no count.
+__device__ __forceinline__ float sum_of_none(const AttnArgs& a, int b, int len, int lane) {
+  if (!a.mask) return len > 0 ? NAN : 0.0f;
+  for (int key0 = 0; key0 < len; key0 += 64)
+    if (__any(key0 + lane < len && a.mask[b * a.mask_batch + key0 + lane] != 0)) return NAN;
+  return 0.0f;
+}
+
 // A tile of KT rows of one tensor on its way from memory through registers to LDS. Where
 // rows lie evenly (row i of a tile, i = u G + g, at u steps and g heads from the tile's
 // start) and near, a piece's address is the tile's, which is the same for all lanes, and
@@ -468,10 +478,10 @@ __device__ __forceinline__ void attend(const T* kt, const T* vt, const Spots& sp
   l += sum;
 }
 
-// O and lse of a row, l being the whole sum.
+// O and lse of a row, l being the whole sum (0 only where no key counts).
 __device__ __forceinline__ void finish(const AttnArgs& a, int b, int hk, int row, const v16f (&o)[kOB],
                                        float m, float l, int h) {
-  const bool empty = m == -INFINITY && l == 0.0f;
+  const bool empty = l == 0.0f;
   const float inv = empty ? 0.0f : 1.0f / l;
   if (a.lse && h == 0)
     a.lse[stat_at(a, b, hk, row)] = empty ? -INFINITY : (m + __log2f(l)) * kLn2;
@@ -552,6 +562,7 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<1>)) void k_attn_short(Att
     }
     const int row = rt * 128 + wave * 32 + r32;
     l += other_half(l);
+    if (l == 0.0f && !(bits[0].none() && bits[1].none())) l = NAN;  // as sum_of_none
     if (row < a.R) finish(a, b, hk, row, o, m, l, h);
   }
 }
@@ -707,9 +718,13 @@ __global__ __launch_bounds__(kThreads, kForwardWaves<WK>) void k_attn_forward(At
     }
     m = top;
   }
+  if (a.splits == 1 && __any(l == 0.0f)) {
+    const float none = sum_of_none(a, b, len, lane);
+    l = l == 0.0f ? none : l;
+  }
   if (row >= a.R) return;
   if (a.splits == 1) return finish(a, b, hk, row, o, m, l, h);
-  const bool empty = m == -INFINITY && l == 0.0f;
+  const bool empty = l == 0.0f;  // k_attn_join looks whether any part has keys
   const float inv = empty ? 0.0f : 1.0f / l;
   const int64_t n = (int64_t)a.B * a.H * a.Lq, at = stat_at(a, b, hk, row);
   float* p = a.part + (sp * n + at) * a.D;
@@ -745,10 +760,11 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
       for (int i = 0; i < 3; ++i) acc[i] = __builtin_fmaf(f, p[j][i], acc[i]);
     }
   }
-  const bool empty = total == 0.0f;
-  const float inv = empty ? 0.0f : 1.0f / total;
   const int l = (int)(at % a.Lq);
   const int64_t bh = at / a.Lq;
+  if (total == 0.0f) total = sum_of_none(a, (int)(bh / a.H), key_len(a, (int)(bh / a.H)), lane);
+  const bool empty = total == 0.0f;
+  const float inv = empty ? 0.0f : 1.0f / total;
   T* p = reinterpret_cast<T*>(a.o.p) + bh / a.H * a.o.batch + l * a.o.row + bh % a.H * a.o.head;
 #pragma unroll
   for (int i = 0; i < 3; ++i)

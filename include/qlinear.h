@@ -620,7 +620,8 @@ ql_status qlinear_heads_grad(const ql_heads* d, const ql_heads_view* dq, const q
  * O = softmax(scale Q K^T) V by head; query head h reads key head h / (heads /
  * kv_heads). Keys that do not count (past k_lens[b], or with k_mask 0) take no part:
  * nothing of them is multiplied, so infinities and NaN there do no harm. A query
- * without any key that counts gets O = 0 and lse = -infinity.
+ * without any key that counts gets O = 0 and lse = -infinity; one whose keys count and all
+ * score -infinity has no softmax, and gets NaN.
  */
 typedef struct {
   int32_t batch, q_len, k_len;  /* >= 0; batch * heads * q_len and batch * kv_heads * k_len < 2^31 */

@@ -1,0 +1,63 @@
+"""Corners of a conditioned block's operators, infinities first. Formulas, bounds and inputs
+are those of test_gpu_block.py."""
+from __future__ import annotations
+
+import math
+
+import pytest
+
+from tests.parity import say
+from tests.test_gpu_block import Attn, _round, _same_lse, _within, torch  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ attention ----
+
+ALL_LOW = [
+    # Lq, Lk, heads, kv, dim, type: every way the forward pass ends
+    (40, 100, 2, 2, 64, "bf16"),     # keys in LDS
+    (100, 100, 2, 2, 72, "f32"),
+    (200, 200, 2, 1, 64, "bf16"),    # tiles of keys
+    (70, 100, 2, 2, 160, "f32"),
+    (3, 100, 4, 2, 64, "f32"),       # waves that share the keys
+    (3, 1500, 4, 2, 64, "f32"),      # parts joined
+    (5, 1500, 2, 2, 128, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", ALL_LOW, ids=str)
+def test_attention_every_score_minus_infinity(torch, case):  # noqa: F811
+    """A query whose keys count and all score -infinity has no softmax: NaN, as the formula
+    says, and so have its gradients. One without keys still gets 0, and neither touches
+    another sequence."""
+    say(f"[attention, all scores -inf] {case}")
+    Lq, Lk, H, G, D, dt = case
+    c = Attn(torch, 4, Lq, Lk, H, G, D, dt, "holes")
+    c.lens = torch.tensor([Lk, Lk, 0, Lk // 2], dtype=torch.int32, device="cuda")
+    c.mask[:, 0] = True
+    c.ok = c.mask & (torch.arange(Lk, device="cuda") < c.lens[:, None])
+    c.q[:] = c.q.abs() + 0.1
+    c.k[1], c.v[1] = c.k[1].nan_to_num(), c.v[1].nan_to_num(posinf=0.0)
+    for b in (0, 3):
+        c.k[b] = torch.where(c.ok[b, :, None, None], -math.inf, 1.0).to(c.k.dtype)
+        c.v[b] = 1.0
+    layer = c.layer()
+    out, lse = layer.forward(c.q, c.k, c.v, lens=c.lens, mask=c.mask, save=True)
+    grads = layer.grad(c.dout, c.q, c.k, c.v, out, lse, lens=c.lens, mask=c.mask)
+    dq, dk, dv = grads
+    for b in (0, 3):
+        assert bool(out[b].isnan().all()) and bool(lse[b].isnan().all())
+        assert bool(dq[b].isnan().all())
+        for d in (dk, dv):
+            assert bool(d[b, c.ok[b]].isnan().all()) and bool((d[b, ~c.ok[b]] == 0).all())
+    assert bool((out[2] == 0).all()) and bool((lse[2] == -math.inf).all())
+    assert all(bool((d[2] == 0).all()) for d in grads)
+    one = Attn(torch, 1, Lq, Lk, H, G, D, dt, "none")
+    one.q, one.k, one.v, one.dout, one.ok = (x[1:2] for x in (c.q, c.k, c.v, c.dout, c.ok))
+    ref, tol, ref_lse, lse_tol = one.forward()
+    _within(out[1:2], ref, tol + _round(torch, ref, out.dtype), "out")
+    _same_lse(torch, lse[1:2], ref_lse, lse_tol)
+    ref, tol = one.grads(out[1:2], lse[1:2])
+    for g, r, e, name in zip(grads, ref, tol, ("dq", "dk", "dv")):
+        _within(g[1:2], r, e + _round(torch, r, g.dtype), name)
