@@ -1031,13 +1031,14 @@ __global__ __launch_bounds__(kThreads, kDkvWaves) void k_attn_dkv(AttnArgs a) {
     const int n = a.R - t * RT, at = (t - t0) % NB;
     T* to = lds + at * kTile;
     const auto keep = [&](int i) { return i < n; };
-    if (n >= RT) {
-      qs.template put<true>(to, tid, a.D, keep);
+    // Past the last row dO is zero and q that row again: with an lse of infinity P is 0 there
+    // whenever the last row's own is a number, also for a key of -infinity, where q = 0
+    // would score NaN.
+    qs.template put<true>(to, tid, a.D, keep);
+    if (n >= RT)
       gs.template put<true>(to + RT * kPitch, tid, a.D, keep);
-    } else {
-      qs.template put<false>(to, tid, a.D, keep);
+    else
       gs.template put<false>(to + RT * kPitch, tid, a.D, keep);
-    }
     if (tid < 2 * RT) stats[at][tid / RT][tid % RT] = stat;
   };
   if (t0 < t1) {

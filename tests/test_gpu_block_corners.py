@@ -61,3 +61,30 @@ def test_attention_every_score_minus_infinity(torch, case):  # noqa: F811
     ref, tol = one.grads(out[1:2], lse[1:2])
     for g, r, e, name in zip(grads, ref, tol, ("dq", "dk", "dv")):
         _within(g[1:2], r, e + _round(torch, r, g.dtype), name)
+
+
+LOW_KEY = [
+    # Lq, Lk, heads, kv, dim, type: rows that do not fill their last tile
+    (40, 70, 2, 2, 64, "bf16"),
+    (45, 70, 4, 2, 72, "f32"),
+    (33, 200, 6, 2, 128, "bf16"),
+    (1301, 40, 2, 2, 64, "bf16"),    # rows shared out
+    (301, 77, 2, 2, 96, "f32"),
+]
+
+
+@pytest.mark.parametrize("case", LOW_KEY, ids=str)
+def test_attention_grad_of_a_key_that_scores_minus_infinity(torch, case):  # noqa: F811
+    """A key of -infinity that counts weighs nothing: its gradients are sums of zeros. (Those
+    of the queries hold 0 times the key, NaN.)"""
+    say(f"[attention grad, a key of -inf] {case}")
+    c = Attn(torch, 2, *case, "none")
+    c.q[:] = c.q.abs() + 0.1
+    c.k[:, 7] = -math.inf
+    out, lse = c.layer().forward(c.q, c.k, c.v, save=True)
+    dq, dk, dv = c.layer().grad(c.dout, c.q, c.k, c.v, out, lse)
+    c.ok[:, 7] = False
+    ref, tol = c.grads(out, lse)
+    assert bool(dq.isnan().all())
+    _within(dk, ref[1], tol[1] + _round(torch, ref[1], dk.dtype), "dk")
+    _within(dv, ref[2], tol[2] + _round(torch, ref[2], dv.dtype), "dv")
