@@ -594,7 +594,8 @@ ql_status qlinear_heads_workspace(const ql_heads* d, int64_t* bytes);
 /*
  * q, k, v (y_dtype; a part of 0 heads is not looked at) from x. A pair (a, b) becomes
  * (a cos - b sin, a sin + b cos) of its angle; angles are formed in fp64 and reduced
- * there, so far positions keep their accuracy; statistics are fp32.
+ * there, so far positions keep their accuracy; statistics are fp32. Where the sine is 0 (channels
+ * that do not turn, positions of 0) a channel takes nothing of another, whatever that holds.
  *   x   : DEVICE [batch, positions, heads * dim], strides in elements, row >= heads * dim.
  *   pos : DEVICE pos_dtype, n_axes values a position (dense), batch stride pos_batch
  *         elements (0: all images share them). NULL with n_axes = 0.
