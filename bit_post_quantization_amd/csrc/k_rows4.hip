@@ -361,10 +361,11 @@ hipError_t run(const Rows4Args& a, hipStream_t s) {
   if constexpr (SRC != kForm)
     k_rows4_digits<<<dim3((a.units + 15) / 16, a.M < 32768 ? a.M : 32768, (a.M + 32767) / 32768), 256, 0, s>>>(a);
   const int x = SRC == kRead ? 0 : digit_bytes(a.M, a.units) + a.M * a.units * 4;
-  const int box = kWaves * NT * MB * 1024, lds = x > box ? x : box;
+  constexpr int box = kWaves * NT * MB * 1024;
+  static_assert(box <= kXBytes, "kXBytes is the most that a call asks for");
+  const int lds = x > box ? x : box;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_rows4<NT, MB, GS, SRC, S>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const hipError_t e = allow_lds<&k_rows4<NT, MB, GS, SRC, S>, kXBytes>();
     if (e != hipSuccess) return e;
   }
   const int blocks = (a.M + 15) / 16;

@@ -5,9 +5,29 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/qlinear.h"
 
 namespace ql {
+
+// Before launches of a kernel with more than 64 KB of LDS: its limit of dynamic LDS, once a
+// device, to the most that any of its calls asks for. The limit is the kernel's, shared by all
+// host threads: one that sets it to its own call's need could lower it between another's
+// setting and launch.
+template <auto Kernel, int Bytes>
+hipError_t allow_lds() {
+  static std::atomic<uint64_t> devices{0};
+  int device = 0;
+  hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+  if (devices.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kernel),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, Bytes);
+  if (e == hipSuccess) devices.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // -------------------------------------------------------------- 4-bit rows ----
 

@@ -7,7 +7,7 @@ import math
 import pytest
 
 from tests.parity import say
-from tests.test_gpu_block import Attn, Heads, _round, _same_lse, _within, torch  # noqa: F401
+from tests.test_gpu_block import Attn, Heads, Rows4, _round, _same_lse, _within, torch  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +132,33 @@ def test_heads_at_position_zero(torch, pairs):  # noqa: F811
     for got, ref in zip(c.layer().forward(c.x, c.pos), c.split(c.x)):
         assert torch.equal(got.nan_to_num(9e9), ref.nan_to_num(9e9))
         assert torch.equal(got.isnan(), ref.isnan())
+
+
+# ----------------------------------------------------------------- 4-bit rows ----
+
+def test_rows4_from_two_host_threads(torch):  # noqa: F811
+    """Calls of one kernel with unlike needs of LDS, from two threads at once."""
+    import threading
+    from bit_post_quantization_amd import GroupLinear4
+    c = Rows4(torch, 8, 4096, 400, 64, "f32", "f32", "silu", True)
+    layer = c.layer()
+    assert isinstance(layer, GroupLinear4)
+    want = {m: layer.apply(c.X[:m]) for m in (8, 5)}
+    torch.cuda.synchronize()
+    failed = []
+
+    def calls(m):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                outs = [layer.apply(c.X[:m]) for _ in range(300)]
+                torch.cuda.current_stream().synchronize()
+            failed.extend(m for o in outs if not torch.equal(o, want[m]))
+        except Exception as e:  # noqa: BLE001  (a thread's failure is reported by the test)
+            failed.append(e)
+
+    threads = [threading.Thread(target=calls, args=(m,)) for m in (8, 5)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed[:3]
