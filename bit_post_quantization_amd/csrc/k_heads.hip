@@ -438,22 +438,31 @@ __global__ __launch_bounds__(1024) void k_heads_gamma(HeadsArgs a) {
 
 // ------------------------------------------------------------------ launch ----
 
+// How a call's rows are read.
+int mode_of(const HeadsArgs& a) { return !a.vec ? kByElement : a.halves && a.n_axes ? kApart : kAdjacent; }
+
 template <typename XT, typename YT, int G, int C>
 hipError_t run(const HeadsArgs& a, bool grad, dim3 grid, hipStream_t s) {
-  const int mode = !a.vec ? kByElement : a.halves && a.n_axes ? kApart : kAdjacent;
+  const int mode = mode_of(a);
   const size_t lds = (size_t)a.tokens * (mode == kAdjacent ? a.D / 2 : a.D) * sizeof(float2);
-#define QL_HEADS_MODE(M)                                      \
-  if (mode == M) {                                            \
-    if (grad)                                                 \
-      k_heads_grad<XT, YT, G, C, M><<<grid, kThreads, lds, s>>>(a); \
-    else                                                      \
-      k_heads<XT, YT, G, C, M><<<grid, kThreads, lds, s>>>(a);   \
+  // the kernels' own LDS and the turns of kMaxTokens tokens pass 64 KB at long heads of few
+  constexpr int most = kMaxTokens * kMaxDim * (int)sizeof(float2);
+  hipError_t e = hipSuccess;
+#define QL_HEADS_MODE(M)                                                              \
+  if (mode == M) {                                                                    \
+    if (grad) {                                                                       \
+      if (M != kAdjacent) e = allow_lds<&k_heads_grad<XT, YT, G, C, M>, most>();      \
+      if (e == hipSuccess) k_heads_grad<XT, YT, G, C, M><<<grid, kThreads, lds, s>>>(a); \
+    } else {                                                                          \
+      if (M != kAdjacent) e = allow_lds<&k_heads<XT, YT, G, C, M>, most>();           \
+      if (e == hipSuccess) k_heads<XT, YT, G, C, M><<<grid, kThreads, lds, s>>>(a);   \
+    }                                                                                 \
   }
   QL_HEADS_MODE(kAdjacent)
   QL_HEADS_MODE(kApart)
   QL_HEADS_MODE(kByElement)
 #undef QL_HEADS_MODE
-  return hipGetLastError();
+  return e == hipSuccess ? hipGetLastError() : e;
 }
 
 // Lanes of a head: as few as keep a lane's values in registers with room for other waves,
@@ -481,15 +490,28 @@ hipError_t go(const HeadsArgs& a, bool grad, dim3 grid, hipStream_t s) {
   return a.y_bf16 ? pick<float, bf16>(a, grad, grid, s) : pick<float, float>(a, grad, grid, s);
 }
 
-// Tokens of a workgroup: enough rows for four passes of its lanes, unless that
-// leaves fewer workgroups than fill the chip.
-int tokens_of(int64_t all, int heads, int D, bool x_bf16) {
-  const int groups = kThreads / (x_bf16 ? lanes_of<bf16>(D) : lanes_of<float>(D));
+// LDS of k_heads but for the turns: the gammas, the partners, the tokens' starts, and a room for
+// each head where partners trade places.
+int fixed_lds(const HeadsArgs& a, int lanes) {
+  const int padded = a.D == 64 || a.D == 128 ? a.D : (a.D + 31) / 32 * 32;
+  const int rooms = mode_of(a) == kAdjacent ? 16 : kThreads / lanes * (padded + 1) * 4;
+  return 2 * kMaxDim * 4 + kMaxDim + kMaxTokens * (int)sizeof(Starts) + 64 + rooms;
+}
+
+// Tokens of a workgroup: enough rows for four passes of its lanes, unless that leaves fewer
+// workgroups than fill the chip; forward no more than leave LDS for two workgroups on a compute
+// unit (three heads of 160 a token, pairs in halves, bf16, 120000 tokens: 251 us with the 32 tokens
+// that take 87 KB, 164 with the 27 that take 80, 182 with 14 and 64). The gradient, whose workgroups
+// take one part's heads each and walk over many tokens, keeps them (502, 564, 828).
+int tokens_of(const HeadsArgs& a, int64_t all, int heads, bool grad) {
+  const int lanes = a.x_bf16 ? lanes_of<bf16>(a.D) : lanes_of<float>(a.D), groups = kThreads / lanes;
   int t = 1;
   while (t < kMaxTokens && t * heads < 4 * groups &&
          (t * heads < groups || all / (2 * t) >= 1024))
     t *= 2;
-  return t;
+  const int each = (mode_of(a) == kAdjacent ? a.D / 2 : a.D) * (int)sizeof(float2);
+  const int most = (80 * 1024 - fixed_lds(a, lanes)) / each;
+  return grad || t < most ? t : most;
 }
 
 }  // namespace
@@ -502,7 +524,7 @@ int heads_grad_groups(int64_t tokens, int heads) {
 hipError_t launch_heads(const HeadsArgs& args, hipStream_t s) {
   HeadsArgs a = args;
   const int64_t all = (int64_t)a.B * a.L;
-  a.tokens = tokens_of(all, a.heads[0] + a.heads[1] + a.heads[2], a.D, a.x_bf16);
+  a.tokens = tokens_of(a, all, a.heads[0] + a.heads[1] + a.heads[2], false);
   return go(a, false, dim3((unsigned)((all + a.tokens - 1) / a.tokens)), s);
 }
 
@@ -511,7 +533,7 @@ hipError_t launch_heads_grad(const HeadsArgs& args, hipStream_t s) {
   const int64_t all = (int64_t)a.B * a.L;
   if (all > 0) {
     const int most = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
-    a.tokens = tokens_of(all, most > a.heads[2] ? most : a.heads[2], a.D, a.x_bf16);
+    a.tokens = tokens_of(a, all, most > a.heads[2] ? most : a.heads[2], true);
     const hipError_t e = go(a, true, dim3((unsigned)a.groups, 3), s);
     if (e != hipSuccess) return e;
   }

@@ -134,6 +134,36 @@ def test_heads_at_position_zero(torch, pairs):  # noqa: F811
         assert torch.equal(got.isnan(), ref.isnan())
 
 
+HEADS_LDS = [
+    # heads long and few, positions many: a workgroup's tokens and rooms fill LDS
+    (1, 3000, (1, 1, 1), 160, (40, 60, 60), "halves", "bf16", "bf16", "f32", "rms", "shared"),
+    (1, 3000, (1, 1, 1), 136, (40, 40, 40), "halves", "bf16", "f32", "f32", "rms", "own"),
+    (2, 1500, (2, 1, 1), 120, (120,), "halves", "bf16", "bf16", "bf16", "rms", "shared"),
+    (1, 3000, (1, 1, 1), 112, (40, 40), "halves", "bf16", "bf16", "f32", "none", "shared"),
+    (1, 3000, (1, 1, 1), 160, (160,), "halves", "f32", "f32", "f32", "rms", "shared"),
+    (1, 40000, (1, 0, 0), 160, (80, 80), "halves", "bf16", "bf16", "f32", "rms", "shared"),
+]
+
+
+@pytest.mark.parametrize("shift", [0, 3])
+@pytest.mark.parametrize("case", HEADS_LDS, ids=str)
+def test_heads_with_much_lds(torch, case, shift):  # noqa: F811
+    say(f"[heads, much LDS] {case} {shift}")
+    c = Heads(torch, *case)
+    wide = torch.zeros(*c.x.shape[:2], c.x.shape[2] + shift, device="cuda", dtype=c.x.dtype)
+    wide[:, :, shift:] = c.x
+    for got, ref, tol, h in zip(c.layer().forward(wide[:, :, shift:], c.pos),
+                                c.formula(c.x.double()), c.bounds(), c.heads):
+        if h:
+            _within(got, ref, tol + _round(torch, ref, got.dtype), "y")
+    dx, dgq, dgk = c.layer().grad(c.dy, wide[:, :, shift:], c.pos)
+    ref, tol = c.grads()
+    _within(dx, ref[0], tol[0] + _round(torch, ref[0], dx.dtype), "dx")
+    if c.norm == "rms":
+        for got, r, e in zip((dgq, dgk), ref[1:], tol[1:]):
+            _within(got, r, e + _round(torch, r, got.dtype), "dgamma")
+
+
 # ----------------------------------------------------------------- 4-bit rows ----
 
 def test_rows4_from_two_host_threads(torch):  # noqa: F811
