@@ -5,9 +5,10 @@
 // A modulation linear reads a conditioning vector an image: the weights are most of what
 // moves (N K / 2 bytes), so the kernel is built to read them once, in order, with many
 // loads in flight, and to do little for each code. The product is one of integers:
-// act(X) is written in fixed point, for each row and unit of 128 inputs 30 bits below
-// the largest value's power of two, as four signed 8-bit digits (t = x + 0x00808080, the
-// bytes of t ^ 0x00808080). What that drops is 2^-31 of the unit's largest value,
+// act(X) is written in fixed point, for each row and unit of 128 inputs 31 bits below
+// the power of two above the largest value, as four signed 8-bit digits (t = x + 0x00808080, the
+// bytes of t ^ 0x00808080; they hold up to 0x7f7f7f7f, so 30 bits where the value is within
+// 0.4 % of that power). What that drops is at most 1.004 * 2^-31 of the unit's largest value,
 // and nothing of values within 2^-6 of it. v_mfma_i32_16x16x64_i8 (x32 for groups of 32)
 // multiplies 16 output channels' codes by 16 rows' digits exactly; codes go in as
 // 16 times their value, so that eight of them take three operations (in bf16, with X in
@@ -101,17 +102,19 @@ __device__ __forceinline__ float digits(const Rows4Args& a, int m, int k, uint2 
     finite = finite && fabsf(v[j]) < INFINITY;
     top = fmaxf(top, fabsf(v[j]));
   }
-  int t = finite ? (int)(__float_as_uint(top) >> 23) : 255;
+  // largest value's exponent, one more where its mantissa, as 31 bits, is past 0x7f7f7f7f
+  int t = finite ? (int)((__float_as_uint(top) + 0x010101u) >> 23) : 256;
   t = max(t, (int)xor_lane_u<1>(t));
   t = max(t, (int)xor_lane_u<2>(t));
   t = max(t, (int)xor_lane_u<4>(t));
   t = max(t, (int)xor_lane_u<8>(t));
-  // largest value < 2^(t - 126), t = 255: not finite; worths stay normal numbers
-  const int e = max(t, 35) - 126;
+  // largest value <= 0x7f7f7f7f 2^(e - 31), t = 256: not finite; worths are powers of two that
+  // fp32 has, down to its smallest
+  const int e = max(t, 12) - 126;
   uint32_t x[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int i = (int)rintf(ldexpf(v[j], 30 - e));
+    const int i = (int)rintf(ldexpf(v[j], 31 - e));
     x[j] = ((uint32_t)i + 0x00808080u) ^ 0x00808080u;
   }
 #pragma unroll
@@ -125,7 +128,7 @@ __device__ __forceinline__ float digits(const Rows4Args& a, int m, int k, uint2 
 #pragma unroll
     for (int d = 0; d < 4; ++d) (h ? out[d].y : out[d].x) = w[d];
   }
-  return t == 255 ? NAN : ldexpf(1.0f, e - 34);
+  return t == 256 ? NAN : ldexpf(1.0f, e - 35);
 }
 
 // LDS for rows' digits: whole kilobytes, as they are copied.

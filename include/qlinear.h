@@ -539,10 +539,11 @@ ql_status qlinear_rows4_workspace(const ql_rows4* d, int32_t M, int64_t* bytes);
  * code[n,k] act(X[m,k]), sums in fp32.
  *   X : DEVICE [M,K] of x_dtype, row stride ldx >= K elements, M <= 2^20.
  *   Y : DEVICE fp32 out [M,N], row stride ldy >= N; overlaps nothing else.
- * act(X) is multiplied in fixed point, exact to 2^-31 of the largest value of each 128
- * inputs of a row; an infinity or a NaN among them makes the row's outputs NaN. Values
- * beyond 2^100 may overflow. Meant for few rows: the weights are read again for every
- * 16 to 48 of them. M = 0 enqueues nothing.
+ * act(X) is multiplied in fixed point: an input is off by at most 1.004 * 2^-31 of the largest
+ * value among its row's 128 (inputs 128 i .. 128 i + 127), or 2^-146 if that is more. So it
+ * keeps fp32's own accuracy down to 2^-7 of that largest value, and less of it further down. An
+ * infinity or a NaN makes the row's outputs NaN. Meant for few rows: the weights are read again
+ * for every 16 to 48 of them. M = 0 enqueues nothing.
  */
 ql_status qlinear_rows4(const ql_rows4* d, const void* X, int64_t ldx, int32_t M, float* Y,
                         int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream);

@@ -7,7 +7,7 @@ import math
 import pytest
 
 from tests.parity import say
-from tests.test_gpu_block import Attn, Heads, Rows4, _round, _same_lse, _within, torch  # noqa: F401
+from tests.test_gpu_block import EPS, Attn, Heads, Rows4, _gen, _round, _same_lse, _within, torch  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -165,6 +165,40 @@ def test_heads_with_much_lds(torch, case, shift):  # noqa: F811
 
 
 # ----------------------------------------------------------------- 4-bit rows ----
+
+def test_rows4_bound_of_one_input(torch):  # noqa: F811
+    """Each output reads one small input behind a code of 7, and none the unit's large one:
+    off by no more than 1.004 * 2^-31 of that large one (half a step of the fixed point, which
+    lies 31 bits below its power of two; 30 where it is within 0.4 % of the next), times 7,
+    and two roundings."""
+    from bit_post_quantization_amd import GroupLinear4
+    K, N, M = 128, 127, 64
+    codes = torch.zeros(N, K, dtype=torch.int8, device="cuda")
+    codes[torch.arange(N), torch.arange(1, K)] = 7
+    layer = GroupLinear4.from_codes(codes, torch.ones(N, 1, device="cuda"), 128)
+    X = torch.empty(M, K, device="cuda").normal_(generator=_gen(torch, 1))
+    large = 2.0 ** 10 * torch.linspace(1.0, 2.0, M, device="cuda")
+    large[1], large[2] = 2047.9999, -2.0 ** 10 * 1.9922  # next to the border
+    X[:, 0] = large
+    got = layer.apply(X).double()
+    ref = 7 * X[:, 1:].double()
+    step = 1.004 * 2.0 ** -31 * large.double().abs()[:, None]
+    bound = 7 * step + 2 * EPS * (ref.abs() + 7 * step)
+    worst = float(((got - ref).abs() / bound).max())
+    say(f"  worst {worst:.3f} of the bound")
+    assert worst <= 1.0
+
+
+@pytest.mark.parametrize("power", [-112, -105, -95, 60, 96])
+def test_rows4_rows_of_any_size(torch, power):  # noqa: F811
+    """The fixed point follows a row's size: down to 2^-114, where it stays, and up to where
+    the sums themselves leave fp32 (codes and scales of up to 9 and 512 inputs of up to 8
+    make 2^16)."""
+    c = Rows4(torch, 3, 512, 65, 64, "f32", "f32", "none", False)
+    c.X *= 2.0 ** power
+    ref, tol = c.formula()
+    _within(c.layer().apply(c.X), ref, tol, "Y")
+
 
 def test_rows4_from_two_host_threads(torch):  # noqa: F811
     """Calls of one kernel with unlike needs of LDS, from two threads at once."""
