@@ -33,7 +33,6 @@ namespace {
 typedef __bf16 bf16;
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef bf16 v8h __attribute__((ext_vector_type(8)));
-typedef bf16 v4h __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
@@ -334,23 +333,47 @@ __global__ __launch_bounds__(256) void k_rows4_join(Rows4Args a) {
 }
 
 // How a call is cut. Digits are formed in every workgroup while that is little work (up
-// to 16384 values; at 2 x 1152 a launch of its own for them makes 11 us of 7), else once. A
-// workgroup takes as many tiles as leave one a compute unit (at 8 rows, K 4096, N 24576
-// six tiles take 24 us, four 31), four at groups of 32, whose scales fill the registers.
+// to 16384 values; at 2 x 1152 a launch of its own for them makes 11 us of 7), else once.
 // More than 16 rows go to workgroups by 16, by 32 or 48 where those still fill 200 compute
 // units (77 rows, K 4608, N 1151: 22 us by 48, 18 by 32, 20 by 16).
+//
+// A workgroup takes 1, 2, 4 or 6 tiles, whichever ends first where workgroups run in rounds of
+// one a compute unit and a round takes the time of its tiles and of about one more (its digits and
+// its joining; two and a half where digits of groups of 64 or 128 come from memory). 8 rows, K 4096,
+// groups of 64, bf16 scales, us by 1, 2, 4 and 6 tiles:
+//   N 12288 19.6 19.2 16.7 20.0    N 16400 27.8 25.2 26.9 20.6    N 24576 37.3 28.7 30.7 24.7
+//   N 24592 41.0 34.8 30.7 36.7    N 28672 42.5 35.9 31.6 38.4    N 49152 69.1 51.3 44.9 42.6
+// 2 rows of fp32, K 1152, N 16400: 9.3 9.8 11.8 8.9; 16 rows, K 4096, N 18432, digits from memory:
+// 36.1 29.9 27.1 21.3. Fewer tiles where a unit's scales leave too few registers (N 24576, K 4096):
+// fp32 scales in groups of 32 take two at most (44 36 46 75; bf16 ones all six, 44 36 38 32), and
+// digits from memory four, in groups of 32 (48 37 40 40) and with fp32 scales in groups of 64 (45 33
+// 30 34). Two tiles of 48 rows in groups of 32 spill up to 37 registers and still pay (48 rows: 95
+// us, one tile 109; 77 rows, N 4608: 54, 51).
 struct Cut {
   int src, NT, MB, splits;
 };
-Cut cut(int M, int N, int K, int group) {
+// The most tiles of a workgroup for its form.
+constexpr int most_tiles(int src, int group, bool s_bf16) {
+  return group == 32 ? (!s_bf16 ? 2 : src == kRead ? 4 : 6)
+                     : group == 64 && src == kRead && !s_bf16 ? 4 : 6;
+}
+Cut cut(int M, int N, int K, int group, bool s_bf16) {
   Cut c{};
   const int tiles = (N + 15) / 16, units = (K + kUnit - 1) / kUnit;
   c.MB = M > 32 && tiles * (int64_t)((M + 47) / 48) >= 200 ? 3 : M > 16 && tiles * (int64_t)((M + 31) / 32) >= 200 ? 2 : 1;
   const int64_t groups = (M + 16 * c.MB - 1) / (16 * c.MB);
   const bool fits = M <= 16 && digit_bytes(M, units) + M * units * 4 <= kXBytes;
   c.src = !fits ? kRead : M * units * kUnit <= 16384 ? kForm : kCopy;
-  const int64_t each = tiles * groups / 256;  // tiles of a workgroup, one a compute unit
-  c.NT = c.MB > 1 ? (each >= 2 ? 2 : 1) : each >= 6 && group > 32 ? 6 : each >= 4 ? 4 : each >= 2 ? 2 : 1;
+  const int most = c.MB > 1 ? 2 : most_tiles(c.src, group, s_bf16);
+  const int more = c.src == kRead && group > 32 ? 5 : 2;  // of half tiles
+  int64_t best = 0;
+  for (const int n : {1, 2, 4, 6}) {
+    const int64_t rounds = ((tiles + n - 1) / n * groups + 255) / 256, time = rounds * (2 * n + more);
+    if (n <= most && (n == 1 || time <= best)) {
+      best = time;
+      c.NT = n;
+    }
+  }
   const int64_t base = (tiles + c.NT - 1) / c.NT * groups;
   int64_t n = 256 / base;
   if (base > 96 || units < 16) n = 1;
@@ -379,9 +402,12 @@ hipError_t run(const Rows4Args& a, hipStream_t s) {
 
 template <int NT, int MB, int SRC, typename S>
 hipError_t pick_group(const Rows4Args& a, hipStream_t s) {
-  if (a.group == 32) return run<NT, MB, 1, SRC, S>(a, s);
-  if (a.group == 64) return run<NT, MB, 2, SRC, S>(a, s);
-  return run<NT, MB, 4, SRC, S>(a, s);
+  constexpr bool b = sizeof(S) == 2;
+  if constexpr (MB > 1 || NT <= most_tiles(SRC, 32, b))
+    if (a.group == 32) return run<NT, MB, 1, SRC, S>(a, s);
+  if constexpr (MB > 1 || NT <= most_tiles(SRC, 64, b))
+    if (a.group == 64) return run<NT, MB, 2, SRC, S>(a, s);
+  return a.group == 128 ? run<NT, MB, 4, SRC, S>(a, s) : hipErrorInvalidValue;
 }
 
 template <int NT, int MB, int SRC>
@@ -522,7 +548,7 @@ Rows4Layout rows4_layout(const ql_rows4& d) {
 Rows4Ws rows4_ws(const ql_rows4& d, int M) {
   Rows4Ws w{};
   if (M < 1) return w;
-  const Cut c = cut(M, d.N, d.K, d.group);
+  const Cut c = cut(M, d.N, d.K, d.group, d.s_dtype == QL_BF16);
   const int64_t units = (d.K + kUnit - 1) / kUnit, blocks = (M + 15) / 16;
   if (c.src != kForm) {
     w.worths = blocks * 16 * units * kUnitBytes;
@@ -534,7 +560,7 @@ Rows4Ws rows4_ws(const ql_rows4& d, int M) {
 
 hipError_t launch_rows4(const Rows4Args& args, hipStream_t s) {
   Rows4Args a = args;
-  const Cut c = cut(a.M, a.N, a.K, a.group);
+  const Cut c = cut(a.M, a.N, a.K, a.group, a.s_bf16);
   a.splits = c.splits;
   hipError_t e = hipErrorInvalidValue;
 #define QL_ROWS4(T)                                               \

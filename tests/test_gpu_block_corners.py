@@ -226,3 +226,29 @@ def test_rows4_from_two_host_threads(torch):  # noqa: F811
     for t in threads:
         t.join()
     assert not failed, failed[:3]
+
+
+ROWS4_TILES = [
+    # M, K, N, group, x, s, act, bias: six tiles, four and two of every form that takes them, and
+    # widths next to where a round of workgroups ends
+    (8, 2304, 24576, 32, "bf16", "bf16", "silu", True),
+    (4, 1152, 24600, 32, "f32", "bf16", "none", True),
+    (8, 2304, 24600, 32, "f32", "f32", "none", False),
+    (16, 4096, 12288, 32, "bf16", "bf16", "none", True),
+    (16, 4096, 12300, 64, "bf16", "f32", "silu", True),
+    (16, 4096, 24576, 64, "f32", "bf16", "none", False),
+    (2, 128, 4096, 128, "f32", "f32", "none", True),
+    (2, 128, 4097, 128, "f32", "f32", "none", True),
+    (1, 128, 8208, 64, "bf16", "f32", "silu", True),
+    (3, 256, 24592, 64, "f32", "bf16", "none", True),
+    (20, 256, 8200, 32, "bf16", "f32", "none", True),
+    (40, 256, 4500, 32, "f32", "bf16", "none", True),
+]
+
+
+@pytest.mark.parametrize("case", ROWS4_TILES, ids=str)
+def test_rows4_tiles_of_a_workgroup(torch, case):  # noqa: F811
+    say(f"[rows4 tiles] {case}")
+    c = Rows4(torch, *case)
+    ref, tol = c.formula()
+    _within(c.layer().apply(c.X), ref, tol, "Y")
