@@ -516,8 +516,7 @@ int tokens_of(const HeadsArgs& a, int64_t all, int heads, bool grad) {
 
 }  // namespace
 
-int heads_grad_groups(int64_t tokens, int heads) {
-  (void)heads;
+int heads_grad_groups(int64_t tokens) {
   return (int)(tokens < 512 ? (tokens < 1 ? 1 : tokens) : 512);
 }
 

@@ -93,7 +93,7 @@ struct HeadsArgs {
   int groups;     // workgroups of the gradient
 };
 // Workgroups of the gradient call (each has a row of partial sums).
-int heads_grad_groups(int64_t tokens, int heads);
+int heads_grad_groups(int64_t tokens);
 hipError_t launch_heads(const HeadsArgs& a, hipStream_t s);
 hipError_t launch_heads_grad(const HeadsArgs& a, hipStream_t s);
 

@@ -243,7 +243,7 @@ ql::HeadsArgs heads_args(const ql_heads* d, const void* x, int64_t xb, int64_t x
 }
 
 int heads_groups(const ql_heads* d) {
-  return ql::heads_grad_groups((int64_t)d->batch * d->positions, d->q_heads + d->k_heads);
+  return ql::heads_grad_groups((int64_t)d->batch * d->positions);
 }
 
 int64_t heads_ws(const ql_heads* d) {
