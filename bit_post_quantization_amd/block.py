@@ -101,6 +101,15 @@ def qlinear_attention_grad(desc: QlAttn, dout, q, k, v, out, lse, dq, dk, dv, wo
                                     workspace, workspace_bytes, stream))
 
 
+def _keep(dev: int, *tensors) -> None:
+    """Memory of tensors (None: no matter) goes to no other use before the current stream is
+    done with it."""
+    stream = torch.cuda.current_stream(dev)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 # ----------------------------------------------------------------- 4-bit rows ----
 
 class GroupLinear4:
@@ -156,11 +165,12 @@ class GroupLinear4:
         self._sizes = {}  # descriptor and workspace bytes by type and rows of a call
 
     def _ready(self, dev: int) -> int:
-        """The current stream's handle, on which the packed weights may be read from now on."""
+        """The current stream's handle, on which the packed weights and the bias may be read from
+        now on."""
         _need(dev == self.packed.get_device(), "the layer's weights are not on the current device")
         s = _stream(dev)
         if s != self._made_on:  # their memory outlives the layer until this stream is done
-            self.packed.record_stream(torch.cuda.current_stream(dev))
+            _keep(dev, self.packed, self.bias)
         return s
 
     def apply(self, X, out=None, stream=None):
@@ -291,9 +301,8 @@ class HeadNormRope:
             at = _flat(pos, "pos", dev, kind, (shape[0], *want) if own else want)
             pb = want[0] * want[1] if own else 0
         s = _stream(dev)
-        if s != self._made_on and self.freqs is not None:
-            # the table's memory outlives the layer until this stream is done
-            self.freqs.record_stream(torch.cuda.current_stream(dev))
+        if s != self._made_on:  # what the layer holds outlives it until this stream is done
+            _keep(dev, self.freqs, self.gamma_q, self.gamma_k)
         return dev, s, size, xb, xr, at, pb
 
     def _size(self, dt, shape, kind):

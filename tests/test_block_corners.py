@@ -1,0 +1,48 @@
+"""What a conditioned block's operators refuse or keep alive in corners of their calls, on the
+CPU."""
+from __future__ import annotations
+
+import torch
+
+from bit_post_quantization_amd import block
+from tests.test_block_binding import _rows, on_cpu  # noqa: F401
+
+
+class _Kept:
+    """A tensor's place: which streams were told of it."""
+
+    def __init__(self):
+        self.on = []
+
+    def record_stream(self, stream):
+        self.on.append(stream)
+
+    def get_device(self):
+        return -1
+
+    def data_ptr(self):
+        return 0x1000
+
+
+def test_what_a_layer_holds_outlives_it_on_other_streams(on_cpu, monkeypatch):  # noqa: F811
+    """Kernels on another stream than the layer's read its packed weights and bias, or its
+    frequencies and gammas: all of them are recorded there, and nothing on its own stream."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: "side")
+    r = _rows()
+    r.packed, r.bias = _Kept(), _Kept()
+    r.apply(torch.zeros(2, 128))
+    assert r.packed.on == [] and r.bias.on == []
+    r._made_on = 8
+    r.apply(torch.zeros(2, 128))
+    assert r.packed.on == ["side"] and r.bias.on == ["side"]
+    h = block.HeadNormRope((1, 1, 0), 8)
+    h.gamma_q, h.gamma_k = _Kept(), _Kept()
+    x = torch.zeros(1, 2, 16)
+    h.forward(x)
+    assert h.gamma_q.on == [] and h.gamma_k.on == []
+    h._made_on = 8
+    h.forward(x)
+    assert h.gamma_q.on == ["side"] and h.gamma_k.on == ["side"]
+    h.gamma_q = None  # 1
+    h.forward(x)
+    assert h.gamma_k.on == ["side", "side"]
