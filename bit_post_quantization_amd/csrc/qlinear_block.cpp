@@ -548,15 +548,13 @@ ql_status qlinear_heads_grad(const ql_heads* d, const ql_heads_view* dq, const q
     a.vec = a.vec && whole(dx, size_of(d->x_dtype), d->batch, dx_batch, d->positions, dx_row, 1, 0);
     if (dx == x || (dx == a.y[0].p || dx == a.y[1].p || dx == a.y[2].p))
       return fail(QL_ERR_ARG, "dx must differ from x, dq, dk and dv");
-    const void* const g[2] = {dgamma_q, dgamma_k};
-    for (int i = 0; i < 2; ++i)
-      if (g[i] && (g[i] == g[1 - i] || g[i] == d->gamma_q || g[i] == d->gamma_k || g[i] == dx))
-        return fail(QL_ERR_ARG, "dgamma_q and dgamma_k must differ from each other, the gammas and dx");
   } else {
     a = heads_args(d, nullptr, 0, 0, nullptr, 0, {nullptr, nullptr, nullptr});
-    if (dgamma_q && dgamma_q == dgamma_k)
-      return fail(QL_ERR_ARG, "dgamma_q and dgamma_k must differ");
   }
+  const void* const g[2] = {dgamma_q, dgamma_k};  // written without positions too
+  for (int i = 0; i < 2; ++i)
+    if (g[i] && (g[i] == g[1 - i] || g[i] == d->gamma_q || g[i] == d->gamma_k || g[i] == dx))
+      return fail(QL_ERR_ARG, "dgamma_q and dgamma_k must differ from each other, the gammas and dx");
   a.dx = dx;
   a.db = dx_batch;
   a.dr = dx_row;

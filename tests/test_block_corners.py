@@ -5,7 +5,18 @@ from __future__ import annotations
 import torch
 
 from bit_post_quantization_amd import block
+from tests.test_block_abi import A, ARG, U, _heads, _heads_calls
 from tests.test_block_binding import _rows, on_cpu  # noqa: F401
+
+
+def test_heads_empty_batch_keeps_its_parameters():
+    """Gradients of a batch without positions are written too (zeros): over the gammas they are
+    refused as in any other call."""
+    d = _heads(positions=0, gamma_q=A, gamma_k=A + 512)
+    none = dict(x=U, pos=U, q=None, k=None, v=None, dx=U, ws=U, nb=0)
+    for gq, gk in ((A, U), (U, A + 512), (A + 512, U), (A + 1024, A + 1024)):
+        _, b, _, msg = _heads_calls(d, gq=gq, gk=gk, **none)
+        assert b == ARG and "must differ" in msg, (gq, gk, msg)
 
 
 class _Kept:
