@@ -253,6 +253,8 @@ int64_t heads_ws(const ql_heads* d) {
 
 // --------------------------------------------------------------- attention ----
 
+float base2(float scale) { return (float)((double)scale * 1.4426950408889634074); }
+
 ql_status check_attn(const ql_attn* d) {
   if (!d) return fail(QL_ERR_ARG, "descriptor is NULL");
   if (d->batch < 0 || d->q_len < 0 || d->k_len < 0)
@@ -265,8 +267,10 @@ ql_status check_attn(const ql_attn* d) {
     return fail(QL_ERR_ARG, "dim = %d must be a positive multiple of 8", d->dim);
   if (d->dim > 160) return fail(QL_ERR_UNSUPPORTED, "dim = %d: at most 160", d->dim);
   if (!dtype_ok(d->dtype)) return fail(QL_ERR_ARG, "bad dtype %d", (int)d->dtype);
-  if (!(d->scale > 0.0f) || !std::isfinite(d->scale))
-    return fail(QL_ERR_ARG, "scale = %g must be positive and finite", (double)d->scale);
+  // the kernels multiply with scale log2(e)
+  if (!(d->scale > 0.0f) || !std::isfinite(base2(d->scale)))
+    return fail(QL_ERR_ARG, "scale = %g must be positive and less than 2^128 / log2(e)",
+                (double)d->scale);
   typedef __int128 wide;
   if ((wide)d->batch * d->heads * d->q_len >= (wide)1 << 31 ||
       (wide)d->batch * d->kv_heads * d->k_len >= (wide)1 << 31 ||
@@ -312,7 +316,7 @@ ql::AttnArgs attn_args(const ql_attn* d) {
          (int64_t)a.B * a.Hk / (2 * a.unit) >= 32)
     a.unit *= 2;
   a.scale = d->scale;
-  a.scale2 = (float)((double)d->scale * 1.4426950408889634074);
+  a.scale2 = base2(d->scale);
   a.bf16 = d->dtype == QL_BF16;
   return a;
 }

@@ -630,7 +630,7 @@ typedef struct {
   int32_t heads, kv_heads;      /* heads a positive multiple of kv_heads */
   int32_t dim;                  /* 8 .. 160, a multiple of 8 */
   ql_dtype dtype;               /* of all tensors by heads */
-  float scale;                  /* > 0, finite */
+  float scale;                  /* > 0, < 2^128 / log2(e) */
   const int32_t* k_lens;        /* DEVICE [batch], clamped to [0, k_len], or NULL for k_len */
   const uint8_t* k_mask;        /* DEVICE [batch, k_len], 0: does not count; or NULL */
   int64_t mask_batch;           /* batch stride of k_mask in bytes */

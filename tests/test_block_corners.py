@@ -2,10 +2,12 @@
 CPU."""
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
-from bit_post_quantization_amd import block
-from tests.test_block_abi import A, ARG, U, _heads, _heads_calls
+from bit_post_quantization_amd import _lib, block
+from tests.test_block_abi import A, ARG, OK, U, _attn, _heads, _heads_calls, _msg
 from tests.test_block_binding import _rows, on_cpu  # noqa: F401
 
 
@@ -17,6 +19,15 @@ def test_heads_empty_batch_keeps_its_parameters():
     for gq, gk in ((A, U), (U, A + 512), (A + 512, U), (A + 1024, A + 1024)):
         _, b, _, msg = _heads_calls(d, gq=gq, gk=gk, **none)
         assert b == ARG and "must differ" in msg, (gq, gk, msg)
+
+
+def test_attention_scale_past_its_base_two_form():
+    """scale log2(e) is what the kernels multiply with: it has to be finite too."""
+    n, L = ctypes.c_int64(), _lib.load()
+    for scale, status in ((3e38, ARG), (2.4e38, ARG), (2.3e38, OK), (1e-30, OK)):
+        assert L.qlinear_attention_workspace(ctypes.byref(_attn(scale=scale)), 0,
+                                             ctypes.byref(n)) == status, scale
+        assert status == OK or "scale" in _msg()
 
 
 class _Kept:
