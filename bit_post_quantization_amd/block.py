@@ -20,7 +20,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from ._lib import QlAttn, QlHeads, QlHeadsView, QlRows4, check
+from ._lib import QL_ERR_ARG, QlAttn, QLError, QlHeads, QlHeadsView, QlRows4, check
 from .ops import (_ACTS, _DT, _F32, _F64, _I32, _L, _NAMES, _byref, _device, _flat, _need, _on,
                   _ptr, _refuse, _remember, _rows, _stream)
 
@@ -110,6 +110,13 @@ def _keep(dev: int, *tensors) -> None:
             t.record_stream(stream)
 
 
+def _fit(*sizes: int) -> None:
+    """Sizes go to the C ABI as 32-bit numbers, which ctypes would cut off."""
+    for n in sizes:
+        if not -(1 << 31) <= n < 1 << 31:
+            raise QLError(QL_ERR_ARG, f"size {n}: less than 2^31")
+
+
 # ----------------------------------------------------------------- 4-bit rows ----
 
 class GroupLinear4:
@@ -126,6 +133,7 @@ class GroupLinear4:
     def __init__(self, W, group: int = 128, bias=None, act: str = "none", s_dtype: str = "f32",
                  stream=None):
         _need(isinstance(W, torch.Tensor) and W.dim() == 2, "W must be [N, K]")
+        _fit(*W.shape, group)
         _need(W.dtype in _DT, f"W is {W.dtype}: f32 or bf16 only")
         _need(s_dtype in _NAMES, f"s_dtype {s_dtype!r} is not one of {sorted(_NAMES)}")
         w = _flat(W, "W", _device(), W.dtype, W.shape)
@@ -137,6 +145,7 @@ class GroupLinear4:
         """From codes int8 [N, K] in [-8, 7] and scales [N, ceil(K / group)], f32 or bf16."""
         self = cls.__new__(cls)
         _need(isinstance(codes, torch.Tensor) and codes.dim() == 2, "codes must be [N, K]")
+        _fit(*codes.shape)
         _need(group in (32, 64, 128), f"group = {group} must be 32, 64 or 128")
         _need(scales.dtype in _DT, f"scales is {scales.dtype}: f32 or bf16 only")
         dev, (N, K) = _device(), codes.shape
@@ -182,6 +191,7 @@ class GroupLinear4:
         size = self._sizes.get((dt, M))
         if size is None:
             _need(dt in _DT, f"X is {dt}: f32 or bf16 only")
+            _fit(M)
             d = QlRows4.from_buffer_copy(self.desc)
             d.x_dtype = _DT[dt]
             size = _remember(self._sizes, (dt, M), (d, qlinear_rows4_workspace(d, M)))
@@ -246,6 +256,7 @@ class HeadNormRope:
         _need(y_dtype in _NAMES, f"y_dtype {y_dtype!r} is not one of {sorted(_NAMES)}")
         _need(len(heads) == 3, "heads must be (query, key, value heads)")
         _need(len(axes) <= _lib.QL_MAX_AXES, f"at most {_lib.QL_MAX_AXES} axes")
+        _fit(dim, *heads, *axes)
         given = [t for t in (gamma_q, gamma_k) if t is not None]
         w = given[0].dtype if given else _F32
         _need(w in _DT, f"gamma_q is {w}: f32 or bf16 only")
@@ -309,6 +320,7 @@ class HeadNormRope:
         _need(dt in _DT, f"x is {dt}: f32 or bf16 only")
         n = sum(self.heads) * self.dim
         _need(len(shape) == 3 and shape[2] == n, f"x is {tuple(shape)}, not [B, L, {n}]")
+        _fit(*shape)
         d = QlHeads.from_buffer_copy(self.desc)
         d.batch, d.positions, d.x_dtype = shape[0], shape[1], _DT[dt]
         d.pos_dtype = _lib.QL_POS_I32 if kind is None else _POS[kind]
@@ -389,6 +401,7 @@ class CrossAttention:
                  scale: Optional[float] = None):
         self.heads, self.dim = heads, dim
         self.kv_heads = heads if kv_heads is None else kv_heads
+        _fit(heads, dim, self.kv_heads)
         self.desc = QlAttn(batch=0, q_len=0, k_len=0, heads=heads, kv_heads=self.kv_heads, dim=dim,
                            dtype=_lib.QL_F32, scale=dim ** -0.5 if scale is None else scale)
         qlinear_attention_workspace(self.desc)  # its checks
@@ -415,6 +428,7 @@ class CrossAttention:
     def _size(self, key, q, k, grad):
         _need(q.dim() == 4 and k.dim() == 4, "q and k must be [B, L, heads, dim]")
         _need(q.dtype in _DT, f"q is {q.dtype}: f32 or bf16 only")
+        _fit(*q.shape, *k.shape)
         d = QlAttn.from_buffer_copy(self.desc)
         d.batch, d.q_len, d.k_len, d.dtype = q.shape[0], q.shape[1], k.shape[1], _DT[q.dtype]
         D, shapes, dense = self.dim, [], []

@@ -4,9 +4,10 @@ from __future__ import annotations
 
 import ctypes
 
+import pytest
 import torch
 
-from bit_post_quantization_amd import _lib, block
+from bit_post_quantization_amd import QLError, _lib, block
 from tests.test_block_abi import A, ARG, OK, U, _attn, _heads, _heads_calls, _msg
 from tests.test_block_binding import _rows, on_cpu  # noqa: F401
 
@@ -28,6 +29,35 @@ def test_attention_scale_past_its_base_two_form():
         assert L.qlinear_attention_workspace(ctypes.byref(_attn(scale=scale)), 0,
                                              ctypes.byref(n)) == status, scale
         assert status == OK or "scale" in _msg()
+
+
+HUGE = (1 << 32) + 5  # as an int32: 5
+
+
+def test_sizes_past_32_bits_are_refused(on_cpu):  # noqa: F811
+    """Sizes reach the C ABI as 32-bit numbers: what does not fit is refused, not cut off."""
+    far = lambda *s: torch.zeros(1).expand(*s)  # noqa: E731
+    a = block.CrossAttention(1, 8)
+    h = block.HeadNormRope((1, 0, 0), 8, norm="none")
+    r = _rows()
+    small = torch.zeros(1, 3, 1, 8)
+    for call in (lambda: r.apply(far(HUGE, 128)),
+                 lambda: h.forward(far(1, HUGE, 8)),
+                 lambda: h.forward(far(HUGE, 1, 8)),
+                 lambda: a.forward(far(1, HUGE, 1, 8), small, small),
+                 lambda: a.forward(small, far(1, HUGE, 1, 8), far(1, HUGE, 1, 8)),
+                 lambda: a.forward(far(HUGE, 1, 1, 8), far(HUGE, 1, 1, 8), far(HUGE, 1, 1, 8)),
+                 lambda: block.CrossAttention(HUGE, 8),
+                 lambda: block.CrossAttention(1, (1 << 32) + 8),
+                 lambda: block.HeadNormRope((HUGE, 0, 0), 8),
+                 lambda: block.HeadNormRope((1, 0, 0), (1 << 32) + 8),
+                 lambda: block.HeadNormRope((1, 0, 0), 8, axes=((1 << 32) + 2,)),
+                 lambda: block.GroupLinear4(far(HUGE, 32)),
+                 lambda: block.GroupLinear4.from_codes(far(HUGE, 32), small, 32),
+                 lambda: block.CrossAttention(4 - (1 << 32), 8)):
+        with pytest.raises(QLError) as e:
+            call()
+        assert "2^31" in str(e.value), e.value
 
 
 class _Kept:
