@@ -164,6 +164,44 @@ def test_heads_with_much_lds(torch, case, shift):  # noqa: F811
             _within(got, r, e + _round(torch, r, got.dtype), "dgamma")
 
 
+@pytest.mark.parametrize("x,y", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
+def test_heads_neighbours_in_unaligned_rows(torch, x, y):  # noqa: F811
+    c = Heads(torch, 2, 33, (3, 2, 2), 72, (36, 20), "adjacent", x, y, "f32", "rms", "own")
+    wide = torch.full((2, 33, 3 + 7 * 72 + 4), math.nan, device="cuda", dtype=c.x.dtype)
+    wide[:, :, 3:-4] = c.x
+    for got, ref, tol in zip(c.layer().forward(wide[:, :, 3:-4], c.pos), c.formula(c.x.double()),
+                             c.bounds()):
+        _within(got, ref, tol + _round(torch, ref, got.dtype), "y")
+    dx, dgq, dgk = c.layer().grad(c.dy, wide[:, :, 3:-4], c.pos)
+    ref, tol = c.grads()
+    for got, r, e in zip((dx, dgq, dgk), ref, tol):
+        _within(got, r, e + _round(torch, r, got.dtype), "gradient")
+
+
+@pytest.mark.parametrize("shift", [0, 8, 3])
+def test_heads_grad_into_strided_rows(torch, shift):  # noqa: F811
+    """dx with strides of its own, as the C ABI takes them: a slice of wider rows of a longer
+    sequence, with and without room for vectors."""
+    from bit_post_quantization_amd import block
+    c = Heads(torch, 2, 21, (3, 2, 2), 64, (32, 16), "halves", "bf16", "bf16", "f32", "rms", "own")
+    layer = c.layer()
+    want = layer.grad(c.dy, c.x, c.pos)
+    width = c.x.shape[2]
+    room = torch.full((2, 30, width + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    dx = room[:, 4:25, shift:shift + width]
+    dev, s, size, xb, xr, at, pb = layer._call(c.x, c.pos)
+    dq, dk, dv = layer._views(c.dy, ("dq", "dk", "dv"), dev, size)
+    dgq, dgk = torch.empty_like(c.gq), torch.empty_like(c.gk)
+    ws = torch.empty(size[1], dtype=torch.uint8, device="cuda")
+    block.qlinear_heads_grad(size[0], dq, dk, dv, c.x.data_ptr(), xb, xr, at, pb, dx.data_ptr(),
+                             dx.stride(0), dx.stride(1), dgq.data_ptr(), dgk.data_ptr(),
+                             ws.data_ptr(), size[1], s)
+    for a, b in zip((dx, dgq, dgk), want):
+        assert torch.equal(a, b)
+    dx.fill_(7.0)
+    assert bool((room == 7).all())
+
+
 # ----------------------------------------------------------------- 4-bit rows ----
 
 def test_rows4_bound_of_one_input(torch):  # noqa: F811
