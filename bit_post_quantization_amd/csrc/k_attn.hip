@@ -61,8 +61,8 @@ typedef __attribute__((address_space(3))) v4s* lds_v4s;
 #define QL_AT_F32_bf16 0
 #define QL_AT_IS_F32_(t) QL_AT_F32_##t
 #define QL_AT_IS_F32(t) QL_AT_IS_F32_(t)
-// 128 keys in LDS: all but the longest heads in fp32.
-#define QL_AT_SHORT (!QL_AT_IS_F32(QL_AT_T) || QL_AT_DC <= 8)
+// Few keys stay in LDS (k_attn_short, attn_plan): all but long heads.
+#define QL_AT_SHORT (QL_AT_IS_F32(QL_AT_T) ? QL_AT_DC <= 6 : QL_AT_DC <= 8)
 
 typedef QL_AT_T T;
 constexpr int DC = QL_AT_DC;

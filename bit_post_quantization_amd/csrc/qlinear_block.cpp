@@ -339,8 +339,11 @@ namespace ql {
 //     2 x 512 queries, 2048 keys, 16 heads of 72: 37 at 256, 34 at 512, 41 at 1024; but
 //     256 queries, 4608 keys, 16 heads: 28 at 256, 33 at 512, 40 at 1024
 //   few keys, workgroups that go through several tiles of rows, 512: 16 x 1024 queries, up to
-//     120 keys, 16 heads of 72: 35 at 256, 33 at 512, 37 at 768; with the kernel that does
-//     not keep the keys in LDS 38 (30 with it, later)
+//     120 keys, 16 heads of 72: 35 at 256, 33 at 512, 37 at 768
+//   few keys: up to which heads they stay in LDS (else its tiles follow each other), 16 x 1024
+//     queries, kept/not at 77 keys, at 120: bf16, 16 heads of 72 28/38, 31/39; 8 of 128 22/26,
+//     26/27; of 136 32/33, 42/33 (4 x 4096 queries, 77 keys: 30/34); of 160, where keeping spills,
+//     37/36, 45/36; fp32, at 77 keys, 8 of 72 59/64; of 96 65/75; of 128 82/77
 //   gradient, bf16, 512: 2 x 8190 queries, 512 and 156 keys, 16 heads on 8: 377 at 256, 280
 //     at 512; fp32, 256: 8 x 256 queries, 77 keys, 16 heads of 72: 71 at 256, 78 at 512
 AttnPlan attn_plan(const ql_attn& d) {
@@ -356,7 +359,7 @@ AttnPlan attn_plan(const ql_attn& d) {
   const int64_t most = tiles / (p.narrow ? 2 : 4);
   s = s < most ? s : most;
   p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
-  if (!p.narrow && p.splits == 1 && d.k_len <= 128 && (bf16 || d.dim <= 128)) {
+  if (!p.narrow && p.splits == 1 && d.k_len <= 128 && d.dim <= (bf16 ? 128 : 96)) {
     const int64_t each = base / 512;
     p.per_group = (int)(each < 1 ? 1 : each > p.row_tiles ? p.row_tiles : each);
   }
