@@ -494,13 +494,13 @@ __global__ __launch_bounds__(256) void k_rows4_quantize(PackArgs a) {
   }
 }
 
-// Four codes or one scale a thread.
+// Eight codes or one scale a thread: a launch has less than 2^32 of them.
 __global__ __launch_bounds__(256) void k_rows4_unpack(PackArgs a, int8_t* codes, void* scales) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (codes && i < (int64_t)a.N * (a.K / 4)) {
-    const int n = (int)(i / (a.K / 4)), k = (int)(i % (a.K / 4)) * 4;
-    const uint32_t w = a.packed[word_at(a, n, k)] >> (4 * (k % 8));
-    for (int j = 0; j < 4; ++j)
+  if (codes && i < (int64_t)a.N * (a.K / 8)) {
+    const int n = (int)(i / (a.K / 8)), k = (int)(i % (a.K / 8)) * 8;
+    const uint32_t w = a.packed[word_at(a, n, k)];
+    for (int j = 0; j < 8; ++j)
       codes[(int64_t)n * a.K + k + j] = (int8_t)((int)(w << (28 - 4 * j)) >> 28);
   }
   if (scales && i < (int64_t)a.N * a.groups) {
@@ -606,7 +606,7 @@ hipError_t launch_rows4_quantize(const ql_rows4& d, const void* W, bool w_bf16, 
 
 hipError_t launch_rows4_unpack(const ql_rows4& d, int8_t* codes, void* scales, hipStream_t s) {
   const PackArgs a = pack_args(d, d.packed);
-  const int64_t n = (int64_t)a.N * (a.K / 4), m = (int64_t)a.N * a.groups;
+  const int64_t n = (int64_t)a.N * (a.K / 8), m = (int64_t)a.N * a.groups;
   k_rows4_unpack<<<blocks(n > m ? n : m), 256, 0, s>>>(a, codes, scales);
   return hipGetLastError();
 }

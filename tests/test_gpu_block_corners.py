@@ -290,3 +290,26 @@ def test_rows4_tiles_of_a_workgroup(torch, case):  # noqa: F811
     c = Rows4(torch, *case)
     ref, tol = c.formula()
     _within(c.layer().apply(c.X), ref, tol, "Y")
+
+
+def test_rows4_largest_weights(torch):  # noqa: F811
+    """One code short of 2^34: packed, multiplied and unpacked, with the last rows of the
+    weights as the first."""
+    from bit_post_quantization_amd import GroupLinear4
+    N, K, group = 1649373, 10416, 128
+    g = _gen(torch, 7)
+    codes = torch.empty(N, K, dtype=torch.int8, device="cuda")
+    for part in codes.split(1 << 17):
+        part.random_(-8, 8, generator=g)
+    scales = torch.rand(N, -(-K // group), generator=g, device="cuda") + 0.5
+    layer = GroupLinear4.from_codes(codes, scales, group)
+    X = torch.empty(2, K, device="cuda").normal_(generator=g)
+    y = layer.apply(X)
+    some = torch.cat([torch.arange(64), torch.arange(N - 64, N),
+                      torch.randint(0, N, (128,), generator=torch.Generator().manual_seed(1))]).cuda()
+    W = codes[some].double() * scales[some].double().repeat_interleave(group, 1)[:, :K]
+    x = X.double()
+    _within(y[:, some], x @ W.t(), (8 * EPS + 16 * EPS + 4 * math.sqrt(K) * EPS) * (x.abs() @ W.abs().t()), "Y")
+    got, got_scales = layer.weights()
+    assert torch.equal(got_scales, scales)
+    assert all(torch.equal(a, b) for a, b in zip(got.split(1 << 17), codes.split(1 << 17)))
