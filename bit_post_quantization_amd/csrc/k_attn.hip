@@ -18,23 +18,27 @@
 // The softmax runs in base 2 (scale2 = scale log2 e), one pass, with the running
 // maximum and sum in fp32; O is rescaled only where a maximum of the wave rose past 2^8.
 // Roundings: bf16 tensors give bf16 weights P and, in the gradient, bf16 dS (off by at
-// most 2^-8 of themselves, as the rounded result is); fp32 tensors stay
-// fp32 throughout.
+// most 2^-8 of themselves, as the rounded result is), which the bf16 instruction takes at 7.7
+// times the fp32 one's rate; fp32 tensors stay fp32 throughout.
 //
 // Measured per call (MI355X; bf16 unless said; the library's bf16 matrix product reaches
 // 1185 TFLOP/s here, its fp32 one 154, a copy 5.4 TB/s):
-//   2 x 4096 queries, 4608 keys, 16 heads of 128: 335-355 us, 870-920 TFLOP/s (cards and runs differ)
+//   2 x 4096 queries, 4608 keys, 16 heads of 128: 337-349 us, 890-920 TFLOP/s (the first calls
+//     after a pause take up to 372, before the clock is up)
 //   16 x 1024 queries, prompts of up to 120 keys, 16 heads of 72: 24 us, 3.3 TB/s
 //   4 x 1 query over 4608 keys, 16 heads of 64: 19 us, 3.9 TB/s
 //   gradient, 2 x 8190 queries, prompts of 512 and 156, 16 heads on 8 of 128: 257-277 us,
 //     400-430 TFLOP/s of the five products that it takes (seven are done), 680 for two
 //     sequences of 4096 x 4096 with 16 heads
-//   gradient, 8 x 256 queries, 77 keys with holes, 16 heads of 72, fp32: 66-70 us
-// What bounds the large ones: LDS gives one operand of 1 KB in the time of one 32x32x16
-// product, so the products wait for it whenever all SIMDs are at them (with operands from
-// registers instead the first case takes 239 us); 64 rows a wave, which would halve that,
-// do not fit two waves a SIMD at 128 channels, and with one the compiler keeps neither
-// file free of copies (438 us).
+//   gradient, 8 x 256 queries, 77 keys with holes, 16 heads of 72, fp32: 66-71 us
+//   fp32, 2 x 2048 queries and keys: 8 heads of 128 287 us, 16 of 72 371, gradient of 16 of 72
+//     1437; 4 x 1 query over 4608 keys, 16 heads of 64: 57
+// What bounds the large ones: the way of operands from LDS. It is latency, not LDS's rate (busy 34 %
+// of the first case, 24-26 % of the gradient, without conflicts): the products of two waves a SIMD
+// do not cover it (with operands from registers instead the first case takes 239 us). 64 rows a wave,
+// which would halve the reads, do not fit two waves a SIMD at 128 channels, and with one the
+// compiler keeps neither file free of copies (438 us). k_attn_dkv, whose tiles are 32 rows with one
+// more on its way, waits 58 % of its waves' time; in fp32 it also leaves waves without keys idle.
 //
 // This file is compiled once for each type and number DC of 16-channel blocks
 // of a head (QL_AT_T, QL_AT_DC); heads of other sizes are padded with zeros in LDS.
@@ -399,13 +403,13 @@ __device__ __forceinline__ bool bit_of(const KeyBits<W>& k, int i) {
   return (x >> (i & 31)) & 1;
 }
 
-// Waves a SIMD that the registers are to allow: two where they fit, at most a few of them
+// Waves a SIMD that the registers are to allow: two where they fit, at most eleven of them
 // spilled (us with one and with two; bf16, forward, 128 channels: 709, 390, 4 x 4096 queries
 // and keys, 8 heads of 160, nine spilled: 545, 371; fp32, 2 x 2048 queries and keys: forward, 8
 // heads of 96: 250, 224, 8 of 128: 326, 286 (with tiles of 32 keys, below), but one query a
 // sequence and 4096 keys, 16 heads on 8 of 128: 125, 158; gradient, 16 heads of 64: 1112, 920,
 // both kernels 8 of 96: 801, 906, 8 of 128: 1036, 1632). Of 160 channels in fp32 LDS holds
-// one workgroup.
+// one workgroup, and k_attn_dkv's 32 keys a wave spill 92 registers even so.
 constexpr bool kPairs = sizeof(T) == 2;
 template <int WK> constexpr int kForwardWaves = kPairs || DC <= (WK == 1 ? 8 : 6) ? 2 : 1;
 constexpr int kDqWaves = DC <= (kPairs ? 8 : 6) ? 2 : 1, kDkvWaves = DC <= (kPairs ? 8 : 4) ? 2 : 1;
@@ -816,6 +820,7 @@ __global__ __launch_bounds__(kThreads, kDqWaves) void k_attn_dq(AttnArgs a) {
     if (h == 0 && row < a.R) a.delta[at] = delta;
     if (kRowsAt < kTile) __syncthreads();  // the first tile goes there
   }
+  // back in base two: one rounding more, of P's own size times 2^-24 |lse|, as the saved lse's own
   float lse2 = a.lse[at] * kLog2e;
   if (lse2 == -INFINITY) lse2 = INFINITY;  // no key counts: P = 0
   const T* const kp = reinterpret_cast<const T*>(a.k.p) + b * a.k.batch + hk * a.k.head;
@@ -1020,7 +1025,7 @@ __global__ __launch_bounds__(kThreads, kDkvWaves) void k_attn_dkv(AttnArgs a) {
       const int r = t * RT + tid % RT;
       const int64_t at = stat_at(a, b, hk, min(r, a.R - 1));
       if (tid < RT) {
-        stat = a.lse[at] * kLog2e;
+        stat = a.lse[at] * kLog2e;  // rounded as in k_attn_dq
         if (stat == -INFINITY || r >= a.R) stat = INFINITY;  // P = 0
       } else {
         stat = r < a.R ? a.delta[at] : 0.0f;

@@ -15,9 +15,14 @@
 // three terms, it was 28, and the rows' terms 6 bytes instead of 4). A group's four sums
 // are joined in fp32 and scaled: 28 operations for 16 by 16 outputs.
 //
-// Measured: 2 rows, K 1152, N 6912: 5.8 us of kernel (latency); 8 rows, K 4096, N 24576:
-// 4 us of digits and 21 of products, 2.2-2.5 TB/s of the two (adding up as many bytes takes 25); 77 rows,
-// K 4608, N 1151, groups of 32: 4 and 15 us, bound by the joining of its sums and latency.
+// Measured: 2 rows, K 1152, N 6912: 5.6 us of kernel (latency); 8 rows, K 4096, N 24576: 21.4 us a
+// call, of kernels 3-4 for the digits and 18-20 for the products, 2.5 TB/s in all: a wave asks for two
+// of its four units' codes, and for the others only once the workgroup, the only one on its
+// compute unit, has all rows' digits; 77 rows, K 4608, N 1151, groups of 32: 4 and 14 us, bound by
+// the joining of its sums and latency. Beside one large input the digits of the others are coarser:
+// against 64 bits, 8 rows, K 1152, N 4096, one input R times the rest whose codes are 0, outputs are off
+// by 7e-8 of their size up to R = 100, 8e-8 at 1e3, 2e-7 at 4e3, 1.5e-6 at 3e4, 5e-5 at 1e6 (products
+// in fp32: 3e-7).
 //
 // The waves of a workgroup share out the units of its NT tiles of 16 channels and join
 // in LDS. The digits come from LDS where the rows fit: formed there by the workgroup, if

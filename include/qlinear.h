@@ -644,7 +644,8 @@ ql_status qlinear_attention_workspace(const ql_attn* d, int32_t grad, int64_t* b
  * out from q [batch, q_len, heads, dim] and k, v [batch, k_len, kv_heads, dim]; views
  * start at multiples of 16 bytes and so do their strides. Products and sums
  * run in fp32 on the matrix cores; with bf16 tensors the softmax's weights are
- * rounded to bf16 before they meet v, its statistics stay fp32.
+ * rounded to bf16 before they meet v, its statistics stay fp32 (fp32 tensors keep the weights
+ * too).
  *   lse : NULL, or DEVICE fp32 out [batch, heads, q_len]: log of the sum of
  *         exp(scale q k), which the gradient takes.
  * out and lse overlap nothing else.
