@@ -32,7 +32,7 @@
 //     sequences of 4096 x 4096 with 16 heads
 //   gradient, 8 x 256 queries, 77 keys with holes, 16 heads of 72, fp32: 66-71 us
 //   fp32, 2 x 2048 queries and keys: 8 heads of 128 287 us, 16 of 72 371, gradient of 16 of 72
-//     1437; 4 x 1 query over 4608 keys, 16 heads of 64: 57
+//     1437; 4 x 1 query over 4608 keys, 16 heads of 64: 52
 // What bounds the large ones: the way of operands from LDS. It is latency, not LDS's rate (busy 34 %
 // of the first case, 24-26 % of the gradient, without conflicts): the products of two waves a SIMD
 // do not cover it (with operands from registers instead the first case takes 239 us). 64 rows a wave,
@@ -573,7 +573,9 @@ __global__ __launch_bounds__(kThreads, (kForwardWaves<1>)) void k_attn_short(Att
 #endif
 
 // WK waves of a workgroup share its keys, 4 / WK its rows: one, or two in fp32 for up to 64
-// rows (4 x 1 query over 4608 keys, 16 heads of 64: 65 us, 91 with one). In bf16 few rows
+// rows (one query a sequence, us with two and with one: 4 x 4608 keys, 16 heads of 64: 52, 55; 4 x
+// 1000 keys 21, 28; 2 x 4096, 8 of 128 38, 47; 64 queries, 2 x 2048 keys, 16 of 72: 29, 37; only of
+// many long heads one is faster: 8 x 4096 keys, 16 on 8 of 128: 103, 87). In bf16 few rows
 // too are faster with one, the other waves helping to load (8 x 1 query of 32 heads on 8 of
 // 128, 4096 keys: 36 us; with four, 57): two tiles fit LDS.
 template <int WK>

@@ -340,6 +340,9 @@ namespace ql {
 //     256 queries, 4608 keys, 16 heads: 28 at 256, 33 at 512, 40 at 1024
 //   few keys, workgroups that go through several tiles of rows, 512: 16 x 1024 queries, up to
 //     120 keys, 16 heads of 72: 35 at 256, 33 at 512, 37 at 768
+//   forward, waves that share the keys (fp32, up to 64 rows), one a compute unit for heads past 96
+//     and two for others, 2 x 1 query, 4096 keys at 256, 512 and 768: 16 heads of 64 31 31 41, of
+//     72 41 40 52; 8 of 128 38 46 46, of 160 47 56 56; 4 x 1, 4608 keys, 16 of 64: 56 52 57
 //   few keys: up to which heads they stay in LDS (else its tiles follow each other), 16 x 1024
 //     queries, kept/not at 77 keys, at 120: bf16, 16 heads of 72 28/38, 31/39; 8 of 128 22/26,
 //     26/27; of 136 32/33, 42/33 (4 x 4096 queries, 77 keys: 30/34); of 160, where keeping spills,
@@ -355,7 +358,7 @@ AttnPlan attn_plan(const ql_attn& d) {
   p.row_tiles = ceil_div(R, p.narrow ? 64 : 128);
   const int64_t tiles = ceil_div(d.k_len, 64);
   const int64_t base = bh * p.row_tiles;
-  int64_t s = base > 0 ? (p.narrow ? 768 : 512) / base : 1;
+  int64_t s = base > 0 ? (p.narrow && d.dim > 96 ? 256 : 512) / base : 1;
   const int64_t most = tiles / (p.narrow ? 2 : 4);
   s = s < most ? s : most;
   p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
