@@ -407,7 +407,7 @@ __device__ __forceinline__ bool bit_of(const KeyBits<W>& k, int i) {
 // spilled (us with one and with two; bf16, forward, 128 channels: 709, 390, 4 x 4096 queries
 // and keys, 8 heads of 160, nine spilled: 545, 371; fp32, 2 x 2048 queries and keys: forward, 8
 // heads of 96: 250, 224, 8 of 128: 326, 286 (with tiles of 32 keys, below), but one query a
-// sequence and 4096 keys, 16 heads on 8 of 128: 125, 158; gradient, 16 heads of 64: 1112, 920,
+// sequence and 4096 keys, 16 heads on 8 of 128: 103, 118; gradient, 16 heads of 64: 1112, 920,
 // both kernels 8 of 96: 801, 906, 8 of 128: 1036, 1632). Of 160 channels in fp32 LDS holds
 // one workgroup, and k_attn_dkv's 32 keys a wave spill 92 registers even so.
 constexpr bool kPairs = sizeof(T) == 2;

@@ -17,8 +17,8 @@
 // four pairs, and element by element, as other heads would need, 213).
 //
 // Measured: one clip, 17550 tokens of 32 + 4 + 4 heads of 128, bf16: 97-102 us, 3.5-3.7 TB/s, for
-// pairs in halves (LDS is busy 64 % of it, 38 % with conflicts), 78 (4.6) for neighbours; gradient, 18432 tokens of 3 x 16 heads of 128,
-// bf16: 132 us, 5.1 TB/s, and 7 for the sum of dgamma.
+// pairs in halves (LDS is busy 64 % of it, 38 % with conflicts), 78 (4.6) for neighbours;
+// gradient, 18432 tokens of 3 x 16 heads of 128, bf16: 132 us, 5.1 TB/s, and 7 for the sum of dgamma.
 #include "ql_block.h"
 #include "ql_device.h"
 
