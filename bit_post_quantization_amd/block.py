@@ -117,6 +117,11 @@ def _fit(*sizes: int) -> None:
             raise QLError(QL_ERR_ARG, f"size {n}: less than 2^31")
 
 
+def _there(t, name: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise QLError(QL_ERR_ARG, f"{name} is not a tensor")
+
+
 # ----------------------------------------------------------------- 4-bit rows ----
 
 class GroupLinear4:
@@ -147,6 +152,7 @@ class GroupLinear4:
         _need(isinstance(codes, torch.Tensor) and codes.dim() == 2, "codes must be [N, K]")
         _fit(*codes.shape)
         _need(group in (32, 64, 128), f"group = {group} must be 32, 64 or 128")
+        _there(scales, "scales")
         _need(scales.dtype in _DT, f"scales is {scales.dtype}: f32 or bf16 only")
         dev, (N, K) = _device(), codes.shape
         c = _flat(codes, "codes", dev, torch.int8, codes.shape)
@@ -187,6 +193,8 @@ class GroupLinear4:
         if stream is not None:
             with _on(stream):
                 return self.apply(X, out)
+        _there(X, "X")
+        _need(X.dim() == 2, f"X must be [M, {self.K}]")
         dev, M, dt = _device(), X.shape[0], X.dtype
         size = self._sizes.get((dt, M))
         if size is None:
@@ -224,6 +232,7 @@ class GroupLinear4:
 def _view(t, name: str, dev: int, dtype, shape, dense) -> QlHeadsView:
     """A [B, L, H, D] tensor, whose channels are contiguous, as the C ABI takes it; `dense`
     are the strides of a packed one."""
+    _there(t, name)
     if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
         _refuse(t, name, dev, dtype, shape)
     if t.is_contiguous():
@@ -288,6 +297,7 @@ class HeadNormRope:
         """(device, stream, size, x's batch and row stride, positions' address and batch
         stride) of a call; a size is (descriptor, workspace bytes, shapes of q, k and v,
         their dense strides)."""
+        _there(x, "x")
         dev, dt, shape = _device(), x.dtype, x.shape
         if x.get_device() != dev or dev != self._dev:
             _need(dev == self._dev, "the layer was made on another device")
@@ -403,13 +413,14 @@ class CrossAttention:
         self.kv_heads = heads if kv_heads is None else kv_heads
         _fit(heads, dim, self.kv_heads)
         self.desc = QlAttn(batch=0, q_len=0, k_len=0, heads=heads, kv_heads=self.kv_heads, dim=dim,
-                           dtype=_lib.QL_F32, scale=dim ** -0.5 if scale is None else scale)
+                           dtype=_lib.QL_F32, scale=max(dim, 1) ** -0.5 if scale is None else scale)
         qlinear_attention_workspace(self.desc)  # its checks
         self._sizes = {}  # descriptor and workspace bytes by size of call
 
     def _call(self, dev, q, k, lens, mask, grad):
         """(descriptor, workspace bytes, shapes of queries and keys, their dense strides)
         of a call."""
+        _there(k, "k")
         key = (q.dtype, q.shape, k.shape, grad)
         size = self._sizes.get(key)
         if size is None:
@@ -418,8 +429,10 @@ class CrossAttention:
             return size
         d = QlAttn.from_buffer_copy(size[0])
         if lens is not None:
+            _there(lens, "lens")
             d.k_lens = _flat(lens, "lens", dev, _I32, (d.batch,))
         if mask is not None:
+            _there(mask, "mask")
             _need(mask.dtype in (torch.bool, torch.uint8), f"mask is {mask.dtype}, not bool")
             d.mask_batch = _rows(mask, "mask", dev, mask.dtype, (d.batch, d.k_len))
             d.k_mask = mask.data_ptr()
@@ -444,6 +457,7 @@ class CrossAttention:
         if stream is not None:
             with _on(stream):
                 return self.forward(q, k, v, lens, mask, out, save)
+        _there(q, "q")
         dev, dt = _device(), q.dtype
         d, nb, qs, ks, qd, kd = self._call(dev, q, k, lens, mask, 0)
         vq, vk = _view(q, "q", dev, dt, qs, qd), _view(k, "k", dev, dt, ks, kd)
@@ -465,11 +479,13 @@ class CrossAttention:
         if stream is not None:
             with _on(stream):
                 return self.grad(dout, q, k, v, out, lse, lens, mask, into)
+        _there(q, "q")
         dev, dt = _device(), q.dtype
         d, nb, qs, ks, qd, kd = self._call(dev, q, k, lens, mask, 1)
         vq, vk = _view(q, "q", dev, dt, qs, qd), _view(k, "k", dev, dt, ks, kd)
         vv, vd = _view(v, "v", dev, dt, ks, kd), _view(dout, "dout", dev, dt, qs, qd)
         vo = _view(out, "out", dev, dt, qs, qd)
+        _there(lse, "lse")
         at = _flat(lse, "lse", dev, _F32, (qs[0], qs[2], qs[1]))
         if into is None:
             into = [torch.empty(s, dtype=dt, device=q.device) for s in (qs, ks, ks)]

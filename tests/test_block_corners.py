@@ -98,3 +98,23 @@ def test_what_a_layer_holds_outlives_it_on_other_streams(on_cpu, monkeypatch):  
     h.gamma_q = None  # 1
     h.forward(x)
     assert h.gamma_k.on == ["side", "side"]
+
+
+def test_missing_arguments_are_refused(on_cpu, monkeypatch):  # noqa: F811
+    """A tensor that is not there, or a size of 0, raises what other arguments that do not fit
+    raise."""
+    a, x = block.CrossAttention(2, 64), torch.zeros(1, 3, 2, 64)
+    h, rows = block.HeadNormRope((1, 1, 0), 8, norm="none"), torch.zeros(1, 2, 16)
+    lse, part = torch.zeros(1, 2, 3), torch.zeros(1, 2, 1, 8, dtype=torch.bfloat16)
+    codes = torch.zeros(4, 32, dtype=torch.int8)
+    for call in (lambda: a.forward(x, x, None), lambda: a.forward(x, None, x),
+                 lambda: a.forward(None, x, x), lambda: a.grad(None, x, x, x, x, lse),
+                 lambda: a.grad(x, x, x, x, x, None),
+                 lambda: a.grad(x, x, x, x, x, lse, into=(x, None, x)),
+                 lambda: a.forward(x, x, x, lens=3), lambda: a.forward(x, x, x, mask=[True] * 3),
+                 lambda: h.forward(None), lambda: h.forward(rows, out=(part, None, None)),
+                 lambda: h.grad((part, None, None), rows), lambda: _rows().apply(None),
+                 lambda: block.CrossAttention(2, 0), lambda: block.CrossAttention(2, -8),
+                 lambda: block.GroupLinear4.from_codes(codes, None, 32)):
+        with pytest.raises(QLError):
+            call()

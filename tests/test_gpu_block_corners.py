@@ -7,7 +7,8 @@ import math
 import pytest
 
 from tests.parity import say
-from tests.test_gpu_block import EPS, Attn, Heads, Rows4, _gen, _round, _same_lse, _within, torch  # noqa: F401
+from tests.test_gpu_block import (EPS, Attn, Heads, Rows4, _gen, _round, _same_lse,  # noqa: F401
+                                  _sum, _within, torch)
 
 pytestmark = pytest.mark.gpu
 
@@ -306,10 +307,11 @@ def test_rows4_largest_weights(torch):  # noqa: F811
     X = torch.empty(2, K, device="cuda").normal_(generator=g)
     y = layer.apply(X)
     some = torch.cat([torch.arange(64), torch.arange(N - 64, N),
-                      torch.randint(0, N, (128,), generator=torch.Generator().manual_seed(1))]).cuda()
+                      torch.randint(0, N, (128,), generator=torch.Generator().manual_seed(1))])
+    some = some.cuda()
     W = codes[some].double() * scales[some].double().repeat_interleave(group, 1)[:, :K]
     x = X.double()
-    _within(y[:, some], x @ W.t(), (8 * EPS + 16 * EPS + 4 * math.sqrt(K) * EPS) * (x.abs() @ W.abs().t()), "Y")
+    _within(y[:, some], x @ W.t(), (8 * EPS + _sum(K)) * (x.abs() @ W.abs().t()), "Y")
     got, got_scales = layer.weights()
     assert torch.equal(got_scales, scales)
     assert all(torch.equal(a, b) for a, b in zip(got.split(1 << 17), codes.split(1 << 17)))
